@@ -30,6 +30,8 @@ SOURCES = [
     ("csrc/svq_encode.hip", []),
     ("csrc/svq_calib.hip", []),
     ("csrc/svq_scratch.hip", []),
+    ("csrc/svq_ffn.cpp", []),
+    ("csrc/svq_ffn.hip", []),
 ]
 # kept for callers that list the flags of the exact-path kernels
 HIPCC_FLAGS = COMMON_FLAGS + ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]

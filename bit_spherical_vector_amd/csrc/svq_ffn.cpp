@@ -1,0 +1,236 @@
+// Host side of the feed-forward calls (include/svq_ffn.h): argument checks,
+// workspace layout and dispatch.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "svq_ffn.h"
+
+using namespace svq;
+
+namespace {
+
+bool valid_dt(svq_dtype t) { return t == SVQ_BF16 || t == SVQ_F32; }
+bool valid_act(svq_act a) { return (int)a >= SVQ_ACT_NONE && (int)a <= SVQ_ACT_GELU_TANH; }
+size_t size_of(svq_dtype t) { return t == SVQ_F32 ? 4 : 2; }
+bool aligned(const void *p, int64_t row_elems, size_t esz, size_t to) {
+  return (((uintptr_t)p) | ((uintptr_t)row_elems * esz)) % to == 0;
+}
+int64_t pad4(int64_t n) { return (n + 3) / 4 * 4; }
+
+}  // namespace
+
+extern "C" {
+
+svq_status svq_linear_epilogue(const svq_handle *w, const void *x, int64_t m, int64_t ldx,
+                               const svq_epilogue *ep, void *y, int64_t ldy, svq_dtype ydt,
+                               void *workspace, size_t *workspace_bytes, void *stream) {
+  if (!w || !ep || !workspace_bytes) return SVQ_ERR_INVALID_ARG;
+  const svq_status st = check_handle(w);
+  if (st != SVQ_OK) return st;
+  if (!valid_act(ep->act) || (ep->bias && !valid_dt(ep->bias_dt))) return SVQ_ERR_INVALID_ARG;
+  if (ep->residual && (!valid_dt(ep->residual_dt) || ep->ldr < w->n)) return SVQ_ERR_INVALID_ARG;
+  EpiArgs e;
+  std::memset(&e, 0, sizeof(e));
+  e.act = (int32_t)ep->act;
+  e.bias = ep->bias;
+  e.bias_f32 = ep->bias_dt == SVQ_F32;
+  e.bias_vec = aligned(ep->bias, 0, 1, 4 * size_of(ep->bias_dt));
+  if (ep->residual) {
+    e.res = ep->residual;
+    e.ldr = ep->ldr;
+    e.res_f32 = ep->residual_dt == SVQ_F32;
+    e.res_vec = aligned(ep->residual, ep->ldr, size_of(ep->residual_dt), 4 * size_of(ep->residual_dt));
+    if (ep->residual == y && (ep->ldr != ldy || ep->residual_dt != ydt)) return SVQ_ERR_INVALID_ARG;
+  }
+  return linear_epi(w, 1, workspace ? &x : nullptr, &ldx, m, workspace ? &y : nullptr, &ldy, ydt, &e, workspace,
+                    workspace_bytes, stream);
+}
+
+svq_status svq_linear_glu(const svq_handle *gate, const svq_handle *up, const void *x, int64_t m,
+                          int64_t ldx, svq_act act, const void *bias_gate, const void *bias_up,
+                          svq_dtype bias_dt, void *y, int64_t ldy, svq_dtype ydt,
+                          void *workspace, size_t *workspace_bytes, void *stream) {
+  if (!gate || !up || !workspace_bytes) return SVQ_ERR_INVALID_ARG;
+  svq_status st = check_handle(gate);
+  if (st == SVQ_OK) st = check_handle(up);
+  if (st != SVQ_OK) return st;
+  if (gate->n != up->n || gate->k != up->k) return SVQ_ERR_INVALID_ARG;
+  if (!valid_act(act) || !valid_dt(ydt)) return SVQ_ERR_INVALID_ARG;
+  if ((bias_gate || bias_up) && !valid_dt(bias_dt)) return SVQ_ERR_INVALID_ARG;
+  if (m < 1 || m > (1 << 24) || ldx < gate->k || ldy < gate->n) return SVQ_ERR_INVALID_ARG;
+  const int64_t ldp = pad4(gate->n);
+  const svq_handle w[2] = {*gate, *up};
+  const int64_t lx[2] = {ldx, ldx}, ly[2] = {ldp, ldp};
+  size_t inner = 0;
+  st = linear_epi(w, 2, nullptr, lx, m, nullptr, ly, SVQ_F32, nullptr, nullptr, &inner, stream);
+  if (st != SVQ_OK) return st;
+  const size_t part = align256((size_t)m * ldp * 4), need = 2 * part + inner;
+  if (!workspace) {
+    *workspace_bytes = need;
+    return SVQ_OK;
+  }
+  if (!x || !y) return SVQ_ERR_INVALID_ARG;
+  if (*workspace_bytes < need) return SVQ_ERR_BUFFER_TOO_SMALL;
+  uint8_t *ws = (uint8_t *)workspace;
+  const void *xs[2] = {x, x};
+  void *ys[2] = {ws, ws + part};
+  st = linear_epi(w, 2, xs, lx, m, ys, ly, SVQ_F32, nullptr, ws + 2 * part, &inner, stream);
+  if (st != SVQ_OK) return st;
+  GluArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.g = (const float *)ws;
+  a.u = (const float *)(ws + part);
+  a.rows = m;
+  a.ldp = ldp;
+  a.bias_g = bias_gate;
+  a.bias_u = bias_up;
+  a.bias_f32 = bias_dt == SVQ_F32;
+  a.act = (int32_t)act;
+  a.y = y;
+  a.ldy = ldy;
+  a.n = gate->n;
+  a.ydt = (int32_t)ydt;
+  return launch_glu(a, (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
+}
+
+svq_status svq_moe_route(const void *x, int64_t m, int64_t ldx, const void *w, svq_dtype wdt,
+                         int32_t num_experts, int32_t k, int64_t ldw, const float *select_bias,
+                         svq_route_score score, int32_t renormalize, float scale, int32_t topk,
+                         int32_t *ids, float *weights, void *workspace, size_t *workspace_bytes,
+                         void *stream) {
+  if (!workspace_bytes) return SVQ_ERR_INVALID_ARG;
+  if (num_experts < 1 || num_experts > MAX_EXPERTS) return SVQ_ERR_UNSUPPORTED;
+  if (topk < 1 || topk > num_experts) return SVQ_ERR_INVALID_ARG;
+  if (topk > ROUTE_MAX_TOPK) return SVQ_ERR_UNSUPPORTED;
+  if (m < 1 || m > (1 << 20) || k < 1 || ldx < k || ldw < k) return SVQ_ERR_INVALID_ARG;
+  if (k > SVQ_MAX_K) return SVQ_ERR_UNSUPPORTED;
+  if (!valid_dt(wdt) || (renormalize != 0 && renormalize != 1)) return SVQ_ERR_INVALID_ARG;
+  if (score != SVQ_ROUTE_SOFTMAX && score != SVQ_ROUTE_SIGMOID) return SVQ_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return SVQ_ERR_INVALID_ARG;
+  const size_t need = 256;  // nothing is kept between launches
+  if (!workspace) {
+    *workspace_bytes = need;
+    return SVQ_OK;
+  }
+  if (!x || !w || !ids || !weights) return SVQ_ERR_INVALID_ARG;
+  if (*workspace_bytes < need) return SVQ_ERR_BUFFER_TOO_SMALL;
+  RouteArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = (const uint16_t *)x;
+  a.m = m;
+  a.ldx = ldx;
+  a.w = w;
+  a.ldw = ldw;
+  a.select_bias = select_bias;
+  a.k = k;
+  a.num_experts = num_experts;
+  a.topk = topk;
+  a.score = (int32_t)score;
+  a.renormalize = renormalize;
+  a.w_f32 = wdt == SVQ_F32;
+  a.vec = k % 8 == 0 && aligned(x, ldx, 2, 16) && aligned(w, ldw, size_of(wdt), 16);
+  a.scale = scale;
+  a.ids = ids;
+  a.weights = weights;
+  return launch_route(a, compute_units(), (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
+}
+
+svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_handle *down,
+                       int32_t num_experts, const void *x, int64_t ldx, const int32_t *expert_ids,
+                       const float *weights, int64_t m, int32_t topk, svq_act act,
+                       const void *residual, int64_t ldr, svq_dtype residual_dt, void *y,
+                       int64_t ldy, svq_dtype ydt, void *workspace, size_t *workspace_bytes,
+                       void *stream) {
+  if (!gate || !up || !down || !workspace_bytes) return SVQ_ERR_INVALID_ARG;
+  if (num_experts < 1 || num_experts > MAX_EXPERTS) return SVQ_ERR_UNSUPPORTED;
+  if (topk < 1 || topk > num_experts || m < 1 || m > (1 << 20)) return SVQ_ERR_INVALID_ARG;
+  if (!valid_act(act) || !valid_dt(ydt)) return SVQ_ERR_INVALID_ARG;
+  const svq_handle *const sets[3] = {gate, up, down};
+  for (int c = 0; c < 3; ++c)
+    for (int32_t e = 0; e < num_experts; ++e) {
+      const svq_status st = check_handle(&sets[c][e]);
+      if (st != SVQ_OK) return st;
+      if (sets[c][e].n != sets[c][0].n || sets[c][e].k != sets[c][0].k) return SVQ_ERR_INVALID_ARG;
+    }
+  if (gate->n != up->n || gate->k != up->k || down->k != gate->n) return SVQ_ERR_INVALID_ARG;
+  if (ldx < gate->k || ldy < down->n) return SVQ_ERR_INVALID_ARG;
+  if (residual && (!valid_dt(residual_dt) || ldr < down->n)) return SVQ_ERR_INVALID_ARG;
+  const int64_t S = m * topk;
+  const int32_t f = gate->n, n = down->n;
+  const int64_t ldf = pad4(f), ldh = (f + 7) / 8 * 8, ldd = pad4(n);
+  // workspace: gate and up sums, the inner activation, the slots' outputs,
+  // then the products' own workspace (used in turn)
+  size_t inner = 0, ws1 = 0, ws2 = 0;
+  svq_status st = svq_moe_linear(gate, num_experts, nullptr, ldx, 0, nullptr, m, topk, nullptr, ldf, SVQ_F32,
+                                 nullptr, &ws1, stream);
+  if (st == SVQ_OK)
+    st = svq_moe_linear(down, num_experts, nullptr, ldh, 1, nullptr, m, topk, nullptr, ldd, SVQ_F32, nullptr,
+                        &ws2, stream);
+  if (st != SVQ_OK) return st;
+  inner = ws1 > ws2 ? ws1 : ws2;
+  const size_t b_g = align256((size_t)S * ldf * 4), b_h = align256((size_t)S * ldh * 2),
+               b_d = align256((size_t)S * ldd * 4);
+  // up to 64 slots the inner activation is kept to 16 bits of mantissa: two
+  // bf16 halves, each through the down product
+  const int halves = S <= 64 ? 2 : 1;
+  const size_t need = 2 * b_g + halves * (b_h + b_d) + inner;
+  if (!workspace) {
+    *workspace_bytes = need;
+    return SVQ_OK;
+  }
+  if (!x || !expert_ids || !weights || !y) return SVQ_ERR_INVALID_ARG;
+  if (residual == y && (ldr != ldy || residual_dt != ydt)) return SVQ_ERR_INVALID_ARG;
+  if (*workspace_bytes < need) return SVQ_ERR_BUFFER_TOO_SMALL;
+  uint8_t *ws = (uint8_t *)workspace;
+  float *g = (float *)ws, *u = (float *)(ws + b_g);
+  uint8_t *h = ws + 2 * b_g;
+  float *d = (float *)(ws + 2 * b_g + halves * b_h);
+  uint8_t *iw = ws + 2 * b_g + halves * (b_h + b_d);
+  size_t cap = inner;
+  st = svq_moe_linear(gate, num_experts, x, ldx, 0, expert_ids, m, topk, g, ldf, SVQ_F32, iw, &cap, stream);
+  if (st == SVQ_OK)
+    st = svq_moe_linear(up, num_experts, x, ldx, 0, expert_ids, m, topk, u, ldf, SVQ_F32, iw, &cap, stream);
+  if (st != SVQ_OK) return st;
+  GluArgs ga;
+  std::memset(&ga, 0, sizeof(ga));
+  ga.g = g;
+  ga.u = u;
+  ga.rows = S;
+  ga.ldp = ldf;
+  ga.act = (int32_t)act;
+  ga.y = h;
+  ga.y_lo = halves == 2 ? h + b_h : nullptr;
+  ga.ldy = ldh;
+  ga.n = f;
+  ga.ydt = SVQ_BF16;
+  if (launch_glu(ga, (hipStream_t)stream) != hipSuccess) return SVQ_ERR_HIP;
+  st = svq_moe_linear(down, num_experts, h, ldh, 1, expert_ids, m, topk, d, ldd, SVQ_F32, iw, &cap, stream);
+  CombineArgs ca;
+  std::memset(&ca, 0, sizeof(ca));
+  if (halves == 2 && st == SVQ_OK) {
+    float *d_lo = (float *)((uint8_t *)d + b_d);
+    st = svq_moe_linear(down, num_experts, h + b_h, ldh, 1, expert_ids, m, topk, d_lo, ldd, SVQ_F32, iw, &cap,
+                        stream);
+    ca.d_lo = d_lo;
+  }
+  if (st != SVQ_OK) return st;
+  ca.d = d;
+  ca.ldd = ldd;
+  ca.ids = expert_ids;
+  ca.weights = weights;
+  ca.m = m;
+  ca.topk = topk;
+  ca.num_experts = num_experts;
+  ca.res = residual;
+  ca.ldr = ldr;
+  ca.res_f32 = residual_dt == SVQ_F32;
+  ca.y = y;
+  ca.ldy = ldy;
+  ca.n = n;
+  ca.ydt = (int32_t)ydt;
+  return launch_combine(ca, (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,62 @@
+// Launch interfaces of the feed-forward calls (not part of the public ABI).
+#pragma once
+#include "svq_internal.h"
+
+#include "../../include/svq_ffn.h"
+
+namespace svq {
+
+// ---- host code shared with svq_host.cpp ------------------------------------
+svq_status linear_epi(const svq_handle *w, int32_t count, const void *const *x, const int64_t *ldx, int64_t m,
+                      void *const *y, const int64_t *ldy, svq_dtype ydt, const EpiArgs *epi,
+                      void *workspace, size_t *workspace_bytes, void *stream);
+svq_status check_handle(const svq_handle *w);
+int compute_units();  // of the current device
+
+// ---- elementwise steps -------------------------------------------------------
+struct GluArgs {
+  const float *g, *u;  // [rows][ldp]
+  int64_t rows, ldp;
+  const void *bias_g, *bias_u;  // [n] or null
+  int32_t bias_f32, act;
+  void *y;
+  void *y_lo;  // bf16 rest of every value, or null
+  int64_t ldy;
+  int32_t n, ydt;
+};
+hipError_t launch_glu(const GluArgs &a, hipStream_t s);
+
+struct CombineArgs {
+  const float *d;     // [m * topk][ldd]
+  const float *d_lo;  // added to d, or null
+  int64_t ldd;
+  const int32_t *ids;
+  const float *weights;
+  int64_t m;
+  int32_t topk, num_experts;
+  const void *res;
+  int64_t ldr;
+  int32_t res_f32;
+  void *y;
+  int64_t ldy;
+  int32_t n, ydt;
+};
+hipError_t launch_combine(const CombineArgs &a, hipStream_t s);
+
+// ---- router --------------------------------------------------------------------
+constexpr int ROUTE_MAX_TOPK = 32;
+struct RouteArgs {
+  const uint16_t *x;
+  int64_t m, ldx;
+  const void *w;  // [num_experts][ldw], bf16 or fp32 (w_f32)
+  int64_t ldw;
+  const float *select_bias;
+  int32_t k, num_experts, topk, score, renormalize, w_f32;
+  int32_t vec;  // k a multiple of 8, every row 16-byte aligned
+  float scale;
+  int32_t *ids;
+  float *weights;
+};
+hipError_t launch_route(const RouteArgs &a, int cus, hipStream_t s);
+
+}  // namespace svq

@@ -490,10 +490,11 @@ static size_t plan_splits(const svq_handle *w, int32_t count, int m_pad, int bm,
   return bytes;
 }
 
+// epi: epilogue of the product (count == 1), or null.
 static svq_status linear_impl(const svq_handle *w, int32_t count, const void *const *xs,
                               const int64_t *ldx, int64_t m, void *const *ys, const int64_t *ldy,
                               svq_dtype ydt, void *workspace, size_t *workspace_bytes,
-                              void *stream) {
+                              void *stream, const EpiArgs *epi = nullptr) {
   if (!workspace_bytes || !w) return SVQ_ERR_INVALID_ARG;
   if (count < 1 || count > GV_MAX_JOBS) return SVQ_ERR_INVALID_ARG;
   if (m < 1 || m > (1 << 24)) return SVQ_ERR_INVALID_ARG;
@@ -536,7 +537,12 @@ static svq_status linear_impl(const svq_handle *w, int32_t count, const void *co
       }
       size_t cap = *workspace_bytes;
       const int64_t mc = m - r0 < EXACT_MAX_M ? m - r0 : EXACT_MAX_M;
-      st = linear_impl(w, count, xc, ldx, mc, yc, ldy, ydt, workspace, &cap, stream);
+      EpiArgs ec;
+      if (epi) {
+        ec = *epi;
+        if (ec.res) ec.res = (const uint8_t *)ec.res + (size_t)(r0 * ec.ldr) * (ec.res_f32 ? 4 : 2);
+      }
+      st = linear_impl(w, count, xc, ldx, mc, yc, ldy, ydt, workspace, &cap, stream, epi ? &ec : nullptr);
       if (st != SVQ_OK) return st;
     }
     return SVQ_OK;
@@ -589,6 +595,7 @@ static svq_status linear_impl(const svq_handle *w, int32_t count, const void *co
   if (exact) {
     GemvBatch b;
     std::memset(&b, 0, sizeof(b));
+    b.epi = epi;
     b.count = count;
     b.m = (int)m;
     b.ydt = (int)ydt;
@@ -633,6 +640,7 @@ static svq_status linear_impl(const svq_handle *w, int32_t count, const void *co
     // every (tile group, K range) of every matrix
     SbBatch b;
     std::memset(&b, 0, sizeof(b));
+    b.epi = epi;
     b.count = count;
     b.m = (int)m;
     b.ydt = (int)ydt;
@@ -684,6 +692,7 @@ static svq_status linear_impl(const svq_handle *w, int32_t count, const void *co
     // launch), then one GEMM launch over all of them, longest k first
     PrefillBatch b;
     std::memset(&b, 0, sizeof(b));
+    b.epi = epi;
     b.count = count;
     b.ydt = (int)ydt;
     uint8_t *ws = (uint8_t *)workspace;
@@ -763,6 +772,21 @@ static svq_status linear_impl(const svq_handle *w, int32_t count, const void *co
   }
   return e == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
 }
+
+}  // extern "C"
+
+namespace svq {
+// The product and its checks for the calls of svq_ffn.cpp.
+svq_status linear_epi(const svq_handle *w, int32_t count, const void *const *x, const int64_t *ldx, int64_t m,
+                      void *const *y, const int64_t *ldy, svq_dtype ydt, const EpiArgs *epi,
+                      void *workspace, size_t *workspace_bytes, void *stream) {
+  return linear_impl(w, count, x, ldx, m, y, ldy, ydt, workspace, workspace_bytes, stream, epi);
+}
+svq_status check_handle(const svq_handle *w) { return validate_handle(w); }
+int compute_units() { return device_cus(); }
+}  // namespace svq
+
+extern "C" {
 
 svq_status svq_linear(const svq_handle *w, const void *x, int64_t m, int64_t ldx, void *y,
                       int64_t ldy, svq_dtype ydt, void *workspace, size_t *workspace_bytes,

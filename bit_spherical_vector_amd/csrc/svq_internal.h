@@ -83,6 +83,16 @@ struct MatView {
   int32_t n_tiles, units;
 };
 
+// Epilogue of a product: y = act(acc + bias[n]) + res[row * ldr + n].  bias
+// and res may be null; act is an svq_act value.
+struct EpiArgs {
+  const void *bias;  // [n], fp32 (bias_f32) or bf16
+  const void *res;   // [m][ldr], fp32 (res_f32) or bf16
+  int64_t ldr;
+  int32_t act, bias_f32, res_f32;
+  int32_t bias_vec, res_vec;  // rows allow loads of four values
+};
+
 // ---- dense path ---------------------------------------------------------
 // Exact path, m = 2..4: a gather launch writes every matrix's permuted,
 // per-unit scaled fp16 activations to the workspace (xg: row a of unit u at
@@ -119,6 +129,7 @@ struct GemvBatch {
   int32_t red_off;          // LDS offset of the partial sums (after the tables)
   int32_t touch_begin;      // gather launch: first of the 8*count table-touch blocks
   int32_t xvec;             // every activation row starts 16-byte aligned
+  const EpiArgs *epi;       // host: epilogue of a single-matrix call, or null
 };
 constexpr size_t GV_LDS_LIMIT = 160 * 1024;  // LDS per workgroup on gfx950
 constexpr int GV_WAVES = 4;
@@ -215,6 +226,7 @@ struct SbBatch {
   JobStarts starts, prep_starts;
   SbJob job[GV_MAX_JOBS];
   int32_t count, m, ydt;
+  const EpiArgs *epi;  // host: epilogue of a single-matrix call, or null
 };
 // Block shape of one matrix: tiles per block, units per range, ranges,
 // tile groups.  `items` = work items per block the call aims for
@@ -262,6 +274,7 @@ struct PrefillBatch {
   PrefillJob job[GV_MAX_JOBS];
   int32_t count, ydt;
   int32_t yvec;  // every output row of every job starts 16-byte aligned
+  const EpiArgs *epi;  // host: epilogue of a single-matrix call, or null
 };
 int prefill_bm(int m);      // activation rows per block tile: 256 (m >= PREFILL_MIN_M) or 64
 int prefill_m_pad(int m);   // m rounded up to prefill_bm(m)

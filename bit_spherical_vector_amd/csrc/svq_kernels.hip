@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "svq_device.h"
+#include "svq_epilogue.h"
 #include "../../include/svq.h"
 
 namespace svq {
@@ -420,10 +421,11 @@ __device__ __forceinline__ void gemv_item(const GvItem<M> &it, const DirAddr &dm
 
 // Main launch, one block: tiles t0 .. t0+Reff-1 of matrix w (U units each),
 // activations gathered at xg / xs (row a of unit u at xg + (a*U + u) * 1 KB).
-template <int M>
+template <int M, typename EPI = NoEpi>
 __device__ void gemv_main_block(const MatView &w, const uint8_t *__restrict__ xg,
-                                const float *__restrict__ xs, void *__restrict__ y, int64_t ldy,
-                                int ydt, int t0, int Reff, int red_off, uint8_t *smem) {
+                                const float *__restrict__ xs, void *y, int64_t ldy,
+                                int ydt, int t0, int Reff, int red_off, uint8_t *smem,
+                                const EPI &epi = EPI()) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform
   const int U = w.units, F = Reff * U;
@@ -563,7 +565,7 @@ __device__ void gemv_main_block(const MatView &w, const uint8_t *__restrict__ xg
 #pragma unroll
     for (int p = 0; p < GV_WAVES * 4; ++p) sum += s_red[((t * GV_WAVES * 4 + p) * 4 + j) * 4 * M + ri * M + a];
     const int n = (t0 + t) * 16 + row;
-    if (n < w.n) store_out(y, (size_t)a * ldy + n, sum, ydt);
+    if (n < w.n) store_out(y, (size_t)a * ldy + n, epi(sum, a, n), ydt);
   }
 }
 
@@ -575,6 +577,17 @@ __global__ __launch_bounds__(256) void gemv_batched_kernel(GemvBatch b) {
   const int t0 = ((int)blockIdx.x - b.starts.first[j]) * jb.R;
   const int Reff = min(jb.R, jb.w.n_tiles - t0);
   gemv_main_block<M>(jb.w, jb.xg, jb.xs, jb.y, jb.ldy, b.ydt, t0, Reff, b.red_off, smem);
+}
+
+// The main launch of one matrix with its epilogue.
+template <int M>
+__global__ __launch_bounds__(256) void gemv_epi_kernel(GemvBatch b, EpiArgs ea) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const GemvJob &jb = b.job[0];
+  const int t0 = (int)blockIdx.x * jb.R;
+  const int Reff = min(jb.R, jb.w.n_tiles - t0);
+  const Epi epi{ea};
+  gemv_main_block<M, Epi>(jb.w, jb.xg, jb.xs, jb.y, jb.ldy, b.ydt, t0, Reff, b.red_off, smem, epi);
 }
 
 
@@ -590,6 +603,14 @@ static hipError_t check_no_static_lds(Kern k) {
 
 template <int M>
 static hipError_t launch_gemv_m(GemvBatch &b, int blocks, size_t smem, hipStream_t s) {
+  if (b.epi) {
+    static const hipError_t epi_ok = check_no_static_lds(gemv_epi_kernel<M>);
+    if (epi_ok != hipSuccess) return epi_ok;
+    const hipError_t e = allow_smem(gemv_epi_kernel<M>, smem);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gemv_epi_kernel<M>), dim3(blocks), dim3(256), smem, s, b, *b.epi);
+    return hipGetLastError();
+  }
   static const hipError_t lds_ok = check_no_static_lds(gemv_batched_kernel<M>);
   if (lds_ok != hipSuccess) return lds_ok;
   hipError_t e = allow_smem(gemv_batched_kernel<M>, smem);
@@ -766,10 +787,10 @@ __device__ __forceinline__ void gf_item(const ItemCodes &c, const uint8_t *xu, u
 
 // XVEC: every activation row starts 16-byte aligned (vector staging loads).
 // BD: the matrix's direction bits (table layout, see above).
-template <int M, bool XVEC, int BD>
+template <int M, bool XVEC, int BD, typename EPI = NoEpi>
 __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ x, int64_t ldx,
-                                 void *__restrict__ y, int64_t ldy, int ydt, int rt0, int R,
-                                 int Reff, uint8_t *smem) {
+                                 void *y, int64_t ldy, int ydt, int rt0, int R,
+                                 int Reff, uint8_t *smem, const EPI &epi = EPI()) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform
   const int U = w.units, Kp = U * UNIT_SLOTS, K = w.k;
@@ -1036,7 +1057,7 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
 #pragma unroll
     for (int p = 0; p < GV_WAVES; ++p) sum += s_red[(((t * GV_WAVES + p) * 4 + ri) * M + a) * 4 + j];
     const int n = (rt0 + t) * 16 + row;
-    if (n < w.n) store_out(y, (size_t)a * ldy + n, sum, ydt);
+    if (n < w.n) store_out(y, (size_t)a * ldy + n, epi(sum, a, n), ydt);
   }
 }
 
@@ -1064,8 +1085,33 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void g
 }
 
 
+// The fused launch of one matrix with its epilogue.
+template <bool XVEC>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void gemv_fused_epi_kernel(GemvBatch b,
+                                                                                                   EpiArgs ea) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const GemvJob &jb = b.job[0];
+  const int rt0 = (int)blockIdx.x * jb.R;
+  const int Reff = min(jb.R, jb.w.n_tiles - rt0);
+  const Epi epi{ea};
+  if (jb.w.bd >= 8)
+    gemv_fused_block<1, XVEC, 8, Epi>(jb.w, jb.x, jb.ldx, jb.y, jb.ldy, b.ydt, rt0, jb.R, Reff, smem, epi);
+  else if (jb.w.bd == 7)
+    gemv_fused_block<1, XVEC, 7, Epi>(jb.w, jb.x, jb.ldx, jb.y, jb.ldy, b.ydt, rt0, jb.R, Reff, smem, epi);
+  else
+    gemv_fused_block<1, XVEC, 6, Epi>(jb.w, jb.x, jb.ldx, jb.y, jb.ldy, b.ydt, rt0, jb.R, Reff, smem, epi);
+}
+
 template <bool XVEC>
 static hipError_t launch_fused_x(GemvBatch &b, int blocks, size_t smem, hipStream_t s) {
+  if (b.epi) {
+    static const hipError_t epi_ok = check_no_static_lds(gemv_fused_epi_kernel<XVEC>);
+    if (epi_ok != hipSuccess) return epi_ok;
+    const hipError_t e = allow_smem(gemv_fused_epi_kernel<XVEC>, smem);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gemv_fused_epi_kernel<XVEC>), dim3(blocks), dim3(256), smem, s, b, *b.epi);
+    return hipGetLastError();
+  }
   static const hipError_t lds_ok = check_no_static_lds(gemv_fused_kernel<XVEC>);
   if (lds_ok != hipSuccess) return lds_ok;
   hipError_t e = allow_smem(gemv_fused_kernel<XVEC>, smem);

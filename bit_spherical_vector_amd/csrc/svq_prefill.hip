@@ -39,6 +39,7 @@
 #include <type_traits>
 
 #include "svq_device.h"
+#include "svq_epilogue.h"
 #include "../../include/svq.h"
 
 namespace svq {
@@ -129,11 +130,40 @@ struct DqTile {
   const int32_t *ymap;
 };
 
+// Output of a tile with an epilogue: each wave's accumulators go through its
+// private 16 KB of LDS as fp32, 32 rows a pass, and come back four columns a
+// lane, where bias, activation and residual apply once per value in a short
+// loop (in the unrolled accumulator order the activation's code would be
+// repeated for every register).
+template <int NI, int NJ, int TM, int TN, typename EPI>
+__device__ __forceinline__ void epi_store(const DqTile &T, const f16x (&C)[NI][NJ], uint8_t *s_wave, int wm,
+                                          int wn, int lane, int rt0, const EPI &epi) {
+  static_assert(32 * TN * 4 <= 16384, "a pass fits the wave's LDS");
+  float *s_c = (float *)s_wave;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        s_c[((e & 3) + 8 * (e >> 2) + 4 * (lane >> 5)) * TN + 32 * j + (lane & 31)] = C[i][j][e];
+    __syncthreads();
+    for (int q = lane; q < 32 * TN / 4; q += 64) {
+      const int r = q / (TN / 4), n0 = rt0 * UNIT_ROWS + TN * wn + 4 * (q % (TN / 4));
+      const int rr = TM * wm + 32 * i + r;
+      if (rr >= T.m_valid || n0 >= T.nlim) continue;
+      const f4 v = *(const f4 *)(s_c + 4 * q);
+      epi.store4(T.y, T.ldy, T.bf, T.yvec, v, T.m0 + rr, n0, T.nlim);
+    }
+    __syncthreads();
+  }
+}
+
 // BM = 256: four waves in a 2 x 2 grid of 128 x 128 tiles, one block per CU.
 // BM = 64 (activation row counts below 256): four waves side by side, each
 // 64 x 64, with a register budget for two blocks per CU.
-template <int BM>
-__device__ __forceinline__ void dq_tile(const DqTile &T, uint8_t *smem) {
+template <int BM, typename EPI = NoEpi>
+__device__ __forceinline__ void dq_tile(const DqTile &T, uint8_t *smem, const EPI &epi_args = EPI()) {
   constexpr int WM = BM == 256 ? 2 : 1, WN = 4 / WM;  // wave grid
   constexpr int TM = BM / WM, TN = P_BN / WN;         // wave tile
   constexpr int NI = TM / 32, NJ = TN / 32;           // 32 x 32 accumulator blocks
@@ -312,6 +342,10 @@ __device__ __forceinline__ void dq_tile(const DqTile &T, uint8_t *smem) {
   // region, as many 32-row blocks per pass as fit, and writes them back as
   // whole 16-byte pieces of consecutive output columns.
   __syncthreads();
+  if constexpr (EPI::on) {
+    epi_store<NI, NJ, TM, TN>(T, C, smem + wv * 16384, wm, wn, lane, rt0, epi_args);
+    return;
+  }
   {
     // the output type is a template parameter of the body: a test per
     // element in the unrolled loops left a branch at every store
@@ -440,7 +474,8 @@ __device__ __forceinline__ void w8_store(const ItemCodes &c, uint8_t *bst, const
   }
 }
 
-__device__ void dq_tile_w8(const DqTile &T, uint8_t *smem) {
+template <typename EPI = NoEpi>
+__device__ void dq_tile_w8(const DqTile &T, uint8_t *smem, const EPI &epi_args = EPI()) {
   constexpr int NI = 4, NJ = 2, TM = 128, TN = 64;
   const MatView &w = T.w;
   const int nt = T.nt, u0 = T.u0, u1 = T.u1, m0 = T.m0;
@@ -568,6 +603,10 @@ __device__ void dq_tile_w8(const DqTile &T, uint8_t *smem) {
     rB = nB;
   }
 
+  if constexpr (EPI::on) {
+    epi_store<NI, NJ, TM, TN>(T, C, smem + wv * 16384, wm, wn, lane, rt0, epi_args);
+    return;
+  }
   // Epilogue.  A tile whose rows and columns all lie inside the output is
   // stored straight from the accumulators: for each accumulator element the
   // lanes 0..31 (and 32..63) write 32 consecutive columns of one output row,
@@ -738,9 +777,50 @@ void prefill_w8_kernel(PrefillBatch b) {
   dq_tile_w8(T, smem);
 }
 
+// One matrix with its epilogue, without a K split (with one, the partial
+// tiles come from the plain kernels above and the reduce launch applies it).
+__device__ __forceinline__ bool epi_tile(const PrefillBatch &b, int bm, DqTile &T) {
+  const PrefillJob &J = b.job[0];
+  const int local = (int)blockIdx.x;
+  if (local >= J.tiles_n * J.tiles_m) return false;  // padding block (uniform, before any barrier)
+  T.w = J.w;
+  T.xb = J.xb;
+  T.m0 = local % J.tiles_m * bm;
+  T.m_valid = J.m - T.m0;
+  T.nt = local / J.tiles_m;
+  T.u0 = 0;
+  T.u1 = J.w.units;
+  T.ymap = nullptr;
+  T.y = J.y;
+  T.ldy = J.ldy;
+  T.nlim = J.w.n;
+  T.bf = b.ydt == 0;
+  T.yvec = b.yvec != 0;
+  return true;
+}
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void prefill_epi64_kernel(PrefillBatch b, EpiArgs ea) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  DqTile T;
+  if (!epi_tile(b, 64, T)) return;
+  const Epi epi{ea};
+  dq_tile<64, Epi>(T, smem, epi);
+}
+__global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void prefill_w8_epi_kernel(PrefillBatch b, EpiArgs ea) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  DqTile T;
+  if (!epi_tile(b, 256, T)) return;
+  const Epi epi{ea};
+  dq_tile_w8<Epi>(T, smem, epi);
+}
+
 // Sum of the K-split partial tiles of every split job, in split order:
 // y[row][n] = sum_s part[s][row][n], four columns per thread.
-__global__ __launch_bounds__(256) void prefill_reduce_kernel(PrefillBatch b) {
+// ea: nothing, or the EpiArgs of a single matrix.
+template <typename... EA>
+__global__ __launch_bounds__(256) void prefill_reduce_kernel(PrefillBatch b, EA... ea) {
+  const auto epi = make_epi(ea...);
   const int jn = find_job(b.red_starts, b.count);
   const PrefillJob &J = b.job[jn];
   if (J.splits <= 1) return;
@@ -756,12 +836,19 @@ __global__ __launch_bounds__(256) void prefill_reduce_kernel(PrefillBatch b) {
     acc.z += v.z;
     acc.w += v.w;
   }
+  if constexpr (epi.on) {
+    epi.store4(J.y, J.ldy, b.ydt == 0, b.yvec != 0, (f4){acc.x, acc.y, acc.z, acc.w}, row, n, J.w.n);
+    return;
+  }
   const float o[4] = {acc.x, acc.y, acc.z, acc.w};
   for (int l = 0; l < 4 && n + l < J.w.n; ++l) store_out(J.y, (size_t)row * J.ldy + n + l, o[l], b.ydt);
 }
 
 hipError_t launch_prefill_reduce(PrefillBatch &b, int blocks, hipStream_t s) {
-  hipLaunchKernelGGL(prefill_reduce_kernel, dim3(blocks), dim3(256), 0, s, b);
+  if (b.epi)
+    hipLaunchKernelGGL(prefill_reduce_kernel<EpiArgs>, dim3(blocks), dim3(256), 0, s, b, *b.epi);
+  else
+    hipLaunchKernelGGL(prefill_reduce_kernel<>, dim3(blocks), dim3(256), 0, s, b);
   return hipGetLastError();
 }
 
@@ -878,6 +965,18 @@ hipError_t launch_prefill_prep(PrefillBatch &b, int blocks, size_t lds, bool xve
 
 
 hipError_t launch_prefill_batched(PrefillBatch &b, int bm, int blocks, hipStream_t s) {
+  if (b.epi && b.job[0].splits == 1) {
+    if (bm == 256) {
+      const hipError_t e = allow_smem(prefill_w8_epi_kernel, W8_SMEM);
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL(prefill_w8_epi_kernel, dim3(blocks), dim3(W8_THREADS), W8_SMEM, s, b, *b.epi);
+    } else {
+      const hipError_t e = allow_smem(prefill_epi64_kernel, P_SMEM);
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL(prefill_epi64_kernel, dim3(blocks), dim3(256), P_SMEM, s, b, *b.epi);
+    }
+    return hipGetLastError();
+  }
   if (bm == 256) {
     hipError_t e = allow_smem(prefill_w8_kernel, W8_SMEM);
     if (e != hipSuccess) return e;

@@ -58,6 +58,7 @@
 // them in range order and writes the output, so results do not depend on
 // timing.
 #include "svq_device.h"
+#include "svq_epilogue.h"
 #include "../../include/svq.h"
 
 namespace svq {
@@ -142,7 +143,12 @@ __device__ __forceinline__ const uint8_t *sb_unit(const MatView &w, int t, int u
   return w.base + w.off_codes + ((size_t)t * w.units + u) * UNIT_BYTES;
 }
 
-__global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b) {
+// ea: nothing, or the EpiArgs of a single matrix.  (The body stands in the
+// kernel itself: behind a function call the job records, indexed at run time,
+// would be copied out of the kernel arguments.)
+template <typename... EA>
+__global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b, EA... ea) {
+  const auto epi = make_epi(ea...);
   const int jn = find_job(b.starts, b.count);
   const SbJob &J = b.job[jn];
   const MatView &w = J.w;
@@ -280,7 +286,7 @@ __global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b) {
 #pragma unroll
   for (int t = 0; t < SB_TMAX; ++t) {
     const int n = (t0 + t) * UNIT_ROWS + nn;
-    if (t < tn && n < w.n) store_out(J.y, (size_t)m * J.ldy + n, acc[t] * J.xinv, b.ydt);
+    if (t < tn && n < w.n) store_out(J.y, (size_t)m * J.ldy + n, epi(acc[t] * J.xinv, m, n), b.ydt);
   }
   (void)j;
 }
@@ -351,7 +357,10 @@ hipError_t launch_sb(SbBatch &b, int prep_blocks, int blocks, hipStream_t s) {
   hipLaunchKernelGGL(sb_prep_kernel, dim3(prep_blocks), dim3(256), 0, s, b);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(sb_gemm_kernel, dim3(blocks), dim3(256), SB_SMEM, s, b);
+  if (b.epi)
+    hipLaunchKernelGGL(sb_gemm_kernel<EpiArgs>, dim3(blocks), dim3(256), SB_SMEM, s, b, *b.epi);
+  else
+    hipLaunchKernelGGL(sb_gemm_kernel<>, dim3(blocks), dim3(256), SB_SMEM, s, b);
   return hipGetLastError();
 }
 

@@ -36,6 +36,10 @@ SVQ_F32 = 1
 EXPORTED = ("svq_pack", "svq_linear", "svq_linear_batched", "svq_linear_noalloc",
             "svq_moe_linear", "svq_moe_linear_batched", "svq_encode", "svq_encode_weighted", "svq_esg_perm", "svq_abs_select",
             "svq_status_string")
+# the feed-forward calls (include/svq_ffn.h)
+EXPORTED_FFN = ("svq_linear_epilogue", "svq_linear_glu", "svq_moe_route", "svq_moe_ffn")
+ACTIVATIONS = ("none", "relu", "silu", "gelu", "gelu_tanh")  # svq_act by name
+ROUTE_SCORES = ("softmax", "sigmoid")                        # svq_route_score by name
 SVQ_SCRATCH_BYTES = 64 << 20
 SVQ_NO_EXACT_SPLIT = -(1 << 31)
 
@@ -67,6 +71,13 @@ class Handle(ctypes.Structure):
         ("off_codes", ctypes.c_uint64), ("code_bytes", ctypes.c_uint64),
         ("padded_code_bytes", ctypes.c_uint64), ("bytes", ctypes.c_uint64),
         ("xscale_log2", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class Epilogue(ctypes.Structure):
+    _fields_ = [
+        ("bias", ctypes.c_void_p), ("bias_dt", ctypes.c_int), ("act", ctypes.c_int),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("residual_dt", ctypes.c_int),
     ]
 
 
@@ -132,6 +143,18 @@ def _load() -> ctypes.CDLL:
                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                    ctypes.POINTER(ctypes.c_int32), ctypes.c_void_p, ctypes.c_void_p,
                                    ctypes.POINTER(ctypes.c_size_t), ctypes.c_void_p]
+    i32, i64, ptr, size_p = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)
+    hp, en = ctypes.POINTER(Handle), ctypes.c_int
+    lib.svq_linear_epilogue.restype = en
+    lib.svq_linear_epilogue.argtypes = [hp, ptr, i64, i64, ctypes.POINTER(Epilogue), ptr, i64, en, ptr, size_p, ptr]
+    lib.svq_linear_glu.restype = en
+    lib.svq_linear_glu.argtypes = [hp, hp, ptr, i64, i64, en, ptr, ptr, en, ptr, i64, en, ptr, size_p, ptr]
+    lib.svq_moe_route.restype = en
+    lib.svq_moe_route.argtypes = [ptr, i64, i64, ptr, en, i32, i32, i64, ptr, en, i32, ctypes.c_float, i32,
+                                  ptr, ptr, ptr, size_p, ptr]
+    lib.svq_moe_ffn.restype = en
+    lib.svq_moe_ffn.argtypes = [hp, hp, hp, i32, ptr, i64, ptr, ptr, i64, i32, en, ptr, i64, en, ptr, i64, en,
+                                ptr, size_p, ptr]
     return lib
 
 
@@ -611,3 +634,276 @@ def encode(w, perm, bd: int, codebook, radius, stream=None):
                        codes.data_ptr(), ws.data_ptr(), need, _stream_handle(stream))
     _check(st, "svq_encode")
     return codes
+
+
+# ---------------------------------------------------------------------------
+# The feed-forward calls (include/svq_ffn.h).  The *Call classes hold the
+# marshalled arguments and the workspace of one call, for a program that makes
+# it many times: tensors are the caller's and must outlive the object, and
+# objects that share a workspace must be called in one stream's order.  Each
+# call goes to the given stream, or to the one that is current when it is made.
+# ---------------------------------------------------------------------------
+
+def _dt(t, what: str) -> int:
+    import torch
+    if t.dtype == torch.float32:
+        return SVQ_F32
+    if t.dtype == torch.bfloat16:
+        return SVQ_BF16
+    raise ValueError(f"{what} must be bf16 or fp32")
+
+
+def _matrix_arg(t, what: str, rows: int, cols: int, device, dtypes=None) -> int:
+    """Checks a 2-D device operand of at least ``cols`` columns; returns its
+    row stride."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be 2-D, {rows} rows of {cols} columns or more, with unit column stride")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"{what} has the wrong type ({t.dtype})")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"the rows of {what} overlap")
+    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+
+
+def _vector_arg(t, what: str, n: int, device, dtype=None) -> None:
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.device != device:
+        raise ValueError(f"{what} must be a contiguous vector of {n} values on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+
+
+def _choice(name: str, names, what: str) -> int:
+    if name not in names:
+        raise ValueError(f"{what} must be one of {', '.join(names)}")
+    return names.index(name)
+
+
+def _overlaps(a, b) -> bool:
+    """Whether the address ranges of two tensors meet."""
+    def span(t):
+        if t.numel() == 0:
+            return t.data_ptr(), t.data_ptr()
+        last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
+class _Call:
+    """One prepared call: ``fn(*args)`` with the workspace, its size and the
+    stream appended."""
+
+    def _prepare(self, name: str, args, device, workspace, stream) -> None:
+        import torch
+        self.name, self.args, self.device = name, tuple(args), device
+        self.fn = getattr(LIB, name)
+        self.stream = None if stream is None else int(stream.cuda_stream)
+        nbytes = ctypes.c_size_t(0)
+        _check(self.fn(*self.args, None, ctypes.byref(nbytes), None), f"{name} (workspace query)")
+        if workspace is None or workspace.numel() * workspace.element_size() < nbytes.value:
+            workspace = torch.empty(max(nbytes.value, 1), dtype=torch.uint8, device=device)
+        self.workspace = workspace
+        self.ws_ptr = workspace.data_ptr()
+        self.ws_size = ctypes.c_size_t(workspace.numel() * workspace.element_size())
+        self.ws_size_ref = ctypes.byref(self.ws_size)
+
+    def __call__(self) -> None:
+        import torch
+        stream = self.stream
+        if self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                if stream is None:
+                    stream = torch.cuda.current_stream().cuda_stream
+                st = self.fn(*self.args, self.ws_ptr, self.ws_size_ref, stream)
+        else:
+            if stream is None:
+                stream = torch.cuda.current_stream().cuda_stream
+            st = self.fn(*self.args, self.ws_ptr, self.ws_size_ref, stream)
+        if st != SVQ_OK:
+            _check(st, self.name)
+
+
+class EpilogueCall(_Call):
+    """y = act(x @ What^T + bias) + residual (svq_linear_epilogue).
+
+    x: bf16 [m, >= k]; y: bf16 or fp32 [m, n]; bias: [n], residual: [m, n],
+    each bf16 or fp32 or None; act: a name of ``ACTIVATIONS``.  residual may
+    be y itself (the product is then added to it)."""
+
+    def __init__(self, pm: PackedMatrix, x, y, bias=None, act: str = "none", residual=None, workspace=None,
+                 stream=None):
+        import torch
+        m, dev = x.shape[0], x.device
+        ldx = _matrix_arg(x, "x", m, pm.k, dev, (torch.bfloat16,))
+        ldy = _matrix_arg(y, "y", m, pm.n, dev, (torch.bfloat16, torch.float32))
+        ep = Epilogue(act=_choice(act, ACTIVATIONS, "act"))
+        if bias is not None:
+            _vector_arg(bias, "bias", pm.n, dev)
+            ep.bias, ep.bias_dt = bias.data_ptr(), _dt(bias, "bias")
+        if residual is not None:
+            ep.ldr = _matrix_arg(residual, "residual", m, pm.n, dev, (torch.bfloat16, torch.float32))
+            ep.residual, ep.residual_dt = residual.data_ptr(), _dt(residual, "residual")
+            same = residual.data_ptr() == y.data_ptr() and residual.dtype == y.dtype and (m == 1 or ep.ldr == ldy)
+            if not same and _overlaps(residual, y):
+                raise ValueError("residual overlaps y without being y")
+            if same:
+                ep.ldr = ldy
+        self.keep = (pm, x, y, bias, residual, ep)
+        self._prepare("svq_linear_epilogue", (ctypes.byref(pm.handle), x.data_ptr(), m, ldx, ctypes.byref(ep),
+                                              y.data_ptr(), ldy, _dt(y, "y")), dev, workspace, stream)
+
+
+class GluCall(_Call):
+    """y = act(x @ Gate^T + bias_gate) * (x @ Up^T + bias_up) (svq_linear_glu).
+
+    x: bf16 [m, >= k]; y: bf16 or fp32 [m, n]; the biases: [n] of one type
+    (bf16 or fp32), each may be None."""
+
+    def __init__(self, pm_gate: PackedMatrix, pm_up: PackedMatrix, x, y, act: str = "silu", bias_gate=None,
+                 bias_up=None, workspace=None, stream=None):
+        import torch
+        m, dev = x.shape[0], x.device
+        ldx = _matrix_arg(x, "x", m, pm_gate.k, dev, (torch.bfloat16,))
+        ldy = _matrix_arg(y, "y", m, pm_gate.n, dev, (torch.bfloat16, torch.float32))
+        kinds = []
+        for b, what in ((bias_gate, "bias_gate"), (bias_up, "bias_up")):
+            if b is not None:
+                _vector_arg(b, what, pm_gate.n, dev)
+                kinds.append(_dt(b, what))
+        if len(set(kinds)) > 1:
+            raise ValueError("bias_gate and bias_up must be of one type")
+        self.keep = (pm_gate, pm_up, x, y, bias_gate, bias_up)
+        self._prepare("svq_linear_glu",
+                      (ctypes.byref(pm_gate.handle), ctypes.byref(pm_up.handle), x.data_ptr(), m, ldx,
+                       _choice(act, ACTIVATIONS, "act"), None if bias_gate is None else bias_gate.data_ptr(),
+                       None if bias_up is None else bias_up.data_ptr(), kinds[0] if kinds else SVQ_F32,
+                       y.data_ptr(), ldy, _dt(y, "y")), dev, workspace, stream)
+
+
+class MoeRouteCall(_Call):
+    """Router of an expert layer (svq_moe_route): fills ids (int32 [m, topk])
+    and weights (fp32 [m, topk]) from x (bf16 [m, >= k]) and the router
+    weights w ([experts, k], bf16 or fp32)."""
+
+    def __init__(self, x, w, ids, weights, score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                 select_bias=None, workspace=None, stream=None):
+        import torch
+        (m, topk), dev = ids.shape, x.device
+        e, k = w.shape
+        ldx = _matrix_arg(x, "x", m, k, dev, (torch.bfloat16,))
+        ldw = _matrix_arg(w, "w", e, k, dev, (torch.bfloat16, torch.float32))
+        for t, what, dtype in ((ids, "ids", torch.int32), (weights, "weights", torch.float32)):
+            if tuple(t.shape) != (m, topk) or not t.is_contiguous() or t.dtype != dtype or t.device != dev:
+                raise ValueError(f"{what} must be a contiguous {dtype} tensor of [m, topk] on {dev}")
+        if select_bias is not None:
+            _vector_arg(select_bias, "select_bias", e, dev, torch.float32)
+        self.keep = (x, w, ids, weights, select_bias)
+        self._prepare("svq_moe_route",
+                      (x.data_ptr(), m, ldx, w.data_ptr(), _dt(w, "w"), e, k, ldw,
+                       None if select_bias is None else select_bias.data_ptr(),
+                       _choice(score, ROUTE_SCORES, "score"), int(bool(renormalize)), float(scale), topk,
+                       ids.data_ptr(), weights.data_ptr()), dev, workspace, stream)
+
+
+class MoeFfnCall(_Call):
+    """A whole expert layer (svq_moe_ffn):
+    y[t] = residual[t] + sum_j weights[t, j] * Down_e(act(Gate_e x[t]) * (Up_e x[t])), e = expert_ids[t, j].
+
+    gates, ups, downs: the packed experts (sequences of one length); x: bf16
+    [m, >= k]; expert_ids: int32 [m, topk]; weights: fp32 [m, topk]; y: bf16
+    or fp32 [m, n]; residual: [m, n], bf16 or fp32, y itself, or None."""
+
+    def __init__(self, gates: Sequence[PackedMatrix], ups: Sequence[PackedMatrix], downs: Sequence[PackedMatrix],
+                 x, expert_ids, weights, y, act: str = "silu", residual=None, workspace=None, stream=None):
+        import torch
+        if not gates or not len(gates) == len(ups) == len(downs):
+            raise ValueError("gates, ups and downs must be sequences of one length")
+        (m, topk), dev = expert_ids.shape, x.device
+        k, n = gates[0].k, downs[0].n
+        ldx = _matrix_arg(x, "x", m, k, dev, (torch.bfloat16,))
+        ldy = _matrix_arg(y, "y", m, n, dev, (torch.bfloat16, torch.float32))
+        for t, what, dtype in ((expert_ids, "expert_ids", torch.int32), (weights, "weights", torch.float32)):
+            if tuple(t.shape) != (m, topk) or not t.is_contiguous() or t.dtype != dtype or t.device != dev:
+                raise ValueError(f"{what} must be a contiguous {dtype} tensor of [m, topk] on {dev}")
+        ldr, rdt = 0, SVQ_BF16
+        if residual is not None:
+            ldr = _matrix_arg(residual, "residual", m, n, dev, (torch.bfloat16, torch.float32))
+            rdt = _dt(residual, "residual")
+            same = residual.data_ptr() == y.data_ptr() and residual.dtype == y.dtype and (m == 1 or ldr == ldy)
+            if not same and _overlaps(residual, y):
+                raise ValueError("residual overlaps y without being y")
+            if same:
+                ldr = ldy
+        sets = [handle_array(p) for p in (gates, ups, downs)]
+        self.keep = (list(gates), list(ups), list(downs), sets, x, expert_ids, weights, y, residual)
+        self._prepare("svq_moe_ffn",
+                      (*sets, len(gates), x.data_ptr(), ldx, expert_ids.data_ptr(), weights.data_ptr(), m, topk,
+                       _choice(act, ACTIVATIONS, "act"), None if residual is None else residual.data_ptr(), ldr,
+                       rdt, y.data_ptr(), ldy, _dt(y, "y")), dev, workspace, stream)
+
+
+def _run_on(stream, device, make):
+    """make() with ``stream`` current, so that what it allocates belongs to
+    that stream (a workspace freed afterwards is not handed to another stream
+    while the call still uses it)."""
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            return make()
+        with torch.cuda.stream(stream):
+            return make()
+
+
+def linear_epilogue(pm: PackedMatrix, x, bias=None, act: str = "none", residual=None, out=None, out_dtype=None,
+                    stream=None):
+    """act(x @ What^T + bias) + residual; see :class:`EpilogueCall`."""
+    import torch
+
+    def make():
+        y = out if out is not None else torch.empty((x.shape[0], pm.n), dtype=out_dtype or torch.bfloat16,
+                                                    device=x.device)
+        EpilogueCall(pm, x, y, bias=bias, act=act, residual=residual)()
+        return y
+    return _run_on(stream, x.device, make)
+
+
+def linear_glu(pm_gate: PackedMatrix, pm_up: PackedMatrix, x, act: str = "silu", bias_gate=None, bias_up=None,
+               out=None, out_dtype=None, stream=None):
+    """act(x @ Gate^T + bias_gate) * (x @ Up^T + bias_up); see :class:`GluCall`."""
+    import torch
+
+    def make():
+        y = out if out is not None else torch.empty((x.shape[0], pm_gate.n), dtype=out_dtype or torch.bfloat16,
+                                                    device=x.device)
+        GluCall(pm_gate, pm_up, x, y, act=act, bias_gate=bias_gate, bias_up=bias_up)()
+        return y
+    return _run_on(stream, x.device, make)
+
+
+def moe_route(x, w, topk: int, score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+              select_bias=None, stream=None):
+    """(ids, weights) of each token's topk experts; see :class:`MoeRouteCall`."""
+    import torch
+
+    def make():
+        ids = torch.empty((x.shape[0], topk), dtype=torch.int32, device=x.device)
+        weights = torch.empty((x.shape[0], topk), dtype=torch.float32, device=x.device)
+        MoeRouteCall(x, w, ids, weights, score=score, renormalize=renormalize, scale=scale,
+                     select_bias=select_bias)()
+        return ids, weights
+    return _run_on(stream, x.device, make)
+
+
+def moe_ffn(gates: Sequence[PackedMatrix], ups: Sequence[PackedMatrix], downs: Sequence[PackedMatrix], x,
+            expert_ids, weights, act: str = "silu", residual=None, out=None, out_dtype=None, stream=None):
+    """A whole expert layer; see :class:`MoeFfnCall`."""
+    import torch
+
+    def make():
+        y = out if out is not None else torch.empty((x.shape[0], downs[0].n), dtype=out_dtype or torch.bfloat16,
+                                                    device=x.device)
+        MoeFfnCall(gates, ups, downs, x, expert_ids, weights, y, act=act, residual=residual)()
+        return y
+    return _run_on(stream, x.device, make)
