@@ -47,12 +47,12 @@ __device__ __forceinline__ f4 load_f4(const void *p, size_t i, int f32, bool vec
 
 // No epilogue: the product kernels' default.
 struct NoEpi {
-  static constexpr bool on = false;
+  static constexpr bool on = false, partial = false;
   __device__ __forceinline__ float operator()(float v, int, int) const { return v; }
 };
 
 struct Epi {
-  static constexpr bool on = true;
+  static constexpr bool on = true, partial = false;
   EpiArgs a;
   // output row `row`, column n
   __device__ __forceinline__ float operator()(float v, int row, int n) const {
@@ -98,6 +98,16 @@ struct Epi {
         for (int l = 0; l < 4; ++l) p[l] = v[l];
       }
     }
+  }
+};
+
+// The sums go to an fp32 row that another block reads in the same launch:
+// device-scope stores, coherent between the XCDs' caches.
+struct PartEpi {
+  static constexpr bool on = true, partial = true;
+  float *row;
+  __device__ __forceinline__ void put(float v, int n) const {
+    __hip_atomic_store(row + n, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 };
 

@@ -158,6 +158,37 @@ svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_h
   if (ldx < gate->k || ldy < down->n) return SVQ_ERR_INVALID_ARG;
   if (residual && (!valid_dt(residual_dt) || ldr < down->n)) return SVQ_ERR_INVALID_ARG;
   const int64_t S = m * topk;
+  if (moe_ffn_few_fits(gate, up, down, num_experts, S)) {
+    MoeFfnArgs fa;
+    std::memset(&fa, 0, sizeof(fa));
+    fa.gate = gate;
+    fa.up = up;
+    fa.down = down;
+    fa.num_experts = num_experts;
+    fa.x = x;
+    fa.ldx = ldx;
+    fa.ids = expert_ids;
+    fa.weights = weights;
+    fa.m = m;
+    fa.topk = topk;
+    fa.act = (int32_t)act;
+    fa.res = residual;
+    fa.ldr = ldr;
+    fa.res_f32 = residual_dt == SVQ_F32;
+    fa.y = y;
+    fa.ldy = ldy;
+    fa.ydt = (int32_t)ydt;
+    size_t need = 0;
+    if (launch_moe_ffn_few(fa, nullptr, &need, nullptr) != hipSuccess) return SVQ_ERR_HIP;
+    if (!workspace) {
+      *workspace_bytes = need;
+      return SVQ_OK;
+    }
+    if (!x || !expert_ids || !weights || !y) return SVQ_ERR_INVALID_ARG;
+    if (residual == y && (ldr != ldy || residual_dt != ydt)) return SVQ_ERR_INVALID_ARG;
+    if (*workspace_bytes < need) return SVQ_ERR_BUFFER_TOO_SMALL;
+    return launch_moe_ffn_few(fa, workspace, &need, (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
+  }
   const int32_t f = gate->n, n = down->n;
   const int64_t ldf = pad4(f), ldh = (f + 7) / 8 * 8, ldd = pad4(n);
   // workspace: gate and up sums, the inner activation, the slots' outputs,
@@ -172,10 +203,7 @@ svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_h
   inner = ws1 > ws2 ? ws1 : ws2;
   const size_t b_g = align256((size_t)S * ldf * 4), b_h = align256((size_t)S * ldh * 2),
                b_d = align256((size_t)S * ldd * 4);
-  // up to 64 slots the inner activation is kept to 16 bits of mantissa: two
-  // bf16 halves, each through the down product
-  const int halves = S <= 64 ? 2 : 1;
-  const size_t need = 2 * b_g + halves * (b_h + b_d) + inner;
+  const size_t need = 2 * b_g + b_h + b_d + inner;
   if (!workspace) {
     *workspace_bytes = need;
     return SVQ_OK;
@@ -186,8 +214,8 @@ svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_h
   uint8_t *ws = (uint8_t *)workspace;
   float *g = (float *)ws, *u = (float *)(ws + b_g);
   uint8_t *h = ws + 2 * b_g;
-  float *d = (float *)(ws + 2 * b_g + halves * b_h);
-  uint8_t *iw = ws + 2 * b_g + halves * (b_h + b_d);
+  float *d = (float *)(ws + 2 * b_g + b_h);
+  uint8_t *iw = ws + 2 * b_g + b_h + b_d;
   size_t cap = inner;
   st = svq_moe_linear(gate, num_experts, x, ldx, 0, expert_ids, m, topk, g, ldf, SVQ_F32, iw, &cap, stream);
   if (st == SVQ_OK)
@@ -201,21 +229,14 @@ svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_h
   ga.ldp = ldf;
   ga.act = (int32_t)act;
   ga.y = h;
-  ga.y_lo = halves == 2 ? h + b_h : nullptr;
   ga.ldy = ldh;
   ga.n = f;
   ga.ydt = SVQ_BF16;
   if (launch_glu(ga, (hipStream_t)stream) != hipSuccess) return SVQ_ERR_HIP;
   st = svq_moe_linear(down, num_experts, h, ldh, 1, expert_ids, m, topk, d, ldd, SVQ_F32, iw, &cap, stream);
+  if (st != SVQ_OK) return st;
   CombineArgs ca;
   std::memset(&ca, 0, sizeof(ca));
-  if (halves == 2 && st == SVQ_OK) {
-    float *d_lo = (float *)((uint8_t *)d + b_d);
-    st = svq_moe_linear(down, num_experts, h + b_h, ldh, 1, expert_ids, m, topk, d_lo, ldd, SVQ_F32, iw, &cap,
-                        stream);
-    ca.d_lo = d_lo;
-  }
-  if (st != SVQ_OK) return st;
   ca.d = d;
   ca.ldd = ldd;
   ca.ids = expert_ids;

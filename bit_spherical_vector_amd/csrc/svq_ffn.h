@@ -20,15 +20,13 @@ struct GluArgs {
   const void *bias_g, *bias_u;  // [n] or null
   int32_t bias_f32, act;
   void *y;
-  void *y_lo;  // bf16 rest of every value, or null
   int64_t ldy;
   int32_t n, ydt;
 };
 hipError_t launch_glu(const GluArgs &a, hipStream_t s);
 
 struct CombineArgs {
-  const float *d;     // [m * topk][ldd]
-  const float *d_lo;  // added to d, or null
+  const float *d;  // [m * topk][ldd]
   int64_t ldd;
   const int32_t *ids;
   const float *weights;
@@ -42,6 +40,28 @@ struct CombineArgs {
   int32_t n, ydt;
 };
 hipError_t launch_combine(const CombineArgs &a, hipStream_t s);
+
+// ---- expert layer ---------------------------------------------------------
+struct MoeFfnArgs {
+  const svq_handle *gate, *up, *down;  // host arrays of num_experts
+  int32_t num_experts;
+  const void *x;
+  int64_t ldx;
+  const int32_t *ids;
+  const float *weights;
+  int64_t m;
+  int32_t topk, act;
+  const void *res;
+  int64_t ldr;
+  int32_t res_f32, ydt;
+  void *y;
+  int64_t ldy;
+};
+// The per-slot form: at most 64 slots whose rows fit a block's LDS.
+bool moe_ffn_few_fits(const svq_handle *gate, const svq_handle *up, const svq_handle *down, int32_t num_experts,
+                      int64_t slots);
+// ws null: only *need.
+hipError_t launch_moe_ffn_few(const MoeFfnArgs &f, void *ws, size_t *need, hipStream_t s);
 
 // ---- router --------------------------------------------------------------------
 constexpr int ROUTE_MAX_TOPK = 32;

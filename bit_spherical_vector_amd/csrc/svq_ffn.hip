@@ -22,10 +22,7 @@ __global__ __launch_bounds__(256) void glu_kernel(GluArgs a) {
       if (n0 + l >= a.n) break;
       if (a.bias_g) g[l] += load_f(a.bias_g, n0 + l, a.bias_f32);
       if (a.bias_u) u[l] += load_f(a.bias_u, n0 + l, a.bias_f32);
-      const float h = act_apply(g[l], a.act) * u[l];
-      store_out(a.y, (size_t)r * a.ldy + n0 + l, h, a.ydt);
-      if (a.y_lo)  // what the bf16 value leaves
-        store_out(a.y_lo, (size_t)r * a.ldy + n0 + l, h - bf16_bits_to_f32(f32_to_bf16_bits(h)), a.ydt);
+      store_out(a.y, (size_t)r * a.ldy + n0 + l, act_apply(g[l], a.act) * u[l], a.ydt);
     }
   }
 }
@@ -50,8 +47,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(CombineArgs a) {
       const int64_t s = t * a.topk + j;
       const int e = a.ids[s];
       if (e < 0 || e >= a.num_experts) continue;
-      f4 d = *(const f4 *)(a.d + s * a.ldd + n0);
-      if (a.d_lo) d += *(const f4 *)(a.d_lo + s * a.ldd + n0);
+      const f4 d = *(const f4 *)(a.d + s * a.ldd + n0);
       const float w = a.weights[s];
 #pragma unroll
       for (int l = 0; l < 4; ++l) v[l] = __builtin_fmaf(w, d[l], v[l]);

@@ -167,10 +167,11 @@ __host__ __device__ constexpr int gf_off_stage(int bd) { return bd >= 8 ? gf_off
 struct GfLds {
   int scale, red, xp, stage, total;
 };
-// r: row tiles per block (the cross-wave partial sums hold r tiles)
-__host__ __device__ inline GfLds gf_lds(int bd, int k, int units, int m, int r) {
+// r: row tiles per block (the cross-wave partial sums hold r tiles); esz:
+// bytes per staged activation
+__host__ __device__ inline GfLds gf_lds(int bd, int k, int units, int m, int r, int esz = 2) {
   GfLds L;
-  const int stage = (k * 2 + 15) & ~15, dir = gf_dir_bytes(bd);
+  const int stage = (k * esz + 15) & ~15, dir = gf_dir_bytes(bd);
   L.stage = gf_off_stage(bd);
   int off = bd >= 8 ? gf_off_d(bd) + (dir > stage ? dir : stage) : L.stage + stage;
   L.scale = off;

@@ -29,6 +29,7 @@
 
 #include "svq_device.h"
 #include "svq_epilogue.h"
+#include "svq_ffn.h"
 #include "../../include/svq.h"
 
 namespace svq {
@@ -785,17 +786,32 @@ __device__ __forceinline__ void gf_item(const ItemCodes &c, const uint8_t *xu, u
   gemv_group_mul<M, 3>(S01, S23, A1, D1, R1, tmp);
 }
 
+// Activations of a fused block: bf16 rows x, or (InGlu) the gated product
+// act(g) * u of two fp32 rows, formed while the row is staged and staged in
+// fp32, so that it is rounded once, to fp16 under its unit's scale.
+struct InBf16 {
+  static constexpr bool glu = false;
+  static constexpr int esz = 2;
+};
+struct InGlu {
+  static constexpr bool glu = true;
+  static constexpr int esz = 4;
+  const float *g, *u;  // 16-byte aligned rows of k values
+  int act;
+};
+constexpr int GF_GLU_BATCH = 2;  // 16-byte pieces of g and u prefetched per thread
+
 // XVEC: every activation row starts 16-byte aligned (vector staging loads).
 // BD: the matrix's direction bits (table layout, see above).
-template <int M, bool XVEC, int BD, typename EPI = NoEpi>
+template <int M, bool XVEC, int BD, typename EPI = NoEpi, typename IN = InBf16>
 __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ x, int64_t ldx,
                                  void *y, int64_t ldy, int ydt, int rt0, int R,
-                                 int Reff, uint8_t *smem, const EPI &epi = EPI()) {
+                                 int Reff, uint8_t *smem, const EPI &epi = EPI(), const IN &in = IN()) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform
   const int U = w.units, Kp = U * UNIT_SLOTS, K = w.k;
   constexpr int rows = 1 << BD;
-  const GfLds L = gf_lds(BD, K, U, M, R);
+  const GfLds L = gf_lds(BD, K, U, M, R, IN::esz);
   float *s_scale = (float *)(smem + L.scale);             // [U][M] 2^-e per unit
   float *s_red = (float *)(smem + L.red);                 // [GF_MAX_R][W][4][M][4]
   uint16_t *s_xp = (uint16_t *)(smem + L.xp);             // [M][Kp] fp16
@@ -830,7 +846,14 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
   for (int j = 0; j < GF_PRE_UNITS; ++j)
     pvec[j] = *(const u4 *)(perm + min(g_lo + j, U - 1) * UNIT_SLOTS + 8 * lane);
   u4 xv[M][GF_STAGE_BATCH];
-  if (XVEC) {
+  f4 gv[GF_GLU_BATCH], uv[GF_GLU_BATCH];
+  if constexpr (IN::glu) {
+#pragma unroll
+    for (int b = 0; b < GF_GLU_BATCH; ++b) {
+      gv[b] = ((const f4 *)in.g)[min(tid + 256 * b, K / 4 - 1)];
+      uv[b] = ((const f4 *)in.u)[min(tid + 256 * b, K / 4 - 1)];
+    }
+  } else if (XVEC) {
 #pragma unroll
     for (int a = 0; a < M; ++a)
 #pragma unroll
@@ -897,7 +920,17 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
   for (int a = 0; a < M; ++a) {
     const uint16_t *xr = x + (int64_t)a * ldx;
     if (a > 0) __syncthreads();  // previous row's gathers are done
-    if (XVEC) {
+    if constexpr (IN::glu) {
+      auto put = [&](int j, f4 gg, f4 uu) __attribute__((always_inline)) {
+#pragma unroll
+        for (int l = 0; l < 4; ++l) gg[l] = act_apply(gg[l], in.act) * uu[l];
+        if (j < K / 4) ((f4 *)s_stage)[j] = gg;
+      };
+#pragma unroll
+      for (int b = 0; b < GF_GLU_BATCH; ++b) put(tid + 256 * b, gv[b], uv[b]);
+      for (int j = tid + 256 * GF_GLU_BATCH; j < K / 4; j += 256)
+        put(j, ((const f4 *)in.g)[j], ((const f4 *)in.u)[j]);
+    } else if (XVEC) {
 #pragma unroll
       for (int b = 0; b < GF_STAGE_BATCH; ++b) {
         const int j = tid + 256 * b;
@@ -925,6 +958,35 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
     // the remaining three together when the wave has them; slots past the
     // wave's units read a clamped unit and store nothing.
     const int npre = min(g_hi - g_lo + 1, GF_PRE_UNITS);  // may be <= 0
+    if constexpr (IN::glu) {
+      // fp32 staging: one unit at a time
+      auto gather_unit = [&](const u4 &pv, int uu) __attribute__((always_inline)) {
+        const bool valid = uu * UNIT_SLOTS + 8 * lane < K;
+        float v[8], mx = 0.f;
+#pragma unroll
+        for (int l = 0; l < 4; ++l) {
+          v[2 * l] = valid ? lds_f32(gf_off_stage(BD) + word_shl<0, 2>(pv[l])) : 0.f;
+          v[2 * l + 1] = valid ? lds_f32(gf_off_stage(BD) + word_shl<1, 2>(pv[l])) : 0.f;
+          mx = fmaxf(mx, fmaxf(fabsf(v[2 * l]), fabsf(v[2 * l + 1])));
+        }
+        mx = wave_max(mx);
+        const int e = mx > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
+        u4 h;
+#pragma unroll
+        for (int l = 0; l < 4; ++l) {
+          const _Float16 lo = (_Float16)ldexpf(v[2 * l], e), hi = (_Float16)ldexpf(v[2 * l + 1], e);
+          h[l] = (uint32_t)__builtin_bit_cast(uint16_t, lo) | ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
+        }
+        ((u4 *)s_xp)[64 * uu + lane] = h;
+        if (lane == 0) s_scale[uu] = ldexpf(1.f, -e);
+      };
+#pragma unroll
+      for (int jj = 0; jj < GF_PRE_UNITS; ++jj)
+        if (jj < npre) gather_unit(pvec[jj], g_lo + jj);
+      for (int uu = g_lo + GF_PRE_UNITS; uu <= g_hi; ++uu)
+        gather_unit(*(const u4 *)(perm + uu * UNIT_SLOTS + 8 * lane), uu);
+      continue;
+    }
     auto gather_group = [&](auto J0, auto NJ) __attribute__((always_inline)) {
       constexpr int j0 = decltype(J0)::value, nj = decltype(NJ)::value;
       uint32_t pr[nj][4], mx[nj];
@@ -1057,7 +1119,11 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
 #pragma unroll
     for (int p = 0; p < GV_WAVES; ++p) sum += s_red[(((t * GV_WAVES + p) * 4 + ri) * M + a) * 4 + j];
     const int n = (rt0 + t) * 16 + row;
-    if (n < w.n) store_out(y, (size_t)a * ldy + n, epi(sum, a, n), ydt);
+    if constexpr (EPI::partial) {
+      if (n < w.n) epi.put(sum, n);
+    } else {
+      if (n < w.n) store_out(y, (size_t)a * ldy + n, epi(sum, a, n), ydt);
+    }
   }
 }
 
@@ -1159,6 +1225,117 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void m
     gemv_fused_block<1, XVEC, 7>(w, xr, mb.ldx[c], yq, mb.ldy[c], ydt, rt0, R, reff, smem);
   else
     gemv_fused_block<1, XVEC, 6>(w, xr, mb.ldx[c], yq, mb.ldy[c], ydt, rt0, R, reff, smem);
+}
+
+// ---------------------------------------------------------------------------
+// A whole expert layer for a few slots (at most MOE_EXACT_MAX_SLOTS), in two
+// launches:
+//
+//   moe_gate_up_kernel   g = Gate_e x, u = Up_e x of every slot, fp32 (the
+//                        per-slot block above; z = projection);
+//   moe_down_kernel      block (row-tile group, slot): h = act(g) * u is
+//                        formed while the block stages its activations (a
+//                        few values a thread, against a launch and a round
+//                        trip for a pass of its own), the slot's down
+//                        product goes to memory as fp32, and the last block
+//                        of a token's row-tile group to arrive sums the
+//                        topk slots in slot order, so the result does not
+//                        depend on who is last.
+//
+// The arrival counters are cleared by the first launch, so the workspace may
+// hold anything.
+// ---------------------------------------------------------------------------
+struct MoeDownArgs {
+  MoeShape sh;
+  const float *g, *u;  // [slots][ldf]
+  int64_t ldf;
+  float *part;         // [slots][ldd]
+  int64_t ldd;
+  int32_t *cnt;        // [m][row-tile groups]
+  const int32_t *ids;
+  const float *weights;
+  const void *res;
+  int64_t ldr;
+  void *y;
+  int64_t ldy;
+  int32_t res_f32, ydt, topk, act, R;
+};
+
+template <bool XVEC>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void moe_gate_up_kernel(
+    MoeGemvBatch mb, ExpertTable tab, const int32_t *__restrict__ ids, int topk, int32_t *cnt, int n_cnt) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  if (cnt && (blockIdx.x | blockIdx.y | blockIdx.z) == 0)
+    for (int i = threadIdx.x; i < n_cnt; i += 256) cnt[i] = 0;
+  const int c = blockIdx.z, q = blockIdx.y;
+  const MoeShape &sh = mb.sh[c];
+  const int R = mb.R[c], rt0 = blockIdx.x * R;
+  const int e = ids[q];
+  if (rt0 >= sh.n_tiles || e < 0 || e >= sh.num_experts) return;  // block-uniform; such a slot is never read
+  float *yq = (float *)mb.y[c] + (size_t)q * mb.ldy[c];
+  const MatView w = expert_view(sh, tab, c * sh.num_experts + e);
+  const uint16_t *xr = mb.x[c] + (int64_t)(q / topk) * mb.ldx[c];
+  const int reff = min(R, w.n_tiles - rt0);
+  if (w.bd >= 8)
+    gemv_fused_block<1, XVEC, 8>(w, xr, 0, yq, 0, 1, rt0, R, reff, smem);
+  else if (w.bd == 7)
+    gemv_fused_block<1, XVEC, 7>(w, xr, 0, yq, 0, 1, rt0, R, reff, smem);
+  else
+    gemv_fused_block<1, XVEC, 6>(w, xr, 0, yq, 0, 1, rt0, R, reff, smem);
+}
+
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void moe_down_kernel(MoeDownArgs a,
+                                                                                             ExpertTable tab) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int q = blockIdx.y, t = q / a.topk, rt0 = blockIdx.x * a.R;
+  const int e = a.ids[q];
+  const int reff = min(a.R, a.sh.n_tiles - rt0);
+  if (e >= 0 && e < a.sh.num_experts) {  // block-uniform
+    const MatView w = expert_view(a.sh, tab, e);
+    const PartEpi epi{a.part + (size_t)q * a.ldd};
+    const InGlu in{a.g + (size_t)q * a.ldf, a.u + (size_t)q * a.ldf, a.act};
+    if (w.bd >= 8)
+      gemv_fused_block<1, true, 8, PartEpi, InGlu>(w, nullptr, 0, nullptr, 0, 1, rt0, a.R, reff, smem, epi, in);
+    else if (w.bd == 7)
+      gemv_fused_block<1, true, 7, PartEpi, InGlu>(w, nullptr, 0, nullptr, 0, 1, rt0, a.R, reff, smem, epi, in);
+    else
+      gemv_fused_block<1, true, 6, PartEpi, InGlu>(w, nullptr, 0, nullptr, 0, 1, rt0, a.R, reff, smem, epi, in);
+  }
+  // the slot's partial rows are complete in memory before the block is
+  // counted (stores and loads of them are device-scope, coherent between the
+  // XCDs' caches); the flag lies over the radius table, which no wave reads
+  // any more
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  int *flag = (int *)smem;
+  if (threadIdx.x == 0) {
+    int32_t *c = a.cnt + (size_t)t * gridDim.x + blockIdx.x;
+    *flag = __hip_atomic_fetch_add(c, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.topk - 1;
+  }
+  __syncthreads();
+  if (!*flag) return;
+  constexpr int B = 8;  // slots requested together
+  for (int o = threadIdx.x; o < reff * 16; o += 256) {
+    const int n = rt0 * 16 + o;
+    if (n >= a.sh.n) break;
+    float acc = 0.f;
+    for (int j0 = 0; j0 < a.topk; j0 += B) {
+      float v[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int s = t * a.topk + min(j0 + b, a.topk - 1);
+        v[b] = __hip_atomic_load(a.part + (size_t)s * a.ldd + n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int s = t * a.topk + min(j0 + b, a.topk - 1);
+        const int es = a.ids[s];
+        if (j0 + b < a.topk && es >= 0 && es < a.sh.num_experts) acc = __builtin_fmaf(a.weights[s], v[b], acc);
+      }
+    }
+    if (a.res) acc += load_f(a.res, (size_t)t * a.ldr + n, a.res_f32);
+    store_out(a.y, (size_t)t * a.ldy + n, acc, a.ydt);
+  }
 }
 
 // Routing for the grouped GEMM: counting sort of slots by expert and a list
@@ -1432,6 +1609,114 @@ hipError_t launch_moe(const svq_handle *const *experts, int32_t count, int32_t E
     hipLaunchKernelGGL(moe_gemv_kernel<true>, grid, dim3(256), smem, s, mb, tab, ids, x_per_slot, topk, ydt);
   else
     hipLaunchKernelGGL(moe_gemv_kernel<false>, grid, dim3(256), smem, s, mb, tab, ids, x_per_slot, topk, ydt);
+  return hipGetLastError();
+}
+
+// Row tiles per block of a per-slot launch: about 5 units per wave to amortise
+// the gather, while the launch keeps >= 256 blocks.
+static int moe_slot_tiles(const MoeShape &sh, int S) {
+  constexpr int ITEMS_PER_WAVE = 5;
+  int R = sh.units <= ITEMS_PER_WAVE ? 4 : (sh.units <= 2 * ITEMS_PER_WAVE ? 2 : 1);
+  while (R > 1 && ((sh.n_tiles + R - 1) / R) * S < 256) R /= 2;
+  return R;
+}
+
+bool moe_ffn_few_fits(const svq_handle *gate, const svq_handle *up, const svq_handle *down, int32_t E, int64_t S) {
+  if (S > MOE_EXACT_MAX_SLOTS) return false;
+  const svq_handle *const sets[3] = {gate, up, down};
+  for (int c = 0; c < 3; ++c) {
+    const MoeShape sh = moe_shape(sets[c], E);
+    const int R = moe_slot_tiles(sh, (int)S);
+    for (int e = 0; e < E; ++e)
+      if ((size_t)gf_lds(sets[c][e].bd, sh.k, sh.units, 1, R, c == 2 ? 4 : 2).total > GV_LDS_LIMIT) return false;
+  }
+  return true;
+}
+
+hipError_t launch_moe_ffn_few(const MoeFfnArgs &f, void *ws, size_t *need, hipStream_t s) {
+  const int S = (int)(f.m * f.topk), E = f.num_experts;
+  const MoeShape shg = moe_shape(f.gate, E), shd = moe_shape(f.down, E);
+  const int64_t ldf = (shg.n + 3) / 4 * 4, ldd = shd.n;
+  const int R = moe_slot_tiles(shd, S), groups = (shd.n_tiles + R - 1) / R;
+  const size_t b_g = align256((size_t)S * ldf * 4), b_p = align256((size_t)S * ldd * 4);
+  *need = 2 * b_g + b_p + align256((size_t)f.m * groups * 4);
+  if (!ws) return hipSuccess;
+  uint8_t *p = (uint8_t *)ws;
+  MoeDownArgs d;
+  std::memset(&d, 0, sizeof(d));
+  d.sh = shd;
+  d.g = (const float *)p;
+  d.u = (const float *)(p + b_g);
+  d.ldf = ldf;
+  d.part = (float *)(p + 2 * b_g);
+  d.ldd = ldd;
+  d.cnt = (int32_t *)(p + 2 * b_g + b_p);
+  d.ids = f.ids;
+  d.weights = f.weights;
+  d.res = f.res;
+  d.ldr = f.ldr;
+  d.res_f32 = f.res_f32;
+  d.y = f.y;
+  d.ldy = f.ldy;
+  d.ydt = f.ydt;
+  d.topk = f.topk;
+  d.act = f.act;
+  d.R = R;
+
+  // gate and up in one launch while their experts share one table
+  const int per = 2 * E <= MAX_EXPERTS ? 2 : 1;
+  const svq_handle *const gu[2] = {f.gate, f.up};
+  const bool xvec = (((uintptr_t)f.x | ((uintptr_t)f.ldx * 2)) & 15) == 0;
+  static const hipError_t ok_t = check_no_static_lds(moe_gate_up_kernel<true>);
+  static const hipError_t ok_f = check_no_static_lds(moe_gate_up_kernel<false>);
+  static const hipError_t ok_d = check_no_static_lds(moe_down_kernel);
+  hipError_t e = ok_t != hipSuccess ? ok_t : (ok_f != hipSuccess ? ok_f : ok_d);
+  if (e != hipSuccess) return e;
+  for (int c0 = 0; c0 < 2; c0 += per) {
+    MoeGemvBatch mb;
+    std::memset(&mb, 0, sizeof(mb));
+    ExpertTable tab;
+    std::memset(&tab, 0, sizeof(tab));
+    const int Rg = moe_slot_tiles(shg, S);
+    size_t smem = 0;
+    for (int c = 0; c < per; ++c) {
+      for (int x = 0; x < E; ++x) {
+        tab.base[c * E + x] = (const uint8_t *)gu[c0 + c][x].dev;
+        tab.bd[c * E + x] = (uint8_t)gu[c0 + c][x].bd;
+        const size_t b = gemv_fused_smem_bytes(shg.k, shg.units, gu[c0 + c][x].bd, Rg);
+        smem = b > smem ? b : smem;
+      }
+      mb.sh[c] = moe_shape(gu[c0 + c], E);
+      mb.x[c] = (const uint16_t *)f.x;
+      mb.ldx[c] = f.ldx;
+      mb.y[c] = p + (c0 + c) * b_g;
+      mb.ldy[c] = ldf;
+      mb.R[c] = Rg;
+    }
+    e = xvec ? allow_smem(moe_gate_up_kernel<true>, smem) : allow_smem(moe_gate_up_kernel<false>, smem);
+    if (e != hipSuccess) return e;
+    const dim3 grid((shg.n_tiles + Rg - 1) / Rg, S, per);
+    int32_t *cnt = c0 == 0 ? d.cnt : nullptr;
+    const int n_cnt = (int)(f.m * groups);
+    if (xvec)
+      hipLaunchKernelGGL(moe_gate_up_kernel<true>, grid, dim3(256), smem, s, mb, tab, f.ids, f.topk, cnt, n_cnt);
+    else
+      hipLaunchKernelGGL(moe_gate_up_kernel<false>, grid, dim3(256), smem, s, mb, tab, f.ids, f.topk, cnt, n_cnt);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  ExpertTable tab;
+  std::memset(&tab, 0, sizeof(tab));
+  size_t smem = 0;
+  for (int x = 0; x < E; ++x) {
+    tab.base[x] = (const uint8_t *)f.down[x].dev;
+    tab.bd[x] = (uint8_t)f.down[x].bd;
+    const size_t b = (size_t)gf_lds(f.down[x].bd, shd.k, shd.units, 1, R, 4).total;
+    smem = b > smem ? b : smem;
+  }
+  e = allow_smem(moe_down_kernel, smem);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(moe_down_kernel, dim3(groups, S), dim3(256), smem, s, d, tab);
   return hipGetLastError();
 }
 
