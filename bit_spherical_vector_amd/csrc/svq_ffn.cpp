@@ -109,7 +109,7 @@ svq_status svq_moe_route(const void *x, int64_t m, int64_t ldx, const void *w, s
   if (!valid_dt(wdt) || (renormalize != 0 && renormalize != 1)) return SVQ_ERR_INVALID_ARG;
   if (score != SVQ_ROUTE_SOFTMAX && score != SVQ_ROUTE_SIGMOID) return SVQ_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return SVQ_ERR_INVALID_ARG;
-  const size_t need = 256;  // nothing is kept between launches
+  const size_t need = align256((size_t)m * num_experts * 8);  // the logits
   if (!workspace) {
     *workspace_bytes = need;
     return SVQ_OK;
@@ -134,7 +134,8 @@ svq_status svq_moe_route(const void *x, int64_t m, int64_t ldx, const void *w, s
   a.scale = scale;
   a.ids = ids;
   a.weights = weights;
-  return launch_route(a, compute_units(), (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
+  a.logits = (double *)workspace;
+  return launch_route(a, (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
 }
 
 svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_handle *down,

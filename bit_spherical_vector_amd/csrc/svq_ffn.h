@@ -65,6 +65,7 @@ hipError_t launch_moe_ffn_few(const MoeFfnArgs &f, void *ws, size_t *need, hipSt
 
 // ---- router --------------------------------------------------------------------
 constexpr int ROUTE_MAX_TOPK = 32;
+constexpr int ROUTE_FEW = 16;  // tokens summed on the vector units, at most
 struct RouteArgs {
   const uint16_t *x;
   int64_t m, ldx;
@@ -76,7 +77,8 @@ struct RouteArgs {
   float scale;
   int32_t *ids;
   float *weights;
+  double *logits;  // [m][num_experts] (workspace)
 };
-hipError_t launch_route(const RouteArgs &a, int cus, hipStream_t s);
+hipError_t launch_route(const RouteArgs &a, hipStream_t s);
 
 }  // namespace svq

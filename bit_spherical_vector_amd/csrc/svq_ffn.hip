@@ -73,46 +73,46 @@ hipError_t launch_combine(const CombineArgs &a, hipStream_t s) {
 // Router
 // ---------------------------------------------------------------------------
 //
-// A block of 16 waves takes T tokens and all experts, so that logits, scores
-// and the choice need one launch and no memory between them.  Wave w sums the
-// logits of experts w + 16 i, eight at a time: a lane holds the eight
-// channels 512c + 8 lane .. + 7 of its T tokens as doubles and multiplies
-// them with the same channels of each expert's row, so a weight is converted
-// once for T tokens.  Products of bf16 values are exact in double and the
-// sums keep 53 bits: the choice is that of the exact logits up to differences
-// of about 1e-15 of their size.  The vector units do double FMAs at the rate
-// of the matrix cores' double MFMAs on this chip, without padding few tokens
-// to 16 rows.
-constexpr int RT_WAVES = 16;
-constexpr int RT_EG = 8;  // experts a wave sums side by side
+// Two launches: logits in double to the workspace, then the choice.  Products
+// of bf16 values are exact in double and the sums keep 53 bits, so the choice
+// is that of the exact logits up to differences of about 1e-15 of their size.
+// (One launch with a block per token and all experts in it was slower at
+// every size: one token read the whole router matrix through one compute
+// unit, 18.7 us against the two launches together; 512 tokens read it 256
+// times.)
 
 template <bool F32>
 struct RtRow {
   u4 v[F32 ? 2 : 1];
 };
 
-// Channels k0 .. k0 + 7 of a row (zeros past k); vec: the row allows 16-byte
+// Channels k0 .. k0 + 7 of a row, zeros past k; vec: the row allows 16-byte
 // loads and k is a multiple of 8.
 template <bool F32>
 __device__ __forceinline__ RtRow<F32> rt_load(const void *row, int k0, int k, bool vec) {
   RtRow<F32> r;
   if (vec) {
-    const int at = min(k0, k - 8);  // clamped loads; the caller's x is zero past k
+    const int at = min(k0, k - 8);
     if constexpr (F32) {
       r.v[0] = *(const u4 *)((const float *)row + at);
       r.v[1] = *(const u4 *)((const float *)row + at + 4);
     } else {
       r.v[0] = *(const u4 *)((const uint16_t *)row + at);
     }
+    if (k0 >= k) {
+      r.v[0] = (u4){0u, 0u, 0u, 0u};
+      if constexpr (F32) r.v[1] = r.v[0];
+    }
   } else {
 #pragma unroll
-    for (int l = 0; l < 4; ++l) {
-      const int a = min(k0 + 2 * l, k - 1), b = min(k0 + 2 * l + 1, k - 1);
+    for (int l = 0; l < 8; ++l) {
+      const int at = min(k0 + l, k - 1);
       if constexpr (F32) {
-        r.v[l >> 1][2 * (l & 1)] = ((const uint32_t *)row)[a];
-        r.v[l >> 1][2 * (l & 1) + 1] = ((const uint32_t *)row)[b];
+        const uint32_t b = ((const uint32_t *)row)[at];
+        r.v[l >> 2][l & 3] = k0 + l < k ? b : 0u;
       } else {
-        r.v[0][l] = (uint32_t)((const uint16_t *)row)[a] | ((uint32_t)((const uint16_t *)row)[b] << 16);
+        const uint32_t b = k0 + l < k ? ((const uint16_t *)row)[at] : 0u;
+        r.v[0][l >> 1] = (l & 1) ? r.v[0][l >> 1] | (b << 16) : b;
       }
     }
   }
@@ -130,8 +130,101 @@ __device__ __forceinline__ double shfl_xor_f64(double v, int d) {
   const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)b, d), hi = (uint32_t)__shfl_xor((int)(b >> 32), d);
   return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
 }
-__device__ __forceinline__ int64_t shfl_xor_i64(int64_t v, int d) {
-  return __builtin_bit_cast(int64_t, shfl_xor_f64(__builtin_bit_cast(double, v), d));
+
+// Few tokens: a wave per expert and RT_TOKENS tokens, the lanes along k (eight
+// channels each), a double FMA per product, RT_CHUNKS chunks of 512 channels
+// in flight.
+constexpr int RT_TOKENS = 4;
+constexpr int RT_CHUNKS = 4;
+template <int T, bool WF32>
+__global__ __launch_bounds__(256) void moe_logits_few_kernel(RouteArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int e = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  if (e >= a.num_experts) return;  // wave-uniform; no barrier in this kernel
+  const int64_t t0 = (int64_t)blockIdx.y * T;
+  const int k = a.k;
+  const bool vec = a.vec != 0;
+  const char *wr = (const char *)a.w + (size_t)e * a.ldw * (WF32 ? 4 : 2);
+  const uint16_t *xr[T];
+  double acc[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    xr[t] = a.x + min(t0 + t, a.m - 1) * a.ldx;
+    acc[t] = 0.0;
+  }
+  for (int c = 0; c < k; c += 512 * RT_CHUNKS) {
+    RtRow<WF32> w[RT_CHUNKS];
+    RtRow<false> x[RT_CHUNKS][T];
+#pragma unroll
+    for (int i = 0; i < RT_CHUNKS; ++i) w[i] = rt_load<WF32>(wr, c + 512 * i + 8 * lane, k, vec);
+#pragma unroll
+    for (int i = 0; i < RT_CHUNKS; ++i)
+#pragma unroll
+      for (int t = 0; t < T; ++t) x[i][t] = rt_load<false>(xr[t], c + 512 * i + 8 * lane, k, vec);
+#pragma unroll
+    for (int i = 0; i < RT_CHUNKS; ++i)
+#pragma unroll
+      for (int l = 0; l < 8; ++l) {
+        const double wd = rt_get<WF32>(w[i], l);
+#pragma unroll
+        for (int t = 0; t < T; ++t) acc[t] = __builtin_fma(rt_get<false>(x[i][t], l), wd, acc[t]);
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    double v = acc[t];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v += shfl_xor_f64(v, d);
+    if (lane == 0 && t0 + t < a.m) a.logits[(t0 + t) * a.num_experts + e] = v;
+  }
+}
+
+// Many tokens: a block of 16 waves takes 16 tokens x 16 experts, each wave
+// every 16th chunk of 32 channels through v_mfma_f64_16x16x4_f64 (element j
+// of the eight channels a lane loads is one MFMA: its four k indices are
+// channels 8g + j of the lane groups g), then the waves' tiles are summed in
+// wave order.
+typedef double d4 __attribute__((ext_vector_type(4)));
+constexpr int RT_WAVES = 16;
+template <bool WF32>
+__global__ __launch_bounds__(RT_WAVES * 64) void moe_logits_kernel(RouteArgs a) {
+  __shared__ double s_red[RT_WAVES][256];
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int k = a.k, e0 = (int)blockIdx.x * 16;
+  const int64_t t0 = (int64_t)blockIdx.y * 16;
+  const bool vec = a.vec != 0;
+  const uint16_t *xr = a.x + min(t0 + i, a.m - 1) * a.ldx;
+  const char *wr = (const char *)a.w + (size_t)min(e0 + i, a.num_experts - 1) * a.ldw * (WF32 ? 4 : 2);
+  d4 c = {0.0, 0.0, 0.0, 0.0};
+  constexpr int B = 4;  // chunks in flight
+  for (int c0 = 32 * wv; c0 < k; c0 += 32 * RT_WAVES * B) {
+    RtRow<WF32> w[B];
+    RtRow<false> x[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      x[b] = rt_load<false>(xr, c0 + 32 * RT_WAVES * b + 8 * g, k, vec);
+      w[b] = rt_load<WF32>(wr, c0 + 32 * RT_WAVES * b + 8 * g, k, vec);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      if (c0 + 32 * RT_WAVES * b >= k) break;  // wave-uniform
+#pragma unroll
+      for (int l = 0; l < 8; ++l)
+        c = __builtin_amdgcn_mfma_f64_16x16x4f64(rt_get<false>(x[b], l), rt_get<WF32>(w[b], l), c, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) s_red[wv][64 * r + lane] = c[r];
+  __syncthreads();
+  if (tid >= 256) return;
+  double v = 0.0;
+#pragma unroll
+  for (int w = 0; w < RT_WAVES; ++w) v += s_red[w][tid];
+  // accumulator register r of lane 16 g + i: token g + 4 r, expert i
+  const int64_t t = t0 + ((tid >> 4) & 3) + 4 * (tid >> 6);
+  const int e = e0 + (tid & 15);
+  if (t < a.m && e < a.num_experts) a.logits[t * a.num_experts + e] = v;
 }
 
 // Order-preserving integer of a key: NaN below every number, -0 equal to +0.
@@ -141,158 +234,85 @@ __device__ __forceinline__ int64_t rt_order(double key) {
   return b >= 0 ? b : (b ^ INT64_MAX);
 }
 
-template <int T, bool WF32>
-__global__ __launch_bounds__(RT_WAVES * 64) void moe_route_topk_kernel(RouteArgs a) {
-  __shared__ double s_logit[T][MAX_EXPERTS];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t t0 = (int64_t)blockIdx.x * T;
-  const int k = a.k, E = a.num_experts;
-  const bool vec = a.vec != 0;
-  const size_t wsz = WF32 ? 4 : 2;
-  const uint16_t *xr[T];
-#pragma unroll
-  for (int t = 0; t < T; ++t) xr[t] = a.x + min(t0 + t, a.m - 1) * a.ldx;
-
-  for (int e0 = wv; e0 < E; e0 += RT_WAVES * RT_EG) {
-    const char *wr[RT_EG];
-#pragma unroll
-    for (int i = 0; i < RT_EG; ++i)
-      wr[i] = (const char *)a.w + (size_t)min(e0 + RT_WAVES * i, E - 1) * a.ldw * wsz;
-    double acc[RT_EG][T];
-#pragma unroll
-    for (int i = 0; i < RT_EG; ++i)
-#pragma unroll
-      for (int t = 0; t < T; ++t) acc[i][t] = 0.0;
-    for (int c = 0; c < k; c += 512) {
-      const int k0 = c + 8 * lane;
-      RtRow<WF32> wrow[RT_EG];
-      RtRow<false> xrow[T];
-#pragma unroll
-      for (int t = 0; t < T; ++t) xrow[t] = rt_load<false>(xr[t], k0, k, vec);
-#pragma unroll
-      for (int i = 0; i < RT_EG; ++i) wrow[i] = rt_load<WF32>(wr[i], k0, k, vec);
-#pragma unroll
-      for (int l = 0; l < 8; ++l) {
-        double xv[T];
-#pragma unroll
-        for (int t = 0; t < T; ++t) xv[t] = rt_get<false>(xrow[t], l);
-        if (k0 + l < k) {
-#pragma unroll
-          for (int i = 0; i < RT_EG; ++i) {
-            const double wd = rt_get<WF32>(wrow[i], l);
-#pragma unroll
-            for (int t = 0; t < T; ++t) acc[i][t] = __builtin_fma(xv[t], wd, acc[i][t]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < RT_EG; ++i) {
-#pragma unroll
-      for (int t = 0; t < T; ++t) {
-        double v = acc[i][t];
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) v += shfl_xor_f64(v, d);
-        const int e = e0 + RT_WAVES * i;
-        if (lane == 0 && e < E) s_logit[t][e] = v;
-      }
-    }
-  }
-  __syncthreads();
-  if (wv >= T || t0 + wv >= a.m) return;
-
-  // wave wv chooses for token t0 + wv; lane holds experts lane + 64 i
-  constexpr int PL = MAX_EXPERTS / 64;
-  const int64_t t = t0 + wv;
-  double p[PL];
-  int64_t key[PL];
-  double mx = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = lane + 64 * i;
-    p[i] = e < E ? s_logit[wv][e] : -INFINITY;
-    if (!a.select_bias) key[i] = e < E ? rt_order(p[i]) : INT64_MIN;
-    mx = fmax(mx, p[i]);
-  }
+// The choice of one token, thread e for expert e: an expert's place is the
+// number of experts before it (larger key, or equal key and lower index), so
+// all places are found at once and no place waits for the one before.
+__global__ __launch_bounds__(MAX_EXPERTS) void moe_topk_kernel(RouteArgs a) {
+  constexpr int W = MAX_EXPERTS / 64;
+  __shared__ double s_w[W], s_p[ROUTE_MAX_TOPK];
+  __shared__ int64_t s_key[MAX_EXPERTS];
+  const int e = threadIdx.x, E = a.num_experts;
+  const int64_t t = blockIdx.x;
+  const bool in = e < E;
+  const double l = in ? a.logits[t * E + e] : -INFINITY;
+  double p;
   if (a.score == SVQ_ROUTE_SOFTMAX) {
+    double mx = l;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) mx = fmax(mx, shfl_xor_f64(mx, d));
-    double sum = 0.0;
+    if ((e & 63) == 0) s_w[e >> 6] = mx;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      p[i] = lane + 64 * i < E ? exp(p[i] - mx) : 0.0;
-      sum += p[i];
-    }
+    for (int w = 0; w < W; ++w) mx = fmax(mx, s_w[w]);
+    __syncthreads();
+    p = in ? exp(l - mx) : 0.0;
+    double sum = p;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += shfl_xor_f64(sum, d);
+    if ((e & 63) == 0) s_w[e >> 6] = sum;
+    __syncthreads();
+    sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) p[i] /= sum;
+    for (int w = 0; w < W; ++w) sum += s_w[w];
+    p /= sum;
   } else {
-#pragma unroll
-    for (int i = 0; i < PL; ++i) p[i] = 1.0 / (1.0 + exp(-p[i]));
+    p = 1.0 / (1.0 + exp(-l));
   }
-  if (a.select_bias) {
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const int e = lane + 64 * i;
-      key[i] = e < E ? rt_order(p[i] + (double)a.select_bias[min(e, E - 1)]) : INT64_MIN;
-    }
+  const int64_t key = in ? rt_order(a.select_bias ? p + (double)a.select_bias[e] : l) : INT64_MIN;
+  s_key[e] = key;
+  __syncthreads();
+  int place = 0;
+  for (int j = 0; j < E; ++j) {
+    const int64_t other = s_key[j];
+    place += other > key || (other == key && j < e) ? 1 : 0;
   }
-  double mine = 0.0, total = 0.0;  // lane j: the score of choice j
-  int id = 0;
-  for (int j = 0; j < a.topk; ++j) {
-    int64_t bk = INT64_MIN;
-    int be = MAX_EXPERTS;
-    double bp = 0.0;
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (key[i] > bk) {  // equal keys keep the lower index (i ascending)
-        bk = key[i];
-        be = lane + 64 * i;
-        bp = p[i];
-      }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t ok = shfl_xor_i64(bk, d);
-      const int oe = __shfl_xor(be, d);
-      const double op = shfl_xor_f64(bp, d);
-      if (ok > bk || (ok == bk && oe < be)) {
-        bk = ok;
-        be = oe;
-        bp = op;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (lane + 64 * i == be) key[i] = INT64_MIN;
-    if (lane == j) {
-      mine = bp;
-      id = be;
-    }
-    total += bp;
+  if (in && place < a.topk) {
+    a.ids[t * a.topk + place] = e;
+    s_p[place] = p;
   }
-  if (lane < a.topk) {
-    if (a.renormalize) mine /= total;
-    a.ids[t * a.topk + lane] = id;
-    a.weights[t * a.topk + lane] = (float)(mine * (double)a.scale);
+  __syncthreads();
+  if (e < a.topk) {
+    double v = s_p[e];
+    if (a.renormalize) {
+      double total = 0.0;
+      for (int j = 0; j < a.topk; ++j) total += s_p[j];
+      v /= total;
+    }
+    a.weights[t * a.topk + e] = (float)(v * (double)a.scale);
   }
 }
 
-template <int T>
-static hipError_t launch_route_t(const RouteArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.m + T - 1) / T)), block(RT_WAVES * 64);
-  if (a.w_f32)
-    hipLaunchKernelGGL((moe_route_topk_kernel<T, true>), grid, block, 0, s, a);
+template <bool WF32>
+static void launch_logits(const RouteArgs &a, hipStream_t s) {
+  const unsigned eb = (unsigned)((a.num_experts + 3) / 4);
+  if (a.m == 1)
+    hipLaunchKernelGGL((moe_logits_few_kernel<1, WF32>), dim3(eb), dim3(256), 0, s, a);
+  else if (a.m <= ROUTE_FEW)
+    hipLaunchKernelGGL((moe_logits_few_kernel<RT_TOKENS, WF32>),
+                       dim3(eb, (unsigned)((a.m + RT_TOKENS - 1) / RT_TOKENS)), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((moe_route_topk_kernel<T, false>), grid, block, 0, s, a);
-  return hipGetLastError();
+    hipLaunchKernelGGL(moe_logits_kernel<WF32>,
+                       dim3((unsigned)((a.num_experts + 15) / 16), (unsigned)((a.m + 15) / 16)),
+                       dim3(RT_WAVES * 64), 0, s, a);
 }
 
-hipError_t launch_route(const RouteArgs &a, int cus, hipStream_t s) {
-  if (a.m <= cus) return launch_route_t<1>(a, s);
-  if (a.m <= 2 * (int64_t)cus) return launch_route_t<2>(a, s);
-  return launch_route_t<4>(a, s);
+hipError_t launch_route(const RouteArgs &a, hipStream_t s) {
+  if (a.w_f32) launch_logits<true>(a, s);
+  else launch_logits<false>(a, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(moe_topk_kernel, dim3((unsigned)a.m), dim3(MAX_EXPERTS), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace svq

@@ -1612,12 +1612,17 @@ hipError_t launch_moe(const svq_handle *const *experts, int32_t count, int32_t E
   return hipGetLastError();
 }
 
-// Row tiles per block of a per-slot launch: about 5 units per wave to amortise
-// the gather, while the launch keeps >= 256 blocks.
-static int moe_slot_tiles(const MoeShape &sh, int S) {
-  constexpr int ITEMS_PER_WAVE = 5;
-  int R = sh.units <= ITEMS_PER_WAVE ? 4 : (sh.units <= 2 * ITEMS_PER_WAVE ? 2 : 1);
-  while (R > 1 && ((sh.n_tiles + R - 1) / R) * S < 256) R /= 2;
+// Row tiles per block of the two launches: as few as give every wave two work
+// items (a block's prologue costs about as much) and let all blocks be
+// resident at once, three to a compute unit.  Measured, 128 experts of
+// 768 x 2048 top 8 (us per layer): one token 17.5 with 2 and 4 row tiles for
+// gate/up and down (1 and 4: 18.2; 2 and 8: 19.2); 3 tokens 24.7 with 4 and 4
+// (2 and 4: 26.2; 4 and 8: 25.8); 7 tokens 40.8 with 8 and 8 (4 and 8: 42.8;
+// 8 and 4: 43.2; 4 and 4: 45.8).
+static int moe_slot_tiles(const MoeShape &sh, int blocks_per_group) {
+  const int slots = 3 * compute_units();
+  int R = 1;
+  while (R < GF_MAX_R && (R * sh.units < 8 || (sh.n_tiles + R - 1) / R * blocks_per_group > slots)) R *= 2;
   return R;
 }
 
@@ -1626,7 +1631,7 @@ bool moe_ffn_few_fits(const svq_handle *gate, const svq_handle *up, const svq_ha
   const svq_handle *const sets[3] = {gate, up, down};
   for (int c = 0; c < 3; ++c) {
     const MoeShape sh = moe_shape(sets[c], E);
-    const int R = moe_slot_tiles(sh, (int)S);
+    const int R = moe_slot_tiles(sh, (int)S * (c == 2 ? 1 : 2));
     for (int e = 0; e < E; ++e)
       if ((size_t)gf_lds(sets[c][e].bd, sh.k, sh.units, 1, R, c == 2 ? 4 : 2).total > GV_LDS_LIMIT) return false;
   }
@@ -1677,7 +1682,7 @@ hipError_t launch_moe_ffn_few(const MoeFfnArgs &f, void *ws, size_t *need, hipSt
     std::memset(&mb, 0, sizeof(mb));
     ExpertTable tab;
     std::memset(&tab, 0, sizeof(tab));
-    const int Rg = moe_slot_tiles(shg, S);
+    const int Rg = moe_slot_tiles(shg, 2 * S);
     size_t smem = 0;
     for (int c = 0; c < per; ++c) {
       for (int x = 0; x < E; ++x) {
