@@ -234,54 +234,82 @@ __device__ __forceinline__ int64_t rt_order(double key) {
   return b >= 0 ? b : (b ^ INT64_MAX);
 }
 
-// The choice of one token, thread e for expert e: an expert's place is the
-// number of experts before it (larger key, or equal key and lower index), so
-// all places are found at once and no place waits for the one before.
-__global__ __launch_bounds__(MAX_EXPERTS) void moe_topk_kernel(RouteArgs a) {
+// The choice of one token: an expert's place is the number of experts before
+// it (larger key, or equal key and lower index), so all places are found at
+// once and no place waits for the one before.  Thread e of each quarter of
+// the block counts a quarter of the experts for expert e; the first quarter
+// holds the scores.
+constexpr int TK_PARTS = 4;
+__global__ __launch_bounds__(TK_PARTS * MAX_EXPERTS) void moe_topk_kernel(RouteArgs a) {
   constexpr int W = MAX_EXPERTS / 64;
-  __shared__ double s_w[W], s_p[ROUTE_MAX_TOPK];
+  __shared__ double s_mx[W], s_sum[W], s_p[ROUTE_MAX_TOPK];
   __shared__ int64_t s_key[MAX_EXPERTS];
-  const int e = threadIdx.x, E = a.num_experts;
+  __shared__ int s_place[MAX_EXPERTS];
+  const int e = threadIdx.x & (MAX_EXPERTS - 1), E = a.num_experts;
+  const int part = __builtin_amdgcn_readfirstlane((int)threadIdx.x / MAX_EXPERTS);
   const int64_t t = blockIdx.x;
-  const bool in = e < E;
-  const double l = in ? a.logits[t * E + e] : -INFINITY;
-  double p;
-  if (a.score == SVQ_ROUTE_SOFTMAX) {
-    double mx = l;
+  const bool in = e < E, soft = a.score == SVQ_ROUTE_SOFTMAX;
+  double l = 0.0, p = 0.0;
+  if (part == 0) {
+    l = in ? a.logits[t * E + e] : -INFINITY;
+    s_place[e] = 0;
+    if (soft) {
+      double mx = l;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) mx = fmax(mx, shfl_xor_f64(mx, d));
-    if ((e & 63) == 0) s_w[e >> 6] = mx;
-    __syncthreads();
+      for (int d = 1; d < 64; d <<= 1) mx = fmax(mx, shfl_xor_f64(mx, d));
+      if ((e & 63) == 0) s_mx[e >> 6] = mx;
+    } else {
+      p = 1.0 / (1.0 + exp(-l));
+    }
+    if (!a.select_bias) s_key[e] = in ? rt_order(l) : INT64_MIN;
+  }
+  __syncthreads();
+  if (part == 0 && soft) {
+    double mx = s_mx[0];
 #pragma unroll
-    for (int w = 0; w < W; ++w) mx = fmax(mx, s_w[w]);
-    __syncthreads();
+    for (int w = 1; w < W; ++w) mx = fmax(mx, s_mx[w]);
     p = in ? exp(l - mx) : 0.0;
     double sum = p;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += shfl_xor_f64(sum, d);
-    if ((e & 63) == 0) s_w[e >> 6] = sum;
+    if ((e & 63) == 0) s_sum[e >> 6] = sum;
+  }
+  if (a.select_bias) {  // keys need the scores
     __syncthreads();
-    sum = 0.0;
+    if (part == 0) {
+      double sum = 0.0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) sum += s_w[w];
-    p /= sum;
-  } else {
-    p = 1.0 / (1.0 + exp(-l));
+      for (int w = 0; w < W; ++w) sum += s_sum[w];
+      const double q = soft ? p / sum : p;
+      s_key[e] = in ? rt_order(q + (double)a.select_bias[e]) : INT64_MIN;
+    }
+    __syncthreads();
   }
-  const int64_t key = in ? rt_order(a.select_bias ? p + (double)a.select_bias[e] : l) : INT64_MIN;
-  s_key[e] = key;
+  if (in) {
+    const int64_t key = s_key[e];
+    const int per = (E + TK_PARTS - 1) / TK_PARTS, j0 = part * per, j1 = min(E, j0 + per);
+    int before = 0;
+#pragma unroll 8
+    for (int j = j0; j < j1; ++j) {
+      const int64_t other = s_key[j];
+      before += other > key || (other == key && j < e) ? 1 : 0;
+    }
+    if (before) atomicAdd(&s_place[e], before);
+  }
   __syncthreads();
-  int place = 0;
-  for (int j = 0; j < E; ++j) {
-    const int64_t other = s_key[j];
-    place += other > key || (other == key && j < e) ? 1 : 0;
-  }
-  if (in && place < a.topk) {
+  const int place = s_place[e];
+  if (part == 0 && in && place < a.topk) {
+    double sum = 1.0;
+    if (soft) {
+      sum = 0.0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) sum += s_sum[w];
+    }
     a.ids[t * a.topk + place] = e;
-    s_p[place] = p;
+    s_p[place] = p / sum;
   }
   __syncthreads();
-  if (e < a.topk) {
+  if (part == 0 && e < a.topk) {
     double v = s_p[e];
     if (a.renormalize) {
       double total = 0.0;
@@ -311,7 +339,7 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t s) {
   else launch_logits<false>(a, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_topk_kernel, dim3((unsigned)a.m), dim3(MAX_EXPERTS), 0, s, a);
+  hipLaunchKernelGGL(moe_topk_kernel, dim3((unsigned)a.m), dim3(TK_PARTS * MAX_EXPERTS), 0, s, a);
   return hipGetLastError();
 }
 
