@@ -60,6 +60,35 @@ svq_status svq_linear_glu(const svq_handle *gate, const svq_handle *up, const vo
   if (!valid_act(act) || !valid_dt(ydt)) return SVQ_ERR_INVALID_ARG;
   if ((bias_gate || bias_up) && !valid_dt(bias_dt)) return SVQ_ERR_INVALID_ARG;
   if (m < 1 || m > (1 << 24) || ldx < gate->k || ldy < gate->n) return SVQ_ERR_INVALID_ARG;
+  if (m == 1) {
+    // one launch while both halves of a block fit in LDS; row tiles per block
+    // so that one round of blocks, one per compute unit, covers the matrices
+    int R = (gate->n_tiles + compute_units() - 1) / compute_units();
+    R = R > GF_MAX_R ? GF_MAX_R : R;
+    while (R > 1 && !glu_fused_smem(gate->k, gate->units, gate->bd, up->bd, R)) --R;
+    if (glu_fused_smem(gate->k, gate->units, gate->bd, up->bd, R)) {
+      const size_t need = 256;  // unused: everything stays in LDS
+      if (!workspace) {
+        *workspace_bytes = need;
+        return SVQ_OK;
+      }
+      if (!x || !y) return SVQ_ERR_INVALID_ARG;
+      if (*workspace_bytes < need) return SVQ_ERR_BUFFER_TOO_SMALL;
+      GluFusedArgs a;
+      std::memset(&a, 0, sizeof(a));
+      a.gate = matrix_view(gate);
+      a.up = matrix_view(up);
+      a.x = (const uint16_t *)x;
+      a.bias_g = bias_gate;
+      a.bias_u = bias_up;
+      a.bias_f32 = bias_dt == SVQ_F32;
+      a.act = (int32_t)act;
+      a.y = y;
+      a.ydt = (int32_t)ydt;
+      a.R = R;
+      return launch_glu_fused(a, (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
+    }
+  }
   const int64_t ldp = pad4(gate->n);
   const svq_handle w[2] = {*gate, *up};
   const int64_t lx[2] = {ldx, ldx}, ly[2] = {ldp, ldp};

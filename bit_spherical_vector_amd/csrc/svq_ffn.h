@@ -11,6 +11,7 @@ svq_status linear_epi(const svq_handle *w, int32_t count, const void *const *x, 
                       void *const *y, const int64_t *ldy, svq_dtype ydt, const EpiArgs *epi,
                       void *workspace, size_t *workspace_bytes, void *stream);
 svq_status check_handle(const svq_handle *w);
+MatView matrix_view(const svq_handle *w);
 int compute_units();  // of the current device
 
 // ---- elementwise steps -------------------------------------------------------
@@ -24,6 +25,18 @@ struct GluArgs {
   int32_t n, ydt;
 };
 hipError_t launch_glu(const GluArgs &a, hipStream_t s);
+
+// One row through both matrices in one launch (R row tiles per block).
+struct GluFusedArgs {
+  MatView gate, up;
+  const uint16_t *x;
+  const void *bias_g, *bias_u;
+  int32_t bias_f32, act;
+  void *y;
+  int32_t ydt, R;
+};
+size_t glu_fused_smem(int k, int units, int bd_gate, int bd_up, int R);  // 0: does not fit
+hipError_t launch_glu_fused(const GluFusedArgs &a, hipStream_t s);
 
 struct CombineArgs {
   const float *d;  // [m * topk][ldd]

@@ -783,6 +783,7 @@ svq_status linear_epi(const svq_handle *w, int32_t count, const void *const *x, 
   return linear_impl(w, count, x, ldx, m, y, ldy, ydt, workspace, workspace_bytes, stream, epi);
 }
 svq_status check_handle(const svq_handle *w) { return validate_handle(w); }
+MatView matrix_view(const svq_handle *w) { return view_of(w); }
 int compute_units() { return device_cus(); }
 }  // namespace svq
 

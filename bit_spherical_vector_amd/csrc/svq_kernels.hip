@@ -803,11 +803,18 @@ constexpr int GF_GLU_BATCH = 2;  // 16-byte pieces of g and u prefetched per thr
 
 // XVEC: every activation row starts 16-byte aligned (vector staging loads).
 // BD: the matrix's direction bits (table layout, see above).
-template <int M, bool XVEC, int BD, typename EPI = NoEpi, typename IN = InBf16>
+// HB: the block's LDS starts there (0, or 65536 for the second half of a
+// two-matrix block, whose table addresses then carry it in byte 2, which the
+// SDWA address ops preserve).  DUAL: threads 0..255 or 256..511 of a block
+// whose other half runs this function too, on another matrix: both halves
+// pass the same barriers whatever their tables' layouts.
+template <int M, bool XVEC, int BD, typename EPI = NoEpi, typename IN = InBf16, bool DUAL = false, int HB = 0>
 __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ x, int64_t ldx,
                                  void *y, int64_t ldy, int ydt, int rt0, int R,
                                  int Reff, uint8_t *smem, const EPI &epi = EPI(), const IN &in = IN()) {
-  const int tid = threadIdx.x, lane = tid & 63;
+  static_assert(HB % 65536 == 0, "the base stays clear of the address bits the SDWA ops write");
+  smem += HB;
+  const int tid = DUAL ? threadIdx.x & 255 : threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform
   const int U = w.units, Kp = U * UNIT_SLOTS, K = w.k;
   constexpr int rows = 1 << BD;
@@ -903,7 +910,7 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
     uint32_t m2 = 0;
 #pragma unroll
     for (int l = 0; l < 4; ++l) {
-      const uint32_t p = stage_pair<gf_off_stage(BD)>(pv[l]);
+      const uint32_t p = stage_pair<HB + gf_off_stage(BD)>(pv[l]);
       pr[l] = valid ? p : 0u;
       m2 = pk_absmax(m2, pr[l]);
     }
@@ -965,8 +972,8 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
         float v[8], mx = 0.f;
 #pragma unroll
         for (int l = 0; l < 4; ++l) {
-          v[2 * l] = valid ? lds_f32(gf_off_stage(BD) + word_shl<0, 2>(pv[l])) : 0.f;
-          v[2 * l + 1] = valid ? lds_f32(gf_off_stage(BD) + word_shl<1, 2>(pv[l])) : 0.f;
+          v[2 * l] = valid ? lds_f32(HB + gf_off_stage(BD) + word_shl<0, 2>(pv[l])) : 0.f;
+          v[2 * l + 1] = valid ? lds_f32(HB + gf_off_stage(BD) + word_shl<1, 2>(pv[l])) : 0.f;
           mx = fmaxf(mx, fmaxf(fabsf(v[2 * l]), fabsf(v[2 * l + 1])));
         }
         mx = wave_max(mx);
@@ -1018,6 +1025,8 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
       const int row = tid, cp = (q + row) & 7;
       *(u4 *)(smem + gf_off_d(BD) + row * 128 + cp * 16) = drow;
     }
+  } else if constexpr (DUAL) {
+    __syncthreads();  // the other half may have bd = 8
   }
   __syncthreads();  // gathered activations, scales and tables are visible
 
@@ -1030,13 +1039,13 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
   for (int ri = 0; ri < 4; ++ri)
 #pragma unroll
     for (int a = 0; a < M; ++a) acc[ri][a] = 0.f;
-  const uint32_t lane4 = (uint32_t)lane << 2;
-  const uint32_t loff = (uint32_t)(lane & 7) << 4;  // bd = 8: the lane's copy
+  const uint32_t lane4 = (uint32_t)HB | (uint32_t)lane << 2;
+  const uint32_t loff = (uint32_t)HB | (uint32_t)(lane & 7) << 4;  // bd = 8: the lane's copy
   uint32_t dad0[4], dad1[4];  // bd <= 7: byte 0 = the lane's copy * 16
   uint32_t rad0[4], rad1[4];  // bd <= 7: byte 0 = 4 * lane
 #pragma unroll
   for (int ri = 0; ri < 4; ++ri) {
-    dad0[ri] = dad1[ri] = (uint32_t)(lane & 15) << 4;
+    dad0[ri] = dad1[ri] = (uint32_t)HB | (uint32_t)(lane & 15) << 4;
     rad0[ri] = rad1[ri] = lane4;
   }
 
@@ -1188,6 +1197,84 @@ static hipError_t launch_fused_x(GemvBatch &b, int blocks, size_t smem, hipStrea
 
 hipError_t launch_gemv_fused(GemvBatch &b, int blocks, size_t smem, hipStream_t s) {
   return b.xvec ? launch_fused_x<true>(b, blocks, smem, s) : launch_fused_x<false>(b, blocks, smem, s);
+}
+
+// ---------------------------------------------------------------------------
+// Gated pair at m = 1: one launch for act(Gate x + bg) * (Up x + bu).
+// ---------------------------------------------------------------------------
+//
+// A block of 8 waves takes R row tiles of both matrices: waves 0..3 run the
+// fused block above on the gate's, waves 4..7 on the up matrix's, each half
+// with its own tables and gathered row (permutations and splits differ) in
+// its own part of LDS; the sums meet in LDS, so nothing goes through memory
+// and no block waits for another.  8 waves per compute unit is what two
+// blocks of the plain launch put there for such sizes.
+constexpr int GLU_HALF = 65536;  // LDS offset of the second half
+
+// Sums of the block's rows, kept in LDS.
+struct LdsEpi {
+  static constexpr bool on = true, partial = true;
+  float *row;  // row n of the matrix at row[n - n0]
+  int n0;
+  __device__ __forceinline__ void put(float v, int n) const { row[n - n0] = v; }
+};
+
+template <bool XVEC, int HB>
+__device__ __forceinline__ void glu_half(const MatView &w, const uint16_t *x, int rt0, int R, int Reff,
+                                         uint8_t *smem) {
+  // the gathered row is dead once every wave is done with its items
+  const LdsEpi epi{(float *)(smem + HB + gf_lds(w.bd, w.k, w.units, 1, R).xp), rt0 * 16};
+  if (w.bd >= 8)
+    gemv_fused_block<1, XVEC, 8, LdsEpi, InBf16, true, HB>(w, x, 0, nullptr, 0, 1, rt0, R, Reff, smem, epi);
+  else if (w.bd == 7)
+    gemv_fused_block<1, XVEC, 7, LdsEpi, InBf16, true, HB>(w, x, 0, nullptr, 0, 1, rt0, R, Reff, smem, epi);
+  else
+    gemv_fused_block<1, XVEC, 6, LdsEpi, InBf16, true, HB>(w, x, 0, nullptr, 0, 1, rt0, R, Reff, smem, epi);
+}
+
+template <bool XVEC>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void glu_fused_kernel(GluFusedArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int rt0 = (int)blockIdx.x * a.R, reff = min(a.R, a.gate.n_tiles - rt0);
+  if (__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8) == 0)
+    glu_half<XVEC, 0>(a.gate, a.x, rt0, a.R, reff, smem);
+  else
+    glu_half<XVEC, GLU_HALF>(a.up, a.x, rt0, a.R, reff, smem);
+  __syncthreads();
+  const float *g = (const float *)(smem + gf_lds(a.gate.bd, a.gate.k, a.gate.units, 1, a.R).xp);
+  const float *u = (const float *)(smem + GLU_HALF + gf_lds(a.up.bd, a.up.k, a.up.units, 1, a.R).xp);
+  for (int o = threadIdx.x; o < reff * 16; o += 512) {
+    const int n = rt0 * 16 + o;
+    if (n >= a.gate.n) break;
+    float gv = g[o], uv = u[o];
+    if (a.bias_g) gv += load_f(a.bias_g, n, a.bias_f32);
+    if (a.bias_u) uv += load_f(a.bias_u, n, a.bias_f32);
+    store_out(a.y, n, act_apply(gv, a.act) * uv, a.ydt);
+  }
+}
+
+// LDS of the launch, or 0 when the pair does not fit.
+size_t glu_fused_smem(int k, int units, int bd_gate, int bd_up, int R) {
+  const size_t g = gf_lds(bd_gate, k, units, 1, R).total, u = gf_lds(bd_up, k, units, 1, R).total;
+  return g <= (size_t)GLU_HALF && GLU_HALF + u <= GV_LDS_LIMIT ? GLU_HALF + u : 0;
+}
+
+hipError_t launch_glu_fused(const GluFusedArgs &a, hipStream_t s) {
+  const size_t smem = glu_fused_smem(a.gate.k, a.gate.units, a.gate.bd, a.up.bd, a.R);
+  if (smem == 0 || a.R > GF_MAX_R) return hipErrorInvalidValue;
+  static const hipError_t ok_t = check_no_static_lds(glu_fused_kernel<true>);
+  static const hipError_t ok_f = check_no_static_lds(glu_fused_kernel<false>);
+  hipError_t e = ok_t != hipSuccess ? ok_t : ok_f;
+  if (e != hipSuccess) return e;
+  const bool xvec = ((uintptr_t)a.x & 15) == 0;
+  e = xvec ? allow_smem(glu_fused_kernel<true>, smem) : allow_smem(glu_fused_kernel<false>, smem);
+  if (e != hipSuccess) return e;
+  const dim3 grid((a.gate.n_tiles + a.R - 1) / a.R);
+  if (xvec)
+    hipLaunchKernelGGL(glu_fused_kernel<true>, grid, dim3(512), smem, s, a);
+  else
+    hipLaunchKernelGGL(glu_fused_kernel<false>, grid, dim3(512), smem, s, a);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------

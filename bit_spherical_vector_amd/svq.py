@@ -710,17 +710,16 @@ class _Call:
         self.ws_size_ref = ctypes.byref(self.ws_size)
 
     def __call__(self) -> None:
-        import torch
-        stream = self.stream
-        if self.device.index != torch.cuda.current_device():
-            with torch.cuda.device(self.device):
-                if stream is None:
-                    stream = torch.cuda.current_stream().cuda_stream
-                st = self.fn(*self.args, self.ws_ptr, self.ws_size_ref, stream)
-        else:
-            if stream is None:
-                stream = torch.cuda.current_stream().cuda_stream
+        # the raw handle of the current stream: torch.cuda.current_stream()
+        # builds a Stream object, 2.8 us against 0.1, and a call of one
+        # launch costs 4.3 us in all
+        index = self.device.index
+        stream = self.stream if self.stream is not None else torch._C._cuda_getCurrentRawStream(index)
+        if index == torch.cuda.current_device():
             st = self.fn(*self.args, self.ws_ptr, self.ws_size_ref, stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = self.fn(*self.args, self.ws_ptr, self.ws_size_ref, stream)
         if st != SVQ_OK:
             _check(st, self.name)
 
