@@ -47,12 +47,12 @@ __device__ __forceinline__ f4 load_f4(const void *p, size_t i, int f32, bool vec
 
 // No epilogue: the product kernels' default.
 struct NoEpi {
-  static constexpr bool on = false, partial = false;
+  static constexpr bool on = false, partial = false, f16 = false;
   __device__ __forceinline__ float operator()(float v, int, int) const { return v; }
 };
 
 struct Epi {
-  static constexpr bool on = true, partial = false;
+  static constexpr bool on = true, partial = false, f16 = false;
   EpiArgs a;
   // output row `row`, column n
   __device__ __forceinline__ float operator()(float v, int row, int n) const {

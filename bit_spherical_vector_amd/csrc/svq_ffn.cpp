@@ -19,6 +19,106 @@ bool aligned(const void *p, int64_t row_elems, size_t esz, size_t to) {
 }
 int64_t pad4(int64_t n) { return (n + 3) / 4 * 4; }
 
+bool has_split(const svq_handle *w) {
+  return w->xscale_log2 != SVQ_NO_EXACT_SPLIT && w->xscale_log2 >= -120 && w->xscale_log2 <= 120;
+}
+
+// K ranges of the tile launch.  64-row tiles: about two blocks per compute
+// unit.  256-row tiles, one block per compute unit: the count that takes the
+// least time when a round of blocks costs UNIT a unit of 512 channels and
+// EDGE for its start and its stores, and a reduce launch follows a split.
+int gemm_splits(int tiles, int units, int bm, double part_mb) {
+  const int cus = compute_units();
+  if (bm == 64) {
+    const int64_t per = ((int64_t)tiles * units + 2 * cus - 1) / (2 * cus);
+    return tiles >= 2 * cus ? 1 : (int)((units + per - 1) / per);
+  }
+  constexpr double UNIT = 13.5, EDGE = 8.0, REDUCE = 4.0, REDUCE_MB = 0.25;  // us
+  int best = 1;
+  double t_best = 1e30;
+  for (int s = 1; s <= units && s <= 16; ++s) {
+    const int ups = (units + s - 1) / s;
+    if ((units + ups - 1) / ups != s) continue;
+    const double t = (double)((tiles * s + cus - 1) / cus) * (ups * UNIT + EDGE) +
+                     (s > 1 ? REDUCE + REDUCE_MB * part_mb * s : 0.0);
+    if (t < t_best) {
+      t_best = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+// The calls beyond 16 rows: plan, workspace, launch (workspace null: only
+// *bytes).
+svq_status ffn_gemm(const svq_handle *const *w, int jobs, const void *x, int64_t m, int64_t ldx, const EpiArgs &epi,
+                    const void *bias_g, void *y, int64_t ldy, svq_dtype ydt, void *workspace, size_t *bytes,
+                    void *stream) {
+  FfnGemmArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const int bm = prefill_bm((int)m);
+  a.jobs = jobs;
+  a.m = (int)m;
+  a.m_pad = prefill_m_pad((int)m);
+  a.tiles_m = a.m_pad / bm;
+  a.tiles_n = prefill_tiles_n(w[0]->n_tiles);
+  a.n_pad = a.tiles_n * PREFILL_BN;
+  const int units = w[0]->units, tiles = a.tiles_m * a.tiles_n;
+  const double part_mb = (double)jobs * a.m_pad * a.n_pad * 4e-6;
+  const int want = gemm_splits(tiles * jobs, units, bm, part_mb);
+  a.ups = (units + want - 1) / want;
+  a.splits = (units + a.ups - 1) / a.ups;
+  const bool parts = bm == 64 || a.splits > 1;
+  // prep: rows per block as the bf16 path, chunk ranges for about 512 blocks
+  a.rpb = prefill_prep_rows(w[0]->k);
+  const int rows = a.m_pad / a.rpb, nch = units * UNIT_SLOTS / 8;
+  const int cs = (512 + rows - 1) / rows < nch / 64 ? (512 + rows - 1) / rows : nch / 64;
+  a.csplit = cs < 1 ? 1 : cs;
+  size_t off = 0;
+  auto take = [&](size_t b) {
+    const size_t at = off;
+    off += align256(b);
+    return at;
+  };
+  const size_t o_rs = take((size_t)a.m_pad * 4);
+  size_t o_xb[2], o_part[2] = {0, 0}, o_swap = 0, o_cnt = 0;
+  for (int j = 0; j < jobs; ++j) o_xb[j] = take((size_t)a.m_pad * units * UNIT_SLOTS * 2);
+  if (parts) {
+    for (int j = 0; j < jobs; ++j) o_part[j] = take((size_t)a.splits * a.m_pad * a.n_pad * 4);
+  } else if (jobs == 2) {
+    o_swap = take((size_t)tiles * 2 * 256 * 256 * 4);
+    o_cnt = take((size_t)tiles * 4);
+    a.n_cnt = tiles;
+  }
+  if (!workspace) {
+    *bytes = off;
+    return SVQ_OK;
+  }
+  if (!x || !y) return SVQ_ERR_INVALID_ARG;
+  if (*bytes < off) return SVQ_ERR_BUFFER_TOO_SMALL;
+  uint8_t *ws = (uint8_t *)workspace;
+  for (int j = 0; j < jobs; ++j) {
+    a.job[j].w = matrix_view(w[j]);
+    a.job[j].xb = (uint16_t *)(ws + o_xb[j]);
+    a.job[j].part = parts ? (float *)(ws + o_part[j]) : nullptr;
+    a.job[j].xinv = std::ldexp(1.0f, -w[j]->xscale_log2);
+  }
+  a.rs = (float *)(ws + o_rs);
+  if (a.n_cnt) {
+    a.swap = (float *)(ws + o_swap);
+    a.cnt = (int32_t *)(ws + o_cnt);
+  }
+  a.x = (const uint16_t *)x;
+  a.ldx = ldx;
+  a.ydt = (int32_t)ydt;
+  a.yvec = aligned(y, ldy, size_of(ydt), 16);
+  a.y = y;
+  a.ldy = ldy;
+  a.epi = epi;
+  a.bias_g = bias_g;
+  return launch_ffn_gemm(a, aligned(x, ldx, 2, 16), (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
+}
+
 }  // namespace
 
 extern "C" {
@@ -43,6 +143,10 @@ svq_status svq_linear_epilogue(const svq_handle *w, const void *x, int64_t m, in
     e.res_f32 = ep->residual_dt == SVQ_F32;
     e.res_vec = aligned(ep->residual, ep->ldr, size_of(ep->residual_dt), 4 * size_of(ep->residual_dt));
     if (ep->residual == y && (ep->ldr != ldy || ep->residual_dt != ydt)) return SVQ_ERR_INVALID_ARG;
+  }
+  if (m > SB_MAX_M && m <= (1 << 24) && has_split(w)) {
+    if (!valid_dt(ydt) || ldx < w->k || ldy < w->n) return SVQ_ERR_INVALID_ARG;
+    return ffn_gemm(&w, 1, x, m, ldx, e, nullptr, y, ldy, ydt, workspace, workspace_bytes, stream);
   }
   return linear_epi(w, 1, workspace ? &x : nullptr, &ldx, m, workspace ? &y : nullptr, &ldy, ydt, &e, workspace,
                     workspace_bytes, stream);
@@ -88,6 +192,15 @@ svq_status svq_linear_glu(const svq_handle *gate, const svq_handle *up, const vo
       a.R = R;
       return launch_glu_fused(a, (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
     }
+  }
+  if (m > SB_MAX_M && has_split(gate) && has_split(up)) {
+    EpiArgs e;
+    std::memset(&e, 0, sizeof(e));
+    e.act = (int32_t)act;
+    e.bias = bias_up;
+    e.bias_f32 = bias_dt == SVQ_F32;
+    const svq_handle *const pair[2] = {gate, up};
+    return ffn_gemm(pair, 2, x, m, ldx, e, bias_gate, y, ldy, ydt, workspace, workspace_bytes, stream);
   }
   const int64_t ldp = pad4(gate->n);
   const svq_handle w[2] = {*gate, *up};

@@ -54,6 +54,33 @@ struct CombineArgs {
 };
 hipError_t launch_combine(const CombineArgs &a, hipStream_t s);
 
+// ---- beyond 16 rows --------------------------------------------------------
+// One matrix with its epilogue, or a gated pair (job 0 the gate), on the
+// 256 x 256 tile (m >= PREFILL_MIN_M) or the 64 x 256 tile.
+struct FfnGemmJob {
+  MatView w;
+  uint16_t *xb;  // fp16 activations in fragment order (workspace)
+  float *part;   // fp32 partial tiles [splits][m_pad][n_pad], or null: none
+  float xinv;    // 2^-xscale_log2 of the matrix's exact split
+};
+struct FfnGemmArgs {
+  FfnGemmJob job[2];
+  int32_t jobs, m, m_pad, tiles_m, tiles_n, n_pad, splits, ups;
+  int32_t rpb, csplit;  // prep: rows per block, chunk ranges
+  const uint16_t *x;
+  int64_t ldx;
+  float *rs;      // inverse row scales [m_pad] (workspace)
+  float *swap;    // gated pair without partial tiles: [tiles][2] tiles of 256 x 256 sums
+  int32_t *cnt;   // and their arrivals
+  int32_t n_cnt;
+  int32_t ydt, yvec;
+  void *y;
+  int64_t ldy;
+  EpiArgs epi;         // gated pair: act, and the up matrix's bias
+  const void *bias_g;  // the gate's bias
+};
+hipError_t launch_ffn_gemm(const FfnGemmArgs &a, bool xvec, hipStream_t s);
+
 // ---- expert layer ---------------------------------------------------------
 struct MoeFfnArgs {
   const svq_handle *gate, *up, *down;  // host arrays of num_experts

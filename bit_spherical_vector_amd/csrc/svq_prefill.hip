@@ -40,6 +40,7 @@
 
 #include "svq_device.h"
 #include "svq_epilogue.h"
+#include "svq_ffn.h"
 #include "../../include/svq.h"
 
 namespace svq {
@@ -130,6 +131,15 @@ struct DqTile {
   const int32_t *ymap;
 };
 
+// The tile product's MFMA: bf16 operands, or fp16 (the feed-forward calls).
+template <bool F16>
+__device__ __forceinline__ f16x p_mfma(const u4 &a, const u4 &b, const f16x &c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
+}
+
 // Output of a tile with an epilogue: each wave's accumulators go through its
 // private 16 KB of LDS as fp32, 32 rows a pass, and come back four columns a
 // lane, where bias, activation and residual apply once per value in a short
@@ -176,7 +186,11 @@ __device__ __forceinline__ void dq_tile(const DqTile &T, uint8_t *smem, const EP
   const int rt0 = nt * (P_BN / UNIT_ROWS);
 
   uint8_t *s_btab = smem + P_OFF_BTAB;
-  for (int j = tid; j < 1024; j += 256) ((u4 *)s_btab)[j] = ((const u4 *)(w.base + w.off_btab))[j];
+  if constexpr (EPI::f16) {
+    for (int j = tid; j < 1024; j += 256) ((u4 *)s_btab)[j] = ((const u4 *)(w.base + w.off_xtab))[2 * j];
+  } else {
+    for (int j = tid; j < 1024; j += 256) ((u4 *)s_btab)[j] = ((const u4 *)(w.base + w.off_btab))[j];
+  }
 
   // A fragments of the wave: 32-row blocks rb = m0/32 + NI*wm + i; step s,
   // substep ks at a_ptr[i] + s * 2048 + ks * 512 elements (one 1 KB block)
@@ -306,9 +320,7 @@ __device__ __forceinline__ void dq_tile(const DqTile &T, uint8_t *smem, const EP
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
-            C[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, af[ks][i]),
-                                                              __builtin_bit_cast(b8, bf[c][j]),
-                                                              C[i][j], 0, 0, 0);
+            C[i][j] = p_mfma<EPI::f16>(af[ks][i], bf[c][j], C[i][j]);
         // the next step's A fragments of this substep, into the registers
         // these MFMAs just read
 #pragma unroll
@@ -342,7 +354,10 @@ __device__ __forceinline__ void dq_tile(const DqTile &T, uint8_t *smem, const EP
   // region, as many 32-row blocks per pass as fit, and writes them back as
   // whole 16-byte pieces of consecutive output columns.
   __syncthreads();
-  if constexpr (EPI::on) {
+  if constexpr (EPI::f16) {
+    epi_args.template finish<NI, NJ, TM, TN>(T, C, smem, wm, wn, lane, rt0);
+    return;
+  } else if constexpr (EPI::on) {
     epi_store<NI, NJ, TM, TN>(T, C, smem + wv * 16384, wm, wn, lane, rt0, epi_args);
     return;
   }
@@ -486,7 +501,11 @@ __device__ void dq_tile_w8(const DqTile &T, uint8_t *smem, const EPI &epi_args =
   const int rt0 = nt * (P_BN / UNIT_ROWS);
 
   uint8_t *s_btab = smem + W8_OFF_BTAB;
-  for (int q = tid; q < 1024; q += W8_THREADS) ((u4 *)s_btab)[q] = ((const u4 *)(w.base + w.off_btab))[q];
+  if constexpr (EPI::f16) {
+    for (int q = tid; q < 1024; q += W8_THREADS) ((u4 *)s_btab)[q] = ((const u4 *)(w.base + w.off_xtab))[2 * q];
+  } else {
+    for (int q = tid; q < 1024; q += W8_THREADS) ((u4 *)s_btab)[q] = ((const u4 *)(w.base + w.off_btab))[q];
+  }
 
   // A: wave wv copies row block wv of each step (4 KB: substeps 0..3)
   const uint16_t *a_src = T.xb + ((size_t)((m0 >> 5) + wv) * S * 4 * 64 + lane) * 8;
@@ -592,9 +611,7 @@ __device__ void dq_tile_w8(const DqTile &T, uint8_t *smem, const EPI &epi_args =
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int jj = 0; jj < NJ; ++jj)
-            C[i][jj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, af[c][i]),
-                                                               __builtin_bit_cast(b8, bf[c][jj]),
-                                                               C[i][jj], 0, 0, 0);
+            C[i][jj] = p_mfma<EPI::f16>(af[c][i], bf[c][jj], C[i][jj]);
       }
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
@@ -603,7 +620,10 @@ __device__ void dq_tile_w8(const DqTile &T, uint8_t *smem, const EPI &epi_args =
     rB = nB;
   }
 
-  if constexpr (EPI::on) {
+  if constexpr (EPI::f16) {
+    epi_args.template finish<NI, NJ, TM, TN>(T, C, smem, wm, wn, lane, rt0);
+    return;
+  } else if constexpr (EPI::on) {
     epi_store<NI, NJ, TM, TN>(T, C, smem + wv * 16384, wm, wn, lane, rt0, epi_args);
     return;
   }
@@ -986,6 +1006,430 @@ hipError_t launch_prefill_batched(PrefillBatch &b, int bm, int blocks, hipStream
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(prefill_batched_kernel<64>, dim3(blocks), dim3(256), P_SMEM, s, b);
   }
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// The feed-forward calls beyond 16 rows (svq_linear_epilogue, svq_linear_glu)
+// ---------------------------------------------------------------------------
+//
+// The tiles above with fp16 operands in place of bf16: weights
+// RNE_fp16(R*D*2^s) (the high halves of the exact split, s per matrix),
+// activations in fp16 after a power-of-two scale per row (largest finite
+// magnitude into [2^14, 2^15): a bf16 value keeps its 8 bits down to 2^-29 of
+// it).  Same instructions per tile, and the weights' rounding, most of the
+// error of the bf16 form (2^-9 a weight), falls to 2^-12.
+//
+// One prep launch stages the rows once for both matrices of a pair.  Then:
+// * 256-row tiles, no K split: a product's epilogue applies to the
+//   accumulators; the tiles of a gated pair meet through memory: a block that
+//   finds its partner's tile arrived takes it, else it leaves its own there,
+//   so whichever ends second finishes both and nobody waits.  (A launch of
+//   its own for the gating reads and writes both sums once more: 33 us of 254
+//   at 2048 x 9728 x 2560.)
+// * otherwise fp32 partial tiles and one reduce launch that sums the K ranges
+//   and applies epilogue or gating.
+
+// Cheaper activations for accumulators in registers: the hardware's exp2 and
+// reciprocal (each within about 1 ulp) in place of expf and a division; the
+// argument's rounding adds |v| 2^-24.
+template <int ACT>
+__device__ __forceinline__ float act_fast(float v) {
+  if constexpr (ACT == SVQ_ACT_RELU) return v < 0.f ? 0.f : v;
+  if constexpr (ACT == SVQ_ACT_SILU)
+    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * v));
+  if constexpr (ACT == SVQ_ACT_GELU) return act_apply(v, SVQ_ACT_GELU);
+  if constexpr (ACT == SVQ_ACT_GELU_TANH) {
+    const float z = v * __builtin_fmaf(0.044715f * v, v, 1.f);
+    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-2.f * 0.79788456080286536f * 1.44269504088896341f * z));
+  }
+  return v;
+}
+template <int ACT>
+__device__ __forceinline__ void act16(f16x &v) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = act_fast<ACT>(v[e]);
+}
+__device__ __forceinline__ void act16(f16x &v, int act) {  // act is uniform
+  switch (act) {
+    case SVQ_ACT_RELU: act16<SVQ_ACT_RELU>(v); break;
+    case SVQ_ACT_SILU: act16<SVQ_ACT_SILU>(v); break;
+    case SVQ_ACT_GELU: act16<SVQ_ACT_GELU>(v); break;
+    case SVQ_ACT_GELU_TANH: act16<SVQ_ACT_GELU_TANH>(v); break;
+    default: break;
+  }
+}
+
+// The 16 scales of accumulator block rows row0 + (e & 3) + 8(e >> 2) (row0 a
+// multiple of 4, plus 4 for the upper lane half), times xinv.
+__device__ __forceinline__ f16x row_scales(const float *rs, int row0, float xinv) {
+  f16x r;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const f4 v = *(const f4 *)(rs + row0 + 8 * q);
+#pragma unroll
+    for (int l = 0; l < 4; ++l) r[4 * q + l] = v[l] * xinv;
+  }
+  return r;
+}
+
+// One accumulator block (16 rows of column n) to y.
+__device__ __forceinline__ void put16(const DqTile &T, const f16x &v, int rr0, int n) {
+  if (n >= T.nlim) return;
+  auto put = [&](auto BF, auto FULL) __attribute__((always_inline)) {
+    constexpr bool bf = decltype(BF)::value, full = decltype(FULL)::value;
+    const size_t rs = (size_t)T.ldy * (bf ? 2 : 4);
+    char *p = (char *)T.y + (size_t)(T.m0 + rr0) * rs + (size_t)n * (bf ? 2 : 4);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int r = (e & 3) + 8 * (e >> 2);
+      if (full || rr0 + r < T.m_valid) {
+        if constexpr (bf) *(uint16_t *)(p + r * rs) = f32_to_bf16_bits(v[e]);
+        else *(float *)(p + r * rs) = v[e];
+      }
+    }
+  };
+  using Y = std::true_type;
+  using N = std::false_type;
+  const bool full = rr0 + 28 <= T.m_valid;
+  if (T.bf) full ? put(Y(), Y()) : put(Y(), N());
+  else full ? put(N(), Y()) : put(N(), N());
+}
+
+// Raw sums of a K range into a partial tile (always whole).
+struct PartTile {
+  static constexpr bool on = true, partial = true, f16 = true;
+  template <int NI, int NJ, int TM, int TN>
+  __device__ __forceinline__ void finish(const DqTile &T, f16x (&C)[NI][NJ], uint8_t *, int wm, int wn, int lane,
+                                         int rt0) const {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        float *p = (float *)T.y + (size_t)(T.m0 + TM * wm + 32 * i + 4 * (lane >> 5)) * T.ldy + rt0 * UNIT_ROWS +
+                   TN * wn + 32 * j + (lane & 31);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[(size_t)((e & 3) + 8 * (e >> 2)) * T.ldy] = C[i][j][e];
+      }
+  }
+};
+
+// act(p + bias) + residual straight from the accumulators.
+struct LinTile {
+  static constexpr bool on = true, partial = false, f16 = true;
+  EpiArgs a;
+  const float *rs;
+  float xinv;
+  template <int NI, int NJ, int TM, int TN>
+  __device__ __forceinline__ void finish(const DqTile &T, f16x (&C)[NI][NJ], uint8_t *, int wm, int wn, int lane,
+                                         int rt0) const {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int rr0 = TM * wm + 32 * i + 4 * (lane >> 5);
+      const f16x sc = row_scales(rs, T.m0 + rr0, xinv);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int n = rt0 * UNIT_ROWS + TN * wn + 32 * j + (lane & 31), nc = min(n, T.nlim - 1);
+        f16x res;
+        if (a.res) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int r = min(rr0 + (e & 3) + 8 * (e >> 2), T.m_valid - 1);
+            res[e] = load_f(a.res, (size_t)(T.m0 + r) * a.ldr + nc, a.res_f32);
+          }
+        }
+        f16x v = C[i][j] * sc;
+        if (a.bias) v += load_f(a.bias, nc, a.bias_f32);
+        act16(v, a.act);
+        if (a.res) v += res;
+        put16(T, v, rr0, n);
+      }
+    }
+  }
+};
+
+// act(g + bg) * (u + bu), the other matrix's tile through memory.
+struct GluTile {
+  static constexpr bool on = true, partial = false, f16 = true;
+  const void *bias_g, *bias_u;
+  int bias_f32, act;
+  const float *rs;
+  float xinv_g, xinv_u;
+  bool up;          // this block's matrix
+  uint64_t *own;    // where this block leaves its tile: [i][j][8][threads] pairs of sums
+  const uint64_t *other;  // and its partner (both may be under way at once)
+  int32_t *cnt;     // the pair's arrivals (cleared by the prep launch)
+  template <int NI, int NJ, int TM, int TN>
+  __device__ __forceinline__ void finish(const DqTile &T, f16x (&C)[NI][NJ], uint8_t *smem, int wm, int wn, int lane,
+                                         int rt0) const {
+    const int tid = threadIdx.x;
+    int *flag = (int *)smem;  // the operand stages are free
+    if (tid == 0) *flag = __hip_atomic_load(cnt, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (*flag == 0) {
+      // device-scope stores (coherent between the XCDs' caches), complete
+      // before the arrival is counted
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint64_t v = (uint64_t)__builtin_bit_cast(uint32_t, (float)C[i][j][2 * e]) |
+                               ((uint64_t)__builtin_bit_cast(uint32_t, (float)C[i][j][2 * e + 1]) << 32);
+            __hip_atomic_store(own + ((size_t)(i * NJ + j) * 8 + e) * W8_THREADS + tid, v, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+          }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();  // also: every wave has read the flag
+      if (tid == 0) *flag = __hip_atomic_fetch_add(cnt, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      if (*flag == 0) return;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int rr0 = TM * wm + 32 * i + 4 * (lane >> 5);
+      const f16x sc = row_scales(rs, T.m0 + rr0, 1.f);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        f16x o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint64_t v = __hip_atomic_load(other + ((size_t)(i * NJ + j) * 8 + e) * W8_THREADS + tid,
+                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          o[2 * e] = __builtin_bit_cast(float, (uint32_t)v);
+          o[2 * e + 1] = __builtin_bit_cast(float, (uint32_t)(v >> 32));
+        }
+        const int n = rt0 * UNIT_ROWS + TN * wn + 32 * j + (lane & 31), nc = min(n, T.nlim - 1);
+        f16x g = (up ? o : C[i][j]) * (sc * xinv_g), u = (up ? C[i][j] : o) * (sc * xinv_u);
+        if (bias_g) g += load_f(bias_g, nc, bias_f32);
+        if (bias_u) u += load_f(bias_u, nc, bias_f32);
+        act16(g, act);
+        put16(T, g * u, rr0, n);
+      }
+    }
+  }
+};
+
+// Prep: fp16 activations of every matrix of the call in fragment order
+// (xb_frag_offset), rows >= m and slots >= k zero, and each row's inverse
+// scale.  A block stages rpb rows (whole, so that the row's scale is known)
+// and writes one of csplit chunk ranges for each matrix.  The blocks of one
+// 32-row fragment block follow each other on one XCD (blocks go to the XCDs
+// round-robin), so the 16 rpb bytes a block contributes to a run of 512 meet
+// in one L2 and leave as whole lines.
+template <bool XVEC>
+__global__ __launch_bounds__(256) void ffn_prep_kernel(FfnGemmArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t s_rows[];
+  __shared__ uint32_t s_mx[8];
+  const int K = a.job[0].w.k, Kp = a.job[0].w.units * UNIT_SLOTS, rpb = a.rpb, tid = threadIdx.x;
+  if (blockIdx.x == 0)
+    for (int i = tid; i < a.n_cnt; i += 256) a.cnt[i] = 0;
+  const int per = 32 / rpb * a.csplit;  // blocks per 32-row block
+  const int xcd = (int)blockIdx.x & 7, idx = (int)blockIdx.x >> 3;
+  const int rb = xcd + 8 * (idx / per), part = idx % per;
+  if (rb * 32 >= a.m_pad) return;  // block-uniform, before any barrier
+  const int r0 = rb * 32 + part / a.csplit * rpb, cs = part % a.csplit;
+  const int nch = Kp / 8, cpb = (nch + a.csplit - 1) / a.csplit;
+  const int c_lo = cs * cpb, c_hi = min(nch, c_lo + cpb);
+  const int ks_ = K + 8, live = min(rpb, a.m - r0);  // rows with data (may be <= 0)
+  if (tid < 8) s_mx[tid] = 0;
+  if (XVEC) {
+    const int n8 = K / 8, tot = max(live, 0) * n8;
+    constexpr int B = 8;  // 16-byte loads in flight per thread
+    for (int q0 = tid; q0 < tot; q0 += 256 * B) {
+      u4 v[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int q = min(q0 + 256 * b, tot - 1), rr = q / n8;
+        v[b] = *(const u4 *)(a.x + (int64_t)(r0 + rr) * a.ldx + 8 * (q - rr * n8));
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int q = q0 + 256 * b, rr = q / n8;
+        if (q < tot) *(u4 *)(s_rows + (size_t)rr * ks_ + 8 * (q - rr * n8)) = v[b];
+      }
+    }
+  } else {
+    for (int rr = 0; rr < live; ++rr)
+      for (int j = tid; j < K; j += 256) s_rows[(size_t)rr * ks_ + j] = a.x[(int64_t)(r0 + rr) * a.ldx + j];
+  }
+  __syncthreads();
+  const int rr = tid % rpb, step = 256 / rpb;
+  const uint16_t *row = s_rows + (size_t)rr * ks_;
+  const bool on = rr < live;
+  // largest finite magnitude of the row (infinities and NaN keep their value
+  // under any scale)
+  uint32_t mx = 0;
+  if (on)
+    for (int c = tid / rpb; c < K / 8; c += step) {
+      const u4 v = *(const u4 *)(row + 8 * c);
+#pragma unroll
+      for (int l = 0; l < 4; ++l) {
+        const uint32_t lo = v[l] & 0x7FFFu, hi = (v[l] >> 16) & 0x7FFFu;
+        mx = max(mx, lo < 0x7F80u ? lo : 0u);
+        mx = max(mx, hi < 0x7F80u ? hi : 0u);
+      }
+    }
+  if (on) atomicMax(&s_mx[rr], mx);
+  __syncthreads();
+  const float mf = bf16_bits_to_f32(s_mx[rr]);
+  const int e = mf > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mf) : 0;
+  if (cs == 0 && tid < rpb) a.rs[r0 + rr] = on ? ldexpf(1.f, -e) : 0.f;
+  const int S = Kp / P_BK;
+  for (int j = 0; j < a.jobs; ++j) {
+    const MatView &w = a.job[j].w;
+    const uint16_t *perm = (const uint16_t *)(w.base + w.off_perm);
+    uint16_t *xb = a.job[j].xb;
+    for (int cb = c_lo + tid / rpb; cb < c_hi; cb += 4 * step) {
+      u4 pv[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) pv[b] = *(const u4 *)(perm + 8 * min(cb + b * step, c_hi - 1));
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int c = cb + b * step;
+        // perm is zero padded, so every index is < k; k is a multiple of 8,
+        // so a chunk is inside k or all padding
+        u4 v;
+#pragma unroll
+        for (int l = 0; l < 4; ++l) {
+          const _Float16 lo = (_Float16)ldexpf(bf16_bits_to_f32(row[pv[b][l] & 0xFFFFu]), e);
+          const _Float16 hi = (_Float16)ldexpf(bf16_bits_to_f32(row[pv[b][l] >> 16]), e);
+          v[l] = (uint32_t)__builtin_bit_cast(uint16_t, lo) | ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
+        }
+        if (!on || 8 * c >= K) v = (u4){0u, 0u, 0u, 0u};
+        if (c < c_hi) *(u4 *)(xb + xb_frag_offset(r0 + rr, 8 * c, S)) = v;
+      }
+    }
+  }
+}
+
+// Block (job, mt, nt, sp) of the tile launch: m-tile fastest, so that blocks
+// sharing an activation tile fall on one XCD; jobs start on multiples of 8.
+__device__ __forceinline__ bool ffn_tile(const FfnGemmArgs &a, int bm, DqTile &T, int &jn, int &tile, int &sp) {
+  const int per = a.tiles_m * a.tiles_n * a.splits, pad = (per + 7) / 8 * 8;
+  jn = (int)blockIdx.x >= pad ? 1 : 0;
+  const int local = (int)blockIdx.x - jn * pad;
+  if (local >= per) return false;  // padding block (uniform, before any barrier)
+  tile = local % (a.tiles_m * a.tiles_n);
+  sp = local / (a.tiles_m * a.tiles_n);
+  T.w = jn ? a.job[1].w : a.job[0].w;
+  T.xb = jn ? a.job[1].xb : a.job[0].xb;
+  T.m0 = tile % a.tiles_m * bm;
+  T.m_valid = a.m - T.m0;
+  T.nt = tile / a.tiles_m;
+  T.u0 = sp * a.ups;
+  T.u1 = min(T.w.units, T.u0 + a.ups);
+  T.ymap = nullptr;
+  T.y = a.y;
+  T.ldy = a.ldy;
+  T.nlim = T.w.n;
+  T.bf = a.ydt == 0;
+  T.yvec = false;
+  return true;
+}
+__device__ __forceinline__ void ffn_part(const FfnGemmArgs &a, int jn, int sp, DqTile &T) {
+  T.y = (jn ? a.job[1].part : a.job[0].part) + (size_t)sp * a.m_pad * a.n_pad;
+  T.ldy = a.n_pad;
+}
+
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void ffn_part64_kernel(FfnGemmArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  DqTile T;
+  int jn, tile, sp;
+  if (!ffn_tile(a, 64, T, jn, tile, sp)) return;
+  ffn_part(a, jn, sp, T);
+  dq_tile<64, PartTile>(T, smem, PartTile());
+}
+__global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void ffn_part256_kernel(FfnGemmArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  DqTile T;
+  int jn, tile, sp;
+  if (!ffn_tile(a, 256, T, jn, tile, sp)) return;
+  ffn_part(a, jn, sp, T);
+  dq_tile_w8<PartTile>(T, smem, PartTile());
+}
+__global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void ffn_linear_kernel(FfnGemmArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  DqTile T;
+  int jn, tile, sp;
+  if (!ffn_tile(a, 256, T, jn, tile, sp)) return;
+  dq_tile_w8<LinTile>(T, smem, LinTile{a.epi, a.rs, a.job[0].xinv});
+}
+__global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void ffn_glu_kernel(FfnGemmArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  DqTile T;
+  int jn, tile, sp;
+  if (!ffn_tile(a, 256, T, jn, tile, sp)) return;
+  const GluTile g{a.bias_g, a.epi.bias, a.epi.bias_f32, a.epi.act, a.rs, a.job[0].xinv, a.job[1].xinv, jn != 0,
+                  (uint64_t *)a.swap + (size_t)(2 * tile + jn) * (256 * 256 / 2),
+                  (const uint64_t *)a.swap + (size_t)(2 * tile + 1 - jn) * (256 * 256 / 2), a.cnt + tile};
+  dq_tile_w8<GluTile>(T, smem, g);
+}
+
+// Sum of the K ranges in range order, then epilogue (one matrix) or gating
+// (two); four columns a thread.
+__global__ __launch_bounds__(256) void ffn_reduce_kernel(FfnGemmArgs a) {
+  const int n_all = a.job[0].w.n, per_row = (n_all + 1023) / 1024;
+  const int row = (int)blockIdx.x / per_row, n = ((int)blockIdx.x % per_row) * 1024 + 4 * (int)threadIdx.x;
+  if (n >= n_all) return;
+  const float rs = a.rs[row];
+  f4 v[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    v[j] = (f4){0.f, 0.f, 0.f, 0.f};
+    if (j < a.jobs) {
+      const float *p = a.job[j].part + (size_t)row * a.n_pad + n;
+      for (int s = 0; s < a.splits; ++s) v[j] += *(const f4 *)(p + (size_t)s * a.m_pad * a.n_pad);
+      v[j] *= rs * a.job[j].xinv;
+    }
+  }
+  if (a.jobs == 1) {
+    const Epi epi{a.epi};
+    epi.store4(a.y, a.ldy, a.ydt == 0, a.yvec != 0, v[0], row, n, n_all);
+    return;
+  }
+#pragma unroll
+  for (int l = 0; l < 4; ++l) {
+    if (n + l >= n_all) break;
+    if (a.bias_g) v[0][l] += load_f(a.bias_g, n + l, a.epi.bias_f32);
+    if (a.epi.bias) v[1][l] += load_f(a.epi.bias, n + l, a.epi.bias_f32);
+    v[0][l] = act_apply(v[0][l], a.epi.act) * v[1][l];
+  }
+  if (n + 4 <= n_all)
+    Epi::store_f4(a.y, (size_t)row * a.ldy + n, v[0], a.ydt == 0, a.yvec != 0);
+  else
+    for (int l = 0; n + l < n_all; ++l) store_out(a.y, (size_t)row * a.ldy + n + l, v[0][l], a.ydt);
+}
+
+template <typename K>
+static hipError_t ffn_launch(K kernel, int blocks, int threads, size_t smem, const FfnGemmArgs &a, hipStream_t s) {
+  const hipError_t e = allow_smem(kernel, smem);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3(blocks), dim3(threads), smem, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_ffn_gemm(const FfnGemmArgs &a, bool xvec, hipStream_t s) {
+  const int bm = prefill_bm(a.m);
+  const size_t lds = prefill_prep_lds(a.rpb, a.job[0].w.k);
+  if (lds + 64 > GV_LDS_LIMIT) return hipErrorInvalidValue;
+  const int rblocks = (a.m_pad / 32 + 7) / 8 * 8;  // 32-row blocks, padded to the XCDs
+  hipError_t e = ffn_launch(xvec ? ffn_prep_kernel<true> : ffn_prep_kernel<false>, rblocks * (32 / a.rpb) * a.csplit,
+                            256, lds, a, s);
+  if (e != hipSuccess) return e;
+  const int per = a.tiles_m * a.tiles_n * a.splits, blocks = a.jobs == 1 ? per : (per + 7) / 8 * 8 + per;
+  const bool direct = a.job[0].part == nullptr;
+  if (bm == 64)
+    e = ffn_launch(ffn_part64_kernel, blocks, 256, P_SMEM, a, s);
+  else if (!direct)
+    e = ffn_launch(ffn_part256_kernel, blocks, W8_THREADS, W8_SMEM, a, s);
+  else if (a.jobs == 1)
+    e = ffn_launch(ffn_linear_kernel, blocks, W8_THREADS, W8_SMEM, a, s);
+  else
+    e = ffn_launch(ffn_glu_kernel, blocks, W8_THREADS, W8_SMEM, a, s);
+  if (e != hipSuccess || direct) return e;
+  hipLaunchKernelGGL(ffn_reduce_kernel, dim3(a.m * ((a.job[0].w.n + 1023) / 1024)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -6,7 +6,8 @@ torch.finfo(t).eps / 2 of the value):
 * a product of k terms: |p - p64| <= P * S + 1e-6 with S = sum |What||x|;
   accumulation in fp32 costs at most one rounding per term (k + 64 of 2^-24,
   64 for the joins of partial sums), and for more than 16 rows the weights
-  are rounded to bf16 (2^-8) first;
+  are rounded to fp16 first (2^-11; a weight so small beside its matrix's
+  largest that it is subnormal there keeps an error of 2^-39 of that one);
 * an activation's slope is at most 1.13 (silu 1.0998, gelu 1.129), so an
   error e of its argument becomes at most 1.13 e, plus a few fp32 roundings
   of the value (expf, one division: 16 of 2^-24);
@@ -57,7 +58,7 @@ def slope_of(act):
 def product(mat, x_bits, rounded_weights):
     """(p, bound of |p_gpu - p|) of one matrix."""
     p, W = so.linear_from_inputs(mat, x_bits)
-    rel = (mat.k + 64) * U32 + (2.0 ** -8 if rounded_weights else 0.0)
+    rel = (mat.k + 64) * U32 + {False: 0.0, True: 2.0 ** -11, "bf16": 2.0 ** -8}[rounded_weights]
     return p, rel * so.abs_bound(x_bits, W) + 1e-6
 
 
@@ -145,7 +146,7 @@ def test_epilogue_without_an_exact_split(svq):
 
 
 def test_plain_epilogue_equals_linear(svq):
-    for n, k, bd, m in SHAPES[:9]:
+    for n, k, bd, m in SHAPES[:8]:
         mat = synth.random_matrix(n, k, bd, seed=(74, n, k))
         x = to_device_bf16(synth.random_activations(m, k, seed=(74, n, m)))
         pm = svq.pack(mat)
@@ -174,7 +175,7 @@ def test_activations_at_their_limits(svq):
 
 
 GLU_SHAPES = [(1, 8, 1), (37, 104, 1), (1000, 520, 1), (2000, 2560, 1), (100, 1032, 2), (48, 640, 4), (33, 520, 5),
-              (300, 4608, 13), (17, 264, 17), (200, 1032, 40), (257, 520, 256), (512, 1024, 300)]
+              (300, 4608, 13), (17, 264, 17), (200, 1032, 40), (257, 520, 256), (512, 1024, 300), (264, 512, 256), (700, 264, 530)]
 
 
 @pytest.mark.parametrize("n,k,m", GLU_SHAPES)
@@ -277,7 +278,7 @@ def moe64(sets, x_bits, ids, wt, act, grouped):
             i = int(ids[t, j])
             if i < 0 or i >= e:
                 continue
-            (g, gb), (u, ub) = product(gates[i], xb, grouped), product(ups[i], xb, grouped)
+            (g, gb), (u, ub) = [product(a[i], xb, grouped and "bf16") for a in (gates, ups)]
             a = act64(g, act)
             h = a * u
             eh = (slope_of(act) * gb + 16 * U32 * np.abs(a)) * np.abs(u) + ub * np.abs(a) + slope_of(act) * gb * ub
