@@ -104,15 +104,33 @@ struct Epi {
 // The sums go to an fp32 row that another block reads in the same launch:
 // device-scope stores, coherent between the XCDs' caches.
 struct PartEpi {
-  static constexpr bool on = true, partial = true;
+  static constexpr bool on = true, partial = true, f16 = false;
   float *row;
-  __device__ __forceinline__ void put(float v, int n) const {
+  __device__ __forceinline__ void put(float v, int, int n) const {
     __hip_atomic_store(row + n, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 };
 
+// A gated pair whose sums meet in memory (see PairArgs).
+struct PairEpi {
+  static constexpr bool on = true, partial = true, f16 = false;
+  PairArgs a;
+  float *row;    // sums of this block's matrix, [m][ldp]
+  int64_t ldp;
+  __device__ __forceinline__ void put(float v, int r, int n) const {
+    __hip_atomic_store(row + (size_t)r * ldp + n, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __device__ __forceinline__ float operator()(float v, int, int) const { return v; }
+};
+__device__ __forceinline__ float pair_value(const PairArgs &a, float g, float u, int n) {
+  if (a.bias_g) g += load_f(a.bias_g, n, a.bias_f32);
+  if (a.bias_u) u += load_f(a.bias_u, n, a.bias_f32);
+  return act_apply(g, a.act) * u;
+}
+
 // The epilogue of a kernel's optional EpiArgs argument.
 __device__ __forceinline__ NoEpi make_epi() { return NoEpi(); }
 __device__ __forceinline__ Epi make_epi(const EpiArgs &a) { return Epi{a}; }
+__device__ __forceinline__ PairEpi make_epi(const PairArgs &a) { return PairEpi{a, nullptr, 0}; }
 
 }  // namespace svq

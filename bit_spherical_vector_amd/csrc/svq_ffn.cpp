@@ -119,6 +119,112 @@ svq_status ffn_gemm(const svq_handle *const *w, int jobs, const void *x, int64_t
   return launch_ffn_gemm(a, aligned(x, ldx, 2, 16), (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
 }
 
+// A gated pair of 2..16 rows: the launches of svq_linear_batched over both
+// matrices with equal plans, the pair joined by whichever block of a group
+// ends last.
+svq_status pair_small(const svq_handle *gate, const svq_handle *up, const void *x, int64_t m, int64_t ldx,
+                      PairArgs pa, void *y, int64_t ldy, svq_dtype ydt, void *workspace, size_t *bytes,
+                      void *stream) {
+  const svq_handle *const w[2] = {gate, up};
+  const int U = gate->units, nt = gate->n_tiles;
+  const bool exact = m <= EXACT_MAX_M;
+  size_t off = 0;
+  auto take = [&](size_t b) {
+    const size_t at = off;
+    off += align256(b);
+    return at;
+  };
+  size_t o_x[2], o_s[2], o_part, o_cnt;
+  SbPlan pl = {};
+  int R = 1;
+  if (exact) {
+    // row tiles per block as for svq_linear_batched, the same for both
+    R = 4 * GV_UNITS_PER_WAVE / U;
+    R = R < 1 ? 1 : (R > GV_MAX_R ? GV_MAX_R : R);
+    while (R < GV_MAX_R && 2 * ((nt + R - 1) / R) > 3 * compute_units()) ++R;
+    for (int j = 0; j < 2; ++j) {
+      o_x[j] = take((size_t)m * U * GV_XG_UNIT_BYTES);
+      o_s[j] = take((size_t)U * 16);
+    }
+    o_part = take((size_t)2 * m * gate->n * 4);
+    pa.n_cnt = (nt + R - 1) / R;
+  } else {
+    pl = sb_plan(nt, U, sb_block_items(2 * (int64_t)nt * U, compute_units()));
+    for (int j = 0; j < 2; ++j) {
+      o_x[j] = take((size_t)U * SB_XA_UNIT_BYTES);
+      o_s[j] = take((size_t)U * 16 * 4);
+    }
+    o_part = take((size_t)pl.groups * pl.tiles * 2 * pl.splits * 1024);
+    pa.n_cnt = pl.groups;
+  }
+  o_cnt = take((size_t)pa.n_cnt * 4);
+  if (!workspace) {
+    *bytes = off;
+    return SVQ_OK;
+  }
+  if (!x || !y) return SVQ_ERR_INVALID_ARG;
+  if (*bytes < off) return SVQ_ERR_BUFFER_TOO_SMALL;
+  uint8_t *ws = (uint8_t *)workspace;
+  pa.part = (float *)(ws + o_part);
+  pa.cnt = (int32_t *)(ws + o_cnt);
+  hipError_t e;
+  if (exact) {
+    GemvBatch b;
+    std::memset(&b, 0, sizeof(b));
+    b.count = 2;
+    b.m = (int)m;
+    b.ydt = (int)ydt;
+    b.xvec = aligned(x, ldx, 2, 16);
+    b.pair = &pa;
+    const int blocks = (nt + R - 1) / R, gather = (int)m * ((U + 3) / 4);
+    for (int j = 0; j < 2; ++j) {
+      GemvJob &J = b.job[j];
+      J.w = matrix_view(w[j]);
+      J.x = (const uint16_t *)x;
+      J.ldx = ldx;
+      J.xg = ws + o_x[j];
+      J.xs = (float *)(ws + o_s[j]);
+      J.y = y;
+      J.ldy = ldy;
+      J.R = R;
+      J.block_begin = b.starts.first[j] = j * blocks;
+      b.gather_starts.first[j] = j * gather;
+    }
+    b.touch_begin = (2 * gather + 7) / 8 * 8;
+    const int bd = gate->bd > up->bd ? gate->bd : up->bd;
+    b.red_off = (int32_t)gemv_smem_bytes((int)m, bd, 0);
+    e = launch_gemv_batched(b, b.touch_begin + 16, gate->k, 2 * blocks, gemv_smem_bytes((int)m, bd, R),
+                            (hipStream_t)stream);
+  } else {
+    SbBatch b;
+    std::memset(&b, 0, sizeof(b));
+    b.count = 2;
+    b.m = (int)m;
+    b.ydt = (int)ydt;
+    b.pair = &pa;
+    for (int j = 0; j < 2; ++j) {
+      SbJob &J = b.job[j];
+      J.w = matrix_view(w[j]);
+      J.x = (const uint16_t *)x;
+      J.ldx = ldx;
+      J.y = y;
+      J.ldy = ldy;
+      J.tiles = pl.tiles;
+      J.upr = pl.upr;
+      J.groups = pl.groups;
+      J.splits = pl.splits;
+      J.xa = ws + o_x[j];
+      J.xs = (float *)(ws + o_s[j]);
+      J.xinv = std::ldexp(1.0f, -w[j]->xscale_log2);
+      J.cnt = pa.cnt;  // cleared by either prep form
+      J.block_begin = b.starts.first[j] = j * pl.groups * pl.splits;
+      J.prep_begin = b.prep_starts.first[j] = j * U;
+    }
+    e = launch_sb(b, 2 * U, 2 * pl.groups * pl.splits, (hipStream_t)stream);
+  }
+  return e == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
+}
+
 }  // namespace
 
 extern "C" {
@@ -201,6 +307,15 @@ svq_status svq_linear_glu(const svq_handle *gate, const svq_handle *up, const vo
     e.bias_f32 = bias_dt == SVQ_F32;
     const svq_handle *const pair[2] = {gate, up};
     return ffn_gemm(pair, 2, x, m, ldx, e, bias_gate, y, ldy, ydt, workspace, workspace_bytes, stream);
+  }
+  if (m > 1 && m <= SB_MAX_M && (m <= EXACT_MAX_M || (has_split(gate) && has_split(up)))) {
+    PairArgs pa;
+    std::memset(&pa, 0, sizeof(pa));
+    pa.bias_g = bias_gate;
+    pa.bias_u = bias_up;
+    pa.bias_f32 = bias_dt == SVQ_F32;
+    pa.act = (int32_t)act;
+    return pair_small(gate, up, x, m, ldx, pa, y, ldy, ydt, workspace, workspace_bytes, stream);
   }
   const int64_t ldp = pad4(gate->n);
   const svq_handle w[2] = {*gate, *up};

@@ -553,6 +553,13 @@ static svq_status linear_impl(const svq_handle *w, int32_t count, const void *co
     int64_t total = 0;
     for (int32_t j = 0; j < count; ++j) total += (int64_t)w[j].n_tiles * w[j].units;
     sb_items = sb_block_items(total, device_cus());
+    // a single matrix with an epilogue: small ones get a block for every four
+    // items (one a wave) instead of SB_ITEMS_MIN (1021 x 2560 at 7 rows: 64
+    // blocks against 22, see the feed-forward figures)
+    if (epi && sb_items == SB_ITEMS_MIN) {
+      const int64_t it = (total + 2 * device_cus() - 1) / (2 * device_cus());
+      sb_items = it < 4 ? 4 : (it < SB_ITEMS_MIN ? (int)it : SB_ITEMS_MIN);
+    }
   }
   // m = 1: the fused launch, when the activation row and its permuted copy
   // fit in LDS beside the tables

@@ -93,6 +93,16 @@ struct EpiArgs {
   int32_t bias_vec, res_vec;  // rows allow loads of four values
 };
 
+// Join of a gated pair: y = act(g + bg) * (u + bu), fp32 sums of both
+// matrices' blocks meeting in `part`, the last of them to arrive finishing.
+struct PairArgs {
+  const void *bias_g, *bias_u;  // [n] or null
+  int32_t bias_f32, act;
+  float *part;   // exchange (workspace)
+  int32_t *cnt;  // arrivals (workspace, cleared by the launch before)
+  int32_t n_cnt;
+};
+
 // ---- dense path ---------------------------------------------------------
 // Exact path, m = 2..4: a gather launch writes every matrix's permuted,
 // per-unit scaled fp16 activations to the workspace (xg: row a of unit u at
@@ -129,6 +139,7 @@ struct GemvBatch {
   int32_t red_off;          // LDS offset of the partial sums (after the tables)
   int32_t touch_begin;      // gather launch: first of the 8*count table-touch blocks
   int32_t xvec;             // every activation row starts 16-byte aligned
+  const PairArgs *pair;     // host: the two jobs are a gated pair, or null
   const EpiArgs *epi;       // host: epilogue of a single-matrix call, or null
 };
 constexpr size_t GV_LDS_LIMIT = 160 * 1024;  // LDS per workgroup on gfx950
@@ -227,7 +238,8 @@ struct SbBatch {
   JobStarts starts, prep_starts;
   SbJob job[GV_MAX_JOBS];
   int32_t count, m, ydt;
-  const EpiArgs *epi;  // host: epilogue of a single-matrix call, or null
+  const EpiArgs *epi;    // host: epilogue of a single-matrix call, or null
+  const PairArgs *pair;  // host: the two jobs are a gated pair, or null
 };
 // Block shape of one matrix: tiles per block, units per range, ranges,
 // tile groups.  `items` = work items per block the call aims for

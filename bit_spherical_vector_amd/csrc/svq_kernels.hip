@@ -221,12 +221,22 @@ __device__ __forceinline__ void gather_block(const uint16_t *__restrict__ perm,
   if (lane == 0) xs_row[4 * u] = ldexpf(1.f, -e);
 }
 
+__device__ __forceinline__ void clear_counts(const PairArgs &a) {
+  for (int i = threadIdx.x; i < a.n_cnt; i += 256) a.cnt[i] = 0;
+}
+
 // Gather launch of the dense path: block = (job, activation row a, group of
 // 4 units), wave = unit.  The launch ends with 8 blocks per job (one per XCD:
 // blocks go to the XCDs round-robin) that only read the job's direction and
 // radius tables, so that the main launch finds them near.
-__global__ __launch_bounds__(256) void gemv_gather_kernel(GemvBatch b) {
+// za: nothing, or the PairArgs of a gated pair, whose arrival counters are
+// cleared here.
+template <typename... ZA>
+__global__ __launch_bounds__(256) void gemv_gather_kernel(GemvBatch b, ZA... za) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  if constexpr (sizeof...(ZA) > 0) {
+    if (blockIdx.x == 0) clear_counts(za...);
+  }
   if ((int)blockIdx.x >= b.touch_begin) {
     const int jt = ((int)blockIdx.x - b.touch_begin) >> 3;
     if (jt < b.count) {
@@ -566,7 +576,11 @@ __device__ void gemv_main_block(const MatView &w, const uint8_t *__restrict__ xg
 #pragma unroll
     for (int p = 0; p < GV_WAVES * 4; ++p) sum += s_red[((t * GV_WAVES * 4 + p) * 4 + j) * 4 * M + ri * M + a];
     const int n = (t0 + t) * 16 + row;
-    if (n < w.n) store_out(y, (size_t)a * ldy + n, epi(sum, a, n), ydt);
+    if constexpr (EPI::partial) {
+      if (n < w.n) epi.put(sum, a, n);
+    } else {
+      if (n < w.n) store_out(y, (size_t)a * ldy + n, epi(sum, a, n), ydt);
+    }
   }
 }
 
@@ -591,6 +605,37 @@ __global__ __launch_bounds__(256) void gemv_epi_kernel(GemvBatch b, EpiArgs ea) 
   gemv_main_block<M, Epi>(jb.w, jb.xg, jb.xs, jb.y, jb.ldy, b.ydt, t0, Reff, b.red_off, smem, epi);
 }
 
+// The main launch of a gated pair (jobs 0 and 1, equal R): a block leaves its
+// sums in memory and counts itself; the second of the two blocks of a
+// row-tile group takes both and writes the output.  (The partial stores are
+// device-scope and complete before the count; the flag lies over the tables,
+// which no wave reads any more.)
+template <int M>
+__global__ __launch_bounds__(256) void gemv_pair_kernel(GemvBatch b, PairArgs pa) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int j = (int)blockIdx.x >= b.starts.first[1] ? 1 : 0;
+  const GemvJob &jb = b.job[j];
+  const int group = (int)blockIdx.x - b.starts.first[j], t0 = group * jb.R;
+  const int Reff = min(jb.R, jb.w.n_tiles - t0);
+  const int n_all = jb.w.n;
+  const int64_t ldp = n_all;
+  const PairEpi epi{pa, pa.part + (size_t)j * M * ldp, ldp};
+  gemv_main_block<M, PairEpi>(jb.w, jb.xg, jb.xs, nullptr, 0, 1, t0, Reff, b.red_off, smem, epi);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  int *flag = (int *)smem;
+  if (threadIdx.x == 0)
+    *flag = __hip_atomic_fetch_add(pa.cnt + group, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (*flag == 0) return;
+  for (int o = threadIdx.x; o < Reff * 16 * M; o += 256) {
+    const int a = o / (Reff * 16), n = t0 * 16 + o - a * Reff * 16;
+    if (n >= n_all) continue;
+    const float g = __hip_atomic_load(pa.part + (size_t)a * ldp + n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const float u = __hip_atomic_load(pa.part + (size_t)(M + a) * ldp + n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    store_out(jb.y, (size_t)a * jb.ldy + n, pair_value(pa, g, u, n), b.ydt);
+  }
+}
 
 // The exact-path kernels address their LDS tables from 0 (see lds_u4), which
 // holds when they declare no static LDS.
@@ -604,6 +649,14 @@ static hipError_t check_no_static_lds(Kern k) {
 
 template <int M>
 static hipError_t launch_gemv_m(GemvBatch &b, int blocks, size_t smem, hipStream_t s) {
+  if (b.pair) {
+    static const hipError_t pair_ok = check_no_static_lds(gemv_pair_kernel<M>);
+    if (pair_ok != hipSuccess) return pair_ok;
+    const hipError_t e = allow_smem(gemv_pair_kernel<M>, smem);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gemv_pair_kernel<M>), dim3(blocks), dim3(256), smem, s, b, *b.pair);
+    return hipGetLastError();
+  }
   if (b.epi) {
     static const hipError_t epi_ok = check_no_static_lds(gemv_epi_kernel<M>);
     if (epi_ok != hipSuccess) return epi_ok;
@@ -623,9 +676,12 @@ static hipError_t launch_gemv_m(GemvBatch &b, int blocks, size_t smem, hipStream
 hipError_t launch_gemv_batched(GemvBatch &b, int gather_blocks, int k_max, int blocks, size_t smem,
                                hipStream_t s) {
   const size_t gsmem = align256((size_t)k_max * 2);
-  hipError_t e = allow_smem(gemv_gather_kernel, gsmem);
+  hipError_t e = b.pair ? allow_smem(gemv_gather_kernel<PairArgs>, gsmem) : allow_smem(gemv_gather_kernel<>, gsmem);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(gemv_gather_kernel, dim3(gather_blocks), dim3(256), gsmem, s, b);
+  if (b.pair)
+    hipLaunchKernelGGL(gemv_gather_kernel<PairArgs>, dim3(gather_blocks), dim3(256), gsmem, s, b, *b.pair);
+  else
+    hipLaunchKernelGGL(gemv_gather_kernel<>, dim3(gather_blocks), dim3(256), gsmem, s, b);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   switch (b.m) {
@@ -1129,7 +1185,7 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
     for (int p = 0; p < GV_WAVES; ++p) sum += s_red[(((t * GV_WAVES + p) * 4 + ri) * M + a) * 4 + j];
     const int n = (rt0 + t) * 16 + row;
     if constexpr (EPI::partial) {
-      if (n < w.n) epi.put(sum, n);
+      if (n < w.n) epi.put(sum, a, n);
     } else {
       if (n < w.n) store_out(y, (size_t)a * ldy + n, epi(sum, a, n), ydt);
     }
@@ -1216,7 +1272,7 @@ struct LdsEpi {
   static constexpr bool on = true, partial = true;
   float *row;  // row n of the matrix at row[n - n0]
   int n0;
-  __device__ __forceinline__ void put(float v, int n) const { row[n - n0] = v; }
+  __device__ __forceinline__ void put(float v, int, int n) const { row[n - n0] = v; }
 };
 
 template <bool XVEC, int HB>

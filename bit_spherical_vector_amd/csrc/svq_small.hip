@@ -57,6 +57,8 @@
 // group to arrive (an arrival counter, cleared by the prep launch) adds
 // them in range order and writes the output, so results do not depend on
 // timing.
+#include <type_traits>
+
 #include "svq_device.h"
 #include "svq_epilogue.h"
 #include "../../include/svq.h"
@@ -143,7 +145,10 @@ __device__ __forceinline__ const uint8_t *sb_unit(const MatView &w, int t, int u
   return w.base + w.off_codes + ((size_t)t * w.units + u) * UNIT_BYTES;
 }
 
-// ea: nothing, or the EpiArgs of a single matrix.  (The body stands in the
+// ea: nothing, the EpiArgs of a single matrix, or the PairArgs of a gated
+// pair (jobs 0 and 1, equal plans): then every block leaves its sums, times
+// its matrix's 2^-s, as a range of its own (the gate's ranges first), and the
+// last of all to arrive finishes the pair.  (The body stands in the
 // kernel itself: behind a function call the job records, indexed at run time,
 // would be copied out of the kernel arguments.)
 template <typename... EA>
@@ -240,6 +245,53 @@ __global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b, EA... ea) {
 #pragma unroll
     for (int ww = 0; ww < SB_WAVES; ++ww)
       acc[t] += *(sb_lds_f_t *)(size_t)(eoff + (ww * SB_TMAX + t) * 1024);
+  }
+  constexpr bool pair = std::is_same_v<decltype(make_epi(ea...)), PairEpi>;
+  if constexpr (pair) {
+    const int total = 2 * J.splits, own = jn * J.splits + r;
+    float *pt = epi.a.part + ((size_t)t0 * total + own) * 256 + tid;
+#pragma unroll
+    for (int t = 0; t < SB_TMAX; ++t)
+      if (t < tn)
+        __hip_atomic_store(pt + (size_t)t * total * 256, acc[t] * J.xinv, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0) {
+      const int prev = __hip_atomic_fetch_add(epi.a.cnt + g, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      *(sb_lds_i_t *)(size_t)SB_OFF_FLAG = prev == total - 1 ? 1 : 0;
+    }
+    __syncthreads();
+    if (*(sb_lds_i_t *)(size_t)SB_OFF_FLAG == 0) return;
+    const float *pa = epi.a.part + (size_t)t0 * total * 256 + tid;
+    float up[SB_TMAX];
+#pragma unroll
+    for (int t = 0; t < SB_TMAX; ++t) acc[t] = up[t] = 0.f;
+    for (int r0 = 0; r0 < J.splits; r0 += 4) {
+      float vg[SB_TMAX][4], vu[SB_TMAX][4];
+#pragma unroll
+      for (int t = 0; t < SB_TMAX; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float *q = pa + ((size_t)min(t, tn - 1) * total + min(r0 + e, J.splits - 1)) * 256;
+          vg[t][e] = __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          vu[t][e] = __hip_atomic_load(q + (size_t)J.splits * 256, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+      for (int t = 0; t < SB_TMAX; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (r0 + e < J.splits) {
+            acc[t] += vg[t][e];
+            up[t] += vu[t][e];
+          }
+    }
+    if (m >= b.m) return;
+#pragma unroll
+    for (int t = 0; t < SB_TMAX; ++t) {
+      const int n = (t0 + t) * UNIT_ROWS + nn;
+      if (t < tn && n < w.n) store_out(J.y, (size_t)m * J.ldy + n, pair_value(epi.a, acc[t], up[t], n), b.ydt);
+    }
+    return;
   }
   if (J.splits > 1) {
     // Partial tiles for the range, then the arrival count of the group.
@@ -353,11 +405,115 @@ __global__ __launch_bounds__(256) void sb_prep_kernel(SbBatch b) {
   if (tid < 16) J.xs[(size_t)u * 16 + tid] = ldexpf(1.f, -e);
 }
 
-hipError_t launch_sb(SbBatch &b, int prep_blocks, int blocks, hipStream_t s) {
-  hipLaunchKernelGGL(sb_prep_kernel, dim3(prep_blocks), dim3(256), 0, s, b);
-  hipError_t e = hipGetLastError();
+// The same fragments and scales for the feed-forward calls, whose matrices
+// share one x: four blocks per unit, each staging the rows whole in LDS with
+// coalesced loads, gathering its unit there and writing one fragment in four.
+// (Gathered from memory by one block per unit, the 2-byte loads of 64 lanes
+// keep one compute unit's address path busy for 3 us.)
+constexpr int SB_PREP_BATCH = 8;  // 16-byte loads in flight per thread
+template <bool XVEC>
+__global__ __launch_bounds__(256) void sb_prep_rows_kernel(SbBatch b, int32_t *cnt, int n_cnt) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t s_rows[];
+  __shared__ float s_max[4][16];
+  const int per = b.job[0].w.units * 4;
+  const int jn = (int)blockIdx.x / per, lb = (int)blockIdx.x - jn * per, u = lb >> 2, part = lb & 3;
+  const SbJob &J = b.job[jn];
+  const MatView &w = J.w;
+  const int tid = threadIdx.x, wv = tid >> 6, L = tid & 63, K = w.k, ks = K + 8;
+  if (blockIdx.x == 0)
+    for (int i = tid; i < n_cnt; i += 256) cnt[i] = 0;
+  const int m = L & 15, s = L >> 4;
+  u4 pv[4];
+#pragma unroll
+  for (int ff = 0; ff < 4; ++ff)  // perm is zero padded to the unit width
+    pv[ff] = *(const u4 *)(w.base + w.off_perm + 2 * (size_t)(u * UNIT_SLOTS + 8 * (16 * wv + 4 * s + ff)));
+  if (XVEC) {
+    const int n8 = K / 8, tot = b.m * n8;
+    for (int q0 = tid; q0 < tot; q0 += 256 * SB_PREP_BATCH) {
+      u4 v[SB_PREP_BATCH];
+#pragma unroll
+      for (int i = 0; i < SB_PREP_BATCH; ++i) {
+        const int q = min(q0 + 256 * i, tot - 1), rr = q / n8;
+        v[i] = *(const u4 *)(J.x + (int64_t)rr * J.ldx + 8 * (q - rr * n8));
+      }
+#pragma unroll
+      for (int i = 0; i < SB_PREP_BATCH; ++i) {
+        const int q = q0 + 256 * i, rr = q / n8;
+        if (q < tot) *(u4 *)(s_rows + (size_t)rr * ks + 8 * (q - rr * n8)) = v[i];
+      }
+    }
+  } else {
+    for (int rr = 0; rr < b.m; ++rr)
+      for (int j = tid; j < K; j += 256) s_rows[(size_t)rr * ks + j] = J.x[(int64_t)rr * J.ldx + j];
+  }
+  __syncthreads();
+  const uint16_t *row = s_rows + (size_t)min(m, b.m - 1) * ks;
+  float v[4][8];
+  float mx = 0.f;
+#pragma unroll
+  for (int ff = 0; ff < 4; ++ff) {
+    // k is a multiple of 8, so eight slots are all inside k or all padding
+    const bool on = m < b.m && u * UNIT_SLOTS + 8 * (16 * wv + 4 * s + ff) < K;
+#pragma unroll
+    for (int l = 0; l < 4; ++l) {
+      const float lo = bf16_bits_to_f32(row[pv[ff][l] & 0xFFFFu]), hi = bf16_bits_to_f32(row[pv[ff][l] >> 16]);
+      v[ff][2 * l] = on ? lo : 0.f;
+      v[ff][2 * l + 1] = on ? hi : 0.f;
+      mx = fmaxf(mx, fmaxf(fabsf(v[ff][2 * l]), fabsf(v[ff][2 * l + 1])));
+    }
+  }
+  mx = fmaxf(mx, __shfl_xor(mx, 16));
+  mx = fmaxf(mx, __shfl_xor(mx, 32));
+  if (L < 16) s_max[wv][L] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(s_max[0][m], s_max[1][m]), fmaxf(s_max[2][m], s_max[3][m]));
+  const int e = mx > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
+#pragma unroll
+  for (int ff = 0; ff < 4; ++ff) {
+    if (ff != part) continue;
+    u4 h;
+#pragma unroll
+    for (int l = 0; l < 4; ++l) {
+      const _Float16 lo = (_Float16)ldexpf(v[ff][2 * l], e), hi = (_Float16)ldexpf(v[ff][2 * l + 1], e);
+      h[l] = (uint32_t)__builtin_bit_cast(uint16_t, lo) | ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
+    }
+    *(u4 *)(J.xa + ((size_t)u * 16 + 4 * wv + ff) * 1024 + 16 * L) = h;
+  }
+  if (part == 0 && tid < 16) J.xs[(size_t)u * 16 + tid] = ldexpf(1.f, -e);
+}
+
+static hipError_t launch_sb_prep_rows(SbBatch &b, hipStream_t s, bool *fits) {
+  const size_t lds = (size_t)b.m * (b.job[0].w.k + 8) * 2;
+  *fits = lds + 1024 <= GV_LDS_LIMIT;
+  if (!*fits) return hipSuccess;
+  const bool xvec = (((uintptr_t)b.job[0].x | ((uintptr_t)b.job[0].ldx * 2)) & 15) == 0;
+  const hipError_t e = xvec ? allow_smem(sb_prep_rows_kernel<true>, lds) : allow_smem(sb_prep_rows_kernel<false>, lds);
   if (e != hipSuccess) return e;
-  if (b.epi)
+  int32_t *cnt = b.pair ? b.pair->cnt : b.job[0].cnt;
+  const int n_cnt = b.pair ? b.pair->n_cnt : (cnt ? b.job[0].groups : 0);
+  const dim3 grid(b.count * b.job[0].w.units * 4);
+  if (xvec)
+    hipLaunchKernelGGL(sb_prep_rows_kernel<true>, grid, dim3(256), lds, s, b, cnt, n_cnt);
+  else
+    hipLaunchKernelGGL(sb_prep_rows_kernel<false>, grid, dim3(256), lds, s, b, cnt, n_cnt);
+  return hipGetLastError();
+}
+
+hipError_t launch_sb(SbBatch &b, int prep_blocks, int blocks, hipStream_t s) {
+  hipError_t e;
+  bool rows = false;
+  if (b.epi || b.pair) {
+    e = launch_sb_prep_rows(b, s, &rows);
+    if (e != hipSuccess) return e;
+  }
+  if (!rows) {
+    hipLaunchKernelGGL(sb_prep_kernel, dim3(prep_blocks), dim3(256), 0, s, b);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (b.pair)
+    hipLaunchKernelGGL(sb_gemm_kernel<PairArgs>, dim3(blocks), dim3(256), SB_SMEM, s, b, *b.pair);
+  else if (b.epi)
     hipLaunchKernelGGL(sb_gemm_kernel<EpiArgs>, dim3(blocks), dim3(256), SB_SMEM, s, b, *b.epi);
   else
     hipLaunchKernelGGL(sb_gemm_kernel<>, dim3(blocks), dim3(256), SB_SMEM, s, b);
