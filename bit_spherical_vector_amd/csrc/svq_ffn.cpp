@@ -416,7 +416,11 @@ svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_h
   if (ldx < gate->k || ldy < down->n) return SVQ_ERR_INVALID_ARG;
   if (residual && (!valid_dt(residual_dt) || ldr < down->n)) return SVQ_ERR_INVALID_ARG;
   const int64_t S = m * topk;
-  if (moe_ffn_few_fits(gate, up, down, num_experts, S)) {
+  const bool few = moe_ffn_few_fits(gate, up, down, num_experts, S);
+  bool split = true;
+  for (int c = 0; c < 3 && !few; ++c)
+    for (int32_t e = 0; e < num_experts; ++e) split = split && has_split(&sets[c][e]);
+  if (few || split) {
     MoeFfnArgs fa;
     std::memset(&fa, 0, sizeof(fa));
     fa.gate = gate;
@@ -437,7 +441,8 @@ svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_h
     fa.ldy = ldy;
     fa.ydt = (int32_t)ydt;
     size_t need = 0;
-    if (launch_moe_ffn_few(fa, nullptr, &need, nullptr) != hipSuccess) return SVQ_ERR_HIP;
+    const auto launch = few ? launch_moe_ffn_few : launch_moe_ffn_grouped;
+    if (launch(fa, nullptr, &need, nullptr) != hipSuccess) return SVQ_ERR_HIP;
     if (!workspace) {
       *workspace_bytes = need;
       return SVQ_OK;
@@ -445,7 +450,7 @@ svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_h
     if (!x || !expert_ids || !weights || !y) return SVQ_ERR_INVALID_ARG;
     if (residual == y && (ldr != ldy || residual_dt != ydt)) return SVQ_ERR_INVALID_ARG;
     if (*workspace_bytes < need) return SVQ_ERR_BUFFER_TOO_SMALL;
-    return launch_moe_ffn_few(fa, workspace, &need, (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
+    return launch(fa, workspace, &need, (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
   }
   const int32_t f = gate->n, n = down->n;
   const int64_t ldf = pad4(f), ldh = (f + 7) / 8 * 8, ldd = pad4(n);

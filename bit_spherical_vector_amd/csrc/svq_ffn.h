@@ -102,6 +102,8 @@ bool moe_ffn_few_fits(const svq_handle *gate, const svq_handle *up, const svq_ha
                       int64_t slots);
 // ws null: only *need.
 hipError_t launch_moe_ffn_few(const MoeFfnArgs &f, void *ws, size_t *need, hipStream_t s);
+// The grouped form; every matrix has an exact split.
+hipError_t launch_moe_ffn_grouped(const MoeFfnArgs &f, void *ws, size_t *need, hipStream_t s);
 
 // ---- router --------------------------------------------------------------------
 constexpr int ROUTE_MAX_TOPK = 32;

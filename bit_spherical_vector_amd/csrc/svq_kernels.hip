@@ -1868,4 +1868,111 @@ hipError_t launch_moe_ffn_few(const MoeFfnArgs &f, void *ws, size_t *need, hipSt
   return hipGetLastError();
 }
 
+// The grouped form, for any number of slots: the tokens in chunks of at most
+// MOE_FUSED_MAX_SLOTS slots (whole tokens), each chunk
+//   gate and up: prep (routing, staging) and product, fp32 sums per slot;
+//   down: prep (act(g) * u formed while its rows are staged, the routing of
+//         the chunk reused) and product;
+//   the sum over each token's slots.
+hipError_t launch_moe_ffn_grouped(const MoeFfnArgs &f, void *ws, size_t *need, hipStream_t s) {
+  const int E = f.num_experts;
+  const MoeShape shg = moe_shape(f.gate, E), shd = moe_shape(f.down, E);
+  int64_t chunk = MOE_FUSED_MAX_SLOTS / f.topk;  // topk <= 256
+  chunk = f.m < chunk ? f.m : chunk;
+  const int64_t S = chunk * f.topk;
+  const int max_work = (int)((S + MOE_SB_ROWS - 1) / MOE_SB_ROWS) + E;
+  const int64_t ldf = (shg.n + 3) / 4 * 4, ldd = (shd.n + 3) / 4 * 4;
+  size_t off = 0;
+  auto take = [&](size_t b) {
+    const size_t at = off;
+    off += align256(b);
+    return at;
+  };
+  const size_t o_sorted = take((size_t)S * 4), o_work = take((size_t)max_work * 12), o_nwork = take(4);
+  size_t o_xs[2], o_xa[2], o_gu[2];
+  for (int c = 0; c < 2; ++c) {
+    o_xs[c] = take((size_t)max_work * MOE_SB_ROWS * 4);
+    o_xa[c] = take(moe_sb_xa_bytes(max_work, shg.units > shd.units ? shg.units : shd.units));
+    o_gu[c] = take((size_t)S * ldf * 4);
+  }
+  const size_t o_d = take((size_t)S * ldd * 4);
+  *need = off;
+  if (!ws) return hipSuccess;
+  uint8_t *p = (uint8_t *)ws;
+  int32_t *work = (int32_t *)(p + o_work), *nwork = (int32_t *)(p + o_nwork), *sorted = (int32_t *)(p + o_sorted);
+  const svq_handle *const gu[2] = {f.gate, f.up};
+  const int per = 2 * E <= MAX_EXPERTS ? 2 : 1;
+  for (int64_t t0 = 0; t0 < f.m; t0 += chunk) {
+    const int64_t mc = f.m - t0 < chunk ? f.m - t0 : chunk;
+    const int32_t *ids = f.ids + t0 * f.topk;
+    const MoeRoute route{ids, (int32_t)(mc * f.topk), 1};
+    const int mw = (int)((mc * f.topk + MOE_SB_ROWS - 1) / MOE_SB_ROWS) + E;
+    const uint16_t *x = (const uint16_t *)f.x + t0 * f.ldx;
+    MoeSbBatch b;
+    ExpertTable tab;
+    MoeF16 h;
+    auto project = [&](int c, int j, const svq_handle *w, const MoeShape &sh) {  // entry j of the launch, buffers c
+      for (int e = 0; e < E; ++e) {
+        tab.base[j * E + e] = (const uint8_t *)w[e].dev;
+        tab.bd[j * E + e] = (uint8_t)w[e].bd;
+        h.xscale[j * E + e] = (int8_t)w[e].xscale_log2;
+      }
+      b.p[j].sh = sh;
+      b.p[j].xa = p + o_xa[c];
+      h.xs[j] = (float *)(p + o_xs[c]);
+    };
+    for (int c0 = 0; c0 < 2; c0 += per) {
+      std::memset(&b, 0, sizeof(b));
+      std::memset(&tab, 0, sizeof(tab));
+      std::memset(&h, 0, sizeof(h));
+      b.count = per;
+      b.vec = (((uintptr_t)x | ((uintptr_t)f.ldx * 2)) & 15) == 0;
+      b.yvec = 1;
+      for (int j = 0; j < per; ++j) {
+        project(c0 + j, j, gu[c0 + j], moe_shape(gu[c0 + j], E));
+        b.p[j].x = x;
+        b.p[j].ldx = f.ldx;
+        b.p[j].y = p + o_gu[c0 + j];
+        b.p[j].ldy = ldf;
+      }
+      const hipError_t e = launch_moe_sb_f16(b, tab, f.topk, route, work, nwork, sorted, mw, h, s);
+      if (e != hipSuccess) return e;
+    }
+    std::memset(&b, 0, sizeof(b));
+    std::memset(&tab, 0, sizeof(tab));
+    std::memset(&h, 0, sizeof(h));
+    b.count = 1;
+    b.yvec = 1;
+    project(0, 0, f.down, shd);
+    b.p[0].y = p + o_d;
+    b.p[0].ldy = ldd;
+    h.g = (const float *)(p + o_gu[0]);
+    h.u = (const float *)(p + o_gu[1]);
+    h.ldf = ldf;
+    h.act = f.act;
+    hipError_t e = launch_moe_sb_f16(b, tab, f.topk, MoeRoute{nullptr, (int32_t)(mc * f.topk), 1}, work, nwork, sorted,
+                                     mw, h, s);
+    if (e != hipSuccess) return e;
+    CombineArgs ca;
+    std::memset(&ca, 0, sizeof(ca));
+    ca.d = (const float *)(p + o_d);
+    ca.ldd = ldd;
+    ca.ids = ids;
+    ca.weights = f.weights + t0 * f.topk;
+    ca.m = mc;
+    ca.topk = f.topk;
+    ca.num_experts = E;
+    ca.res = f.res ? (const uint8_t *)f.res + (size_t)(t0 * f.ldr) * (f.res_f32 ? 4 : 2) : nullptr;
+    ca.ldr = f.ldr;
+    ca.res_f32 = f.res_f32;
+    ca.y = (uint8_t *)f.y + (size_t)(t0 * f.ldy) * (f.ydt == 0 ? 2 : 4);
+    ca.ldy = f.ldy;
+    ca.n = shd.n;
+    ca.ydt = f.ydt;
+    e = launch_combine(ca, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace svq

@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "svq_device.h"
+#include "svq_epilogue.h"
 #include "../../include/svq.h"
 
 namespace svq {
@@ -89,6 +90,126 @@ struct MoeRouteLds {
   int32_t expert;
 };
 
+// The staging and gather of the fp16 form: as the bf16 form below, but the
+// rows' largest finite magnitudes are found in LDS (one wave per row) before
+// the gather, which converts to fp16 under the row's scale.  Rows formed from
+// g and u are staged in fp32, so that act(g) * u is rounded once, here.
+template <bool GLU>
+__device__ __forceinline__ void prep_f16_rows(uint8_t *smem, const MoeSbProj &P, const uint16_t *perm, int x_per_slot,
+                                              int topk, int vec, int wi, int g, int r0, int rows,
+                                              const int32_t *lds_rows, const int32_t *sorted, const MoeF16 &f, int pc,
+                                              int xscale) {
+  constexpr int NT = MOE_SB_PREP_THREADS, USTEP = NT / 256, EZ = GLU ? 4 : 2, PER = 16 / EZ, BATCH = 4;
+  __shared__ int s_exp[16];
+  const MoeShape &sh = P.sh;
+  const int tid = threadIdx.x, w = tid >> 6, L = tid & 63, s = L >> 4, rl = L & 15;
+  const int U = sh.units, kp = U * UNIT_SLOTS, k = sh.k, rb = P.rb;
+  const int stride = kp * EZ + 16;  // bytes per staged row
+  const int q = w & 3, u0 = w >> 2, chunks = kp / PER;
+  auto slot_of = [&](int row) { return lds_rows ? lds_rows[row] : sorted[r0 + row]; };
+  for (int rb0 = 0; rb0 < 16; rb0 += rb) {
+    __syncthreads();  // the previous pass's gathers are done
+    const int nstage = rb * chunks;
+    for (int c0 = 0; c0 < nstage; c0 += BATCH * NT) {
+      u4 v[BATCH], v2[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        v[i] = v2[i] = (u4){0u, 0u, 0u, 0u};
+        const int c = c0 + tid + NT * i;
+        const int rr = c / chunks, cc = c - rr * chunks, row = 16 * g + rb0 + rr;
+        if (c < nstage && row < rows && PER * cc < k) {
+          const int slot = slot_of(row);
+          if constexpr (GLU) {  // k is a multiple of 8
+            v[i] = *(const u4 *)(f.g + (int64_t)slot * f.ldf + 4 * cc);
+            v2[i] = *(const u4 *)(f.u + (int64_t)slot * f.ldf + 4 * cc);
+          } else {
+            const uint16_t *xr = P.x + (int64_t)(x_per_slot ? slot : slot / topk) * P.ldx + 8 * cc;
+            if (vec) {
+              v[i] = *(const u4 *)xr;
+            } else {
+#pragma unroll
+              for (int l = 0; l < 4; ++l) v[i][l] = (uint32_t)xr[2 * l] | ((uint32_t)xr[2 * l + 1] << 16);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int c = c0 + tid + NT * i;
+        const int rr = c / chunks, cc = c - rr * chunks;
+        if constexpr (GLU) {
+#pragma unroll
+          for (int l = 0; l < 4; ++l)
+            v[i][l] = __builtin_bit_cast(uint32_t, act_apply(__builtin_bit_cast(float, (uint32_t)v[i][l]), f.act) *
+                                                       __builtin_bit_cast(float, (uint32_t)v2[i][l]));
+        }
+        if (c < nstage) *(u4 *)(smem + (size_t)rr * stride + 16 * cc) = v[i];
+      }
+    }
+    __syncthreads();
+    if (w < rb) {  // wave-uniform: wave w finds the scale of staged row w
+      uint32_t mx = 0;  // as bits: finite magnitudes order as integers
+      for (int c = L; c < chunks; c += 64) {
+        const u4 v = *(const u4 *)(smem + (size_t)w * stride + 16 * c);
+#pragma unroll
+        for (int l = 0; l < 4; ++l) {
+          if constexpr (GLU) {
+            const uint32_t a = v[l] & 0x7FFFFFFFu;
+            mx = max(mx, a < 0x7F800000u ? a : 0u);
+          } else {
+            const uint32_t lo = (v[l] & 0x7FFFu) << 16, hi = v[l] & 0x7FFF0000u;
+            mx = max(mx, lo < 0x7F800000u ? lo : 0u);
+            mx = max(mx, hi < 0x7F800000u ? hi : 0u);
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
+      const float mf = __builtin_bit_cast(float, mx);
+      const int ex = mf > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mf) : 0;
+      if (L == 0) {
+        s_exp[rb0 + w] = ex;
+        f.xs[pc][(size_t)wi * MOE_SB_ROWS + 16 * g + rb0 + w] = ldexpf(1.f, min(127, -ex - xscale));
+      }
+    }
+    __syncthreads();
+    if (rl < rb0 || rl >= rb0 + rb) continue;  // lane-uniform per pass; no barrier below
+    const uint8_t *xrow = smem + (size_t)(rl - rb0) * stride;
+    const int ex = s_exp[rl];
+    auto get = [&](uint32_t at) __attribute__((always_inline)) {
+      float v;
+      if constexpr (GLU) v = ((const float *)xrow)[at];
+      else v = bf16_bits_to_f32(((const uint16_t *)xrow)[at]);
+      return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)ldexpf(v, ex));
+    };
+    for (int u = u0; u < U; u += USTEP) {
+      u4 pv[4];
+#pragma unroll
+      for (int ci = 0; ci < 4; ++ci) pv[ci] = *(const u4 *)(perm + u * UNIT_SLOTS + 8 * (16 * ci + 4 * s + q));
+#pragma unroll
+      for (int ci = 0; ci < 4; ++ci) {
+        u4 v;
+#pragma unroll
+        for (int l = 0; l < 4; ++l) v[l] = get(pv[ci][l] & 0xFFFFu) | (get(pv[ci][l] >> 16) << 16);
+        // perm entries are < k (zero past k); k is a multiple of 8, so eight
+        // slots are inside k or all padding
+        if (u * UNIT_SLOTS + 8 * (16 * ci + 4 * s + q) >= k) v = (u4){0u, 0u, 0u, 0u};
+        *(u4 *)(P.xa + moe_sb_xa_off(wi, U, u, g) + ((size_t)(4 * ci + q) * 64 + L) * 16) = v;
+      }
+    }
+  }
+}
+template <bool ROUTE>
+__device__ __forceinline__ void prep_f16(uint8_t *smem, const MoeSbProj &P, const uint16_t *perm, int x_per_slot,
+                                         int topk, int vec, int wi, int g, int r0, int rows, const int32_t *lds_rows,
+                                         const int32_t *sorted, const MoeF16 &f, int pc, int e) {
+  const int xscale = f.xscale[pc * P.sh.num_experts + e];
+  if constexpr (ROUTE)
+    prep_f16_rows<false>(smem, P, perm, x_per_slot, topk, vec, wi, g, r0, rows, lds_rows, sorted, f, pc, xscale);
+  else
+    prep_f16_rows<true>(smem, P, perm, x_per_slot, topk, vec, wi, g, r0, rows, lds_rows, sorted, f, pc, xscale);
+}
+
 // Block (work item, row group g), MOE_SB_PREP_THREADS threads: the group's
 // 16 activation rows are staged whole in LDS (rb rows per pass, coalesced
 // 16-byte loads when x and ldx allow them; the row stride carries 16 bytes
@@ -100,10 +221,12 @@ struct MoeRouteLds {
 // slots past k are zeros.  With ROUTE the block first does the routing
 // (above); row group 0 of every item writes the item's work record and
 // sorted slots for the product launch, block 0 the item count.
-template <bool ROUTE>
+// fa: nothing, or the MoeF16 of the fp16 form.
+template <bool ROUTE, typename... FA>
 __global__ __launch_bounds__(MOE_SB_PREP_THREADS) void moe_sb_prep_kernel(
     MoeSbBatch b, ExpertTable tab, int x_per_slot, int topk, MoeRoute route, int32_t *__restrict__ work,
-    int32_t *__restrict__ nwork, int32_t *__restrict__ sorted) {
+    int32_t *__restrict__ nwork, int32_t *__restrict__ sorted, FA... fa) {
+  constexpr bool F16 = sizeof...(FA) > 0;
   constexpr int NT = MOE_SB_PREP_THREADS, USTEP = NT / 256;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ MoeRouteLds R;
@@ -133,7 +256,7 @@ __global__ __launch_bounds__(MOE_SB_PREP_THREADS) void moe_sb_prep_kernel(
       const int q = tid * C + j;
       if (my[j] >= 0 && my[j] < E) {
         atomicAdd(&R.cnt[my[j]], 1);
-      } else if (j < C && q < S && q % (int)gridDim.x == (int)blockIdx.x) {
+      } else if (!F16 && j < C && q < S && q % (int)gridDim.x == (int)blockIdx.x) {
         // a slot with an id outside [0, E): its output row is zeros
         char *yr = (char *)P.y + (size_t)q * P.ldy * (route.ydt == 0 ? 2 : 4);
         for (int c = 0; c < sh.n; ++c) store_out(yr, (size_t)c, 0.f, route.ydt);
@@ -229,6 +352,11 @@ __global__ __launch_bounds__(MOE_SB_PREP_THREADS) void moe_sb_prep_kernel(
     if (16 * g >= rows) return;  // block-uniform
   }
   const int U = sh.units, kp = U * UNIT_SLOTS, k = sh.k;
+  if constexpr (F16) {
+    prep_f16<ROUTE>(smem, P, (const uint16_t *)(tab.base[pc * sh.num_experts + e] + sh.off_perm), x_per_slot, topk, vec,
+                    wi, g, r0, rows, ROUTE ? R.rows : nullptr, sorted, fa..., pc, e);
+    return;
+  }
   const int stride = moe_sb_prep_stride(kp);  // bytes per staged row
   const uint16_t *perm = (const uint16_t *)(tab.base[pc * sh.num_experts + e] + sh.off_perm);
   const int q = w & 3, u0 = w >> 2;
@@ -332,11 +460,13 @@ __device__ __forceinline__ void moe_slice_barrier() { asm volatile("s_waitcnt lg
 // direct global-to-LDS loads the slice barrier had to wait for every
 // outstanding load, codes included: those loads do not complete in order
 // with the others, and nothing tracks their data per register.)
-template <int G>
+// F16: the fp16 form; xs: the item's inverse row scales.
+template <int G, bool F16 = false>
 __device__ __forceinline__ void moe_sb_block(const MatView &w, int tg, int wi, int r0, int rows,
                                              const int32_t *__restrict__ sorted,
                                              const uint8_t *__restrict__ xa, void *__restrict__ y,
-                                             int64_t ldy, int ydt, int yvec, uint8_t *smem) {
+                                             int64_t ldy, int ydt, int yvec, uint8_t *smem,
+                                             const float *__restrict__ xs = nullptr) {
   const int U = w.units, NS = 4 * U;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -383,9 +513,9 @@ __device__ __forceinline__ void moe_sb_block(const MatView &w, int tg, int wi, i
 
   // table, slice 0 and the first unit's codes requested first
   u4 bt[4];
-  const u4 *gbt = (const u4 *)(w.base + w.off_btab);
+  const u4 *gbt = (const u4 *)(w.base + (F16 ? w.off_xtab : w.off_btab));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) bt[i] = gbt[tid + 256 * i];
+  for (int i = 0; i < 4; ++i) bt[i] = gbt[F16 ? 2 * (tid + 256 * i) : tid + 256 * i];
   load_slice(0);
   SbCodes cd[MOE_SB_TW];
 #pragma unroll
@@ -444,8 +574,12 @@ __device__ __forceinline__ void moe_sb_block(const MatView &w, int tg, int wi, i
         const u4 B = moe_signed(D[t][ci], S01[t], S23[t], shf.sg[ci]);
 #pragma unroll
         for (int g = 0; g < G; ++g)
-          C[t][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, A[g]),
-                                                            __builtin_bit_cast(b8, B), C[t][g], 0, 0, 0);
+          if constexpr (F16)
+            C[t][g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, A[g]), __builtin_bit_cast(h8, B),
+                                                             C[t][g], 0, 0, 0);
+          else
+            C[t][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, A[g]),
+                                                              __builtin_bit_cast(b8, B), C[t][g], 0, 0, 0);
       }
     }
   };
@@ -468,6 +602,14 @@ __device__ __forceinline__ void moe_sb_block(const MatView &w, int tg, int wi, i
     slice(U - 1, I3(), I2());
   }
 
+  if constexpr (F16) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const f4 sc = *(const f4 *)(xs + 16 * g + 4 * (int)s);  // rows 16g + 4s .. + 3
+#pragma unroll
+      for (int t = 0; t < MOE_SB_TW; ++t) C[t][g] *= sc;
+    }
+  }
   // The outputs leave through LDS: the block's item rows x its 128 columns
   // n0 + nb (n0 = 128 tg), row stride padded by 16 bytes, then 16-byte pieces
   // of whole rows go to y.  Accumulator element i of lane L is activation
@@ -517,9 +659,16 @@ __device__ __forceinline__ void moe_sb_block(const MatView &w, int tg, int wi, i
   else epi(std::false_type());
 }
 
+// fa: nothing, or the MoeF16Scales of the fp16 form.
+__device__ __forceinline__ const float *item_scales(int, int) { return nullptr; }
+__device__ __forceinline__ const float *item_scales(int pc, int wi, const MoeF16Scales &f) {
+  return f.xs[pc] + (size_t)wi * MOE_SB_ROWS;
+}
+template <typename... FA>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void moe_sb_kernel(
     MoeSbBatch b, ExpertTable tab, const int32_t *__restrict__ work, const int32_t *__restrict__ nwork,
-    const int32_t *__restrict__ sorted, int ydt) {
+    const int32_t *__restrict__ sorted, int ydt, FA... fa) {
+  constexpr bool F16 = sizeof...(FA) > 0;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int pc = blockIdx.y;  // projection
   const MoeSbProj &P = b.p[pc];
@@ -541,10 +690,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void m
   const int wi = l / tgroups, tg = l - wi * tgroups;
   const int e = work[3 * wi], r0 = work[3 * wi + 1], rows = work[3 * wi + 2] - r0;
   const MatView w = expert_view(sh, tab, pc * sh.num_experts + e);
+  const float *xs = item_scales(pc, wi, fa...);
   switch ((rows + 15) >> 4) {  // block-uniform
-    case 1: moe_sb_block<1>(w, tg, wi, r0, rows, sorted, xa, y, ldy, ydt, yvec, smem); break;
-    case 2: moe_sb_block<2>(w, tg, wi, r0, rows, sorted, xa, y, ldy, ydt, yvec, smem); break;
-    default: moe_sb_block<3>(w, tg, wi, r0, rows, sorted, xa, y, ldy, ydt, yvec, smem); break;
+    case 1: moe_sb_block<1, F16>(w, tg, wi, r0, rows, sorted, xa, y, ldy, ydt, yvec, smem, xs); break;
+    case 2: moe_sb_block<2, F16>(w, tg, wi, r0, rows, sorted, xa, y, ldy, ydt, yvec, smem, xs); break;
+    default: moe_sb_block<3, F16>(w, tg, wi, r0, rows, sorted, xa, y, ldy, ydt, yvec, smem, xs); break;
   }
 }
 
@@ -586,12 +736,51 @@ hipError_t launch_moe_sb(MoeSbBatch &b, const ExpertTable &tab, int x_per_slot, 
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  e = allow_smem(moe_sb_kernel, MOE_SB_SMEM);
+  e = allow_smem(moe_sb_kernel<>, MOE_SB_SMEM);
   if (e != hipSuccess) return e;
   // every projection's active pairs fit: the grid covers the widest one
   const int blocks = (max_work * tgroups + MOE_XCDS - 1) / MOE_XCDS * MOE_XCDS;
-  hipLaunchKernelGGL(moe_sb_kernel, dim3(blocks, b.count), dim3(256), MOE_SB_SMEM, s, b, tab, work, nwork,
+  hipLaunchKernelGGL(moe_sb_kernel<>, dim3(blocks, b.count), dim3(256), MOE_SB_SMEM, s, b, tab, work, nwork,
                      sorted, ydt);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_sb_f16(MoeSbBatch &b, const ExpertTable &tab, int topk, const MoeRoute &route, int32_t *work,
+                             int32_t *nwork, int32_t *sorted, int max_work, const MoeF16 &f, hipStream_t s) {
+  if (b.count < 1 || b.count > MOE_BATCH_MAX || route.slots > MOE_FUSED_MAX_SLOTS) return hipErrorInvalidValue;
+  const bool glu = f.g != nullptr;
+  if (glu != (route.ids == nullptr) || (glu && b.count != 1)) return hipErrorInvalidValue;
+  size_t prep_lds = 0;
+  int tgroups = 1;
+  for (int c = 0; c < b.count; ++c) {
+    const size_t stride = (size_t)b.p[c].sh.units * UNIT_SLOTS * (glu ? 4 : 2) + 16;
+    b.p[c].rb = (int)std::max<size_t>(1, std::min<size_t>(16, MOE_SB_PREP_LDS / stride));
+    prep_lds = std::max(prep_lds, b.p[c].rb * stride);
+    tgroups = std::max(tgroups, (b.p[c].sh.n_tiles + MOE_SB_TILES - 1) / MOE_SB_TILES);
+  }
+  if (prep_lds > GV_LDS_LIMIT - sizeof(MoeRouteLds) - 256) return hipErrorInvalidValue;
+  const dim3 pgrid(max_work * MOE_SB_G, b.count), pblock(MOE_SB_PREP_THREADS);
+  hipError_t e;
+  if (!glu) {
+    e = allow_smem(moe_sb_prep_kernel<true, MoeF16>, prep_lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((moe_sb_prep_kernel<true, MoeF16>), pgrid, pblock, prep_lds, s, b, tab, 0, topk, route, work,
+                       nwork, sorted, f);
+  } else {
+    e = allow_smem(moe_sb_prep_kernel<false, MoeF16>, prep_lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((moe_sb_prep_kernel<false, MoeF16>), pgrid, pblock, prep_lds, s, b, tab, 1, topk, route, work,
+                       nwork, sorted, f);
+  }
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  MoeF16Scales sc;
+  for (int c = 0; c < MOE_BATCH_MAX; ++c) sc.xs[c] = f.xs[c];
+  e = allow_smem(moe_sb_kernel<MoeF16Scales>, MOE_SB_SMEM);
+  if (e != hipSuccess) return e;
+  const int blocks = (max_work * tgroups + MOE_XCDS - 1) / MOE_XCDS * MOE_XCDS;
+  hipLaunchKernelGGL(moe_sb_kernel<MoeF16Scales>, dim3(blocks, b.count), dim3(256), MOE_SB_SMEM, s, b, tab, work,
+                     nwork, sorted, 1, sc);
   return hipGetLastError();
 }
 

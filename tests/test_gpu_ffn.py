@@ -58,7 +58,7 @@ def slope_of(act):
 def product(mat, x_bits, rounded_weights):
     """(p, bound of |p_gpu - p|) of one matrix."""
     p, W = so.linear_from_inputs(mat, x_bits)
-    rel = (mat.k + 64) * U32 + {False: 0.0, True: 2.0 ** -11, "bf16": 2.0 ** -8}[rounded_weights]
+    rel = (mat.k + 64) * U32 + (2.0 ** -11 if rounded_weights else 0.0)
     return p, rel * so.abs_bound(x_bits, W) + 1e-6
 
 
@@ -271,21 +271,20 @@ def moe64(sets, x_bits, ids, wt, act, grouped):
     gates, ups, downs = sets
     e, out = len(gates), downs[0].n
     y, b = np.zeros((m, out)), np.zeros((m, out))
-    wr = 2.0 ** -8 if grouped else 0.0
-    hr = 2.0 ** -8 if grouped else 2.0 ** -11
+    wr = 2.0 ** -11 if grouped else 0.0
+    hr = 2.0 ** -11
     for t in range(m):
         xb = x_bits[t:t + 1]
         for j in range(topk):
             i = int(ids[t, j])
             if i < 0 or i >= e:
                 continue
-            (g, gb), (u, ub) = [product(a[i], xb, grouped and "bf16") for a in (gates, ups)]
+            (g, gb), (u, ub) = [product(a[i], xb, grouped) for a in (gates, ups)]
             a = act64(g, act)
             h = a * u
             eh = (slope_of(act) * gb + 16 * U32 * np.abs(a)) * np.abs(u) + ub * np.abs(a) + slope_of(act) * gb * ub
             eh = eh + (hr + U32) * (np.abs(h) + eh)
-            if not grouped:  # fp16 after a scale of the 512-channel unit: a floor of 2^-39 of its largest value
-                eh = eh + 2.0 ** -38 * np.abs(h).max()
+            eh = eh + 2.0 ** -38 * np.abs(h).max()  # fp16 after a scale: a floor of 2^-39 of the largest value
             _, Wd = so.linear_from_inputs(downs[i], np.zeros((1, downs[i].k), dtype=np.uint16))
             d = h @ Wd.T
             ed = eh @ np.abs(Wd).T + (downs[i].k * U32 + 64 * U32 + wr) * ((np.abs(h) + eh) @ np.abs(Wd).T) + 1e-6
