@@ -90,18 +90,21 @@ struct MoeRouteLds {
   int32_t expert;
 };
 
-// The staging and gather of the fp16 form: as the bf16 form below, but the
-// rows' largest finite magnitudes are found in LDS (one wave per row) before
-// the gather, which converts to fp16 under the row's scale.  Rows formed from
-// g and u are staged in fp32, so that act(g) * u is rounded once, here.
+// The staging and gather of the fp16 form: as the bf16 form below, but one
+// wave per row finds the row's largest finite magnitude in LDS and converts
+// the row in place to fp16 under its scale, so that the gather, once per
+// projection, only moves 16-bit values.  Rows formed from g and u are staged
+// in fp32, so that act(g) * u is rounded once, here.  All
+// projections of the call read the same rows: a block stages them once (and
+// routes once) and gathers them through each projection's permutation.
 template <bool GLU>
-__device__ __forceinline__ void prep_f16_rows(uint8_t *smem, const MoeSbProj &P, const uint16_t *perm, int x_per_slot,
-                                              int topk, int vec, int wi, int g, int r0, int rows,
-                                              const int32_t *lds_rows, const int32_t *sorted, const MoeF16 &f, int pc,
-                                              int xscale) {
-  constexpr int NT = MOE_SB_PREP_THREADS, USTEP = NT / 256, EZ = GLU ? 4 : 2, PER = 16 / EZ, BATCH = 4;
-  __shared__ int s_exp[16];
+__device__ __forceinline__ void prep_f16_rows(uint8_t *smem, const MoeSbBatch &b, const ExpertTable &tab, int e,
+                                              int topk, int wi, int g, int r0, int rows, const int32_t *lds_rows,
+                                              const int32_t *sorted, const MoeF16 &f) {
+  constexpr int NT = MOE_SB_PREP_THREADS, USTEP = NT / 256, EZ = GLU ? 4 : 2, PER = 16 / EZ, BATCH = GLU ? 2 : 4;
+  const MoeSbProj &P = b.p[0];
   const MoeShape &sh = P.sh;
+  const int vec = b.vec;
   const int tid = threadIdx.x, w = tid >> 6, L = tid & 63, s = L >> 4, rl = L & 15;
   const int U = sh.units, kp = U * UNIT_SLOTS, k = sh.k, rb = P.rb;
   const int stride = kp * EZ + 16;  // bytes per staged row
@@ -123,7 +126,7 @@ __device__ __forceinline__ void prep_f16_rows(uint8_t *smem, const MoeSbProj &P,
             v[i] = *(const u4 *)(f.g + (int64_t)slot * f.ldf + 4 * cc);
             v2[i] = *(const u4 *)(f.u + (int64_t)slot * f.ldf + 4 * cc);
           } else {
-            const uint16_t *xr = P.x + (int64_t)(x_per_slot ? slot : slot / topk) * P.ldx + 8 * cc;
+            const uint16_t *xr = P.x + (int64_t)(slot / topk) * P.ldx + 8 * cc;
             if (vec) {
               v[i] = *(const u4 *)xr;
             } else {
@@ -167,22 +170,42 @@ __device__ __forceinline__ void prep_f16_rows(uint8_t *smem, const MoeSbProj &P,
       for (int d = 1; d < 64; d <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
       const float mf = __builtin_bit_cast(float, mx);
       const int ex = mf > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mf) : 0;
-      if (L == 0) {
-        s_exp[rb0 + w] = ex;
-        f.xs[pc][(size_t)wi * MOE_SB_ROWS + 16 * g + rb0 + w] = ldexpf(1.f, min(127, -ex - xscale));
+      if (L == 0)
+        for (int pc = 0; pc < b.count; ++pc)
+          f.xs[pc][(size_t)wi * MOE_SB_ROWS + 16 * g + rb0 + w] =
+              ldexpf(1.f, min(127, -ex - f.xscale[pc * sh.num_experts + e]));
+      // ascending chunks: fp16 values (GLU: half as long) overwrite only what
+      // this and earlier steps have read
+      uint8_t *row = smem + (size_t)w * stride;
+      auto half = [&](float v) __attribute__((always_inline)) {
+        return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)ldexpf(v, ex));
+      };
+      for (int c = L; c < chunks; c += 64) {
+        const u4 v = *(const u4 *)(row + 16 * c);
+        if constexpr (GLU) {
+          u2 h;
+#pragma unroll
+          for (int l = 0; l < 2; ++l)
+            h[l] = half(__builtin_bit_cast(float, (uint32_t)v[2 * l])) |
+                   (half(__builtin_bit_cast(float, (uint32_t)v[2 * l + 1])) << 16);
+          *(u2 *)(row + 8 * c) = h;
+        } else {
+          u4 h;
+#pragma unroll
+          for (int l = 0; l < 4; ++l)
+            h[l] = half(bf16_bits_to_f32(v[l] & 0xFFFFu)) |
+                   (half(__builtin_bit_cast(float, v[l] & 0xFFFF0000u)) << 16);
+          *(u4 *)(row + 16 * c) = h;
+        }
       }
     }
     __syncthreads();
     if (rl < rb0 || rl >= rb0 + rb) continue;  // lane-uniform per pass; no barrier below
-    const uint8_t *xrow = smem + (size_t)(rl - rb0) * stride;
-    const int ex = s_exp[rl];
-    auto get = [&](uint32_t at) __attribute__((always_inline)) {
-      float v;
-      if constexpr (GLU) v = ((const float *)xrow)[at];
-      else v = bf16_bits_to_f32(((const uint16_t *)xrow)[at]);
-      return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)ldexpf(v, ex));
-    };
-    for (int u = u0; u < U; u += USTEP) {
+    const uint16_t *xrow = (const uint16_t *)(smem + (size_t)(rl - rb0) * stride);
+    for (int pu = u0; pu < U * b.count; pu += USTEP) {
+      const int pc = pu >= U ? 1 : 0, u = pu - pc * U;  // at most two projections
+      const uint16_t *perm = (const uint16_t *)(tab.base[pc * sh.num_experts + e] + sh.off_perm);
+      uint8_t *xa = pc ? b.p[1].xa : b.p[0].xa;
       u4 pv[4];
 #pragma unroll
       for (int ci = 0; ci < 4; ++ci) pv[ci] = *(const u4 *)(perm + u * UNIT_SLOTS + 8 * (16 * ci + 4 * s + q));
@@ -190,26 +213,16 @@ __device__ __forceinline__ void prep_f16_rows(uint8_t *smem, const MoeSbProj &P,
       for (int ci = 0; ci < 4; ++ci) {
         u4 v;
 #pragma unroll
-        for (int l = 0; l < 4; ++l) v[l] = get(pv[ci][l] & 0xFFFFu) | (get(pv[ci][l] >> 16) << 16);
+        for (int l = 0; l < 4; ++l)
+          v[l] = (uint32_t)xrow[pv[ci][l] & 0xFFFFu] | ((uint32_t)xrow[pv[ci][l] >> 16] << 16);
         // perm entries are < k (zero past k); k is a multiple of 8, so eight
         // slots are inside k or all padding
         if (u * UNIT_SLOTS + 8 * (16 * ci + 4 * s + q) >= k) v = (u4){0u, 0u, 0u, 0u};
-        *(u4 *)(P.xa + moe_sb_xa_off(wi, U, u, g) + ((size_t)(4 * ci + q) * 64 + L) * 16) = v;
+        *(u4 *)(xa + moe_sb_xa_off(wi, U, u, g) + ((size_t)(4 * ci + q) * 64 + L) * 16) = v;
       }
     }
   }
 }
-template <bool ROUTE>
-__device__ __forceinline__ void prep_f16(uint8_t *smem, const MoeSbProj &P, const uint16_t *perm, int x_per_slot,
-                                         int topk, int vec, int wi, int g, int r0, int rows, const int32_t *lds_rows,
-                                         const int32_t *sorted, const MoeF16 &f, int pc, int e) {
-  const int xscale = f.xscale[pc * P.sh.num_experts + e];
-  if constexpr (ROUTE)
-    prep_f16_rows<false>(smem, P, perm, x_per_slot, topk, vec, wi, g, r0, rows, lds_rows, sorted, f, pc, xscale);
-  else
-    prep_f16_rows<true>(smem, P, perm, x_per_slot, topk, vec, wi, g, r0, rows, lds_rows, sorted, f, pc, xscale);
-}
-
 // Block (work item, row group g), MOE_SB_PREP_THREADS threads: the group's
 // 16 activation rows are staged whole in LDS (rb rows per pass, coalesced
 // 16-byte loads when x and ldx allow them; the row stride carries 16 bytes
@@ -223,7 +236,8 @@ __device__ __forceinline__ void prep_f16(uint8_t *smem, const MoeSbProj &P, cons
 // sorted slots for the product launch, block 0 the item count.
 // fa: nothing, or the MoeF16 of the fp16 form.
 template <bool ROUTE, typename... FA>
-__global__ __launch_bounds__(MOE_SB_PREP_THREADS) void moe_sb_prep_kernel(
+__global__ __launch_bounds__(MOE_SB_PREP_THREADS) __attribute__((amdgpu_waves_per_eu(sizeof...(FA) ? 8 : 4)))
+void moe_sb_prep_kernel(
     MoeSbBatch b, ExpertTable tab, int x_per_slot, int topk, MoeRoute route, int32_t *__restrict__ work,
     int32_t *__restrict__ nwork, int32_t *__restrict__ sorted, FA... fa) {
   constexpr bool F16 = sizeof...(FA) > 0;
@@ -353,8 +367,7 @@ __global__ __launch_bounds__(MOE_SB_PREP_THREADS) void moe_sb_prep_kernel(
   }
   const int U = sh.units, kp = U * UNIT_SLOTS, k = sh.k;
   if constexpr (F16) {
-    prep_f16<ROUTE>(smem, P, (const uint16_t *)(tab.base[pc * sh.num_experts + e] + sh.off_perm), x_per_slot, topk, vec,
-                    wi, g, r0, rows, ROUTE ? R.rows : nullptr, sorted, fa..., pc, e);
+    prep_f16_rows<!ROUTE>(smem, b, tab, e, topk, wi, g, r0, rows, ROUTE ? R.rows : nullptr, sorted, fa...);
     return;
   }
   const int stride = moe_sb_prep_stride(kp);  // bytes per staged row
@@ -747,7 +760,7 @@ hipError_t launch_moe_sb(MoeSbBatch &b, const ExpertTable &tab, int x_per_slot, 
 
 hipError_t launch_moe_sb_f16(MoeSbBatch &b, const ExpertTable &tab, int topk, const MoeRoute &route, int32_t *work,
                              int32_t *nwork, int32_t *sorted, int max_work, const MoeF16 &f, hipStream_t s) {
-  if (b.count < 1 || b.count > MOE_BATCH_MAX || route.slots > MOE_FUSED_MAX_SLOTS) return hipErrorInvalidValue;
+  if (b.count < 1 || b.count > 2 || route.slots > MOE_FUSED_MAX_SLOTS) return hipErrorInvalidValue;
   const bool glu = f.g != nullptr;
   if (glu != (route.ids == nullptr) || (glu && b.count != 1)) return hipErrorInvalidValue;
   size_t prep_lds = 0;
@@ -759,7 +772,7 @@ hipError_t launch_moe_sb_f16(MoeSbBatch &b, const ExpertTable &tab, int topk, co
     tgroups = std::max(tgroups, (b.p[c].sh.n_tiles + MOE_SB_TILES - 1) / MOE_SB_TILES);
   }
   if (prep_lds > GV_LDS_LIMIT - sizeof(MoeRouteLds) - 256) return hipErrorInvalidValue;
-  const dim3 pgrid(max_work * MOE_SB_G, b.count), pblock(MOE_SB_PREP_THREADS);
+  const dim3 pgrid(max_work * MOE_SB_G), pblock(MOE_SB_PREP_THREADS);
   hipError_t e;
   if (!glu) {
     e = allow_smem(moe_sb_prep_kernel<true, MoeF16>, prep_lds);
