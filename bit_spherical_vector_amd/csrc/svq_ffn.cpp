@@ -69,8 +69,11 @@ svq_status ffn_gemm(const svq_handle *const *w, int jobs, const void *x, int64_t
   a.ups = (units + want - 1) / want;
   a.splits = (units + a.ups - 1) / a.ups;
   const bool parts = bm == 64 || a.splits > 1;
-  // prep: rows per block as the bf16 path, chunk ranges for about 512 blocks
-  a.rpb = prefill_prep_rows(w[0]->k);
+  // prep: few rows per block (2 rows of 2560, 4096 and 9728 channels: 246, 77
+  // and 136 us a call at 2048 rows; 4: 247, 78, 138; 8: 249, 80, -), chunk
+  // ranges for about 512 blocks
+  a.rpb = 8;
+  while (a.rpb > 2 && prefill_prep_lds(a.rpb, w[0]->k) > 12 * 1024) a.rpb /= 2;
   const int rows = a.m_pad / a.rpb, nch = units * UNIT_SLOTS / 8;
   const int cs = (512 + rows - 1) / rows < nch / 64 ? (512 + rows - 1) / rows : nch / 64;
   a.csplit = cs < 1 ? 1 : cs;

@@ -79,16 +79,18 @@ static_assert(SB_SMEM <= 64 * 1024, "small-batch LDS");
 __device__ __forceinline__ u4 sb_lds(uint32_t addr) { return *(sb_lds_u4_t *)(size_t)addr; }
 
 // Table rows of the four codes (ci = 0..3) of MFMA group q: the hi and lo
-// halves of each code's exact split (32-byte rows by 10-bit index).
+// halves of each code's exact split (32-byte rows by 10-bit index).  HI: the
+// high halves alone, RNE_fp16(R*D*2^s), 16-byte rows.
+template <bool HI>
 __device__ __forceinline__ void sb_reads(uint32_t Lw, uint32_t H, const SbShifts &sh, u4 (&Dh)[4],
                                          u4 (&Dl)[4]) {
 #pragma unroll
   for (int ci = 0; ci < 4; ++ci) {
     const uint32_t lo = __builtin_amdgcn_ubfe(Lw, 8 * ci, 8);
     const uint32_t hi = __builtin_amdgcn_ubfe(H, sh.hi[ci], 2);
-    const uint32_t a = SB_OFF_XTAB + ((lo | (hi << 8)) << 5);
+    const uint32_t a = SB_OFF_XTAB + ((lo | (hi << 8)) << (HI ? 4 : 5));
     Dh[ci] = sb_lds(a);
-    Dl[ci] = sb_lds(a + 16);
+    Dl[ci] = HI ? Dh[ci] : sb_lds(a + 16);
   }
 }
 
@@ -96,6 +98,7 @@ __device__ __forceinline__ void sb_reads(uint32_t Lw, uint32_t H, const SbShifts
 // the record's sign dwords (S1:S0, S3:S2) by 4b0 + ci brings code
 // 4b0 + ci's pair signs to bits 15 and 31 of each dword (bits the shift
 // carries across the dword boundary land below bit 15 and are masked off).
+template <bool HI>
 __device__ __forceinline__ void sb_mul(uint64_t S01, uint64_t S23, const SbShifts &sh,
                                        const u4 (&Dh)[4], const u4 (&Dl)[4], const u4 (&A)[16], int q,
                                        f4 &C) {
@@ -106,34 +109,35 @@ __device__ __forceinline__ void sb_mul(uint64_t S01, uint64_t S23, const SbShift
     const uint32_t m0 = (uint32_t)c01 & SM, m1 = (uint32_t)(c01 >> 32) & SM;
     const uint32_t m2 = (uint32_t)c23 & SM, m3 = (uint32_t)(c23 >> 32) & SM;
     const u4 wh = {Dh[ci][0] ^ m0, Dh[ci][1] ^ m1, Dh[ci][2] ^ m2, Dh[ci][3] ^ m3};
-    const u4 wl = {Dl[ci][0] ^ m0, Dl[ci][1] ^ m1, Dl[ci][2] ^ m2, Dl[ci][3] ^ m3};
+    const u4 wl = {Dl[ci][0] ^ m0, Dl[ci][1] ^ m1, Dl[ci][2] ^ m2, Dl[ci][3] ^ m3};  // HI: unused
     const h8 a = __builtin_bit_cast(h8, A[4 * ci + q]);
     C = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(h8, wh), C, 0, 0, 0);
-    C = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(h8, wl), C, 0, 0, 0);
+    if constexpr (!HI) C = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(h8, wl), C, 0, 0, 0);
   }
 }
 
 // One unit of one row tile: the 16 codes of the lane, 16 MFMAs.
+template <bool HI>
 __device__ __forceinline__ f4 sb_item(const SbCodes &c, const u4 (&A)[16], const SbShifts &sh) {
   f4 C0 = {0.f, 0.f, 0.f, 0.f}, C1 = {0.f, 0.f, 0.f, 0.f};
   u4 H0[4], L0[4], H1[4], L1[4];
   auto s01 = [&](int q) { return (uint64_t)c.S[q][0] | ((uint64_t)c.S[q][1] << 32); };
   auto s23 = [&](int q) { return (uint64_t)c.S[q][2] | ((uint64_t)c.S[q][3] << 32); };
   // the table reads of group q + 1 are in flight while group q is multiplied
-  sb_reads(c.L[0], c.H[0], sh, H0, L0);
-  sb_reads(c.L[1], c.H[1], sh, H1, L1);
+  sb_reads<HI>(c.L[0], c.H[0], sh, H0, L0);
+  sb_reads<HI>(c.L[1], c.H[1], sh, H1, L1);
   __builtin_amdgcn_sched_barrier(0);
-  sb_mul(s01(0), s23(0), sh, H0, L0, A, 0, C0);
+  sb_mul<HI>(s01(0), s23(0), sh, H0, L0, A, 0, C0);
   __builtin_amdgcn_sched_barrier(0);
-  sb_reads(c.L[2], c.H[2], sh, H0, L0);
+  sb_reads<HI>(c.L[2], c.H[2], sh, H0, L0);
   __builtin_amdgcn_sched_barrier(0);
-  sb_mul(s01(1), s23(1), sh, H1, L1, A, 1, C1);
+  sb_mul<HI>(s01(1), s23(1), sh, H1, L1, A, 1, C1);
   __builtin_amdgcn_sched_barrier(0);
-  sb_reads(c.L[3], c.H[3], sh, H1, L1);
+  sb_reads<HI>(c.L[3], c.H[3], sh, H1, L1);
   __builtin_amdgcn_sched_barrier(0);
-  sb_mul(s01(2), s23(2), sh, H0, L0, A, 2, C0);
+  sb_mul<HI>(s01(2), s23(2), sh, H0, L0, A, 2, C0);
   __builtin_amdgcn_sched_barrier(0);
-  sb_mul(s01(3), s23(3), sh, H1, L1, A, 3, C1);
+  sb_mul<HI>(s01(3), s23(3), sh, H1, L1, A, 3, C1);
   return C0 + C1;
 }
 
@@ -151,7 +155,10 @@ __device__ __forceinline__ const uint8_t *sb_unit(const MatView &w, int t, int u
 // last of all to arrive finishes the pair.  (The body stands in the
 // kernel itself: behind a function call the job records, indexed at run time,
 // would be copied out of the kernel arguments.)
-template <typename... EA>
+// HI: with the weights' high halves only (RNE_fp16, 2^-12 a weight at most:
+// an eighth of a bf16 output's own half step; for calls that round to bf16).
+// Half the table reads, which bound the loop, and half the MFMAs.
+template <bool HI, typename... EA>
 __global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b, EA... ea) {
   const auto epi = make_epi(ea...);
   const int jn = find_job(b.starts, b.count);
@@ -180,10 +187,11 @@ __global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b, EA... ea) {
 
   // the bf16 table (requested first), the activation fragments of the
   // run's first unit and the codes of its first two items
-  u4 bt[XTAB_BYTES / 4096];
+  constexpr int NBT = XTAB_BYTES / 4096 / (HI ? 2 : 1);
+  u4 bt[NBT];
   const u4 *gbt = (const u4 *)(w.base + w.off_xtab);
 #pragma unroll
-  for (int i = 0; i < XTAB_BYTES / 4096; ++i) bt[i] = gbt[tid + 256 * i];
+  for (int i = 0; i < NBT; ++i) bt[i] = gbt[HI ? 2 * (tid + 256 * i) : tid + 256 * i];
   __builtin_amdgcn_sched_barrier(0);
   u4 A[16];
   f4 xsc;  // inverse activation scales of the lane's accumulator rows 4s..4s+3
@@ -205,7 +213,7 @@ __global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b, EA... ea) {
   for (int t = 0; t < SB_TMAX; ++t)
     *(sb_lds_u4w_t *)(size_t)(slot0 + t * 1024) = (u4){0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int i = 0; i < XTAB_BYTES / 4096; ++i)
+  for (int i = 0; i < NBT; ++i)
     *(sb_lds_u4w_t *)(size_t)(SB_OFF_XTAB + 16 * (tid + 256 * i)) = bt[i];
   __syncthreads();
 
@@ -219,7 +227,7 @@ __global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b, EA... ea) {
       for (int f = 0; f < 16; ++f) A[f] = xa[64 * f];
       xsc = *(const f4 *)(J.xs + (size_t)(u0 + ui) * 16 + 4 * s);
     }
-    const f4 C = sb_item(cd[k & 1], A, sh) * xsc;
+    const f4 C = sb_item<HI>(cd[k & 1], A, sh) * xsc;
     if (k + 2 < nk) {
       const int i2 = i0 + k + 2, u2 = i2 / tn;
       cd[k & 1] = sb_load_codes(sb_unit(w, t0 + i2 - u2 * tn, u0 + u2), offs);
@@ -511,12 +519,18 @@ hipError_t launch_sb(SbBatch &b, int prep_blocks, int blocks, hipStream_t s) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (b.pair)
-    hipLaunchKernelGGL(sb_gemm_kernel<PairArgs>, dim3(blocks), dim3(256), SB_SMEM, s, b, *b.pair);
+  const dim3 grid(blocks), block(256);
+  const bool hi = b.ydt == 0;
+  if (b.pair && hi)
+    hipLaunchKernelGGL((sb_gemm_kernel<true, PairArgs>), grid, block, SB_SMEM, s, b, *b.pair);
+  else if (b.pair)
+    hipLaunchKernelGGL((sb_gemm_kernel<false, PairArgs>), grid, block, SB_SMEM, s, b, *b.pair);
+  else if (b.epi && hi)
+    hipLaunchKernelGGL((sb_gemm_kernel<true, EpiArgs>), grid, block, SB_SMEM, s, b, *b.epi);
   else if (b.epi)
-    hipLaunchKernelGGL(sb_gemm_kernel<EpiArgs>, dim3(blocks), dim3(256), SB_SMEM, s, b, *b.epi);
+    hipLaunchKernelGGL((sb_gemm_kernel<false, EpiArgs>), grid, block, SB_SMEM, s, b, *b.epi);
   else
-    hipLaunchKernelGGL(sb_gemm_kernel<>, dim3(blocks), dim3(256), SB_SMEM, s, b);
+    hipLaunchKernelGGL(sb_gemm_kernel<false>, grid, block, SB_SMEM, s, b);
   return hipGetLastError();
 }
 

@@ -7,7 +7,9 @@
  * and validates what it is given; calls that share a workspace must be
  * ordered on one stream; nothing is kept from one call for the next).
  *
- * Numerics.  Up to 16 rows products are those of svq.h.  Beyond, weights
+ * Numerics.  Up to 16 rows products are those of svq.h, except that calls of
+ * 5..16 rows that round to bf16 take weights as fp16 (R*D rounded to 11 bits
+ * under the matrix's power-of-two scale).  Beyond 16 rows weights
  * enter the matrix cores as fp16 (R*D rounded to 11 bits under the matrix's
  * power-of-two scale) and activations as fp16 after a power-of-two scale per
  * row (a bf16 value keeps its bits down to 2^-29 of the row's largest finite

@@ -5,8 +5,8 @@ torch.finfo(t).eps / 2 of the value):
 
 * a product of k terms: |p - p64| <= P * S + 1e-6 with S = sum |What||x|;
   accumulation in fp32 costs at most one rounding per term (k + 64 of 2^-24,
-  64 for the joins of partial sums), and for more than 16 rows the weights
-  are rounded to fp16 first (2^-11; a weight so small beside its matrix's
+  64 for the joins of partial sums), and for more than 16 rows, and from 5
+  rows on for a bf16 output, the weights are rounded to fp16 first (2^-11; a weight so small beside its matrix's
   largest that it is subnormal there keeps an error of 2^-39 of that one);
 * an activation's slope is at most 1.13 (silu 1.0998, gelu 1.129), so an
   error e of its argument becomes at most 1.13 e, plus a few fp32 roundings
@@ -93,8 +93,8 @@ def test_epilogue(svq, n, k, bd, m, kind):
     mat = synth.random_matrix(n, k, bd, seed=(70, n, k))
     x_bits = synth.random_activations(m, k, seed=(71, n, m))
     pm, x = svq.pack(mat), to_device_bf16(x_bits)
-    p, pb = product(mat, x_bits, m > 16)
     out = (torch.float32, torch.bfloat16, torch.bfloat16)[kind]
+    p, pb = product(mat, x_bits, m > (4 if kind else 16))
     bias = (None, vec(n, torch.float32, 1), vec(n, torch.bfloat16, 2))[kind]
     res = (vec(m * n, torch.bfloat16, 3).view(m, n), None, vec(m * n, torch.float32, 4).view(m, n))[kind]
     for act in ACTS:
@@ -120,7 +120,7 @@ def test_epilogue_strided_operands_and_neighbours(svq, m):
     y = wide[1:m + 1, 3:3 + n]
     r = f64(y)
     svq.linear_epilogue(svq.pack(mat), xw[:, 5:5 + k], residual=y, out=y)
-    p, pb = product(mat, x_bits, m > 16)
+    p, pb = product(mat, x_bits, m > 4)
     check(y, p + r, pb + U32 * (np.abs(p) + np.abs(r)), f"in place m={m}")
     wide[1:m + 1, 3:3 + n] = before[1:m + 1, 3:3 + n]
     assert torch.equal(wide, before)
@@ -186,9 +186,9 @@ def test_glu(svq, n, k, m, bds):
     x_bits = synth.random_activations(m, k, seed=(76, n, m))
     x = to_device_bf16(x_bits)
     pg, pu = [svq.pack(a) for a in mats]
-    (g, gb), (u, ub) = [product(a, x_bits, m > 16) for a in mats]
     for act, bt, out in (("silu", None, torch.bfloat16), ("gelu_tanh", torch.float32, torch.float32),
                          ("none", torch.bfloat16, torch.bfloat16)):
+        (g, gb), (u, ub) = [product(a, x_bits, m > (4 if out == torch.bfloat16 else 16)) for a in mats]
         bg = None if bt is None else vec(n, bt, 7)
         bu = None if bt is None or act == "none" else vec(n, bt, 8)
         y = svq.linear_glu(pg, pu, x, act=act, bias_gate=bg, bias_up=bu, out_dtype=out)
@@ -375,12 +375,12 @@ def test_run_of_them_together(svq, m):
     x = to_device_bf16(x_bits)
     bits = lambda t: t.view(torch.int16).cpu().numpy().view(np.uint16)
     h = svq.linear_glu(pms[0], pms[1], x)
-    (g, gb), (u, ub) = [product(a, x_bits, m > 16) for a in mats[:2]]
+    (g, gb), (u, ub) = [product(a, x_bits, m > 4) for a in mats[:2]]
     a = act64(g, "silu")
     ea = SLOPE * gb + 16 * U32 * np.abs(a)
     check(h, a * u, ea * np.abs(u) + ub * np.abs(a) + ea * ub + U32 * np.abs(a * u), "glu")
     x1 = svq.linear_epilogue(pms[2], h, residual=x)
-    p, pb = product(mats[2], bits(h), m > 16)
+    p, pb = product(mats[2], bits(h), m > 4)
     check(x1, p + f64(x), pb + U32 * (np.abs(p) + np.abs(f64(x))), "down")
     ids, wt = svq.moe_route(x1, pms[3], 2)
     rid, rwt = route64(x1, pms[3], 2, "softmax", True, 1.0, None)
