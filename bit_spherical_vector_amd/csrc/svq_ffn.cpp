@@ -56,10 +56,13 @@ svq_status ffn_gemm(const svq_handle *const *w, int jobs, const void *x, int64_t
                     void *stream) {
   FfnGemmArgs a;
   std::memset(&a, 0, sizeof(a));
-  const int bm = prefill_bm((int)m);
+  // 64-row tiles up to two of them; padding to one 256-row tile costs less
+  // from there on
+  const int bm = m > 128 ? 256 : 64;
   a.jobs = jobs;
   a.m = (int)m;
-  a.m_pad = prefill_m_pad((int)m);
+  a.bm = bm;
+  a.m_pad = (int)((m + bm - 1) / bm) * bm;
   a.tiles_m = a.m_pad / bm;
   a.tiles_n = prefill_tiles_n(w[0]->n_tiles);
   a.n_pad = a.tiles_n * PREFILL_BN;
@@ -395,7 +398,7 @@ svq_status svq_moe_route(const void *x, int64_t m, int64_t ldx, const void *w, s
   a.ids = ids;
   a.weights = weights;
   a.logits = (double *)workspace;
-  return launch_route(a, (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
+  return launch_route(a, compute_units(), (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
 }
 
 svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_handle *down,

@@ -56,7 +56,7 @@ hipError_t launch_combine(const CombineArgs &a, hipStream_t s);
 
 // ---- beyond 16 rows --------------------------------------------------------
 // One matrix with its epilogue, or a gated pair (job 0 the gate), on the
-// 256 x 256 tile (m >= PREFILL_MIN_M) or the 64 x 256 tile.
+// 256 x 256 tile (bm 256) or the 64 x 256 tile.
 struct FfnGemmJob {
   MatView w;
   uint16_t *xb;  // fp16 activations in fragment order (workspace)
@@ -65,7 +65,7 @@ struct FfnGemmJob {
 };
 struct FfnGemmArgs {
   FfnGemmJob job[2];
-  int32_t jobs, m, m_pad, tiles_m, tiles_n, n_pad, splits, ups;
+  int32_t jobs, m, bm, m_pad, tiles_m, tiles_n, n_pad, splits, ups;
   int32_t rpb, csplit;  // prep: rows per block, chunk ranges
   const uint16_t *x;
   int64_t ldx;
@@ -97,7 +97,7 @@ struct MoeFfnArgs {
   void *y;
   int64_t ldy;
 };
-// The per-slot form: at most 64 slots whose rows fit a block's LDS.
+// The per-slot form: few slots (see there) whose rows fit a block's LDS.
 bool moe_ffn_few_fits(const svq_handle *gate, const svq_handle *up, const svq_handle *down, int32_t num_experts,
                       int64_t slots);
 // ws null: only *need.
@@ -121,6 +121,6 @@ struct RouteArgs {
   float *weights;
   double *logits;  // [m][num_experts] (workspace)
 };
-hipError_t launch_route(const RouteArgs &a, hipStream_t s);
+hipError_t launch_route(const RouteArgs &a, int cus, hipStream_t s);
 
 }  // namespace svq

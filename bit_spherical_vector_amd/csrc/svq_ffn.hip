@@ -179,52 +179,78 @@ __global__ __launch_bounds__(256) void moe_logits_few_kernel(RouteArgs a) {
   }
 }
 
-// Many tokens: a block of 16 waves takes 16 tokens x 16 experts, each wave
-// every 16th chunk of 32 channels through v_mfma_f64_16x16x4_f64 (element j
+// Many tokens: a block of W waves takes 16 N tokens x 16 N experts, each wave
+// every W-th chunk of 32 channels through v_mfma_f64_16x16x4_f64 (element l
 // of the eight channels a lane loads is one MFMA: its four k indices are
-// channels 8g + j of the lane groups g), then the waves' tiles are summed in
-// wave order.
+// channels 8g + l of the lane groups g), then the waves' tiles are summed in
+// wave order.  One tile and 16 waves fill the chip from few tokens; 2 x 2
+// tiles convert each value once for two MFMAs, for many.
 typedef double d4 __attribute__((ext_vector_type(4)));
-constexpr int RT_WAVES = 16;
-template <bool WF32>
-__global__ __launch_bounds__(RT_WAVES * 64) void moe_logits_kernel(RouteArgs a) {
-  __shared__ double s_red[RT_WAVES][256];
+template <int N, int W, bool WF32>
+__global__ __launch_bounds__(W * 64) void moe_logits_kernel(RouteArgs a) {
+  __shared__ double s_red[W][N * N * 256];
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int k = a.k, e0 = (int)blockIdx.x * 16;
-  const int64_t t0 = (int64_t)blockIdx.y * 16;
+  const int k = a.k, e0 = (int)blockIdx.x * 16 * N;
+  const int64_t t0 = (int64_t)blockIdx.y * 16 * N;
   const bool vec = a.vec != 0;
-  const uint16_t *xr = a.x + min(t0 + i, a.m - 1) * a.ldx;
-  const char *wr = (const char *)a.w + (size_t)min(e0 + i, a.num_experts - 1) * a.ldw * (WF32 ? 4 : 2);
-  d4 c = {0.0, 0.0, 0.0, 0.0};
-  constexpr int B = 4;  // chunks in flight
-  for (int c0 = 32 * wv; c0 < k; c0 += 32 * RT_WAVES * B) {
-    RtRow<WF32> w[B];
-    RtRow<false> x[B];
+  const uint16_t *xr[N];
+  const char *wr[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    xr[n] = a.x + min(t0 + 16 * n + i, a.m - 1) * a.ldx;
+    wr[n] = (const char *)a.w + (size_t)min(e0 + 16 * n + i, a.num_experts - 1) * a.ldw * (WF32 ? 4 : 2);
+  }
+  d4 c[N][N];
+#pragma unroll
+  for (int p = 0; p < N; ++p)
+#pragma unroll
+    for (int q = 0; q < N; ++q) c[p][q] = (d4){0.0, 0.0, 0.0, 0.0};
+  constexpr int B = 4 / N;  // chunks in flight
+  for (int c0 = 32 * wv; c0 < k; c0 += 32 * W * B) {
+    RtRow<WF32> w[B][N];
+    RtRow<false> x[B][N];
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        x[b][n] = rt_load<false>(xr[n], c0 + 32 * W * b + 8 * g, k, vec);
+        w[b][n] = rt_load<WF32>(wr[n], c0 + 32 * W * b + 8 * g, k, vec);
+      }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      x[b] = rt_load<false>(xr, c0 + 32 * RT_WAVES * b + 8 * g, k, vec);
-      w[b] = rt_load<WF32>(wr, c0 + 32 * RT_WAVES * b + 8 * g, k, vec);
-    }
+      if (c0 + 32 * W * b >= k) break;  // wave-uniform
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      if (c0 + 32 * RT_WAVES * b >= k) break;  // wave-uniform
+      for (int l = 0; l < 8; ++l) {
+        double xd[N], wd[N];
 #pragma unroll
-      for (int l = 0; l < 8; ++l)
-        c = __builtin_amdgcn_mfma_f64_16x16x4f64(rt_get<false>(x[b], l), rt_get<WF32>(w[b], l), c, 0, 0, 0);
+        for (int n = 0; n < N; ++n) {
+          xd[n] = rt_get<false>(x[b][n], l);
+          wd[n] = rt_get<WF32>(w[b][n], l);
+        }
+#pragma unroll
+        for (int p = 0; p < N; ++p)
+#pragma unroll
+          for (int q = 0; q < N; ++q) c[p][q] = __builtin_amdgcn_mfma_f64_16x16x4f64(xd[p], wd[q], c[p][q], 0, 0, 0);
+      }
     }
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r) s_red[wv][64 * r + lane] = c[r];
-  __syncthreads();
-  if (tid >= 256) return;
-  double v = 0.0;
+  for (int p = 0; p < N; ++p)
 #pragma unroll
-  for (int w = 0; w < RT_WAVES; ++w) v += s_red[w][tid];
-  // accumulator register r of lane 16 g + i: token g + 4 r, expert i
-  const int64_t t = t0 + ((tid >> 4) & 3) + 4 * (tid >> 6);
-  const int e = e0 + (tid & 15);
-  if (t < a.m && e < a.num_experts) a.logits[t * a.num_experts + e] = v;
+    for (int q = 0; q < N; ++q)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s_red[wv][(p * N + q) * 256 + 64 * r + lane] = c[p][q][r];
+  __syncthreads();
+  for (int o = tid; o < N * N * 256; o += W * 64) {
+    double v = 0.0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) v += s_red[w][o];
+    // accumulator register r of lane 16 g + i: token g + 4 r, expert i
+    const int64_t t = t0 + 16 * ((o >> 8) / N) + ((o >> 4) & 3) + 4 * ((o >> 6) & 3);
+    const int e = e0 + 16 * ((o >> 8) % N) + (o & 15);
+    if (t < a.m && e < a.num_experts) a.logits[t * a.num_experts + e] = v;
+  }
 }
 
 // Order-preserving integer of a key: NaN below every number, -0 equal to +0.
@@ -236,10 +262,11 @@ __device__ __forceinline__ int64_t rt_order(double key) {
 
 // The choice of one token: an expert's place is the number of experts before
 // it (larger key, or equal key and lower index), so all places are found at
-// once and no place waits for the one before.  Thread e of each quarter of
-// the block counts a quarter of the experts for expert e; the first quarter
-// holds the scores.
-constexpr int TK_PARTS = 4;
+// once and no place waits for the one before.  Thread e of each part of the
+// block counts a part of the experts for expert e; the first part holds the
+// scores.  Four parts while all blocks are resident at once (one token:
+// 3.4 us against 5.7 with one part; 512: 4.8 against 7.5), one beyond.
+template <int TK_PARTS>
 __global__ __launch_bounds__(TK_PARTS * MAX_EXPERTS) void moe_topk_kernel(RouteArgs a) {
   constexpr int W = MAX_EXPERTS / 64;
   __shared__ double s_mx[W], s_sum[W], s_p[ROUTE_MAX_TOPK];
@@ -320,26 +347,35 @@ __global__ __launch_bounds__(TK_PARTS * MAX_EXPERTS) void moe_topk_kernel(RouteA
   }
 }
 
+template <int N, int W, bool WF32>
+static void launch_logit_tiles(const RouteArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL((moe_logits_kernel<N, W, WF32>),
+                     dim3((unsigned)((a.num_experts + 16 * N - 1) / (16 * N)), (unsigned)((a.m + 16 * N - 1) / (16 * N))),
+                     dim3(W * 64), 0, s, a);
+}
 template <bool WF32>
-static void launch_logits(const RouteArgs &a, hipStream_t s) {
+static void launch_logits(const RouteArgs &a, int cus, hipStream_t s) {
   const unsigned eb = (unsigned)((a.num_experts + 3) / 4);
   if (a.m == 1)
     hipLaunchKernelGGL((moe_logits_few_kernel<1, WF32>), dim3(eb), dim3(256), 0, s, a);
   else if (a.m <= ROUTE_FEW)
     hipLaunchKernelGGL((moe_logits_few_kernel<RT_TOKENS, WF32>),
                        dim3(eb, (unsigned)((a.m + RT_TOKENS - 1) / RT_TOKENS)), dim3(256), 0, s, a);
+  else if ((a.m + 31) / 32 * ((a.num_experts + 31) / 32) < cus)  // one 2 x 2 block per compute unit at least
+    launch_logit_tiles<1, 16, WF32>(a, s);
   else
-    hipLaunchKernelGGL(moe_logits_kernel<WF32>,
-                       dim3((unsigned)((a.num_experts + 15) / 16), (unsigned)((a.m + 15) / 16)),
-                       dim3(RT_WAVES * 64), 0, s, a);
+    launch_logit_tiles<2, 8, WF32>(a, s);
 }
 
-hipError_t launch_route(const RouteArgs &a, hipStream_t s) {
-  if (a.w_f32) launch_logits<true>(a, s);
-  else launch_logits<false>(a, s);
+hipError_t launch_route(const RouteArgs &a, int cus, hipStream_t s) {
+  if (a.w_f32) launch_logits<true>(a, cus, s);
+  else launch_logits<false>(a, cus, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_topk_kernel, dim3((unsigned)a.m), dim3(TK_PARTS * MAX_EXPERTS), 0, s, a);
+  if (a.m <= 2 * (int64_t)cus)
+    hipLaunchKernelGGL(moe_topk_kernel<4>, dim3((unsigned)a.m), dim3(4 * MAX_EXPERTS), 0, s, a);
+  else
+    hipLaunchKernelGGL(moe_topk_kernel<1>, dim3((unsigned)a.m), dim3(MAX_EXPERTS), 0, s, a);
   return hipGetLastError();
 }
 

@@ -1411,7 +1411,7 @@ static hipError_t ffn_launch(K kernel, int blocks, int threads, size_t smem, con
 }
 
 hipError_t launch_ffn_gemm(const FfnGemmArgs &a, bool xvec, hipStream_t s) {
-  const int bm = prefill_bm(a.m);
+  const int bm = a.bm;
   const size_t lds = prefill_prep_lds(a.rpb, a.job[0].w.k);
   if (lds + 64 > GV_LDS_LIMIT) return hipErrorInvalidValue;
   const int rblocks = (a.m_pad / 32 + 7) / 8 * 8;  // 32-row blocks, padded to the XCDs

@@ -18,9 +18,10 @@
  * activation, gating, residual and the sum over a token's experts are fp32;
  * each output is rounded once, to nearest even.  The inner activation of an
  * expert layer (act(gate) * up) enters the down product as fp16 (11
- * significant bits) after a power-of-two scale: up to 64 slots (m * topk)
- * one per 512 permuted channels, beyond one per row, and there all three
- * products run in the form for more than 16 rows.
+ * significant bits) after a power-of-two scale: for few slots
+ * (m * topk up to 64 or 5/4 num_experts) one per 512 permuted channels, beyond
+ * one per row, and there all three products run in the form for more than 16
+ * rows.
  */
 #ifndef SVQ_FFN_H
 #define SVQ_FFN_H
