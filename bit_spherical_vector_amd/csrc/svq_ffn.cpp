@@ -9,6 +9,13 @@
 
 using namespace svq;
 
+namespace svq {
+size_t glu_fused_smem(int k, int units, int bd_gate, int bd_up, int R) {
+  const size_t g = gf_lds(bd_gate, k, units, 1, R).total, u = gf_lds(bd_up, k, units, 1, R).total;
+  return g <= (size_t)GLU_HALF && GLU_HALF + u <= GV_LDS_LIMIT ? GLU_HALF + u : 0;
+}
+}  // namespace svq
+
 namespace {
 
 bool valid_dt(svq_dtype t) { return t == SVQ_BF16 || t == SVQ_F32; }
@@ -18,6 +25,9 @@ bool aligned(const void *p, int64_t row_elems, size_t esz, size_t to) {
   return (((uintptr_t)p) | ((uintptr_t)row_elems * esz)) % to == 0;
 }
 int64_t pad4(int64_t n) { return (n + 3) / 4 * 4; }
+// Workspace regions start at multiples of 256 bytes from its base and are
+// read in 16-byte pieces.
+bool bad_workspace(const void *ws) { return ((uintptr_t)ws & 15) != 0; }
 
 bool has_split(const svq_handle *w) {
   return w->xscale_log2 != SVQ_NO_EXACT_SPLIT && w->xscale_log2 >= -120 && w->xscale_log2 <= 120;
@@ -66,6 +76,7 @@ svq_status ffn_gemm(const svq_handle *const *w, int jobs, const void *x, int64_t
   a.tiles_m = a.m_pad / bm;
   a.tiles_n = prefill_tiles_n(w[0]->n_tiles);
   a.n_pad = a.tiles_n * PREFILL_BN;
+  if ((int64_t)a.tiles_m * a.tiles_n > (1 << 28)) return SVQ_ERR_UNSUPPORTED;  // tile indexes are 32-bit
   const int units = w[0]->units, tiles = a.tiles_m * a.tiles_n;
   const double part_mb = (double)jobs * a.m_pad * a.n_pad * 4e-6;
   const int want = gemm_splits(tiles * jobs, units, bm, part_mb);
@@ -238,7 +249,7 @@ extern "C" {
 svq_status svq_linear_epilogue(const svq_handle *w, const void *x, int64_t m, int64_t ldx,
                                const svq_epilogue *ep, void *y, int64_t ldy, svq_dtype ydt,
                                void *workspace, size_t *workspace_bytes, void *stream) {
-  if (!w || !ep || !workspace_bytes) return SVQ_ERR_INVALID_ARG;
+  if (!w || !ep || !workspace_bytes || bad_workspace(workspace)) return SVQ_ERR_INVALID_ARG;
   const svq_status st = check_handle(w);
   if (st != SVQ_OK) return st;
   if (!valid_act(ep->act) || (ep->bias && !valid_dt(ep->bias_dt))) return SVQ_ERR_INVALID_ARG;
@@ -268,7 +279,7 @@ svq_status svq_linear_glu(const svq_handle *gate, const svq_handle *up, const vo
                           int64_t ldx, svq_act act, const void *bias_gate, const void *bias_up,
                           svq_dtype bias_dt, void *y, int64_t ldy, svq_dtype ydt,
                           void *workspace, size_t *workspace_bytes, void *stream) {
-  if (!gate || !up || !workspace_bytes) return SVQ_ERR_INVALID_ARG;
+  if (!gate || !up || !workspace_bytes || bad_workspace(workspace)) return SVQ_ERR_INVALID_ARG;
   svq_status st = check_handle(gate);
   if (st == SVQ_OK) st = check_handle(up);
   if (st != SVQ_OK) return st;
@@ -363,7 +374,7 @@ svq_status svq_moe_route(const void *x, int64_t m, int64_t ldx, const void *w, s
                          svq_route_score score, int32_t renormalize, float scale, int32_t topk,
                          int32_t *ids, float *weights, void *workspace, size_t *workspace_bytes,
                          void *stream) {
-  if (!workspace_bytes) return SVQ_ERR_INVALID_ARG;
+  if (!workspace_bytes || bad_workspace(workspace)) return SVQ_ERR_INVALID_ARG;
   if (num_experts < 1 || num_experts > MAX_EXPERTS) return SVQ_ERR_UNSUPPORTED;
   if (topk < 1 || topk > num_experts) return SVQ_ERR_INVALID_ARG;
   if (topk > ROUTE_MAX_TOPK) return SVQ_ERR_UNSUPPORTED;
@@ -407,7 +418,7 @@ svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_h
                        const void *residual, int64_t ldr, svq_dtype residual_dt, void *y,
                        int64_t ldy, svq_dtype ydt, void *workspace, size_t *workspace_bytes,
                        void *stream) {
-  if (!gate || !up || !down || !workspace_bytes) return SVQ_ERR_INVALID_ARG;
+  if (!gate || !up || !down || !workspace_bytes || bad_workspace(workspace)) return SVQ_ERR_INVALID_ARG;
   if (num_experts < 1 || num_experts > MAX_EXPERTS) return SVQ_ERR_UNSUPPORTED;
   if (topk < 1 || topk > num_experts || m < 1 || m > (1 << 20)) return SVQ_ERR_INVALID_ARG;
   if (!valid_act(act) || !valid_dt(ydt)) return SVQ_ERR_INVALID_ARG;
@@ -426,7 +437,11 @@ svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_h
   bool split = true;
   for (int c = 0; c < 3 && !few; ++c)
     for (int32_t e = 0; e < num_experts; ++e) split = split && has_split(&sets[c][e]);
-  if (few || split) {
+  const bool grouped = split && down->k <= MOE_GROUPED_MAX_INNER;
+  // what is left runs as separate products, which need more slots than the
+  // per-slot launch takes
+  if (!few && !grouped && S <= 64) return SVQ_ERR_UNSUPPORTED;
+  if (few || grouped) {
     MoeFfnArgs fa;
     std::memset(&fa, 0, sizeof(fa));
     fa.gate = gate;

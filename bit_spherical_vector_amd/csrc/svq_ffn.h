@@ -27,6 +27,7 @@ struct GluArgs {
 hipError_t launch_glu(const GluArgs &a, hipStream_t s);
 
 // One row through both matrices in one launch (R row tiles per block).
+constexpr int GLU_HALF = 65536;  // LDS offset of the second matrix's half of a block
 struct GluFusedArgs {
   MatView gate, up;
   const uint16_t *x;
@@ -35,7 +36,7 @@ struct GluFusedArgs {
   void *y;
   int32_t ydt, R;
 };
-size_t glu_fused_smem(int k, int units, int bd_gate, int bd_up, int R);  // 0: does not fit
+size_t glu_fused_smem(int k, int units, int bd_gate, int bd_up, int R);  // LDS, or 0: does not fit
 hipError_t launch_glu_fused(const GluFusedArgs &a, hipStream_t s);
 
 struct CombineArgs {
@@ -102,7 +103,9 @@ bool moe_ffn_few_fits(const svq_handle *gate, const svq_handle *up, const svq_ha
                       int64_t slots);
 // ws null: only *need.
 hipError_t launch_moe_ffn_few(const MoeFfnArgs &f, void *ws, size_t *need, hipStream_t s);
-// The grouped form; every matrix has an exact split.
+// The grouped form; every matrix has an exact split and the inner width is at
+// most MOE_GROUPED_MAX_INNER (its rows are staged in LDS as fp32).
+constexpr int MOE_GROUPED_MAX_INNER = 36 * 1024;
 hipError_t launch_moe_ffn_grouped(const MoeFfnArgs &f, void *ws, size_t *need, hipStream_t s);
 
 // ---- router --------------------------------------------------------------------

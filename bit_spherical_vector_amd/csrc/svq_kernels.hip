@@ -1265,8 +1265,6 @@ hipError_t launch_gemv_fused(GemvBatch &b, int blocks, size_t smem, hipStream_t 
 // its own part of LDS; the sums meet in LDS, so nothing goes through memory
 // and no block waits for another.  8 waves per compute unit is what two
 // blocks of the plain launch put there for such sizes.
-constexpr int GLU_HALF = 65536;  // LDS offset of the second half
-
 // Sums of the block's rows, kept in LDS.
 struct LdsEpi {
   static constexpr bool on = true, partial = true;
@@ -1307,12 +1305,6 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void g
     if (a.bias_u) uv += load_f(a.bias_u, n, a.bias_f32);
     store_out(a.y, n, act_apply(gv, a.act) * uv, a.ydt);
   }
-}
-
-// LDS of the launch, or 0 when the pair does not fit.
-size_t glu_fused_smem(int k, int units, int bd_gate, int bd_up, int R) {
-  const size_t g = gf_lds(bd_gate, k, units, 1, R).total, u = gf_lds(bd_up, k, units, 1, R).total;
-  return g <= (size_t)GLU_HALF && GLU_HALF + u <= GV_LDS_LIMIT ? GLU_HALF + u : 0;
 }
 
 hipError_t launch_glu_fused(const GluFusedArgs &a, hipStream_t s) {

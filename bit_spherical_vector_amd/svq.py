@@ -674,6 +674,14 @@ def _vector_arg(t, what: str, n: int, device, dtype=None) -> None:
         raise ValueError(f"{what} must be {dtype}")
 
 
+def _matrices_on(device, *sets) -> None:
+    """Checks that packed matrices lie on the operands' device."""
+    for pms in sets:
+        for pm in pms:
+            if pm.buf is not None and pm.buf.device != device:
+                raise ValueError(f"a packed matrix is on {pm.buf.device}, not on {device}")
+
+
 def _choice(name: str, names, what: str) -> int:
     if name not in names:
         raise ValueError(f"{what} must be one of {', '.join(names)}")
@@ -735,6 +743,7 @@ class EpilogueCall(_Call):
                  stream=None):
         import torch
         m, dev = x.shape[0], x.device
+        _matrices_on(dev, (pm,))
         ldx = _matrix_arg(x, "x", m, pm.k, dev, (torch.bfloat16,))
         ldy = _matrix_arg(y, "y", m, pm.n, dev, (torch.bfloat16, torch.float32))
         ep = Epilogue(act=_choice(act, ACTIVATIONS, "act"))
@@ -764,6 +773,7 @@ class GluCall(_Call):
                  bias_up=None, workspace=None, stream=None):
         import torch
         m, dev = x.shape[0], x.device
+        _matrices_on(dev, (pm_gate, pm_up))
         ldx = _matrix_arg(x, "x", m, pm_gate.k, dev, (torch.bfloat16,))
         ldy = _matrix_arg(y, "y", m, pm_gate.n, dev, (torch.bfloat16, torch.float32))
         kinds = []
@@ -821,6 +831,7 @@ class MoeFfnCall(_Call):
             raise ValueError("gates, ups and downs must be sequences of one length")
         (m, topk), dev = expert_ids.shape, x.device
         k, n = gates[0].k, downs[0].n
+        _matrices_on(dev, gates, ups, downs)
         ldx = _matrix_arg(x, "x", m, k, dev, (torch.bfloat16,))
         ldy = _matrix_arg(y, "y", m, n, dev, (torch.bfloat16, torch.float32))
         for t, what, dtype in ((expert_ids, "expert_ids", torch.int32), (weights, "weights", torch.float32)):

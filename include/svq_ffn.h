@@ -4,7 +4,7 @@
  * of a mixture of experts and a whole expert layer.  Same library, same
  * packed matrices, same rules as svq.h (ownership, errors, streams,
  * workspaces: a call with workspace == NULL only reports the bytes needed
- * and validates what it is given; calls that share a workspace must be
+ * and validates what it is given; a workspace starts on 16 bytes; calls that share a workspace must be
  * ordered on one stream; nothing is kept from one call for the next).
  *
  * Numerics.  Up to 16 rows products are those of svq.h, except that calls of
@@ -110,7 +110,10 @@ svq_status svq_moe_route(const void *x, int64_t m, int64_t ldx, const void *w, s
  *                   it may be y itself (ldr == ldy, same type), no other
  *                   overlap with y is allowed.
  *   y:              device [m][ldy] of type ydt, ldy >= down's n.
- *   workspace, stream: as for svq_moe_linear. */
+ *   workspace, stream: as for svq_moe_linear.
+ * SVQ_ERR_UNSUPPORTED: up to 64 slots, rows too long for a block's LDS (an
+ * inner width beyond 36864, or beyond about 20000 with matrices that admit no
+ * exact split). */
 svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_handle *down,
                        int32_t num_experts, const void *x, int64_t ldx, const int32_t *expert_ids,
                        const float *weights, int64_t m, int32_t topk, svq_act act,

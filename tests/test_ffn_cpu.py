@@ -166,6 +166,19 @@ def test_ffn_refusals(over, want):
     assert _ffn(ws=FAKE, nbytes=1 << 40, **over)[0] == want
 
 
+def test_ffn_refuses_an_inner_width_beyond_lds():
+    n = 40000
+    assert _ffn(n=n, m=3, ldx=520)[0] == UNSUPPORTED
+    assert _ffn(n=36864, m=3)[0] == 0
+
+
+def test_misaligned_workspaces_are_refused():
+    assert _epilogue(ws=FAKE + 8, nbytes=1 << 30)[0] == BAD
+    assert _glu(ws=FAKE + 4, nbytes=1 << 30)[0] == BAD
+    assert _route(ws=FAKE + 1, nbytes=1 << 30)[0] == BAD
+    assert _ffn(ws=FAKE + 2, nbytes=1 << 30)[0] == BAD
+
+
 def test_ffn_workspace():
     for m in (1, 8, 32, 33, 600):
         st, need = _ffn(m=m, x=None, y=None, ids=None, wt=None)

@@ -84,7 +84,8 @@ def f64(t):
 # reach full 256 x 256 tiles, K splits and neither
 SHAPES = [(1, 8, 7, 1), (37, 104, 6, 1), (512, 1024, 8, 1), (100, 1032, 7, 2), (48, 640, 6, 4), (33, 520, 8, 5),
           (130, 2048, 7, 16), (300, 4608, 6, 9), (17, 264, 7, 17), (200, 1032, 8, 40), (515, 648, 6, 63),
-          (257, 520, 7, 256), (512, 512, 8, 300), (600, 1544, 6, 515)]
+          (257, 520, 7, 256), (512, 512, 8, 300), (600, 1544, 6, 515),
+          (64, 9728, 7, 16), (90, 264, 8, 129)]
 
 
 @pytest.mark.parametrize("n,k,bd,m", SHAPES)
@@ -126,23 +127,59 @@ def test_epilogue_strided_operands_and_neighbours(svq, m):
     assert torch.equal(wide, before)
 
 
-def test_epilogue_without_an_exact_split(svq):
-    """Tables that admit no fp16 split run four rows at a time: the residual
-    follows the rows."""
-    n, k, m = 40, 72, 11
-    mat = synth.random_matrix(n, k, 7, seed=(73, n, k))
+def no_split(svq, n, k, seed):
+    """A matrix whose tables admit no split into two fp16 halves."""
+    mat = synth.random_matrix(n, k, 7, seed=(73, seed, k))
     mat.radius = mat.radius.copy()
     mat.radius[0], mat.radius[1] = 0x3C01, 0x7B53
     mat.codebook = mat.codebook.copy()
     mat.codebook[0, :] = 0x0001
     pm = svq.pack(mat)
     assert pm.handle.xscale_log2 == svq.SVQ_NO_EXACT_SPLIT
+    return mat, pm
+
+
+def product_bf16(mat, x_bits, m):
+    """Without a split: exact up to 16 rows, bf16 weights beyond."""
+    p, b = product(mat, x_bits, False)
+    W = so.linear_from_inputs(mat, x_bits[:1])[1]
+    return p, b + (2.0 ** -8 * so.abs_bound(x_bits, W) if m > 16 else 0.0)
+
+
+@pytest.mark.parametrize("m", [1, 3, 11, 20, 300])
+def test_without_an_exact_split(svq, m):
+    """Tables that admit no fp16 split: four rows at a time up to 16 rows (the
+    residual follows the rows), the bf16 form beyond; the gated pair as two
+    products and a step."""
+    n, k = 40, 72
+    (mat, pm), (mat2, pm2) = no_split(svq, n, k, 1), no_split(svq, n, k, 2)
     x_bits = synth.random_activations(m, k, seed=(73, 1, m))
+    x = to_device_bf16(x_bits)
     res = vec(m * n, torch.float32, 6).view(m, n)
-    y = svq.linear_epilogue(pm, to_device_bf16(x_bits), act="relu", residual=res, out_dtype=torch.float32)
-    p, pb = product(mat, x_bits, False)
+    y = svq.linear_epilogue(pm, x, act="relu", residual=res, out_dtype=torch.float32)
+    p, pb = product_bf16(mat, x_bits, m)
     a, r = np.maximum(p, 0), f64(res)
-    check(y, a + r, pb + U32 * (np.abs(a) + np.abs(r)), "four rows at a time")
+    check(y, a + r, pb + U32 * (np.abs(a) + np.abs(r)), "epilogue")
+    u, ub = product_bf16(mat2, x_bits, m)
+    y = svq.linear_glu(pm, pm2, x, act="relu", out_dtype=torch.float32)
+    check(y, a * u, pb * np.abs(u) + ub * np.abs(a) + pb * ub + U32 * np.abs(a * u), "glu")
+
+
+def test_moe_without_an_exact_split(svq):
+    """The expert layer with one matrix that admits no split: per-slot as ever,
+    as separate products beyond."""
+    e, f, k, topk = 3, 72, 40, 2
+    (gm, gp), (um, up), (dm, dp) = experts(svq, e, f, k, 100), experts(svq, e, f, k, 101), experts(svq, e, k, f, 102)
+    gm[1], gp[1] = no_split(svq, f, k, 3)
+    for m in (5, 40):
+        x_bits = synth.random_activations(m, k, seed=(103, k, m))
+        rng = np.random.default_rng([103, m])
+        ids = np.stack([rng.permutation(e)[:topk] for _ in range(m)]).astype(np.int32)
+        wt = rng.random((m, topk)).astype(np.float32)
+        y = svq.moe_ffn(gp, up, dp, to_device_bf16(x_bits), torch.from_numpy(ids).cuda(), torch.from_numpy(wt).cuda(),
+                        out_dtype=torch.float32)
+        ref, bound = moe64((gm, um, dm), x_bits, ids, wt, "silu", m * topk > 64, bf16=True)
+        check(y, ref, bound, f"m={m}")
 
 
 def test_plain_epilogue_equals_linear(svq):
@@ -176,7 +213,8 @@ def test_activations_at_their_limits(svq):
 
 
 GLU_SHAPES = [(1, 8, 1), (37, 104, 1), (1000, 520, 1), (2000, 2560, 1), (100, 1032, 2), (48, 640, 4), (33, 520, 5),
-              (300, 4608, 13), (17, 264, 17), (200, 1032, 40), (257, 520, 256), (512, 1024, 300), (264, 512, 256), (700, 264, 530)]
+              (300, 4608, 13), (17, 264, 17), (200, 1032, 40), (257, 520, 256), (512, 1024, 300), (264, 512, 256), (700, 264, 530),
+              (40, 9728, 1), (24, 16384, 1), (64, 9728, 16), (90, 264, 129)]
 
 
 @pytest.mark.parametrize("n,k,m", GLU_SHAPES)
@@ -265,21 +303,22 @@ def experts(svq, e, n, k, seed):
     return mats, [svq.pack(a) for a in mats]
 
 
-def moe64(sets, x_bits, ids, wt, act, grouped):
+def moe64(sets, x_bits, ids, wt, act, grouped, bf16=False):
     """(y without the residual, bound) from the definition."""
     m, topk = ids.shape
     gates, ups, downs = sets
     e, out = len(gates), downs[0].n
     y, b = np.zeros((m, out)), np.zeros((m, out))
-    wr = 2.0 ** -11 if grouped else 0.0
-    hr = 2.0 ** -11
+    wr = (2.0 ** -8 if bf16 else 2.0 ** -11) if grouped else 0.0
+    hr = 2.0 ** -8 if bf16 and grouped else 2.0 ** -11
     for t in range(m):
         xb = x_bits[t:t + 1]
         for j in range(topk):
             i = int(ids[t, j])
             if i < 0 or i >= e:
                 continue
-            (g, gb), (u, ub) = [product(a[i], xb, grouped) for a in (gates, ups)]
+            (g, gb), (u, ub) = [(product_bf16(a[i], xb, 64) if bf16 and grouped else product(a[i], xb, grouped))
+                                  for a in (gates, ups)]
             a = act64(g, act)
             h = a * u
             eh = (slope_of(act) * gb + 16 * U32 * np.abs(a)) * np.abs(u) + ub * np.abs(a) + slope_of(act) * gb * ub
@@ -329,8 +368,23 @@ def test_moe_ffn(svq, e, f, k, m, topk, kind):
     check(y, ref, bound, f"moe e={e} f={f} k={k} m={m}")
 
 
-def test_moe_ffn_in_place_and_all_slots_empty(svq):
-    e, f, k, m, topk = 4, 40, 72, 5, 2
+def test_moe_ffn_long_rows(svq):
+    """Rows too long for a block's LDS: a few slots through the grouped form;
+    an inner width beyond it is refused."""
+    e, f, k, m = 2, 8, 40000, 3
+    (gm, gp), (um, up), (dm, dp) = experts(svq, e, f, k, 105), experts(svq, e, f, k, 106), experts(svq, e, 24, f, 107)
+    x_bits = synth.random_activations(m, k, seed=(105, k, m))
+    ids = np.array([[0], [1], [1]], dtype=np.int32)
+    wt = np.ones((m, 1), dtype=np.float32)
+    y = svq.moe_ffn(gp, up, dp, to_device_bf16(x_bits), torch.from_numpy(ids).cuda(), torch.from_numpy(wt).cuda(),
+                    out_dtype=torch.float32)
+    ref, bound = moe64((gm, um, dm), x_bits, ids, wt, "silu", True)
+    check(y, ref, bound, "long rows")
+
+
+@pytest.mark.parametrize("m", [5, 90])
+def test_moe_ffn_in_place_and_all_slots_empty(svq, m):
+    e, f, k, topk = 4, 40, 72, 2
     _, gp = experts(svq, e, f, k, 85)
     _, up = experts(svq, e, f, k, 86)
     _, dp = experts(svq, e, k, f, 87)
