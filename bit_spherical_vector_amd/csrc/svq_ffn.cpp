@@ -88,6 +88,7 @@ svq_status ffn_gemm(const svq_handle *const *w, int jobs, const void *x, int64_t
   // ranges for about 512 blocks
   a.rpb = 8;
   while (a.rpb > 2 && prefill_prep_lds(a.rpb, w[0]->k) > 12 * 1024) a.rpb /= 2;
+  if (prefill_prep_lds(a.rpb, w[0]->k) + 1024 > GV_LDS_LIMIT) a.rpb = 1;  // k beyond 40000
   const int rows = a.m_pad / a.rpb, nch = units * UNIT_SLOTS / 8;
   const int cs = (512 + rows - 1) / rows < nch / 64 ? (512 + rows - 1) / rows : nch / 64;
   a.csplit = cs < 1 ? 1 : cs;
@@ -233,7 +234,8 @@ svq_status pair_small(const svq_handle *gate, const svq_handle *up, const void *
       J.xa = ws + o_x[j];
       J.xs = (float *)(ws + o_s[j]);
       J.xinv = std::ldexp(1.0f, -w[j]->xscale_log2);
-      J.cnt = pa.cnt;  // cleared by either prep form
+      J.part = pa.part;  // the pair's ranges share one exchange and its arrivals,
+      J.cnt = pa.cnt;    // which either prep form clears
       J.block_begin = b.starts.first[j] = j * pl.groups * pl.splits;
       J.prep_begin = b.prep_starts.first[j] = j * U;
     }

@@ -85,7 +85,7 @@ def f64(t):
 SHAPES = [(1, 8, 7, 1), (37, 104, 6, 1), (512, 1024, 8, 1), (100, 1032, 7, 2), (48, 640, 6, 4), (33, 520, 8, 5),
           (130, 2048, 7, 16), (300, 4608, 6, 9), (17, 264, 7, 17), (200, 1032, 8, 40), (515, 648, 6, 63),
           (257, 520, 7, 256), (512, 512, 8, 300), (600, 1544, 6, 515),
-          (64, 9728, 7, 16), (90, 264, 8, 129)]
+          (64, 9728, 7, 16), (90, 264, 8, 129), (20, 65536, 7, 33)]
 
 
 @pytest.mark.parametrize("n,k,bd,m", SHAPES)
