@@ -30,6 +30,31 @@ __device__ __forceinline__ float act_apply(float v, int act) {
   }
 }
 
+// Cheaper forms for values that are rounded to 11 bits or fewer next: the
+// hardware's exp2 and reciprocal (each within about 1 ulp) in place of expf
+// and a division; the argument's rounding adds |v| 2^-24.
+template <int ACT>
+__device__ __forceinline__ float act_fast(float v) {
+  if constexpr (ACT == SVQ_ACT_RELU) return v < 0.f ? 0.f : v;
+  if constexpr (ACT == SVQ_ACT_SILU)
+    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * v));
+  if constexpr (ACT == SVQ_ACT_GELU) return act_apply(v, SVQ_ACT_GELU);
+  if constexpr (ACT == SVQ_ACT_GELU_TANH) {
+    const float z = v * __builtin_fmaf(0.044715f * v, v, 1.f);
+    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-2.f * 0.79788456080286536f * 1.44269504088896341f * z));
+  }
+  return v;
+}
+__device__ __forceinline__ float act_fast(float v, int act) {
+  switch (act) {
+    case SVQ_ACT_RELU: return act_fast<SVQ_ACT_RELU>(v);
+    case SVQ_ACT_SILU: return act_fast<SVQ_ACT_SILU>(v);
+    case SVQ_ACT_GELU: return act_fast<SVQ_ACT_GELU>(v);
+    case SVQ_ACT_GELU_TANH: return act_fast<SVQ_ACT_GELU_TANH>(v);
+    default: return v;
+  }
+}
+
 __device__ __forceinline__ float load_f(const void *p, size_t i, int f32) {
   return f32 ? ((const float *)p)[i] : bf16_bits_to_f32(((const uint16_t *)p)[i]);
 }

@@ -986,7 +986,7 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
     if constexpr (IN::glu) {
       auto put = [&](int j, f4 gg, f4 uu) __attribute__((always_inline)) {
 #pragma unroll
-        for (int l = 0; l < 4; ++l) gg[l] = act_apply(gg[l], in.act) * uu[l];
+        for (int l = 0; l < 4; ++l) gg[l] = act_fast(gg[l], in.act) * uu[l];
         if (j < K / 4) ((f4 *)s_stage)[j] = gg;
       };
 #pragma unroll

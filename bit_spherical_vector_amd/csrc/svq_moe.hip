@@ -143,7 +143,7 @@ __device__ __forceinline__ void prep_f16_rows(uint8_t *smem, const MoeSbBatch &b
         if constexpr (GLU) {
 #pragma unroll
           for (int l = 0; l < 4; ++l)
-            v[i][l] = __builtin_bit_cast(uint32_t, act_apply(__builtin_bit_cast(float, (uint32_t)v[i][l]), f.act) *
+            v[i][l] = __builtin_bit_cast(uint32_t, act_fast(__builtin_bit_cast(float, (uint32_t)v[i][l]), f.act) *
                                                        __builtin_bit_cast(float, (uint32_t)v2[i][l]));
         }
         if (c < nstage) *(u4 *)(smem + (size_t)rr * stride + 16 * cc) = v[i];

@@ -1030,21 +1030,6 @@ hipError_t launch_prefill_batched(PrefillBatch &b, int bm, int blocks, hipStream
 // * otherwise fp32 partial tiles and one reduce launch that sums the K ranges
 //   and applies epilogue or gating.
 
-// Cheaper activations for accumulators in registers: the hardware's exp2 and
-// reciprocal (each within about 1 ulp) in place of expf and a division; the
-// argument's rounding adds |v| 2^-24.
-template <int ACT>
-__device__ __forceinline__ float act_fast(float v) {
-  if constexpr (ACT == SVQ_ACT_RELU) return v < 0.f ? 0.f : v;
-  if constexpr (ACT == SVQ_ACT_SILU)
-    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * v));
-  if constexpr (ACT == SVQ_ACT_GELU) return act_apply(v, SVQ_ACT_GELU);
-  if constexpr (ACT == SVQ_ACT_GELU_TANH) {
-    const float z = v * __builtin_fmaf(0.044715f * v, v, 1.f);
-    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-2.f * 0.79788456080286536f * 1.44269504088896341f * z));
-  }
-  return v;
-}
 template <int ACT>
 __device__ __forceinline__ void act16(f16x &v) {
 #pragma unroll
