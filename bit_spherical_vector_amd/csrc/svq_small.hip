@@ -81,14 +81,15 @@ __device__ __forceinline__ u4 sb_lds(uint32_t addr) { return *(sb_lds_u4_t *)(si
 // Table rows of the four codes (ci = 0..3) of MFMA group q: the hi and lo
 // halves of each code's exact split (32-byte rows by 10-bit index).  HI: the
 // high halves alone, RNE_fp16(R*D*2^s), 16-byte rows.
-template <bool HI>
+// TAB: LDS address of the table.
+template <bool HI, int TAB = SB_OFF_XTAB>
 __device__ __forceinline__ void sb_reads(uint32_t Lw, uint32_t H, const SbShifts &sh, u4 (&Dh)[4],
                                          u4 (&Dl)[4]) {
 #pragma unroll
   for (int ci = 0; ci < 4; ++ci) {
     const uint32_t lo = __builtin_amdgcn_ubfe(Lw, 8 * ci, 8);
     const uint32_t hi = __builtin_amdgcn_ubfe(H, sh.hi[ci], 2);
-    const uint32_t a = SB_OFF_XTAB + ((lo | (hi << 8)) << (HI ? 4 : 5));
+    const uint32_t a = TAB + ((lo | (hi << 8)) << (HI ? 4 : 5));
     Dh[ci] = sb_lds(a);
     Dl[ci] = HI ? Dh[ci] : sb_lds(a + 16);
   }
@@ -117,23 +118,23 @@ __device__ __forceinline__ void sb_mul(uint64_t S01, uint64_t S23, const SbShift
 }
 
 // One unit of one row tile: the 16 codes of the lane, 16 MFMAs.
-template <bool HI>
+template <bool HI, int TAB = SB_OFF_XTAB>
 __device__ __forceinline__ f4 sb_item(const SbCodes &c, const u4 (&A)[16], const SbShifts &sh) {
   f4 C0 = {0.f, 0.f, 0.f, 0.f}, C1 = {0.f, 0.f, 0.f, 0.f};
   u4 H0[4], L0[4], H1[4], L1[4];
   auto s01 = [&](int q) { return (uint64_t)c.S[q][0] | ((uint64_t)c.S[q][1] << 32); };
   auto s23 = [&](int q) { return (uint64_t)c.S[q][2] | ((uint64_t)c.S[q][3] << 32); };
   // the table reads of group q + 1 are in flight while group q is multiplied
-  sb_reads<HI>(c.L[0], c.H[0], sh, H0, L0);
-  sb_reads<HI>(c.L[1], c.H[1], sh, H1, L1);
+  sb_reads<HI, TAB>(c.L[0], c.H[0], sh, H0, L0);
+  sb_reads<HI, TAB>(c.L[1], c.H[1], sh, H1, L1);
   __builtin_amdgcn_sched_barrier(0);
   sb_mul<HI>(s01(0), s23(0), sh, H0, L0, A, 0, C0);
   __builtin_amdgcn_sched_barrier(0);
-  sb_reads<HI>(c.L[2], c.H[2], sh, H0, L0);
+  sb_reads<HI, TAB>(c.L[2], c.H[2], sh, H0, L0);
   __builtin_amdgcn_sched_barrier(0);
   sb_mul<HI>(s01(1), s23(1), sh, H1, L1, A, 1, C1);
   __builtin_amdgcn_sched_barrier(0);
-  sb_reads<HI>(c.L[3], c.H[3], sh, H1, L1);
+  sb_reads<HI, TAB>(c.L[3], c.H[3], sh, H1, L1);
   __builtin_amdgcn_sched_barrier(0);
   sb_mul<HI>(s01(2), s23(2), sh, H0, L0, A, 2, C0);
   __builtin_amdgcn_sched_barrier(0);
@@ -351,6 +352,120 @@ __global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b, EA... ea) {
   (void)j;
 }
 
+// ---------------------------------------------------------------------------
+// Gated pair without K ranges: both matrices of the same row tiles in one
+// block of 8 waves, 0..3 on the gate's and 4..7 on the up matrix's, each half
+// with its own table and partial sums in its part of LDS (what two blocks of
+// the kernel above hold), so the pair meets in LDS.  (Through memory, as
+// above, the exchange and its arrival cost 3 of 14 us.)
+// ---------------------------------------------------------------------------
+template <bool HI>
+constexpr int sb_half_bytes() { return XTAB_BYTES / (HI ? 2 : 1) + SB_RED_BYTES; }
+
+// One half's sums: thread (tid & 255) returns acc[t] of row tile t, activation
+// row (tid & 255) >> 4, output row tid & 15, as the kernel above.
+template <bool HI, int HB>
+__device__ __forceinline__ void sb_pair_half(const SbJob &J, int g, float (&acc)[SB_TMAX]) {
+  constexpr int OFF_TAB = HB, OFF_RED = HB + XTAB_BYTES / (HI ? 2 : 1), NBT = XTAB_BYTES / 4096 / (HI ? 2 : 1);
+  const MatView &w = J.w;
+  const int tid = threadIdx.x & 255, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int t0 = g * J.tiles, tn = min(J.tiles, w.n_tiles - t0);
+  const int N = w.units * tn;
+  const int i0 = wv * N / SB_WAVES, nk = (wv + 1) * N / SB_WAVES - i0;
+  const uint32_t s = lane >> 4, b0 = (lane >> 2) & 3, j = lane & 3;
+  const uint32_t rec0 = 16 * s + j;
+  const SbOffs offs = {16 * rec0, 16 * rec0 + 4 * b0, 4 * rec0};
+  SbShifts sh;
+#pragma unroll
+  for (int ci = 0; ci < 4; ++ci) {
+    sh.sg[ci] = 4 * b0 + ci;
+    sh.hi[ci] = 8 * b0 + 2 * ci;
+  }
+  const uint32_t slot0 = OFF_RED + wv * SB_TMAX * 1024 + 16 * lane;
+  u4 bt[NBT];
+  const u4 *gbt = (const u4 *)(w.base + w.off_xtab);
+#pragma unroll
+  for (int i = 0; i < NBT; ++i) bt[i] = gbt[HI ? 2 * (tid + 256 * i) : tid + 256 * i];
+  __builtin_amdgcn_sched_barrier(0);
+  u4 A[16];
+  f4 xsc;
+  SbCodes cd[2];
+  int ui = i0 / tn, ti = i0 - ui * tn;
+  auto load_unit = [&](int u) __attribute__((always_inline)) {
+    const u4 *xa = (const u4 *)(J.xa + (size_t)u * SB_XA_UNIT_BYTES) + lane;
+#pragma unroll
+    for (int f = 0; f < 16; ++f) A[f] = xa[64 * f];
+    xsc = *(const f4 *)(J.xs + (size_t)u * 16 + 4 * s);
+  };
+  auto codes_of = [&](int i) __attribute__((always_inline)) {
+    const int u = i / tn;
+    return sb_load_codes(sb_unit(w, t0 + i - u * tn, u), offs);
+  };
+  // unconditional (a wave without items loads item i0 < N anyway)
+  load_unit(ui);
+  cd[0] = codes_of(i0);
+  cd[1] = codes_of(min(i0 + 1, N - 1));
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int t = 0; t < SB_TMAX; ++t) *(sb_lds_u4w_t *)(size_t)(slot0 + t * 1024) = (u4){0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < NBT; ++i) *(sb_lds_u4w_t *)(size_t)(OFF_TAB + 16 * (tid + 256 * i)) = bt[i];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < SB_NMAX; ++k) {
+    if (k >= nk) break;
+    if (k > 0 && ti == 0) load_unit(ui);
+    const f4 C = sb_item<HI, OFF_TAB>(cd[k & 1], A, sh) * xsc;
+    if (k + 2 < nk) cd[k & 1] = codes_of(i0 + k + 2);
+    sb_lds_u4w_t *sl = (sb_lds_u4w_t *)(size_t)(slot0 + ti * 1024);
+    *sl = __builtin_bit_cast(u4, __builtin_bit_cast(f4, *sl) + C);
+    if (++ti == tn) {
+      ti = 0;
+      ++ui;
+    }
+  }
+  __syncthreads();
+  const int m = tid >> 4, nn = tid & 15;
+  const uint32_t eoff = OFF_RED + 256 * (m >> 2) + 16 * nn + 4 * (m & 3);
+#pragma unroll
+  for (int t = 0; t < SB_TMAX; ++t) {
+    acc[t] = 0.f;
+#pragma unroll
+    for (int ww = 0; ww < SB_WAVES; ++ww) acc[t] += *(sb_lds_f_t *)(size_t)(eoff + (ww * SB_TMAX + t) * 1024);
+    acc[t] *= J.xinv;
+  }
+}
+
+template <bool HI>
+__global__ __launch_bounds__(512) void sb_pair_kernel(SbBatch b, PairArgs pa) {
+  constexpr int HB = sb_half_bytes<HI>();
+  const int g = blockIdx.x, tid = threadIdx.x & 255;
+  float acc[SB_TMAX];
+  const bool up = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8) != 0;
+  if (!up) sb_pair_half<HI, 0>(b.job[0], g, acc);
+  else sb_pair_half<HI, HB>(b.job[1], g, acc);
+  // the up half's sums to the gate's threads, over the up half's table (no
+  // wave reads it any more)
+  if (up) {
+#pragma unroll
+    for (int t = 0; t < SB_TMAX; ++t) *(sb_lds_f_t *)(size_t)(HB + (t * 256 + tid) * 4) = acc[t];
+  }
+  __syncthreads();
+  const SbJob &J = b.job[0];
+  const int m = tid >> 4, t0 = g * J.tiles, tn = min(J.tiles, J.w.n_tiles - t0);
+  if (up || m >= b.m) return;
+#pragma unroll
+  for (int t = 0; t < SB_TMAX; ++t) {
+    const int n = (t0 + t) * UNIT_ROWS + (tid & 15);
+    if (t < tn && n < J.w.n)
+      store_out(J.y, (size_t)m * J.ldy + n, pair_value(pa, acc[t], *(sb_lds_f_t *)(size_t)(HB + (t * 256 + tid) * 4), n),
+                b.ydt);
+  }
+}
+static_assert(2 * sb_half_bytes<false>() <= (int)GV_LDS_LIMIT, "both halves of a block in LDS");
+static_assert(SB_TMAX * 256 * 4 <= XTAB_BYTES / 2, "the up sums fit over its table");
+
 // Prep: the permuted activations of every job in fragment order (see the
 // file comment), rows >= m and slots >= k zero; block u of a job writes the
 // 16 fragments of unit u, thread tid the 16-byte pieces of fragments
@@ -521,6 +636,14 @@ hipError_t launch_sb(SbBatch &b, int prep_blocks, int blocks, hipStream_t s) {
   }
   const dim3 grid(blocks), block(256);
   const bool hi = b.ydt == 0;
+  if (b.pair && b.job[0].splits == 1) {
+    const size_t smem = 2 * (size_t)(hi ? sb_half_bytes<true>() : sb_half_bytes<false>());
+    e = hi ? allow_smem(sb_pair_kernel<true>, smem) : allow_smem(sb_pair_kernel<false>, smem);
+    if (e != hipSuccess) return e;
+    if (hi) hipLaunchKernelGGL(sb_pair_kernel<true>, dim3(b.job[0].groups), dim3(512), smem, s, b, *b.pair);
+    else hipLaunchKernelGGL(sb_pair_kernel<false>, dim3(b.job[0].groups), dim3(512), smem, s, b, *b.pair);
+    return hipGetLastError();
+  }
   if (b.pair && hi)
     hipLaunchKernelGGL((sb_gemm_kernel<true, PairArgs>), grid, block, SB_SMEM, s, b, *b.pair);
   else if (b.pair)
