@@ -138,13 +138,8 @@ struct PartEpi {
 
 // A gated pair whose sums meet in memory (see PairArgs).
 struct PairEpi {
-  static constexpr bool on = true, partial = true, f16 = false;
+  static constexpr bool on = true;
   PairArgs a;
-  float *row;    // sums of this block's matrix, [m][ldp]
-  int64_t ldp;
-  __device__ __forceinline__ void put(float v, int r, int n) const {
-    __hip_atomic_store(row + (size_t)r * ldp + n, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
   __device__ __forceinline__ float operator()(float v, int, int) const { return v; }
 };
 __device__ __forceinline__ float pair_value(const PairArgs &a, float g, float u, int n) {
@@ -156,6 +151,6 @@ __device__ __forceinline__ float pair_value(const PairArgs &a, float g, float u,
 // The epilogue of a kernel's optional EpiArgs argument.
 __device__ __forceinline__ NoEpi make_epi() { return NoEpi(); }
 __device__ __forceinline__ Epi make_epi(const EpiArgs &a) { return Epi{a}; }
-__device__ __forceinline__ PairEpi make_epi(const PairArgs &a) { return PairEpi{a, nullptr, 0}; }
+__device__ __forceinline__ PairEpi make_epi(const PairArgs &a) { return PairEpi{a}; }
 
 }  // namespace svq

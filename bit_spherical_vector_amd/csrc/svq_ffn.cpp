@@ -137,9 +137,10 @@ svq_status ffn_gemm(const svq_handle *const *w, int jobs, const void *x, int64_t
   return launch_ffn_gemm(a, aligned(x, ldx, 2, 16), (hipStream_t)stream) == hipSuccess ? SVQ_OK : SVQ_ERR_HIP;
 }
 
-// A gated pair of 2..16 rows: the launches of svq_linear_batched over both
-// matrices with equal plans, the pair joined by whichever block of a group
-// ends last.
+// A gated pair of 2..16 rows: the gather or prep launch of svq_linear_batched
+// over both matrices, then one launch whose blocks take the same row tiles of
+// both (with K ranges, 5..16 rows of more than 4096 channels: a block per
+// matrix and range, joined by whichever ends last).
 svq_status pair_small(const svq_handle *gate, const svq_handle *up, const void *x, int64_t m, int64_t ldx,
                       PairArgs pa, void *y, int64_t ldy, svq_dtype ydt, void *workspace, size_t *bytes,
                       void *stream) {
@@ -152,30 +153,30 @@ svq_status pair_small(const svq_handle *gate, const svq_handle *up, const void *
     off += align256(b);
     return at;
   };
-  size_t o_x[2], o_s[2], o_part, o_cnt;
+  size_t o_x[2], o_s[2], o_part = 0, o_cnt = 0;
   SbPlan pl = {};
   int R = 1;
   if (exact) {
-    // row tiles per block as for svq_linear_batched, the same for both
-    R = 4 * GV_UNITS_PER_WAVE / U;
+    // row tiles of both matrices per block: one round of blocks, one per
+    // compute unit, while the tiles allow it
+    R = (nt + compute_units() - 1) / compute_units();
     R = R < 1 ? 1 : (R > GV_MAX_R ? GV_MAX_R : R);
-    while (R < GV_MAX_R && 2 * ((nt + R - 1) / R) > 3 * compute_units()) ++R;
     for (int j = 0; j < 2; ++j) {
       o_x[j] = take((size_t)m * U * GV_XG_UNIT_BYTES);
       o_s[j] = take((size_t)U * 16);
     }
-    o_part = take((size_t)2 * m * gate->n * 4);
-    pa.n_cnt = (nt + R - 1) / R;
   } else {
     pl = sb_plan(nt, U, sb_block_items(2 * (int64_t)nt * U, compute_units()));
     for (int j = 0; j < 2; ++j) {
       o_x[j] = take((size_t)U * SB_XA_UNIT_BYTES);
       o_s[j] = take((size_t)U * 16 * 4);
     }
-    o_part = take((size_t)pl.groups * pl.tiles * 2 * pl.splits * 1024);
-    pa.n_cnt = pl.groups;
+    if (pl.splits > 1) {  // K ranges meet through memory
+      o_part = take((size_t)pl.groups * pl.tiles * 2 * pl.splits * 1024);
+      o_cnt = take((size_t)pl.groups * 4);
+      pa.n_cnt = pl.groups;
+    }
   }
-  o_cnt = take((size_t)pa.n_cnt * 4);
   if (!workspace) {
     *bytes = off;
     return SVQ_OK;
@@ -183,8 +184,10 @@ svq_status pair_small(const svq_handle *gate, const svq_handle *up, const void *
   if (!x || !y) return SVQ_ERR_INVALID_ARG;
   if (*bytes < off) return SVQ_ERR_BUFFER_TOO_SMALL;
   uint8_t *ws = (uint8_t *)workspace;
-  pa.part = (float *)(ws + o_part);
-  pa.cnt = (int32_t *)(ws + o_cnt);
+  if (pa.n_cnt) {
+    pa.part = (float *)(ws + o_part);
+    pa.cnt = (int32_t *)(ws + o_cnt);
+  }
   hipError_t e;
   if (exact) {
     GemvBatch b;

@@ -93,8 +93,9 @@ struct EpiArgs {
   int32_t bias_vec, res_vec;  // rows allow loads of four values
 };
 
-// Join of a gated pair: y = act(g + bg) * (u + bu), fp32 sums of both
-// matrices' blocks meeting in `part`, the last of them to arrive finishing.
+// Gating of a pair of products: y = act(g + bg) * (u + bu).  Where the two
+// matrices' blocks meet through memory (K ranges), `part` holds their fp32
+// sums and the last of them to arrive finishes.
 struct PairArgs {
   const void *bias_g, *bias_u;  // [n] or null
   int32_t bias_f32, act;
@@ -151,6 +152,10 @@ __host__ __device__ constexpr int gv_copies(int bd) { return bd >= 8 ? 8 : 16; }
 // cross-wave partial sums [R][GV_WAVES][4][4][4][M] fp32 at GemvBatch::red_off.
 constexpr int GV_OFF_RTAB = 0;
 constexpr int GV_OFF_D = RTAB_BYTES;
+// A gated pair's block: the second matrix's half starts there (both halves'
+// tables and at most GV_MAX_R tiles of 4 rows' partial sums below it).
+constexpr int GV_HALF = GV_OFF_D + 32 * 1024 + GV_MAX_R * GV_WAVES * 64 * EXACT_MAX_M * 4;
+static_assert(2 * GV_HALF <= (int)GV_LDS_LIMIT && GV_HALF + GV_OFF_D < 65536, "two halves; offsets fit the instruction");
 // Workspace of the exact path for one matrix of `units` units.
 inline size_t gemv_ws_bytes(int m, int units) {
   return align256((size_t)m * units * GV_XG_UNIT_BYTES) + align256((size_t)units * 16);

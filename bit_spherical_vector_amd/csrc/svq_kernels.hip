@@ -221,22 +221,12 @@ __device__ __forceinline__ void gather_block(const uint16_t *__restrict__ perm,
   if (lane == 0) xs_row[4 * u] = ldexpf(1.f, -e);
 }
 
-__device__ __forceinline__ void clear_counts(const PairArgs &a) {
-  for (int i = threadIdx.x; i < a.n_cnt; i += 256) a.cnt[i] = 0;
-}
-
 // Gather launch of the dense path: block = (job, activation row a, group of
 // 4 units), wave = unit.  The launch ends with 8 blocks per job (one per XCD:
 // blocks go to the XCDs round-robin) that only read the job's direction and
 // radius tables, so that the main launch finds them near.
-// za: nothing, or the PairArgs of a gated pair, whose arrival counters are
-// cleared here.
-template <typename... ZA>
-__global__ __launch_bounds__(256) void gemv_gather_kernel(GemvBatch b, ZA... za) {
+__global__ __launch_bounds__(256) void gemv_gather_kernel(GemvBatch b) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  if constexpr (sizeof...(ZA) > 0) {
-    if (blockIdx.x == 0) clear_counts(za...);
-  }
   if ((int)blockIdx.x >= b.touch_begin) {
     const int jt = ((int)blockIdx.x - b.touch_begin) >> 3;
     if (jt < b.count) {
@@ -326,7 +316,8 @@ struct DirAddr {
 
 // Table reads of the four codes of column group ci: direction rows (signs
 // not yet applied) from the lane's table copy, and radii.
-template <int CI>
+// HB: where the tables' LDS starts.
+template <int CI, int HB>
 __device__ __forceinline__ void gemv_group_reads(const ItemCodes &c, const DirAddr &da,
                                                  uint32_t (&dad)[4], u4 (&D)[4], _Float16 (&R)[4]) {
 #pragma unroll
@@ -338,8 +329,8 @@ __device__ __forceinline__ void gemv_group_reads(const ItemCodes &c, const DirAd
     const int sh = 9 - 2 * i;
     const uint32_t hs = sh >= 0 ? c.H << sh : c.H >> -sh;
     const uint32_t idx2 = (hs & 0x600u) | lo2;      // 10-bit index * 2
-    D[ri] = lds_u4(GV_OFF_D + dad[ri]);
-    R[ri] = lds_f16(GV_OFF_RTAB + idx2);
+    D[ri] = lds_u4(HB + GV_OFF_D + dad[ri]);
+    R[ri] = lds_f16(HB + GV_OFF_RTAB + idx2);
   }
 }
 
@@ -404,7 +395,7 @@ __device__ __forceinline__ void gemv_group_mul(uint64_t S01, uint64_t S23, const
 
 // One work item: the lane's 16 codes, column group by column group, with
 // the table reads of the next group issued before the current one is used.
-template <int M>
+template <int M, int HB>
 __device__ __forceinline__ void gemv_item(const GvItem<M> &it, const DirAddr &dmask, uint32_t (&dad0)[4],
                                           uint32_t (&dad1)[4], float (&tmp)[4][M]) {
   const ItemCodes &c = it.c;
@@ -414,16 +405,16 @@ __device__ __forceinline__ void gemv_item(const GvItem<M> &it, const DirAddr &dm
   _Float16 R0[4], R1[4];
   // phases are kept in this order (scheduling barriers): the reads of group
   // g + 1 are in flight while group g is decoded and multiplied
-  gemv_group_reads<0>(c, dmask, dad0, D0, R0);
-  gemv_group_reads<1>(c, dmask, dad1, D1, R1);
+  gemv_group_reads<0, HB>(c, dmask, dad0, D0, R0);
+  gemv_group_reads<1, HB>(c, dmask, dad1, D1, R1);
   __builtin_amdgcn_sched_barrier(0);
   gemv_group_mul<M, 0>(S01, S23, it.act.template get<0>(), D0, R0, tmp);
   __builtin_amdgcn_sched_barrier(0);
-  gemv_group_reads<2>(c, dmask, dad0, D0, R0);
+  gemv_group_reads<2, HB>(c, dmask, dad0, D0, R0);
   __builtin_amdgcn_sched_barrier(0);
   gemv_group_mul<M, 1>(S01, S23, it.act.template get<1>(), D1, R1, tmp);
   __builtin_amdgcn_sched_barrier(0);
-  gemv_group_reads<3>(c, dmask, dad1, D1, R1);
+  gemv_group_reads<3, HB>(c, dmask, dad1, D1, R1);
   __builtin_amdgcn_sched_barrier(0);
   gemv_group_mul<M, 2>(S01, S23, it.act.template get<2>(), D0, R0, tmp);
   __builtin_amdgcn_sched_barrier(0);
@@ -432,12 +423,14 @@ __device__ __forceinline__ void gemv_item(const GvItem<M> &it, const DirAddr &dm
 
 // Main launch, one block: tiles t0 .. t0+Reff-1 of matrix w (U units each),
 // activations gathered at xg / xs (row a of unit u at xg + (a*U + u) * 1 KB).
-template <int M, typename EPI = NoEpi>
+// HB, DUAL: as for gemv_fused_block below (one half of a two-matrix block).
+template <int M, typename EPI = NoEpi, int HB = 0, bool DUAL = false>
 __device__ void gemv_main_block(const MatView &w, const uint8_t *__restrict__ xg,
                                 const float *__restrict__ xs, void *y, int64_t ldy,
                                 int ydt, int t0, int Reff, int red_off, uint8_t *smem,
                                 const EPI &epi = EPI()) {
-  const int tid = threadIdx.x, lane = tid & 63;
+  smem += HB;
+  const int tid = DUAL ? threadIdx.x & 255 : threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform
   const int U = w.units, F = Reff * U;
   // the wave's items: flat units f = wv + k*GV_WAVES < F, k < n_items (the
@@ -509,7 +502,7 @@ __device__ void gemv_main_block(const MatView &w, const uint8_t *__restrict__ xg
     for (int ri = 0; ri < 4; ++ri)
 #pragma unroll
       for (int a = 0; a < M; ++a) tmp[ri][a] = 0.f;
-    gemv_item<M>(it, dmask, dad0, dad1, tmp);
+    gemv_item<M, HB>(it, dmask, dad0, dad1, tmp);
 #pragma unroll
     for (int a = 0; a < M; ++a)
 #pragma unroll
@@ -605,35 +598,37 @@ __global__ __launch_bounds__(256) void gemv_epi_kernel(GemvBatch b, EpiArgs ea) 
   gemv_main_block<M, Epi>(jb.w, jb.xg, jb.xs, jb.y, jb.ldy, b.ydt, t0, Reff, b.red_off, smem, epi);
 }
 
-// The main launch of a gated pair (jobs 0 and 1, equal R): a block leaves its
-// sums in memory and counts itself; the second of the two blocks of a
-// row-tile group takes both and writes the output.  (The partial stores are
-// device-scope and complete before the count; the flag lies over the tables,
-// which no wave reads any more.)
+// Sums of a block's rows, kept in LDS.
+struct LdsEpi {
+  static constexpr bool on = true, partial = true;
+  float *row;  // row n of the matrix and activation row a at row[a * lda + n - n0]
+  int n0, lda;
+  __device__ __forceinline__ void put(float v, int a, int n) const { row[a * lda + n - n0] = v; }
+  __device__ __forceinline__ float operator()(float v, int, int) const { return v; }
+};
+
+// The main launch of a gated pair (jobs 0 and 1, equal R): a block of 8 waves,
+// 0..3 on the gate's row tiles and 4..7 on the same tiles of the up matrix,
+// each half with its own tables and partial sums in its part of LDS, so the
+// pair meets in LDS.  (As two blocks that met through memory the launch took
+// 13.2 us at 4 rows of 9728 x 2560.)
 template <int M>
-__global__ __launch_bounds__(256) void gemv_pair_kernel(GemvBatch b, PairArgs pa) {
+__global__ __launch_bounds__(512) void gemv_pair_kernel(GemvBatch b, PairArgs pa) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  const int j = (int)blockIdx.x >= b.starts.first[1] ? 1 : 0;
-  const GemvJob &jb = b.job[j];
-  const int group = (int)blockIdx.x - b.starts.first[j], t0 = group * jb.R;
-  const int Reff = min(jb.R, jb.w.n_tiles - t0);
-  const int n_all = jb.w.n;
-  const int64_t ldp = n_all;
-  const PairEpi epi{pa, pa.part + (size_t)j * M * ldp, ldp};
-  gemv_main_block<M, PairEpi>(jb.w, jb.xg, jb.xs, nullptr, 0, 1, t0, Reff, b.red_off, smem, epi);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  const GemvJob &jg = b.job[0], &ju = b.job[1];
+  const int t0 = (int)blockIdx.x * jg.R, Reff = min(jg.R, jg.w.n_tiles - t0), rows = Reff * 16;
+  // the sums go over the half's tables, which no wave reads any more
+  if (__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8) == 0)
+    gemv_main_block<M, LdsEpi, 0, true>(jg.w, jg.xg, jg.xs, nullptr, 0, 1, t0, Reff, b.red_off, smem,
+                                        LdsEpi{(float *)smem, t0 * 16, rows});
+  else
+    gemv_main_block<M, LdsEpi, GV_HALF, true>(ju.w, ju.xg, ju.xs, nullptr, 0, 1, t0, Reff, b.red_off, smem,
+                                              LdsEpi{(float *)(smem + GV_HALF), t0 * 16, rows});
   __syncthreads();
-  int *flag = (int *)smem;
-  if (threadIdx.x == 0)
-    *flag = __hip_atomic_fetch_add(pa.cnt + group, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (*flag == 0) return;
-  for (int o = threadIdx.x; o < Reff * 16 * M; o += 256) {
-    const int a = o / (Reff * 16), n = t0 * 16 + o - a * Reff * 16;
-    if (n >= n_all) continue;
-    const float g = __hip_atomic_load(pa.part + (size_t)a * ldp + n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const float u = __hip_atomic_load(pa.part + (size_t)(M + a) * ldp + n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    store_out(jb.y, (size_t)a * jb.ldy + n, pair_value(pa, g, u, n), b.ydt);
+  const float *g = (const float *)smem, *u = (const float *)(smem + GV_HALF);
+  for (int o = threadIdx.x; o < rows * M; o += 512) {
+    const int a = o / rows, n = t0 * 16 + o - a * rows;
+    if (n < jg.w.n) store_out(jg.y, (size_t)a * jg.ldy + n, pair_value(pa, g[o], u[o], n), b.ydt);
   }
 }
 
@@ -652,9 +647,10 @@ static hipError_t launch_gemv_m(GemvBatch &b, int blocks, size_t smem, hipStream
   if (b.pair) {
     static const hipError_t pair_ok = check_no_static_lds(gemv_pair_kernel<M>);
     if (pair_ok != hipSuccess) return pair_ok;
-    const hipError_t e = allow_smem(gemv_pair_kernel<M>, smem);
+    const hipError_t e = allow_smem(gemv_pair_kernel<M>, GV_HALF + smem);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gemv_pair_kernel<M>), dim3(blocks), dim3(256), smem, s, b, *b.pair);
+    // the plan counts a block per matrix; a launched block takes one of each
+    hipLaunchKernelGGL((gemv_pair_kernel<M>), dim3(blocks / 2), dim3(512), GV_HALF + smem, s, b, *b.pair);
     return hipGetLastError();
   }
   if (b.epi) {
@@ -676,12 +672,9 @@ static hipError_t launch_gemv_m(GemvBatch &b, int blocks, size_t smem, hipStream
 hipError_t launch_gemv_batched(GemvBatch &b, int gather_blocks, int k_max, int blocks, size_t smem,
                                hipStream_t s) {
   const size_t gsmem = align256((size_t)k_max * 2);
-  hipError_t e = b.pair ? allow_smem(gemv_gather_kernel<PairArgs>, gsmem) : allow_smem(gemv_gather_kernel<>, gsmem);
+  hipError_t e = allow_smem(gemv_gather_kernel, gsmem);
   if (e != hipSuccess) return e;
-  if (b.pair)
-    hipLaunchKernelGGL(gemv_gather_kernel<PairArgs>, dim3(gather_blocks), dim3(256), gsmem, s, b, *b.pair);
-  else
-    hipLaunchKernelGGL(gemv_gather_kernel<>, dim3(gather_blocks), dim3(256), gsmem, s, b);
+  hipLaunchKernelGGL(gemv_gather_kernel, dim3(gather_blocks), dim3(256), gsmem, s, b);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   switch (b.m) {
@@ -1265,19 +1258,11 @@ hipError_t launch_gemv_fused(GemvBatch &b, int blocks, size_t smem, hipStream_t 
 // its own part of LDS; the sums meet in LDS, so nothing goes through memory
 // and no block waits for another.  8 waves per compute unit is what two
 // blocks of the plain launch put there for such sizes.
-// Sums of the block's rows, kept in LDS.
-struct LdsEpi {
-  static constexpr bool on = true, partial = true;
-  float *row;  // row n of the matrix at row[n - n0]
-  int n0;
-  __device__ __forceinline__ void put(float v, int, int n) const { row[n - n0] = v; }
-};
-
 template <bool XVEC, int HB>
 __device__ __forceinline__ void glu_half(const MatView &w, const uint16_t *x, int rt0, int R, int Reff,
                                          uint8_t *smem) {
   // the gathered row is dead once every wave is done with its items
-  const LdsEpi epi{(float *)(smem + HB + gf_lds(w.bd, w.k, w.units, 1, R).xp), rt0 * 16};
+  const LdsEpi epi{(float *)(smem + HB + gf_lds(w.bd, w.k, w.units, 1, R).xp), rt0 * 16, 0};
   if (w.bd >= 8)
     gemv_fused_block<1, XVEC, 8, LdsEpi, InBf16, true, HB>(w, x, 0, nullptr, 0, 1, rt0, R, Reff, smem, epi);
   else if (w.bd == 7)
