@@ -91,6 +91,32 @@ struct SbShifts {
   uint32_t sg[4], hi[4];
 };
 
+// Per-half maximum of the magnitudes of packed bf16 pairs, as 16-bit integers
+// (magnitudes order as their bit patterns, infinities and NaN on top).
+typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pk_max_mag(uint32_t m, uint32_t p) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2_t, m),
+                                                                __builtin_bit_cast(us2_t, p & 0x7FFF7FFFu)));
+}
+// The same over finite values only (the rare second look at a row that holds
+// infinities or NaN).
+__device__ __forceinline__ uint32_t pk_max_finite(uint32_t m, uint32_t p) {
+  const uint32_t lo = p & 0x7FFFu, hi = p & 0x7FFF0000u;
+  return pk_max_mag(m, (lo < 0x7F80u ? lo : 0u) | (hi < 0x7F800000u ? hi : 0u));
+}
+// Two values times 2^e as packed fp16.  Rounded toward zero: a scaled bf16
+// value of at least 2^-14 is exact either way.
+__device__ __forceinline__ uint32_t pk_scaled_f16(float a, float b, int e) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(ldexpf(a, e), ldexpf(b, e)));
+}
+__device__ __forceinline__ u4 scaled_f16(const u4 &v, int e) {
+  u4 h;
+#pragma unroll
+  for (int l = 0; l < 4; ++l)
+    h[l] = pk_scaled_f16(bf16_bits_to_f32(v[l] & 0xFFFFu), __builtin_bit_cast(float, v[l] & 0xFFFF0000u), e);
+  return h;
+}
+
 // The job of a batched launch that owns this block (see JobStarts): the
 // number of later job starts at or below blockIdx.x.
 __device__ __forceinline__ int find_job(const JobStarts &st, int count) {

@@ -90,117 +90,111 @@ struct MoeRouteLds {
   int32_t expert;
 };
 
-// The staging and gather of the fp16 form: as the bf16 form below, but one
-// wave per row finds the row's largest finite magnitude in LDS and converts
-// the row in place to fp16 under its scale, so that the gather, once per
-// projection, only moves 16-bit values.  Rows formed from g and u are staged
-// in fp32, so that act(g) * u is rounded once, here.  All
-// projections of the call read the same rows: a block stages them once (and
-// routes once) and gathers them through each projection's permutation.
+// The staging and gather of the fp16 form.  Wave w takes row w of the group:
+// it loads the row (or forms act(g) * u of the slot's two sums), finds the
+// largest finite magnitude across its lanes and leaves the row in LDS as fp16
+// under its scale, so that the gather, once per projection, only moves 16-bit
+// values and the row is rounded once.  All projections of the call read the
+// same rows: a block routes and stages them once.
 template <bool GLU>
 __device__ __forceinline__ void prep_f16_rows(uint8_t *smem, const MoeSbBatch &b, const ExpertTable &tab, int e,
                                               int topk, int wi, int g, int r0, int rows, const int32_t *lds_rows,
                                               const int32_t *sorted, const MoeF16 &f) {
-  constexpr int NT = MOE_SB_PREP_THREADS, USTEP = NT / 256, EZ = GLU ? 4 : 2, PER = 16 / EZ, BATCH = GLU ? 2 : 4;
+  constexpr int NT = MOE_SB_PREP_THREADS, USTEP = NT / 256;
+  // chunks of 8 values a lane keeps between the maximum and the conversion
+  constexpr int PREP_CHUNKS = GLU ? 2 : 4;
   const MoeSbProj &P = b.p[0];
   const MoeShape &sh = P.sh;
-  const int vec = b.vec;
-  const int tid = threadIdx.x, w = tid >> 6, L = tid & 63, s = L >> 4, rl = L & 15;
-  const int U = sh.units, kp = U * UNIT_SLOTS, k = sh.k, rb = P.rb;
-  const int stride = kp * EZ + 16;  // bytes per staged row
-  const int q = w & 3, u0 = w >> 2, chunks = kp / PER;
-  auto slot_of = [&](int row) { return lds_rows ? lds_rows[row] : sorted[r0 + row]; };
+  const int tid = threadIdx.x, L = tid & 63, s = L >> 4, rl = L & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int U = sh.units, k = sh.k, rb = P.rb;
+  const int stride = moe_sb_prep_stride(U * UNIT_SLOTS);  // bytes per staged row
+  const int q = w & 3, u0 = w >> 2, chunks = k / 8;
   for (int rb0 = 0; rb0 < 16; rb0 += rb) {
     __syncthreads();  // the previous pass's gathers are done
-    const int nstage = rb * chunks;
-    for (int c0 = 0; c0 < nstage; c0 += BATCH * NT) {
-      u4 v[BATCH], v2[BATCH];
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        v[i] = v2[i] = (u4){0u, 0u, 0u, 0u};
-        const int c = c0 + tid + NT * i;
-        const int rr = c / chunks, cc = c - rr * chunks, row = 16 * g + rb0 + rr;
-        if (c < nstage && row < rows && PER * cc < k) {
-          const int slot = slot_of(row);
-          if constexpr (GLU) {  // k is a multiple of 8
-            v[i] = *(const u4 *)(f.g + (int64_t)slot * f.ldf + 4 * cc);
-            v2[i] = *(const u4 *)(f.u + (int64_t)slot * f.ldf + 4 * cc);
-          } else {
-            const uint16_t *xr = P.x + (int64_t)(slot / topk) * P.ldx + 8 * cc;
-            if (vec) {
-              v[i] = *(const u4 *)xr;
-            } else {
-#pragma unroll
-              for (int l = 0; l < 4; ++l) v[i][l] = (uint32_t)xr[2 * l] | ((uint32_t)xr[2 * l + 1] << 16);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        const int c = c0 + tid + NT * i;
-        const int rr = c / chunks, cc = c - rr * chunks;
+    const int row = 16 * g + rb0 + w;
+    if (w < rb && row < rows) {  // wave-uniform
+      const int slot = __builtin_amdgcn_readfirstlane(lds_rows ? lds_rows[row] : sorted[r0 + row]);
+      // chunk c of the row: eight values as bf16 pairs, or (GLU) as fp32
+      struct Chunk {
+        u4 v[GLU ? 2 : 1];
+      };
+      const uint16_t *xr = GLU ? nullptr : P.x + (int64_t)(slot / topk) * P.ldx;
+      const float *gr = GLU ? f.g + (int64_t)slot * f.ldf : nullptr, *ur = GLU ? f.u + (int64_t)slot * f.ldf : nullptr;
+      auto load = [&](int c) __attribute__((always_inline)) {
+        Chunk h;
         if constexpr (GLU) {
 #pragma unroll
-          for (int l = 0; l < 4; ++l)
-            v[i][l] = __builtin_bit_cast(uint32_t, act_fast(__builtin_bit_cast(float, (uint32_t)v[i][l]), f.act) *
-                                                       __builtin_bit_cast(float, (uint32_t)v2[i][l]));
+          for (int p = 0; p < 2; ++p) {
+            const f4 gv = *(const f4 *)(gr + 8 * c + 4 * p), uv = *(const f4 *)(ur + 8 * c + 4 * p);
+#pragma unroll
+            for (int l = 0; l < 4; ++l) h.v[p][l] = __builtin_bit_cast(uint32_t, act_fast(gv[l], f.act) * uv[l]);
+          }
+        } else if (b.vec) {
+          h.v[0] = *(const u4 *)(xr + 8 * c);
+        } else {
+#pragma unroll
+          for (int l = 0; l < 4; ++l) h.v[0][l] = (uint32_t)xr[8 * c + 2 * l] | ((uint32_t)xr[8 * c + 2 * l + 1] << 16);
         }
-        if (c < nstage) *(u4 *)(smem + (size_t)rr * stride + 16 * cc) = v[i];
-      }
-    }
-    __syncthreads();
-    if (w < rb) {  // wave-uniform: wave w finds the scale of staged row w
-      uint32_t mx = 0;  // as bits: finite magnitudes order as integers
-      for (int c = L; c < chunks; c += 64) {
-        const u4 v = *(const u4 *)(smem + (size_t)w * stride + 16 * c);
+        return h;
+      };
+      // largest finite magnitude as fp32 bits (magnitudes order as integers)
+      auto magnitude = [&](uint32_t mx, const Chunk &h) __attribute__((always_inline)) {
 #pragma unroll
         for (int l = 0; l < 4; ++l) {
           if constexpr (GLU) {
-            const uint32_t a = v[l] & 0x7FFFFFFFu;
-            mx = max(mx, a < 0x7F800000u ? a : 0u);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const uint32_t a = h.v[p][l] & 0x7FFFFFFFu;
+              mx = max(mx, a < 0x7F800000u ? a : 0u);
+            }
           } else {
-            const uint32_t lo = (v[l] & 0x7FFFu) << 16, hi = v[l] & 0x7FFF0000u;
-            mx = max(mx, lo < 0x7F800000u ? lo : 0u);
-            mx = max(mx, hi < 0x7F800000u ? hi : 0u);
+            const uint32_t m2 = pk_max_finite(0u, h.v[0][l]);
+            mx = max(mx, max(m2 << 16, m2 & 0xFFFF0000u));
           }
         }
-      }
+        return mx;
+      };
+      Chunk keep[PREP_CHUNKS];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < PREP_CHUNKS; ++i)
+        if (L + 64 * i < chunks) keep[i] = load(L + 64 * i);
+#pragma unroll
+      for (int i = 0; i < PREP_CHUNKS; ++i)
+        if (L + 64 * i < chunks) mx = magnitude(mx, keep[i]);
+      for (int c = L + 64 * PREP_CHUNKS; c < chunks; c += 64) mx = magnitude(mx, load(c));  // long rows: loaded again below
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
       const float mf = __builtin_bit_cast(float, mx);
       const int ex = mf > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mf) : 0;
       if (L == 0)
         for (int pc = 0; pc < b.count; ++pc)
-          f.xs[pc][(size_t)wi * MOE_SB_ROWS + 16 * g + rb0 + w] =
-              ldexpf(1.f, min(127, -ex - f.xscale[pc * sh.num_experts + e]));
-      // ascending chunks: fp16 values (GLU: half as long) overwrite only what
-      // this and earlier steps have read
-      uint8_t *row = smem + (size_t)w * stride;
-      auto half = [&](float v) __attribute__((always_inline)) {
-        return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)ldexpf(v, ex));
-      };
-      for (int c = L; c < chunks; c += 64) {
-        const u4 v = *(const u4 *)(row + 16 * c);
+          f.xs[pc][(size_t)wi * MOE_SB_ROWS + row] = ldexpf(1.f, min(127, -ex - f.xscale[pc * sh.num_experts + e]));
+      uint8_t *dst = smem + (size_t)w * stride;
+      auto put = [&](int c, const Chunk &h) __attribute__((always_inline)) {
+        u4 o;
         if constexpr (GLU) {
-          u2 h;
 #pragma unroll
-          for (int l = 0; l < 2; ++l)
-            h[l] = half(__builtin_bit_cast(float, (uint32_t)v[2 * l])) |
-                   (half(__builtin_bit_cast(float, (uint32_t)v[2 * l + 1])) << 16);
-          *(u2 *)(row + 8 * c) = h;
+          for (int l = 0; l < 4; ++l) {  // rounded to nearest: these values are not bf16
+            const _Float16 lo = (_Float16)ldexpf(__builtin_bit_cast(float, (uint32_t)h.v[l >> 1][2 * (l & 1)]), ex);
+            const _Float16 hi = (_Float16)ldexpf(__builtin_bit_cast(float, (uint32_t)h.v[l >> 1][2 * (l & 1) + 1]), ex);
+            o[l] = (uint32_t)__builtin_bit_cast(uint16_t, lo) | ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
+          }
         } else {
-          u4 h;
-#pragma unroll
-          for (int l = 0; l < 4; ++l)
-            h[l] = half(bf16_bits_to_f32(v[l] & 0xFFFFu)) |
-                   (half(__builtin_bit_cast(float, v[l] & 0xFFFF0000u)) << 16);
-          *(u4 *)(row + 16 * c) = h;
+          o = scaled_f16(h.v[0], ex);
         }
-      }
+        *(u4 *)(dst + 16 * c) = o;
+      };
+#pragma unroll
+      for (int i = 0; i < PREP_CHUNKS; ++i)
+        if (L + 64 * i < chunks) put(L + 64 * i, keep[i]);
+      for (int c = L + 64 * PREP_CHUNKS; c < chunks; c += 64) put(c, load(c));
     }
     __syncthreads();
     if (rl < rb0 || rl >= rb0 + rb) continue;  // lane-uniform per pass; no barrier below
+    // rows past the item's hold what the LDS held: their products are never
+    // stored, and no other row's product sees them
     const uint16_t *xrow = (const uint16_t *)(smem + (size_t)(rl - rb0) * stride);
     for (int pu = u0; pu < U * b.count; pu += USTEP) {
       const int pc = pu >= U ? 1 : 0, u = pu - pc * U;  // at most two projections
@@ -223,6 +217,7 @@ __device__ __forceinline__ void prep_f16_rows(uint8_t *smem, const MoeSbBatch &b
     }
   }
 }
+
 // Block (work item, row group g), MOE_SB_PREP_THREADS threads: the group's
 // 16 activation rows are staged whole in LDS (rb rows per pass, coalesced
 // 16-byte loads when x and ldx allow them; the row stride carries 16 bytes
@@ -766,7 +761,7 @@ hipError_t launch_moe_sb_f16(MoeSbBatch &b, const ExpertTable &tab, int topk, co
   size_t prep_lds = 0;
   int tgroups = 1;
   for (int c = 0; c < b.count; ++c) {
-    const size_t stride = (size_t)b.p[c].sh.units * UNIT_SLOTS * (glu ? 4 : 2) + 16;
+    const size_t stride = moe_sb_prep_stride(b.p[c].sh.units * UNIT_SLOTS);
     b.p[c].rb = (int)std::max<size_t>(1, std::min<size_t>(16, MOE_SB_PREP_LDS / stride));
     prep_lds = std::max(prep_lds, b.p[c].rb * stride);
     tgroups = std::max(tgroups, (b.p[c].sh.n_tiles + MOE_SB_TILES - 1) / MOE_SB_TILES);

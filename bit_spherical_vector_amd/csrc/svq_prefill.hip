@@ -1226,13 +1226,17 @@ __global__ __launch_bounds__(256) void ffn_prep_kernel(FfnGemmArgs a) {
       u4 v[B];
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const int q = min(q0 + 256 * b, tot - 1), rr = q / n8;
-        v[b] = *(const u4 *)(a.x + (int64_t)(r0 + rr) * a.ldx + 8 * (q - rr * n8));
+        int rr = 0, c = min(q0 + 256 * b, tot - 1);
+        for (; c >= n8; c -= n8) ++rr;  // at most rpb - 1 steps
+        v[b] = *(const u4 *)(a.x + (int64_t)(r0 + rr) * a.ldx + 8 * c);
       }
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const int q = q0 + 256 * b, rr = q / n8;
-        if (q < tot) *(u4 *)(s_rows + (size_t)rr * ks_ + 8 * (q - rr * n8)) = v[b];
+        int rr = 0, c = q0 + 256 * b;
+        if (c < tot) {
+          for (; c >= n8; c -= n8) ++rr;
+          *(u4 *)(s_rows + (size_t)rr * ks_ + 8 * c) = v[b];
+        }
       }
     }
   } else {
@@ -1241,26 +1245,42 @@ __global__ __launch_bounds__(256) void ffn_prep_kernel(FfnGemmArgs a) {
   }
   __syncthreads();
   const int rr = tid % rpb, step = 256 / rpb;
-  const uint16_t *row = s_rows + (size_t)rr * ks_;
+  uint16_t *row = s_rows + (size_t)rr * ks_;
   const bool on = rr < live;
-  // largest finite magnitude of the row (infinities and NaN keep their value
-  // under any scale)
-  uint32_t mx = 0;
+  // the row's largest finite magnitude (infinities and NaN keep their value
+  // under any scale), then the row in place as scaled fp16, once for every
+  // matrix that gathers it
+  uint32_t m2 = 0;
   if (on)
     for (int c = tid / rpb; c < K / 8; c += step) {
       const u4 v = *(const u4 *)(row + 8 * c);
 #pragma unroll
-      for (int l = 0; l < 4; ++l) {
-        const uint32_t lo = v[l] & 0x7FFFu, hi = (v[l] >> 16) & 0x7FFFu;
-        mx = max(mx, lo < 0x7F80u ? lo : 0u);
-        mx = max(mx, hi < 0x7F80u ? hi : 0u);
-      }
+      for (int l = 0; l < 4; ++l) m2 = pk_max_mag(m2, v[l]);
     }
-  if (on) atomicMax(&s_mx[rr], mx);
+  if (on) atomicMax(&s_mx[rr], max(m2 & 0xFFFFu, m2 >> 16));
   __syncthreads();
-  const float mf = bf16_bits_to_f32(s_mx[rr]);
+  uint32_t mx = s_mx[rr];
+  const bool odd = mx >= 0x7F80u;
+  if (__syncthreads_or(odd ? 1 : 0)) {
+    if (tid < 8) s_mx[tid] = 0;
+    __syncthreads();
+    m2 = 0;
+    if (on)
+      for (int c = tid / rpb; c < K / 8; c += step) {
+        const u4 v = *(const u4 *)(row + 8 * c);
+#pragma unroll
+        for (int l = 0; l < 4; ++l) m2 = pk_max_finite(m2, v[l]);
+      }
+    if (on) atomicMax(&s_mx[rr], max(m2 & 0xFFFFu, m2 >> 16));
+    __syncthreads();
+    mx = s_mx[rr];
+  }
+  const float mf = bf16_bits_to_f32(mx);
   const int e = mf > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mf) : 0;
   if (cs == 0 && tid < rpb) a.rs[r0 + rr] = on ? ldexpf(1.f, -e) : 0.f;
+  if (on)
+    for (int c = tid / rpb; c < K / 8; c += step) *(u4 *)(row + 8 * c) = scaled_f16(*(const u4 *)(row + 8 * c), e);
+  __syncthreads();
   const int S = Kp / P_BK;
   for (int j = 0; j < a.jobs; ++j) {
     const MatView &w = a.job[j].w;
@@ -1277,11 +1297,7 @@ __global__ __launch_bounds__(256) void ffn_prep_kernel(FfnGemmArgs a) {
         // so a chunk is inside k or all padding
         u4 v;
 #pragma unroll
-        for (int l = 0; l < 4; ++l) {
-          const _Float16 lo = (_Float16)ldexpf(bf16_bits_to_f32(row[pv[b][l] & 0xFFFFu]), e);
-          const _Float16 hi = (_Float16)ldexpf(bf16_bits_to_f32(row[pv[b][l] >> 16]), e);
-          v[l] = (uint32_t)__builtin_bit_cast(uint16_t, lo) | ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
-        }
+        for (int l = 0; l < 4; ++l) v[l] = (uint32_t)row[pv[b][l] & 0xFFFFu] | ((uint32_t)row[pv[b][l] >> 16] << 16);
         if (!on || 8 * c >= K) v = (u4){0u, 0u, 0u, 0u};
         if (c < c_hi) *(u4 *)(xb + xb_frag_offset(r0 + rr, 8 * c, S)) = v;
       }

@@ -13,7 +13,7 @@
  * enter the matrix cores as fp16 (R*D rounded to 11 bits under the matrix's
  * power-of-two scale) and activations as fp16 after a power-of-two scale per
  * row (a bf16 value keeps its bits down to 2^-29 of the row's largest finite
- * magnitude; below, the error is at most 2^-40 of it); matrices whose tables
+ * magnitude; below, the error is at most 2^-38 of it); matrices whose tables
  * admit no exact split run svq.h's bf16 form.  Accumulation is fp32.  Bias,
  * activation, gating, residual and the sum over a token's experts are fp32;
  * each output is rounded once, to nearest even.  The inner activation of an
