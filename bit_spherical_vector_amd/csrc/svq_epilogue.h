@@ -30,7 +30,8 @@ __device__ __forceinline__ float act_apply(float v, int act) {
   }
 }
 
-// Cheaper forms for values that are rounded to 11 bits or fewer next: the
+// Cheaper forms for values that are rounded to 11 bits or fewer next, or are
+// sums over weights so rounded: the
 // hardware's exp2 and reciprocal (each within about 1 ulp) in place of expf
 // and a division; the argument's rounding adds |v| 2^-24.
 template <int ACT>

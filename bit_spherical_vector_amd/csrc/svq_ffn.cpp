@@ -119,9 +119,9 @@ svq_status ffn_gemm(const svq_handle *const *w, int jobs, const void *x, int64_t
     a.job[j].w = matrix_view(w[j]);
     a.job[j].xb = (uint16_t *)(ws + o_xb[j]);
     a.job[j].part = parts ? (float *)(ws + o_part[j]) : nullptr;
-    a.job[j].xinv = std::ldexp(1.0f, -w[j]->xscale_log2);
+    a.job[j].xexp = -w[j]->xscale_log2;
   }
-  a.rs = (float *)(ws + o_rs);
+  a.rs = (int32_t *)(ws + o_rs);
   if (a.n_cnt) {
     a.swap = (float *)(ws + o_swap);
     a.cnt = (int32_t *)(ws + o_cnt);

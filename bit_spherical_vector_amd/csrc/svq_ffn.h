@@ -62,7 +62,7 @@ struct FfnGemmJob {
   MatView w;
   uint16_t *xb;  // fp16 activations in fragment order (workspace)
   float *part;   // fp32 partial tiles [splits][m_pad][n_pad], or null: none
-  float xinv;    // 2^-xscale_log2 of the matrix's exact split
+  int32_t xexp;  // -xscale_log2 of the matrix's exact split
 };
 struct FfnGemmArgs {
   FfnGemmJob job[2];
@@ -70,7 +70,7 @@ struct FfnGemmArgs {
   int32_t rpb, csplit;  // prep: rows per block, chunk ranges
   const uint16_t *x;
   int64_t ldx;
-  float *rs;      // inverse row scales [m_pad] (workspace)
+  int32_t *rs;    // exponents of the inverse row scales [m_pad] (workspace)
   float *swap;    // gated pair without partial tiles: [tiles][2] tiles of 256 x 256 sums
   int32_t *cnt;   // and their arrivals
   int32_t n_cnt;

@@ -407,19 +407,19 @@ struct MoeSbBatch {
   int32_t yvec;  // every y and ldy allow 16-byte stores
 };
 // The fp16 form (svq_moe_ffn): activations in fp16 after a power-of-two scale
-// per row, weights RNE_fp16(R*D*2^s).  The prep launch writes each staged
-// row's inverse scale, its expert's 2^-s included, to xs[projection]
+// per row, weights RNE_fp16(R*D*2^s).  The prep launch writes the exponent of
+// each staged row's inverse scale, its expert's -s included, to xs[projection]
 // [work item * MOE_SB_ROWS + row]; with g set the rows are act(g) * u of the
 // slot instead of x (one projection).
 struct MoeF16 {
   int8_t xscale[MAX_EXPERTS];  // s of table entry projection * E + expert
-  float *xs[MOE_BATCH_MAX];
+  int32_t *xs[MOE_BATCH_MAX];
   const float *g, *u;          // [slots][ldf], 16-byte aligned rows
   int64_t ldf;
   int32_t act;
 };
 struct MoeF16Scales {
-  const float *xs[MOE_BATCH_MAX];
+  const int32_t *xs[MOE_BATCH_MAX];
 };
 hipError_t launch_moe_sb_f16(MoeSbBatch &b, const ExpertTable &tab, int topk, const MoeRoute &route,
                              int32_t *work, int32_t *nwork, int32_t *sorted, int max_work,

@@ -1900,7 +1900,7 @@ hipError_t launch_moe_ffn_grouped(const MoeFfnArgs &f, void *ws, size_t *need, h
       }
       b.p[j].sh = sh;
       b.p[j].xa = p + o_xa[c];
-      h.xs[j] = (float *)(p + o_xs[c]);
+      h.xs[j] = (int32_t *)(p + o_xs[c]);
     };
     for (int c0 = 0; c0 < 2; c0 += per) {
       std::memset(&b, 0, sizeof(b));

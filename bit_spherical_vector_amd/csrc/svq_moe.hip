@@ -170,7 +170,7 @@ __device__ __forceinline__ void prep_f16_rows(uint8_t *smem, const MoeSbBatch &b
       const int ex = mf > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mf) : 0;
       if (L == 0)
         for (int pc = 0; pc < b.count; ++pc)
-          f.xs[pc][(size_t)wi * MOE_SB_ROWS + row] = ldexpf(1.f, min(127, -ex - f.xscale[pc * sh.num_experts + e]));
+          f.xs[pc][(size_t)wi * MOE_SB_ROWS + row] = -ex - f.xscale[pc * sh.num_experts + e];
       uint8_t *dst = smem + (size_t)w * stride;
       auto put = [&](int c, const Chunk &h) __attribute__((always_inline)) {
         u4 o;
@@ -468,13 +468,13 @@ __device__ __forceinline__ void moe_slice_barrier() { asm volatile("s_waitcnt lg
 // direct global-to-LDS loads the slice barrier had to wait for every
 // outstanding load, codes included: those loads do not complete in order
 // with the others, and nothing tracks their data per register.)
-// F16: the fp16 form; xs: the item's inverse row scales.
+// F16: the fp16 form; xs: the exponents of the item's inverse row scales.
 template <int G, bool F16 = false>
 __device__ __forceinline__ void moe_sb_block(const MatView &w, int tg, int wi, int r0, int rows,
                                              const int32_t *__restrict__ sorted,
                                              const uint8_t *__restrict__ xa, void *__restrict__ y,
                                              int64_t ldy, int ydt, int yvec, uint8_t *smem,
-                                             const float *__restrict__ xs = nullptr) {
+                                             const int32_t *__restrict__ xs = nullptr) {
   const int U = w.units, NS = 4 * U;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -613,9 +613,13 @@ __device__ __forceinline__ void moe_sb_block(const MatView &w, int tg, int wi, i
   if constexpr (F16) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const f4 sc = *(const f4 *)(xs + 16 * g + 4 * (int)s);  // rows 16g + 4s .. + 3
+      int re[4];  // rows 16g + 4s .. + 3
 #pragma unroll
-      for (int t = 0; t < MOE_SB_TW; ++t) C[t][g] *= sc;
+      for (int i = 0; i < 4; ++i) re[i] = xs[16 * g + 4 * (int)s + i];
+#pragma unroll
+      for (int t = 0; t < MOE_SB_TW; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) C[t][g][i] = ldexpf(C[t][g][i], re[i]);
     }
   }
   // The outputs leave through LDS: the block's item rows x its 128 columns
@@ -668,8 +672,8 @@ __device__ __forceinline__ void moe_sb_block(const MatView &w, int tg, int wi, i
 }
 
 // fa: nothing, or the MoeF16Scales of the fp16 form.
-__device__ __forceinline__ const float *item_scales(int, int) { return nullptr; }
-__device__ __forceinline__ const float *item_scales(int pc, int wi, const MoeF16Scales &f) {
+__device__ __forceinline__ const int32_t *item_scales(int, int) { return nullptr; }
+__device__ __forceinline__ const int32_t *item_scales(int pc, int wi, const MoeF16Scales &f) {
   return f.xs[pc] + (size_t)wi * MOE_SB_ROWS;
 }
 template <typename... FA>
@@ -698,7 +702,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void m
   const int wi = l / tgroups, tg = l - wi * tgroups;
   const int e = work[3 * wi], r0 = work[3 * wi + 1], rows = work[3 * wi + 2] - r0;
   const MatView w = expert_view(sh, tab, pc * sh.num_experts + e);
-  const float *xs = item_scales(pc, wi, fa...);
+  const int32_t *xs = item_scales(pc, wi, fa...);
   switch ((rows + 15) >> 4) {  // block-uniform
     case 1: moe_sb_block<1, F16>(w, tg, wi, r0, rows, sorted, xa, y, ldy, ydt, yvec, smem, xs); break;
     case 2: moe_sb_block<2, F16>(w, tg, wi, r0, rows, sorted, xa, y, ldy, ydt, yvec, smem, xs); break;

@@ -1045,16 +1045,27 @@ __device__ __forceinline__ void act16(f16x &v, int act) {  // act is uniform
   }
 }
 
-// The 16 scales of accumulator block rows row0 + (e & 3) + 8(e >> 2) (row0 a
-// multiple of 4, plus 4 for the upper lane half), times xinv.
-__device__ __forceinline__ f16x row_scales(const float *rs, int row0, float xinv) {
-  f16x r;
+// The 16 row exponents of accumulator block rows row0 + (e & 3) + 8(e >> 2)
+// (row0 a multiple of 4, plus 4 for the upper lane half).
+typedef int i4 __attribute__((ext_vector_type(4)));
+typedef int i16x __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ i16x row_exps(const int32_t *rs, int row0) {
+  i16x r;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const f4 v = *(const f4 *)(rs + row0 + 8 * q);
+    const i4 v = *(const i4 *)(rs + row0 + 8 * q);
 #pragma unroll
-    for (int l = 0; l < 4; ++l) r[4 * q + l] = v[l] * xinv;
+    for (int l = 0; l < 4; ++l) r[4 * q + l] = v[l];
   }
+  return r;
+}
+// v times 2^(row exponent + the matrix's): one instruction a value, and no
+// scale that itself leaves the range of fp32 (a row of 2^-120 under a
+// matrix's 2^-20).
+__device__ __forceinline__ f16x scaled16(const f16x &v, const i16x &re, int xexp) {
+  f16x r;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) r[e] = ldexpf(v[e], re[e] + xexp);
   return r;
 }
 
@@ -1103,15 +1114,15 @@ struct PartTile {
 struct LinTile {
   static constexpr bool on = true, partial = false, f16 = true;
   EpiArgs a;
-  const float *rs;
-  float xinv;
+  const int32_t *rs;
+  int xexp;
   template <int NI, int NJ, int TM, int TN>
   __device__ __forceinline__ void finish(const DqTile &T, f16x (&C)[NI][NJ], uint8_t *, int wm, int wn, int lane,
                                          int rt0) const {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int rr0 = TM * wm + 32 * i + 4 * (lane >> 5);
-      const f16x sc = row_scales(rs, T.m0 + rr0, xinv);
+      const i16x re = row_exps(rs, T.m0 + rr0);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const int n = rt0 * UNIT_ROWS + TN * wn + 32 * j + (lane & 31), nc = min(n, T.nlim - 1);
@@ -1123,7 +1134,7 @@ struct LinTile {
             res[e] = load_f(a.res, (size_t)(T.m0 + r) * a.ldr + nc, a.res_f32);
           }
         }
-        f16x v = C[i][j] * sc;
+        f16x v = scaled16(C[i][j], re, xexp);
         if (a.bias) v += load_f(a.bias, nc, a.bias_f32);
         act16(v, a.act);
         if (a.res) v += res;
@@ -1138,8 +1149,8 @@ struct GluTile {
   static constexpr bool on = true, partial = false, f16 = true;
   const void *bias_g, *bias_u;
   int bias_f32, act;
-  const float *rs;
-  float xinv_g, xinv_u;
+  const int32_t *rs;
+  int xexp_g, xexp_u;
   bool up;          // this block's matrix
   uint64_t *own;    // where this block leaves its tile: [i][j][8][threads] pairs of sums
   const uint64_t *other;  // and its partner (both may be under way at once)
@@ -1174,7 +1185,7 @@ struct GluTile {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int rr0 = TM * wm + 32 * i + 4 * (lane >> 5);
-      const f16x sc = row_scales(rs, T.m0 + rr0, 1.f);
+      const i16x re = row_exps(rs, T.m0 + rr0);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         f16x o;
@@ -1186,7 +1197,7 @@ struct GluTile {
           o[2 * e + 1] = __builtin_bit_cast(float, (uint32_t)(v >> 32));
         }
         const int n = rt0 * UNIT_ROWS + TN * wn + 32 * j + (lane & 31), nc = min(n, T.nlim - 1);
-        f16x g = (up ? o : C[i][j]) * (sc * xinv_g), u = (up ? C[i][j] : o) * (sc * xinv_u);
+        f16x g = scaled16(up ? o : C[i][j], re, xexp_g), u = scaled16(up ? C[i][j] : o, re, xexp_u);
         if (bias_g) g += load_f(bias_g, nc, bias_f32);
         if (bias_u) u += load_f(bias_u, nc, bias_f32);
         act16(g, act);
@@ -1197,8 +1208,8 @@ struct GluTile {
 };
 
 // Prep: fp16 activations of every matrix of the call in fragment order
-// (xb_frag_offset), rows >= m and slots >= k zero, and each row's inverse
-// scale.  A block stages rpb rows (whole, so that the row's scale is known)
+// (xb_frag_offset), rows >= m and slots >= k zero, and the exponent of each
+// row's inverse scale.  A block stages rpb rows (whole, so that the row's scale is known)
 // and writes one of csplit chunk ranges for each matrix.  The blocks of one
 // 32-row fragment block follow each other on one XCD (blocks go to the XCDs
 // round-robin), so the 16 rpb bytes a block contributes to a run of 512 meet
@@ -1277,7 +1288,7 @@ __global__ __launch_bounds__(256) void ffn_prep_kernel(FfnGemmArgs a) {
   }
   const float mf = bf16_bits_to_f32(mx);
   const int e = mf > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mf) : 0;
-  if (cs == 0 && tid < rpb) a.rs[r0 + rr] = on ? ldexpf(1.f, -e) : 0.f;
+  if (cs == 0 && tid < rpb) a.rs[r0 + rr] = on ? -e : 0;
   if (on)
     for (int c = tid / rpb; c < K / 8; c += step) *(u4 *)(row + 8 * c) = scaled_f16(*(const u4 *)(row + 8 * c), e);
   __syncthreads();
@@ -1355,14 +1366,14 @@ __global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2
   DqTile T;
   int jn, tile, sp;
   if (!ffn_tile(a, 256, T, jn, tile, sp)) return;
-  dq_tile_w8<LinTile>(T, smem, LinTile{a.epi, a.rs, a.job[0].xinv});
+  dq_tile_w8<LinTile>(T, smem, LinTile{a.epi, a.rs, a.job[0].xexp});
 }
 __global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void ffn_glu_kernel(FfnGemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   DqTile T;
   int jn, tile, sp;
   if (!ffn_tile(a, 256, T, jn, tile, sp)) return;
-  const GluTile g{a.bias_g, a.epi.bias, a.epi.bias_f32, a.epi.act, a.rs, a.job[0].xinv, a.job[1].xinv, jn != 0,
+  const GluTile g{a.bias_g, a.epi.bias, a.epi.bias_f32, a.epi.act, a.rs, a.job[0].xexp, a.job[1].xexp, jn != 0,
                   (uint64_t *)a.swap + (size_t)(2 * tile + jn) * (256 * 256 / 2),
                   (const uint64_t *)a.swap + (size_t)(2 * tile + 1 - jn) * (256 * 256 / 2), a.cnt + tile};
   dq_tile_w8<GluTile>(T, smem, g);
@@ -1374,7 +1385,7 @@ __global__ __launch_bounds__(256) void ffn_reduce_kernel(FfnGemmArgs a) {
   const int n_all = a.job[0].w.n, per_row = (n_all + 1023) / 1024;
   const int row = (int)blockIdx.x / per_row, n = ((int)blockIdx.x % per_row) * 1024 + 4 * (int)threadIdx.x;
   if (n >= n_all) return;
-  const float rs = a.rs[row];
+  const int re = a.rs[row];
   f4 v[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -1382,7 +1393,8 @@ __global__ __launch_bounds__(256) void ffn_reduce_kernel(FfnGemmArgs a) {
     if (j < a.jobs) {
       const float *p = a.job[j].part + (size_t)row * a.n_pad + n;
       for (int s = 0; s < a.splits; ++s) v[j] += *(const f4 *)(p + (size_t)s * a.m_pad * a.n_pad);
-      v[j] *= rs * a.job[j].xinv;
+#pragma unroll
+      for (int l = 0; l < 4; ++l) v[j][l] = ldexpf(v[j][l], re + a.job[j].xexp);
     }
   }
   if (a.jobs == 1) {

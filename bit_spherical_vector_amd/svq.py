@@ -709,7 +709,8 @@ class _Call:
         self.fn = getattr(LIB, name)
         self.stream = None if stream is None else int(stream.cuda_stream)
         nbytes = ctypes.c_size_t(0)
-        _check(self.fn(*self.args, None, ctypes.byref(nbytes), None), f"{name} (workspace query)")
+        with torch.cuda.device(device):  # the plan follows the device's compute units
+            _check(self.fn(*self.args, None, ctypes.byref(nbytes), None), f"{name} (workspace query)")
         if workspace is None or workspace.numel() * workspace.element_size() < nbytes.value:
             workspace = torch.empty(max(nbytes.value, 1), dtype=torch.uint8, device=device)
         self.workspace = workspace

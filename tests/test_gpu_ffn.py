@@ -421,6 +421,66 @@ def _block_weights(svq, k=264, f=520, e=6, fe=104):
     return mats, [s[0] for s in sets], [*map(svq.pack, mats), router, *[s[1] for s in sets]]
 
 
+def _graded(m, k, seed):
+    """Activations of 2^-4 .. 2^2 in bf16, either sign: times 2^-122 .. 2^118
+    they are normal numbers still."""
+    v = vec(m * k, torch.float32, seed).view(m, k)
+    return (torch.sign(v) * v.abs().clamp(2.0 ** -4, 4.0)).bfloat16()
+
+
+@pytest.mark.parametrize("m", [1, 3, 7, 20, 150, 300])
+@pytest.mark.parametrize("shift", [-122, 100])
+def test_activations_of_any_power_of_two(svq, m, shift):
+    """Every rounding of a product is relative to a power-of-two scale, so x
+    times 2^shift gives y times 2^shift, to the last bit while every sum is
+    normal; one below 2^-126 is held in steps of 2^-149, half of one for each
+    of at most k + 64 roundings.  The gated pair: with the up matrix's sums
+    far below its bias of 1 it is the gate's product, with bias 0 and shift
+    halved it is homogeneous of degree two."""
+    n, k = 72, 1032
+    tiny = (k + 64) * 2.0 ** -150
+    pg, pu = [svq.pack(synth.random_matrix(n, k, bd, seed=(94, bd, k))) for bd in (7, 8)]
+    x = _graded(m, k, 16)
+    xs = (x.float() * 2.0 ** shift).bfloat16()
+    y = svq.linear_epilogue(pg, x, out_dtype=torch.float32)
+    ys = svq.linear_epilogue(pg, xs, out_dtype=torch.float32)
+    assert (np.abs(f64(ys) - f64(y) * 2.0 ** shift) <= tiny).all()
+    half = (x.float() * 2.0 ** (shift // 2)).bfloat16()
+    z = svq.linear_glu(pg, pu, x, act="none", out_dtype=torch.float32)
+    zs = svq.linear_glu(pg, pu, half, act="none", out_dtype=torch.float32)
+    assert (np.abs(f64(zs) - f64(z) * 2.0 ** shift) <= tiny).all()
+    if shift < 0:
+        one = torch.ones(n, device="cuda")
+        zs = svq.linear_glu(pg, pu, xs, act="none", bias_up=one, out_dtype=torch.float32)
+        W = so.linear_from_inputs(synth.random_matrix(n, k, 7, seed=(94, 7, k)), np.zeros((1, k), dtype=np.uint16))[1]
+        p, a = f64(xs) @ W.T, np.abs(f64(xs)) @ np.abs(W).T
+        # as product(): sums, the weights' rounding, subnormal weights (2^-39
+        # of the largest, 0.2, times k values of x, against a weight of 2^-6 at
+        # least on average: 2^-25 k of the sum over them)
+        assert (np.abs(f64(zs) - p) <= ((k + 64) * U32 + 2.0 ** -11 + k * 2.0 ** -25) * a + tiny).all()
+
+
+@pytest.mark.parametrize("m", [5, 90])
+@pytest.mark.parametrize("shift", [-58, 50])
+def test_moe_ffn_activations_of_any_power_of_two(svq, m, shift):
+    """Without an activation the expert layer is homogeneous of degree two in
+    x: h of about 2^(2 shift) and its scale reach the ends of fp32.  An h
+    below 2^-126 is held in steps of 2^-149, which may turn its rounding to
+    fp16 (11 bits) the other way: one step of 2^-137 at most, times a weight."""
+    e, f, k, topk = 3, 104, 264, 2
+    gm, gp = experts(svq, e, f, k, 95)
+    um, up = experts(svq, e, f, k, 96)
+    dm, dp = experts(svq, e, k, f, 97)
+    x = _graded(m, k, 17)
+    g = torch.Generator().manual_seed(18)
+    ids = torch.stack([torch.randperm(e, generator=g)[:topk] for _ in range(m)]).to(torch.int32).cuda()
+    wt = torch.rand((m, topk), generator=g).cuda()
+    y = svq.moe_ffn(gp, up, dp, x, ids, wt, act="none", out_dtype=torch.float32)
+    ys = svq.moe_ffn(gp, up, dp, (x.float() * 2.0 ** shift).bfloat16(), ids, wt, act="none", out_dtype=torch.float32)
+    wmax = max(float(np.abs(so.linear_from_inputs(d, np.zeros((1, f), dtype=np.uint16))[1]).sum(axis=1).max()) for d in dm)
+    assert (np.abs(f64(ys) - f64(y) * 2.0 ** (2 * shift)) <= topk * (wmax + 2) * 2.0 ** -137).all()
+
+
 @pytest.mark.parametrize("m", [1, 4, 16, 48, 300])
 def test_run_of_them_together(svq, m):
     """The whole block against 64 bits, stage by stage on the stages' own
