@@ -33,27 +33,40 @@ bool has_split(const svq_handle *w) {
   return w->xscale_log2 != SVQ_NO_EXACT_SPLIT && w->xscale_log2 >= -120 && w->xscale_log2 <= 120;
 }
 
-// K ranges of the tile launch.  64-row tiles: about two blocks per compute
-// unit.  256-row tiles, one block per compute unit: the count that takes the
-// least time when a round of blocks costs UNIT a unit of 512 channels and
-// EDGE for its start and its stores, and a reduce launch follows a split.
-int gemm_splits(int tiles, int units, int bm, double part_mb) {
+// Tiles of a job that one block sums whole, and the K ranges of the others.
+struct TilePlan {
+  int full, splits, ups;
+};
+// 64-row tiles: all in ranges, for about two blocks per compute unit.
+// 256-row tiles, one block per compute unit: rounds of whole tiles, then the
+// tiles that would fill only a part of the last round in K ranges; the number
+// of rounds and ranges that takes the least time when a round of blocks costs
+// UNIT a unit of 512 channels and EDGE for its start and its stores, and a
+// reduce launch follows partial tiles.  (Either all tiles whole or all in
+// ranges: gated pair 9728 x 2560 at 2048 rows 251 us against 239, at 1024 rows
+// 160 against 142; one 9728 x 2560 matrix at 2048 rows 235 against 179.)
+TilePlan tile_plan(int tiles, int jobs, int units, int bm) {
   const int cus = compute_units();
   if (bm == 64) {
-    const int64_t per = ((int64_t)tiles * units + 2 * cus - 1) / (2 * cus);
-    return tiles >= 2 * cus ? 1 : (int)((units + per - 1) / per);
+    const int all = tiles * jobs;
+    const int64_t per = all >= 2 * cus ? units : ((int64_t)all * units + 2 * cus - 1) / (2 * cus);
+    return {0, (int)((units + per - 1) / per), (int)per};
   }
-  constexpr double UNIT = 13.5, EDGE = 8.0, REDUCE = 4.0, REDUCE_MB = 0.25;  // us
-  int best = 1;
-  double t_best = 1e30;
-  for (int s = 1; s <= units && s <= 16; ++s) {
-    const int ups = (units + s - 1) / s;
-    if ((units + ups - 1) / ups != s) continue;
-    const double t = (double)((tiles * s + cus - 1) / cus) * (ups * UNIT + EDGE) +
-                     (s > 1 ? REDUCE + REDUCE_MB * part_mb * s : 0.0);
-    if (t < t_best) {
-      t_best = t;
-      best = s;
+  constexpr double UNIT = 13.5, EDGE = 8.0, REDUCE = 4.0, REDUCE_MB = 0.25, TILE_MB = 256 * 256 * 4e-6;  // us
+  auto rounds = [&](int64_t blocks, int ups) { return (double)((blocks + cus - 1) / cus) * (ups * UNIT + EDGE); };
+  TilePlan best = {tiles, 1, units};
+  double t_best = rounds((int64_t)tiles * jobs, units);
+  for (int r = 0; r <= (int64_t)tiles * jobs / cus; ++r) {
+    const int full = (int)((int64_t)r * cus / jobs), tail = tiles - full;
+    for (int s = 2; s <= units && s <= 16; ++s) {
+      const int ups = (units + s - 1) / s;
+      if ((units + ups - 1) / ups != s) continue;
+      const double t = rounds((int64_t)full * jobs, units) + rounds((int64_t)tail * jobs * s, ups) + REDUCE +
+                       REDUCE_MB * TILE_MB * tail * jobs * s;
+      if (tail > 0 && t < t_best) {
+        t_best = t;
+        best = {full, s, ups};
+      }
     }
   }
   return best;
@@ -75,14 +88,14 @@ svq_status ffn_gemm(const svq_handle *const *w, int jobs, const void *x, int64_t
   a.m_pad = (int)((m + bm - 1) / bm) * bm;
   a.tiles_m = a.m_pad / bm;
   a.tiles_n = prefill_tiles_n(w[0]->n_tiles);
-  a.n_pad = a.tiles_n * PREFILL_BN;
   if ((int64_t)a.tiles_m * a.tiles_n > (1 << 28)) return SVQ_ERR_UNSUPPORTED;  // tile indexes are 32-bit
   const int units = w[0]->units, tiles = a.tiles_m * a.tiles_n;
-  const double part_mb = (double)jobs * a.m_pad * a.n_pad * 4e-6;
-  const int want = gemm_splits(tiles * jobs, units, bm, part_mb);
-  a.ups = (units + want - 1) / want;
-  a.splits = (units + a.ups - 1) / a.ups;
-  const bool parts = bm == 64 || a.splits > 1;
+  const TilePlan plan = tile_plan(tiles, jobs, units, bm);
+  a.full = plan.full;
+  a.splits = plan.splits;
+  a.ups = plan.ups;
+  const int tail = tiles - a.full;
+  a.part_ld = (a.tiles_n - a.full / a.tiles_m) * PREFILL_BN;
   // prep: few rows per block (2 rows of 2560, 4096 and 9728 channels: 246, 77
   // and 136 us a call at 2048 rows; 4: 247, 78, 138; 8: 249, 80, -), chunk
   // ranges for about 512 blocks
@@ -101,12 +114,12 @@ svq_status ffn_gemm(const svq_handle *const *w, int jobs, const void *x, int64_t
   const size_t o_rs = take((size_t)a.m_pad * 4);
   size_t o_xb[2], o_part[2] = {0, 0}, o_swap = 0, o_cnt = 0;
   for (int j = 0; j < jobs; ++j) o_xb[j] = take((size_t)a.m_pad * units * UNIT_SLOTS * 2);
-  if (parts) {
-    for (int j = 0; j < jobs; ++j) o_part[j] = take((size_t)a.splits * a.m_pad * a.n_pad * 4);
-  } else if (jobs == 2) {
-    o_swap = take((size_t)tiles * 2 * 256 * 256 * 4);
-    o_cnt = take((size_t)tiles * 4);
-    a.n_cnt = tiles;
+  if (tail > 0)
+    for (int j = 0; j < jobs; ++j) o_part[j] = take((size_t)a.splits * a.m_pad * a.part_ld * 4);
+  if (jobs == 2 && a.full > 0) {
+    o_swap = take((size_t)a.full * 2 * 256 * 256 * 4);
+    o_cnt = take((size_t)a.full * 4);
+    a.n_cnt = a.full;
   }
   if (!workspace) {
     *bytes = off;
@@ -118,7 +131,7 @@ svq_status ffn_gemm(const svq_handle *const *w, int jobs, const void *x, int64_t
   for (int j = 0; j < jobs; ++j) {
     a.job[j].w = matrix_view(w[j]);
     a.job[j].xb = (uint16_t *)(ws + o_xb[j]);
-    a.job[j].part = parts ? (float *)(ws + o_part[j]) : nullptr;
+    a.job[j].part = tail > 0 ? (float *)(ws + o_part[j]) : nullptr;
     a.job[j].xexp = -w[j]->xscale_log2;
   }
   a.rs = (int32_t *)(ws + o_rs);

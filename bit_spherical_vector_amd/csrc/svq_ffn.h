@@ -61,17 +61,21 @@ hipError_t launch_combine(const CombineArgs &a, hipStream_t s);
 struct FfnGemmJob {
   MatView w;
   uint16_t *xb;  // fp16 activations in fragment order (workspace)
-  float *part;   // fp32 partial tiles [splits][m_pad][n_pad], or null: none
+  float *part;   // fp32 sums of the K ranges [splits][m_pad][part_ld], columns from the first
+                 // n-tile that has any (workspace)
   int32_t xexp;  // -xscale_log2 of the matrix's exact split
 };
 struct FfnGemmArgs {
   FfnGemmJob job[2];
-  int32_t jobs, m, bm, m_pad, tiles_m, tiles_n, n_pad, splits, ups;
+  int32_t jobs, m, bm, m_pad, tiles_m, tiles_n;
+  // tiles 0 .. full - 1 of each job are summed by one block; the rest by
+  // `splits` blocks of `ups` units, whose partial tiles the reduce launch joins
+  int32_t full, splits, ups, part_ld;
   int32_t rpb, csplit;  // prep: rows per block, chunk ranges
   const uint16_t *x;
   int64_t ldx;
   int32_t *rs;    // exponents of the inverse row scales [m_pad] (workspace)
-  float *swap;    // gated pair without partial tiles: [tiles][2] tiles of 256 x 256 sums
+  float *swap;    // gated pair, whole tiles: [full][2] tiles of 256 x 256 sums
   int32_t *cnt;   // and their arrivals
   int32_t n_cnt;
   int32_t ydt, yvec;

@@ -1092,21 +1092,36 @@ __device__ __forceinline__ void put16(const DqTile &T, const f16x &v, int rr0, i
   else full ? put(N(), Y()) : put(N(), N());
 }
 
-// Raw sums of a K range into a partial tile (always whole).
+// Raw sums of a K range into its tile of a partial matrix (always whole).
 struct PartTile {
   static constexpr bool on = true, partial = true, f16 = true;
+  float *tile;
+  int ld;
   template <int NI, int NJ, int TM, int TN>
-  __device__ __forceinline__ void finish(const DqTile &T, f16x (&C)[NI][NJ], uint8_t *, int wm, int wn, int lane,
-                                         int rt0) const {
+  __device__ __forceinline__ void finish(const DqTile &, f16x (&C)[NI][NJ], uint8_t *, int wm, int wn, int lane,
+                                         int) const {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        float *p = (float *)T.y + (size_t)(T.m0 + TM * wm + 32 * i + 4 * (lane >> 5)) * T.ldy + rt0 * UNIT_ROWS +
-                   TN * wn + 32 * j + (lane & 31);
+        float *p = tile + (size_t)(TM * wm + 32 * i + 4 * (lane >> 5)) * ld + TN * wn + 32 * j + (lane & 31);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) p[(size_t)((e & 3) + 8 * (e >> 2)) * T.ldy] = C[i][j][e];
+        for (int e = 0; e < 16; ++e) p[(size_t)((e & 3) + 8 * (e >> 2)) * ld] = C[i][j][e];
       }
+  }
+};
+
+// Whole tiles (W) and K ranges (part.tile not null) of one launch.
+template <typename W>
+struct MixTile {
+  static constexpr bool on = true, partial = false, f16 = true;
+  W whole;
+  PartTile part;
+  template <int NI, int NJ, int TM, int TN>
+  __device__ __forceinline__ void finish(const DqTile &T, f16x (&C)[NI][NJ], uint8_t *smem, int wm, int wn, int lane,
+                                         int rt0) const {
+    if (part.tile) part.finish<NI, NJ, TM, TN>(T, C, smem, wm, wn, lane, rt0);
+    else whole.template finish<NI, NJ, TM, TN>(T, C, smem, wm, wn, lane, rt0);
   }
 };
 
@@ -1316,22 +1331,34 @@ __global__ __launch_bounds__(256) void ffn_prep_kernel(FfnGemmArgs a) {
   }
 }
 
-// Block (job, mt, nt, sp) of the tile launch: m-tile fastest, so that blocks
-// sharing an activation tile fall on one XCD; jobs start on multiples of 8.
-__device__ __forceinline__ bool ffn_tile(const FfnGemmArgs &a, int bm, DqTile &T, int &jn, int &tile, int &sp) {
-  const int per = a.tiles_m * a.tiles_n * a.splits, pad = (per + 7) / 8 * 8;
-  jn = (int)blockIdx.x >= pad ? 1 : 0;
-  const int local = (int)blockIdx.x - jn * pad;
-  if (local >= per) return false;  // padding block (uniform, before any barrier)
-  tile = local % (a.tiles_m * a.tiles_n);
-  sp = local / (a.tiles_m * a.tiles_n);
+// Block of the tile launch: the whole tiles of job 0, of job 1 (each padded
+// to a multiple of 8 blocks), then the other tiles' K ranges, range by range.
+// Tiles have the m-tile fastest, so that blocks sharing an activation tile
+// fall on one XCD.  part: where a K range leaves its sums, or null.
+__device__ __forceinline__ bool ffn_tile(const FfnGemmArgs &a, int bm, DqTile &T, int &jn, int &tile, float *&part) {
+  const int fpad = (a.full + 7) / 8 * 8, b = (int)blockIdx.x;
+  int sp = 0;
+  part = nullptr;
+  if (b < fpad * a.jobs) {
+    jn = b >= fpad ? 1 : 0;
+    tile = b - jn * fpad;
+    if (tile >= a.full) return false;  // padding block (uniform, before any barrier)
+  } else {
+    const int q = b - fpad * a.jobs, tail = a.tiles_m * a.tiles_n - a.full;
+    sp = q / (tail * a.jobs);
+    const int r = q - sp * tail * a.jobs;
+    jn = r >= tail ? 1 : 0;
+    tile = a.full + r - jn * tail;
+    part = (jn ? a.job[1].part : a.job[0].part) + (size_t)sp * a.m_pad * a.part_ld +
+           (size_t)(tile % a.tiles_m * bm) * a.part_ld + (tile / a.tiles_m - a.full / a.tiles_m) * PREFILL_BN;
+  }
   T.w = jn ? a.job[1].w : a.job[0].w;
   T.xb = jn ? a.job[1].xb : a.job[0].xb;
   T.m0 = tile % a.tiles_m * bm;
   T.m_valid = a.m - T.m0;
   T.nt = tile / a.tiles_m;
-  T.u0 = sp * a.ups;
-  T.u1 = min(T.w.units, T.u0 + a.ups);
+  T.u0 = part ? sp * a.ups : 0;
+  T.u1 = part ? min(T.w.units, T.u0 + a.ups) : T.w.units;
   T.ymap = nullptr;
   T.y = a.y;
   T.ldy = a.ldy;
@@ -1340,59 +1367,59 @@ __device__ __forceinline__ bool ffn_tile(const FfnGemmArgs &a, int bm, DqTile &T
   T.yvec = false;
   return true;
 }
-__device__ __forceinline__ void ffn_part(const FfnGemmArgs &a, int jn, int sp, DqTile &T) {
-  T.y = (jn ? a.job[1].part : a.job[0].part) + (size_t)sp * a.m_pad * a.n_pad;
-  T.ldy = a.n_pad;
-}
 
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void ffn_part64_kernel(FfnGemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   DqTile T;
-  int jn, tile, sp;
-  if (!ffn_tile(a, 64, T, jn, tile, sp)) return;
-  ffn_part(a, jn, sp, T);
-  dq_tile<64, PartTile>(T, smem, PartTile());
+  int jn, tile;
+  float *part;
+  if (!ffn_tile(a, 64, T, jn, tile, part)) return;
+  dq_tile<64, PartTile>(T, smem, PartTile{part, a.part_ld});
 }
 __global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void ffn_part256_kernel(FfnGemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   DqTile T;
-  int jn, tile, sp;
-  if (!ffn_tile(a, 256, T, jn, tile, sp)) return;
-  ffn_part(a, jn, sp, T);
-  dq_tile_w8<PartTile>(T, smem, PartTile());
+  int jn, tile;
+  float *part;
+  if (!ffn_tile(a, 256, T, jn, tile, part)) return;
+  dq_tile_w8<PartTile>(T, smem, PartTile{part, a.part_ld});
 }
 __global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void ffn_linear_kernel(FfnGemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   DqTile T;
-  int jn, tile, sp;
-  if (!ffn_tile(a, 256, T, jn, tile, sp)) return;
-  dq_tile_w8<LinTile>(T, smem, LinTile{a.epi, a.rs, a.job[0].xexp});
+  int jn, tile;
+  float *part;
+  if (!ffn_tile(a, 256, T, jn, tile, part)) return;
+  dq_tile_w8<MixTile<LinTile>>(T, smem, MixTile<LinTile>{{a.epi, a.rs, a.job[0].xexp}, {part, a.part_ld}});
 }
 __global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void ffn_glu_kernel(FfnGemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   DqTile T;
-  int jn, tile, sp;
-  if (!ffn_tile(a, 256, T, jn, tile, sp)) return;
+  int jn, tile;
+  float *part;
+  if (!ffn_tile(a, 256, T, jn, tile, part)) return;
   const GluTile g{a.bias_g, a.epi.bias, a.epi.bias_f32, a.epi.act, a.rs, a.job[0].xexp, a.job[1].xexp, jn != 0,
                   (uint64_t *)a.swap + (size_t)(2 * tile + jn) * (256 * 256 / 2),
                   (const uint64_t *)a.swap + (size_t)(2 * tile + 1 - jn) * (256 * 256 / 2), a.cnt + tile};
-  dq_tile_w8<GluTile>(T, smem, g);
+  dq_tile_w8<MixTile<GluTile>>(T, smem, MixTile<GluTile>{g, {part, a.part_ld}});
 }
 
 // Sum of the K ranges in range order, then epilogue (one matrix) or gating
-// (two); four columns a thread.
+// (two); a block takes four rows of a tile, four columns a thread.
 __global__ __launch_bounds__(256) void ffn_reduce_kernel(FfnGemmArgs a) {
-  const int n_all = a.job[0].w.n, per_row = (n_all + 1023) / 1024;
-  const int row = (int)blockIdx.x / per_row, n = ((int)blockIdx.x % per_row) * 1024 + 4 * (int)threadIdx.x;
-  if (n >= n_all) return;
+  const int groups = a.bm / 4, tile = a.full + (int)blockIdx.x / groups;
+  const int tr = 4 * ((int)blockIdx.x % groups) + ((int)threadIdx.x >> 6), tc = 4 * ((int)threadIdx.x & 63);
+  const int row = tile % a.tiles_m * a.bm + tr, n = tile / a.tiles_m * PREFILL_BN + tc, n_all = a.job[0].w.n;
+  if (row >= a.m || n >= n_all) return;
+  const size_t at = (size_t)row * a.part_ld + n - a.full / a.tiles_m * PREFILL_BN, step = (size_t)a.m_pad * a.part_ld;
   const int re = a.rs[row];
   f4 v[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     v[j] = (f4){0.f, 0.f, 0.f, 0.f};
     if (j < a.jobs) {
-      const float *p = a.job[j].part + (size_t)row * a.n_pad + n;
-      for (int s = 0; s < a.splits; ++s) v[j] += *(const f4 *)(p + (size_t)s * a.m_pad * a.n_pad);
+      const float *p = a.job[j].part + at;
+      for (int s = 0; s < a.splits; ++s) v[j] += *(const f4 *)(p + s * step);
 #pragma unroll
       for (int l = 0; l < 4; ++l) v[j][l] = ldexpf(v[j][l], re + a.job[j].xexp);
     }
@@ -1431,18 +1458,18 @@ hipError_t launch_ffn_gemm(const FfnGemmArgs &a, bool xvec, hipStream_t s) {
   hipError_t e = ffn_launch(xvec ? ffn_prep_kernel<true> : ffn_prep_kernel<false>, rblocks * (32 / a.rpb) * a.csplit,
                             256, lds, a, s);
   if (e != hipSuccess) return e;
-  const int per = a.tiles_m * a.tiles_n * a.splits, blocks = a.jobs == 1 ? per : (per + 7) / 8 * 8 + per;
-  const bool direct = a.job[0].part == nullptr;
+  const int tail = a.tiles_m * a.tiles_n - a.full;
+  const int blocks = (a.full + 7) / 8 * 8 * a.jobs + tail * a.splits * a.jobs;
   if (bm == 64)
     e = ffn_launch(ffn_part64_kernel, blocks, 256, P_SMEM, a, s);
-  else if (!direct)
+  else if (a.full == 0)
     e = ffn_launch(ffn_part256_kernel, blocks, W8_THREADS, W8_SMEM, a, s);
   else if (a.jobs == 1)
     e = ffn_launch(ffn_linear_kernel, blocks, W8_THREADS, W8_SMEM, a, s);
   else
     e = ffn_launch(ffn_glu_kernel, blocks, W8_THREADS, W8_SMEM, a, s);
-  if (e != hipSuccess || direct) return e;
-  hipLaunchKernelGGL(ffn_reduce_kernel, dim3(a.m * ((a.job[0].w.n + 1023) / 1024)), dim3(256), 0, s, a);
+  if (e != hipSuccess || tail == 0) return e;
+  hipLaunchKernelGGL(ffn_reduce_kernel, dim3(tail * (bm / 4)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -45,6 +45,9 @@ struct Regions {
 };
 }  // namespace
 
+namespace check {
+long mixed = 0;  // launches of whole tiles and K ranges
+}
 namespace svq {
 
 hipError_t launch_ffn_gemm(const FfnGemmArgs &a, bool, hipStream_t) {
@@ -55,25 +58,29 @@ hipError_t launch_ffn_gemm(const FfnGemmArgs &a, bool, hipStream_t) {
   CHECK(a.rpb >= 1 && a.rpb <= 8 && 32 % a.rpb == 0, "rows per prep block %d", a.rpb);
   CHECK(prefill_prep_lds(a.rpb, a.job[0].w.k) + 64 <= GV_LDS_LIMIT, "prep LDS");
   R.add(a.rs, (size_t)a.m_pad * 4, "row scales");
-  const bool parts = a.job[0].part != nullptr;
-  CHECK(parts == (a.bm == 64 || a.splits > 1), "partial tiles");
+  const int tail = a.tiles_m * a.tiles_n - a.full;  // tiles in K ranges
+  CHECK(a.full >= 0 && tail >= 0 && (a.bm == 256 || a.full == 0), "whole tiles %d, others %d", a.full, tail);
   for (int j = 0; j < a.jobs; ++j) {
     const MatView &w = a.job[j].w;
-    CHECK(a.tiles_n * 256 >= w.n && a.n_pad == a.tiles_n * 256, "columns");
+    CHECK(a.tiles_n * 256 >= w.n, "columns");
+    CHECK(a.full / a.tiles_m * 256 + a.part_ld == a.tiles_n * 256, "columns of the K ranges");
     R.add(a.job[j].xb, (size_t)a.m_pad * w.units * UNIT_SLOTS * 2, "activations");
-    if (parts) R.add(a.job[j].part, (size_t)a.splits * a.m_pad * a.n_pad * 4, "partial tiles");
+    CHECK((a.job[j].part != nullptr) == (tail > 0), "partial tiles");
+    if (tail > 0) R.add(a.job[j].part, (size_t)a.splits * a.m_pad * a.part_ld * 4, "partial tiles");
     CHECK(a.splits >= 1 && a.splits * a.ups >= w.units && (a.splits - 1) * a.ups < w.units, "K ranges");
     for (int s = 0; s < a.splits; ++s)
       for (int u = s * a.ups; u < std::min(w.units, (s + 1) * a.ups); ++u)
         for (int rt : {0, w.n_tiles - 1})
           check::check_code_load(w, w.off_codes + ((size_t)rt * w.units + u) * UNIT_BYTES, "ffn gemm");
   }
-  if (!parts && a.jobs == 2) {
-    const size_t tiles = (size_t)a.tiles_m * a.tiles_n;
-    R.add(a.swap, tiles * 2 * 65536 * 4, "exchange tiles");
-    R.add(a.cnt, tiles * 4, "arrivals");
-    CHECK(a.n_cnt == (int)tiles, "arrivals cleared");
+  if (a.full > 0 && a.jobs == 2) {
+    R.add(a.swap, (size_t)a.full * 2 * 65536 * 4, "exchange tiles");
+    R.add(a.cnt, (size_t)a.full * 4, "arrivals");
+    CHECK(a.n_cnt == a.full, "arrivals cleared");
+  } else {
+    CHECK(a.n_cnt == 0, "no arrivals");
   }
+  check::mixed += a.full > 0 && tail > 0;
   return hipSuccess;
 }
 

@@ -14,7 +14,7 @@
 namespace check {
 extern const uint8_t *ws_base;
 extern size_t ws_bytes;
-extern long launches, loads_checked;
+extern long launches, loads_checked, mixed;
 }
 
 static int fails = 0;
@@ -141,6 +141,7 @@ int main() {
       });
     }
   }
+  EXPECT(check::mixed > 0, "no plan with a last round in K ranges%s", "");
   for (void *p : owned) std::free(p);
   std::printf("host harness: %ld launches checked, %ld code loads, %d failures\n", check::launches,
               check::loads_checked, fails);

@@ -238,6 +238,31 @@ def test_glu(svq, n, k, m, bds):
         check(y, a * uv, ea * np.abs(uv) + eu * np.abs(a) + ea * eu + U32 * np.abs(a * uv), f"{act} n={n} k={k} m={m}")
 
 
+def test_last_round_in_k_ranges(svq):
+    """More 256-row tiles than compute units: whole tiles for the full rounds,
+    the tiles left over in K ranges that a reduce launch joins; ragged rows
+    and columns in both."""
+    m, k = 2050, 1032                             # nine tiles of rows, three units
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    n = 256 * (cus // 9 + 1) - 5                  # a few tiles past one round
+    mats = [synth.random_matrix(n, k, bd, seed=(98, n, bd)) for bd in (7, 8)]
+    x_bits = synth.random_activations(m, k, seed=(98, n, m))
+    x = to_device_bf16(x_bits)
+    (g, gb), (u, ub) = [product(a, x_bits, True) for a in mats]
+    pg, pu = [svq.pack(a) for a in mats]
+    bias, res = vec(n, torch.float32, 19), vec(m * n, torch.bfloat16, 20).view(m, n)
+    y = svq.linear_epilogue(pg, x, bias=bias, act="relu", residual=res)
+    v, r = g + f64(bias), f64(res)
+    a = np.maximum(v, 0)
+    check(y, a + r, gb + U32 * np.abs(v) + U32 * (a + np.abs(r)), "epilogue")
+    y = svq.linear_glu(pg, pu, x, act="relu", bias_up=bias, out_dtype=torch.float32)
+    a, b = np.maximum(g, 0), u + f64(bias)
+    eb = ub + U32 * np.abs(b)
+    check(y, a * b, gb * np.abs(b) + eb * a + gb * eb + U32 * np.abs(a * b), "glu")
+    first = y.clone()
+    assert torch.equal(svq.linear_glu(pg, pu, x, act="relu", bias_up=bias, out_dtype=torch.float32), first)
+
+
 def route64(x, w, topk, score, renorm, scale, sb):
     logits = f64(x) @ f64(w).T
     if score == "softmax":
