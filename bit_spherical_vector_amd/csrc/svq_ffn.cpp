@@ -44,7 +44,8 @@ struct TilePlan {
 // UNIT a unit of 512 channels and EDGE for its start and its stores, and a
 // reduce launch follows partial tiles.  (Either all tiles whole or all in
 // ranges: gated pair 9728 x 2560 at 2048 rows 251 us against 239, at 1024 rows
-// 160 against 142; one 9728 x 2560 matrix at 2048 rows 235 against 179.)
+// 160 against 142; one 9728 x 2560 matrix with a
+// residual at 2048 rows 235 against 179, 158 since.)
 TilePlan tile_plan(int tiles, int jobs, int units, int bm) {
   const int cus = compute_units();
   if (bm == 64) {

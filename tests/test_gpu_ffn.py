@@ -263,6 +263,29 @@ def test_last_round_in_k_ranges(svq):
     assert torch.equal(svq.linear_glu(pg, pu, x, act="relu", bias_up=bias, out_dtype=torch.float32), first)
 
 
+@pytest.mark.parametrize("out,res_type", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16),
+                                          (torch.bfloat16, torch.float32)])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_whole_tiles_with_aligned_residual(svq, out, res_type, act):
+    """256-row tiles in one K range, aligned rows of y and residual, the last
+    columns fewer than four; in place where the types agree; nothing beside
+    y's columns is written."""
+    n, k, m, ld = 515, 264, 290, 520
+    mat = synth.random_matrix(n, k, 7, seed=(99, n, k))
+    x_bits = synth.random_activations(m, k, seed=(99, n, m))
+    wide = vec(m * ld, out, 21).view(m, ld)
+    before, y = wide.clone(), wide[:, :n]
+    res = y if out == res_type else vec(m * ld, res_type, 22).view(m, ld)[:, :n]
+    r, bias = f64(res), vec(n, torch.float32, 23)
+    svq.linear_epilogue(svq.pack(mat), to_device_bf16(x_bits), bias=bias, act=act, residual=res, out=y)
+    p, pb = product(mat, x_bits, True)
+    v = p + f64(bias)
+    a = act64(v, act)
+    bound = slope_of(act) * (pb + U32 * np.abs(v)) + 16 * U32 * np.abs(a) + U32 * (np.abs(a) + np.abs(r))
+    check(y, a + r, bound, act)
+    assert torch.equal(wide[:, n:], before[:, n:])
+
+
 def route64(x, w, topk, score, renorm, scale, sb):
     logits = f64(x) @ f64(w).T
     if score == "softmax":
