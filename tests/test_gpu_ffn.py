@@ -592,6 +592,41 @@ def test_captured_and_replayed(svq, m):
         assert torch.equal(y, want), f"replay {i}"
 
 
+def test_captured_large_calls_in_one_workspace(svq):
+    """Pairs of 256-row tiles that meet through memory (one unit, so whole
+    tiles) and K ranges with their reduce launch, captured on one workspace
+    that holds anything before each replay."""
+    m, f, k = 300, 1100, 512
+    gate, up = [svq.pack(synth.random_matrix(f, k, bd, seed=(100, bd, k))) for bd in (7, 8)]
+    down = svq.pack(synth.random_matrix(k, f - f % 8, 6, seed=(101, k, f)))
+    x = torch.zeros((m, k), dtype=torch.bfloat16, device="cuda")
+    h = torch.zeros((m, f), dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros_like(x)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    calls = [svq.GluCall(gate, up, x, h, workspace=ws),
+             svq.EpilogueCall(down, h, y, residual=x, workspace=ws)]
+    for c in calls:
+        c()
+        assert c.workspace is ws
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for c in calls:
+            c()
+    for i in range(5):
+        xi = to_device_bf16(synth.random_activations(m, k, seed=(102, i, m)))
+        hi = svq.linear_glu(gate, up, xi)
+        want = svq.linear_epilogue(down, hi, residual=xi)
+        x.copy_(xi)
+        h.fill_(float("nan"))
+        y.fill_(float("nan"))
+        ws.fill_((0xFF, 0x00, 0x01)[i % 3])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(h, hi) and torch.equal(y, want), f"replay {i}"
+
+
 def test_on_another_stream(svq):
     """Calls given a stream run in that stream's order."""
     _, _, (gate, up, down, router, gs, us, ds) = _block_weights(svq)
