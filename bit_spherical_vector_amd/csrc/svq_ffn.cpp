@@ -57,7 +57,8 @@ TilePlan tile_plan(int tiles, int jobs, int units, int bm) {
   auto rounds = [&](int64_t blocks, int ups) { return (double)((blocks + cus - 1) / cus) * (ups * UNIT + EDGE); };
   TilePlan best = {tiles, 1, units};
   double t_best = rounds((int64_t)tiles * jobs, units);
-  const int r_all = (int)((int64_t)tiles * jobs / cus);  // fewer whole rounds than a few below that only add ranges
+  // the last few counts only: still fewer whole rounds just add partial tiles
+  const int r_all = (int)((int64_t)tiles * jobs / cus);
   for (int r = r_all > 3 ? r_all - 3 : 0; r <= r_all; ++r) {
     const int full = (int)((int64_t)r * cus / jobs), tail = tiles - full;
     for (int s = 2; s <= units && s <= 16; ++s) {
