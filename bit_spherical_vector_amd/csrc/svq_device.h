@@ -104,6 +104,14 @@ __device__ __forceinline__ uint32_t pk_max_finite(uint32_t m, uint32_t p) {
   const uint32_t lo = p & 0x7FFFu, hi = p & 0x7FFF0000u;
   return pk_max_mag(m, (lo < 0x7F80u ? lo : 0u) | (hi < 0x7F800000u ? hi : 0u));
 }
+// Magnitude of a finite value, 0 of an infinity or NaN: what a power-of-two
+// scale is taken from.  (From an infinity it would push the finite values
+// beside it out of fp16's range; an infinity or NaN keeps its value under any
+// scale.)
+__device__ __forceinline__ float finite_mag(float v) {
+  const float a = fabsf(v);
+  return a < __builtin_inff() ? a : 0.f;
+}
 // Two values times 2^e as packed fp16.  Rounded toward zero: a scaled bf16
 // value of at least 2^-14 is exact either way.
 __device__ __forceinline__ uint32_t pk_scaled_f16(float a, float b, int e) {

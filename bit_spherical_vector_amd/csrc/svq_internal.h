@@ -228,7 +228,8 @@ struct SbJob {
   const uint16_t *x;    // activations, bf16 [m][ldx]
   int64_t ldx;
   uint8_t *xa;          // fragment-ordered fp16 activations (workspace)
-  float *xs;            // their inverse scales, [units][16] (workspace)
+  float *xs;            // their inverse scales, [units][16] (workspace); those of
+                        // a unit that holds an infinity are stored negative
   float xinv;           // 2^-xscale_log2 of the matrix's exact split
   float *part;          // splits > 1: partial tiles (workspace)
   int32_t *cnt;         // splits > 1: arrival counters (workspace)

@@ -42,7 +42,8 @@ namespace svq {
 // c takes code column c of the unit (permuted slots 8c .. 8c+7; Fig. 6
 // caption: a subvector multiplies eight reordered activations), loads the
 // eight activations x[a][perm[p]] and the wave writes the unit's fp16 copy
-// with a power-of-two scale 2^e (max|x_au| * 2^e in [2^14, 2^15)).  A bf16
+// with a power-of-two scale 2^e (max|x_au| * 2^e in [2^14, 2^15), the maximum
+// over its finite values; infinities and NaN keep theirs).  A bf16
 // value has 8 significant bits, so its scaled copy is exact down to a
 // scaled magnitude of 2^-17 (the fp16 subnormal quantum is 2^-24), i.e. for
 // every |x| >= 2^-31 * max|x_au|; smaller values round to fp16 subnormals.
@@ -208,7 +209,7 @@ __device__ __forceinline__ void gather_block(const uint16_t *__restrict__ perm,
     v[2 * l + 1] = (p0 + 2 * l + 1 < K) ? bf16_bits_to_f32(s_x[pv[l] >> 16]) : 0.f;
   }
 #pragma unroll
-  for (int l = 0; l < 8; ++l) mx = fmaxf(mx, fabsf(v[l]));
+  for (int l = 0; l < 8; ++l) mx = fmaxf(mx, finite_mag(v[l]));
   mx = wave_max(mx);
   const int e = mx > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
   u4 h;
@@ -937,7 +938,7 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
   // power-of-two scale: 2^e with max|x_unit| * 2^e in [2^14, 2^15), i.e.
   // e = 14 - ilogb(max) = 15 - (frexp exponent of max).  pr: the lane's
   // eight slots as packed bf16 pairs; mxb: bf16 bits of the unit's largest
-  // magnitude.
+  // finite magnitude.
   auto gather_store = [&](int a, int uu, const uint32_t (&pr)[4], uint32_t mxb) __attribute__((always_inline)) {
     const float mxw = bf16_bits_to_f32(mxb);
     const int e = mxw > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mxw) : 0;
@@ -967,6 +968,17 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
   };
   auto wave_max_bits = [](uint32_t b) __attribute__((always_inline)) {
     return __builtin_bit_cast(uint32_t, wave_max(__builtin_bit_cast(float, b)));
+  };
+  // The unit's largest finite magnitude: the wave's maximum mxb, or, where
+  // that is an infinity or NaN (wave-uniform, rare), a second look.
+  auto finite_bits = [&](uint32_t mxb, const uint32_t (&pr)[4]) __attribute__((always_inline)) {
+    if (__builtin_expect(mxb >= 0x7F80u, 0)) {
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int l = 0; l < 4; ++l) m2 = pk_max_finite(m2, pr[l]);
+      mxb = wave_max_bits(max(m2 & 0xFFFFu, m2 >> 16));
+    }
+    return mxb;
   };
 
   // One activation row at a time: stage it in LDS, then every wave gathers
@@ -1023,7 +1035,7 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
         for (int l = 0; l < 4; ++l) {
           v[2 * l] = valid ? lds_f32(HB + gf_off_stage(BD) + word_shl<0, 2>(pv[l])) : 0.f;
           v[2 * l + 1] = valid ? lds_f32(HB + gf_off_stage(BD) + word_shl<1, 2>(pv[l])) : 0.f;
-          mx = fmaxf(mx, fmaxf(fabsf(v[2 * l]), fabsf(v[2 * l + 1])));
+          mx = fmaxf(mx, fmaxf(finite_mag(v[2 * l]), finite_mag(v[2 * l + 1])));
         }
         mx = wave_max(mx);
         const int e = mx > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
@@ -1052,7 +1064,7 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
       for (int jj = 0; jj < nj; ++jj) mx[jj] = wave_max_bits(mx[jj]);
 #pragma unroll
       for (int jj = 0; jj < nj; ++jj)
-        if (j0 + jj < npre) gather_store(a, g_lo + j0 + jj, pr[jj], mx[jj]);
+        if (j0 + jj < npre) gather_store(a, g_lo + j0 + jj, pr[jj], finite_bits(mx[jj], pr[jj]));
     };
     static_assert(GF_PRE_UNITS == 5, "gather groups cover 2 + 3 units");
     if (npre > 0) gather_group(std::integral_constant<int, 0>(), std::integral_constant<int, 2>());
@@ -1062,7 +1074,7 @@ __device__ void gemv_fused_block(const MatView &w, const uint16_t *__restrict__ 
       const u4 pv = *(const u4 *)(perm + uu * UNIT_SLOTS + 8 * lane);
       uint32_t pr[4];
       const uint32_t mxb = gather_pairs(pv, uu, pr);
-      gather_store(a, uu, pr, wave_max_bits(mxb));
+      gather_store(a, uu, pr, finite_bits(wave_max_bits(mxb), pr));
     }
   }
   if constexpr (BD == 8) {

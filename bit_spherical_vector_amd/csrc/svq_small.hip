@@ -95,11 +95,23 @@ __device__ __forceinline__ void sb_reads(uint32_t Lw, uint32_t H, const SbShifts
   }
 }
 
+// Packed fp16 values with infinities (and NaN) as zeros.
+__device__ __forceinline__ u4 sb_finite(const u4 &a) {
+  u4 r;
+#pragma unroll
+  for (int l = 0; l < 4; ++l) {
+    const uint32_t lo = a[l] & 0xFFFFu, hi = a[l] & 0xFFFF0000u;
+    r[l] = ((lo & 0x7C00u) == 0x7C00u ? 0u : lo) | ((hi & 0x7C000000u) == 0x7C000000u ? 0u : hi);
+  }
+  return r;
+}
+
 // Signs of the four codes of group q, then their MFMAs.  A 64-bit shift of
 // the record's sign dwords (S1:S0, S3:S2) by 4b0 + ci brings code
 // 4b0 + ci's pair signs to bits 15 and 31 of each dword (bits the shift
 // carries across the dword boundary land below bit 15 and are masked off).
-template <bool HI>
+// FIN: the low halves meet finite activations only (see sb_redo).
+template <bool HI, bool FIN>
 __device__ __forceinline__ void sb_mul(uint64_t S01, uint64_t S23, const SbShifts &sh,
                                        const u4 (&Dh)[4], const u4 (&Dl)[4], const u4 (&A)[16], int q,
                                        f4 &C) {
@@ -113,12 +125,15 @@ __device__ __forceinline__ void sb_mul(uint64_t S01, uint64_t S23, const SbShift
     const u4 wl = {Dl[ci][0] ^ m0, Dl[ci][1] ^ m1, Dl[ci][2] ^ m2, Dl[ci][3] ^ m3};  // HI: unused
     const h8 a = __builtin_bit_cast(h8, A[4 * ci + q]);
     C = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(h8, wh), C, 0, 0, 0);
-    if constexpr (!HI) C = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(h8, wl), C, 0, 0, 0);
+    if constexpr (!HI) {
+      const h8 al = FIN ? __builtin_bit_cast(h8, sb_finite(A[4 * ci + q])) : a;
+      C = __builtin_amdgcn_mfma_f32_16x16x32_f16(al, __builtin_bit_cast(h8, wl), C, 0, 0, 0);
+    }
   }
 }
 
 // One unit of one row tile: the 16 codes of the lane, 16 MFMAs.
-template <bool HI, int TAB = SB_OFF_XTAB>
+template <bool HI, int TAB = SB_OFF_XTAB, bool FIN = false>
 __device__ __forceinline__ f4 sb_item(const SbCodes &c, const u4 (&A)[16], const SbShifts &sh) {
   f4 C0 = {0.f, 0.f, 0.f, 0.f}, C1 = {0.f, 0.f, 0.f, 0.f};
   u4 H0[4], L0[4], H1[4], L1[4];
@@ -128,17 +143,17 @@ __device__ __forceinline__ f4 sb_item(const SbCodes &c, const u4 (&A)[16], const
   sb_reads<HI, TAB>(c.L[0], c.H[0], sh, H0, L0);
   sb_reads<HI, TAB>(c.L[1], c.H[1], sh, H1, L1);
   __builtin_amdgcn_sched_barrier(0);
-  sb_mul<HI>(s01(0), s23(0), sh, H0, L0, A, 0, C0);
+  sb_mul<HI, FIN>(s01(0), s23(0), sh, H0, L0, A, 0, C0);
   __builtin_amdgcn_sched_barrier(0);
   sb_reads<HI, TAB>(c.L[2], c.H[2], sh, H0, L0);
   __builtin_amdgcn_sched_barrier(0);
-  sb_mul<HI>(s01(1), s23(1), sh, H1, L1, A, 1, C1);
+  sb_mul<HI, FIN>(s01(1), s23(1), sh, H1, L1, A, 1, C1);
   __builtin_amdgcn_sched_barrier(0);
   sb_reads<HI, TAB>(c.L[3], c.H[3], sh, H1, L1);
   __builtin_amdgcn_sched_barrier(0);
-  sb_mul<HI>(s01(2), s23(2), sh, H0, L0, A, 2, C0);
+  sb_mul<HI, FIN>(s01(2), s23(2), sh, H0, L0, A, 2, C0);
   __builtin_amdgcn_sched_barrier(0);
-  sb_mul<HI>(s01(3), s23(3), sh, H1, L1, A, 3, C1);
+  sb_mul<HI, FIN>(s01(3), s23(3), sh, H1, L1, A, 3, C1);
   return C0 + C1;
 }
 
@@ -148,6 +163,39 @@ typedef __attribute__((address_space(3))) int sb_lds_i_t;
 
 __device__ __forceinline__ const uint8_t *sb_unit(const MatView &w, int t, int u) {
   return w.base + w.off_codes + ((size_t)t * w.units + u) * UNIT_BYTES;
+}
+
+// A unit that holds an infinity in some row has its scales stored negative.
+__device__ __forceinline__ f4 sb_scales(const f4 &xs) {
+  return (f4){fabsf(xs[0]), fabsf(xs[1]), fabsf(xs[2]), fabsf(xs[3])};
+}
+// A wave's run once more, for a run that met such a unit.  A code's weight is
+// the sum of two halves, and an infinite activation times the low one is NaN
+// (where it is zero) or of the wrong sign; here the low halves are multiplied
+// by the finite activations alone (the infinity times the high half is the
+// product's own value).  Items one at a time and not unrolled: run after the
+// loop, which then carries nothing for it but the marks.  (As a branch in the
+// unrolled loop, whose code it doubled, the seven matrices of a layer took
+// 29.4 us at 16 rows, 28.1 this way.)  Same order of items: rows without an
+// infinity get the sums they had.
+template <int TAB>
+__device__ __forceinline__ void sb_redo(const MatView &w, const uint8_t *xa_all, const float *xs, int t0, int u0,
+                                        int tn, int i0, int nk, const SbOffs &offs, const SbShifts &sh,
+                                        uint32_t slot0, int lane) {
+#pragma unroll
+  for (int t = 0; t < SB_TMAX; ++t) *(sb_lds_u4w_t *)(size_t)(slot0 + t * 1024) = (u4){0u, 0u, 0u, 0u};
+#pragma unroll 1
+  for (int i = i0; i < i0 + nk; ++i) {
+    const int ui = i / tn, ti = i - ui * tn, u = u0 + ui;
+    const u4 *xa = (const u4 *)(xa_all + (size_t)u * SB_XA_UNIT_BYTES) + lane;
+    u4 A[16];
+#pragma unroll
+    for (int f = 0; f < 16; ++f) A[f] = xa[64 * f];
+    const f4 xsc = sb_scales(*(const f4 *)(xs + (size_t)u * 16 + 4 * (lane >> 4)));
+    const f4 C = sb_item<false, TAB, true>(sb_load_codes(sb_unit(w, t0 + ti, u), offs), A, sh) * xsc;
+    sb_lds_u4w_t *sl = (sb_lds_u4w_t *)(size_t)(slot0 + ti * 1024);
+    *sl = __builtin_bit_cast(u4, __builtin_bit_cast(f4, *sl) + C);
+  }
 }
 
 // ea: nothing, the EpiArgs of a single matrix, or the PairArgs of a gated
@@ -218,6 +266,7 @@ __global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b, EA... ea) {
     *(sb_lds_u4w_t *)(size_t)(SB_OFF_XTAB + 16 * (tid + 256 * i)) = bt[i];
   __syncthreads();
 
+  int marks = 0;  // negative once a unit held an infinity
 #pragma unroll
   for (int k = 0; k < SB_NMAX; ++k) {
     if (k >= nk) break;
@@ -228,7 +277,8 @@ __global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b, EA... ea) {
       for (int f = 0; f < 16; ++f) A[f] = xa[64 * f];
       xsc = *(const f4 *)(J.xs + (size_t)(u0 + ui) * 16 + 4 * s);
     }
-    const f4 C = sb_item<HI>(cd[k & 1], A, sh) * xsc;
+    const f4 C = sb_item<HI>(cd[k & 1], A, sh) * sb_scales(xsc);
+    if constexpr (!HI) marks |= __builtin_bit_cast(int, xsc[0]);
     if (k + 2 < nk) {
       const int i2 = i0 + k + 2, u2 = i2 / tn;
       cd[k & 1] = sb_load_codes(sb_unit(w, t0 + i2 - u2 * tn, u0 + u2), offs);
@@ -240,6 +290,8 @@ __global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b, EA... ea) {
       ++ui;
     }
   }
+  if (!HI && __builtin_expect(__builtin_amdgcn_readfirstlane(marks) < 0, 0))
+    sb_redo<SB_OFF_XTAB>(w, J.xa, J.xs, t0, u0, tn, i0, nk, offs, sh, slot0, lane);
   __syncthreads();
 
   // sum of the four waves' slots of each tile, in wave order.  Thread tid
@@ -412,11 +464,13 @@ __device__ __forceinline__ void sb_pair_half(const SbJob &J, int g, float (&acc)
 #pragma unroll
   for (int i = 0; i < NBT; ++i) *(sb_lds_u4w_t *)(size_t)(OFF_TAB + 16 * (tid + 256 * i)) = bt[i];
   __syncthreads();
+  int marks = 0;  // negative once a unit held an infinity
 #pragma unroll
   for (int k = 0; k < SB_NMAX; ++k) {
     if (k >= nk) break;
     if (k > 0 && ti == 0) load_unit(ui);
-    const f4 C = sb_item<HI, OFF_TAB>(cd[k & 1], A, sh) * xsc;
+    const f4 C = sb_item<HI, OFF_TAB>(cd[k & 1], A, sh) * sb_scales(xsc);
+    if constexpr (!HI) marks |= __builtin_bit_cast(int, xsc[0]);
     if (k + 2 < nk) cd[k & 1] = codes_of(i0 + k + 2);
     sb_lds_u4w_t *sl = (sb_lds_u4w_t *)(size_t)(slot0 + ti * 1024);
     *sl = __builtin_bit_cast(u4, __builtin_bit_cast(f4, *sl) + C);
@@ -425,6 +479,8 @@ __device__ __forceinline__ void sb_pair_half(const SbJob &J, int g, float (&acc)
       ++ui;
     }
   }
+  if (!HI && __builtin_expect(__builtin_amdgcn_readfirstlane(marks) < 0, 0))
+    sb_redo<OFF_TAB>(w, J.xa, J.xs, t0, 0, tn, i0, nk, offs, sh, slot0, lane);
   __syncthreads();
   const int m = tid >> 4, nn = tid & 15;
   const uint32_t eoff = OFF_RED + 256 * (m >> 2) + 16 * nn + 4 * (m & 3);
@@ -466,6 +522,29 @@ __global__ __launch_bounds__(512) void sb_pair_kernel(SbBatch b, PairArgs pa) {
 static_assert(2 * sb_half_bytes<false>() <= (int)GV_LDS_LIMIT, "both halves of a block in LDS");
 static_assert(SB_TMAX * 256 * 4 <= XTAB_BYTES / 2, "the up sums fit over its table");
 
+// Row maximum of the preps below over a block's waves: the lanes of one row
+// (m, m + 16, m + 32, m + 48), then the waves.
+template <bool AGAIN>
+__device__ __forceinline__ float sb_row_max(float mx, float (&s_max)[4][16], int wv, int L) {
+  mx = fmaxf(mx, __shfl_xor(mx, 16));
+  mx = fmaxf(mx, __shfl_xor(mx, 32));
+  if (AGAIN) __syncthreads();  // the first call's maxima are read
+  if (L < 16) s_max[wv][L] = mx;
+  __syncthreads();
+  const int m = L & 15;
+  return fmaxf(fmaxf(s_max[0][m], s_max[1][m]), fmaxf(s_max[2][m], s_max[3][m]));
+}
+// The lane's largest finite magnitude (the rare second look at a unit that
+// holds an infinity).
+__device__ __forceinline__ float sb_finite_max(const float (&v)[4][8]) {
+  float mx = 0.f;
+#pragma unroll
+  for (int ff = 0; ff < 4; ++ff)
+#pragma unroll
+    for (int l = 0; l < 8; ++l) mx = fmaxf(mx, finite_mag(v[ff][l]));
+  return mx;
+}
+
 // Prep: the permuted activations of every job in fragment order (see the
 // file comment), rows >= m and slots >= k zero; block u of a job writes the
 // 16 fragments of unit u, thread tid the 16-byte pieces of fragments
@@ -473,8 +552,10 @@ static_assert(SB_TMAX * 256 * 4 <= XTAB_BYTES / 2, "the up sums fit over its tab
 // activation row's largest magnitude over the unit (512 slots) sets its
 // power-of-two scale 2^e (max * 2^e in [2^14, 2^15)): a bf16 value of at
 // least 2^-31 times the maximum is then exact in fp16.  2^-e goes to
-// xs[16u + row].  The first block of a job also clears the job's arrival
-// counters.
+// xs[16u + row].  The maximum is over the finite values: infinities and NaN
+// keep theirs; a unit that holds an infinity in any row is marked by negative
+// scales (see sb_redo).  The first block of a job also clears the
+// job's arrival counters.
 __global__ __launch_bounds__(256) void sb_prep_kernel(SbBatch b) {
   __shared__ float s_max[4][16];
   const int jn = find_job(b.prep_starts, b.count);
@@ -507,12 +588,9 @@ __global__ __launch_bounds__(256) void sb_prep_kernel(SbBatch b) {
 #pragma unroll
     for (int l = 0; l < 8; ++l) mx = fmaxf(mx, fabsf(v[ff][l]));
   }
-  // row maximum: the lanes of one row (m, m + 16, m + 32, m + 48), then the waves
-  mx = fmaxf(mx, __shfl_xor(mx, 16));
-  mx = fmaxf(mx, __shfl_xor(mx, 32));
-  if (L < 16) s_max[wv][L] = mx;
-  __syncthreads();
-  mx = fmaxf(fmaxf(s_max[0][m], s_max[1][m]), fmaxf(s_max[2][m], s_max[3][m]));
+  mx = sb_row_max<false>(mx, s_max, wv, L);
+  const bool inf = __any(mx == __builtin_inff());  // of any row: the same in every wave
+  if (__builtin_expect(inf, 0)) mx = sb_row_max<true>(sb_finite_max(v), s_max, wv, L);
   const int e = mx > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
 #pragma unroll
   for (int ff = 0; ff < 4; ++ff) {
@@ -525,7 +603,7 @@ __global__ __launch_bounds__(256) void sb_prep_kernel(SbBatch b) {
     }
     *(u4 *)(J.xa + ((size_t)u * 16 + f) * 1024 + 16 * L) = h;
   }
-  if (tid < 16) J.xs[(size_t)u * 16 + tid] = ldexpf(1.f, -e);
+  if (tid < 16) J.xs[(size_t)u * 16 + tid] = inf ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
 }
 
 // The same fragments and scales for the feed-forward calls, whose matrices
@@ -585,11 +663,9 @@ __global__ __launch_bounds__(256) void sb_prep_rows_kernel(SbBatch b, int32_t *c
       mx = fmaxf(mx, fmaxf(fabsf(v[ff][2 * l]), fabsf(v[ff][2 * l + 1])));
     }
   }
-  mx = fmaxf(mx, __shfl_xor(mx, 16));
-  mx = fmaxf(mx, __shfl_xor(mx, 32));
-  if (L < 16) s_max[wv][L] = mx;
-  __syncthreads();
-  mx = fmaxf(fmaxf(s_max[0][m], s_max[1][m]), fmaxf(s_max[2][m], s_max[3][m]));
+  mx = sb_row_max<false>(mx, s_max, wv, L);
+  const bool inf = __any(mx == __builtin_inff());  // of any row: the same in every wave
+  if (__builtin_expect(inf, 0)) mx = sb_row_max<true>(sb_finite_max(v), s_max, wv, L);
   const int e = mx > 0.f ? 15 - __builtin_amdgcn_frexp_expf(mx) : 0;
 #pragma unroll
   for (int ff = 0; ff < 4; ++ff) {
@@ -602,7 +678,7 @@ __global__ __launch_bounds__(256) void sb_prep_rows_kernel(SbBatch b, int32_t *c
     }
     *(u4 *)(J.xa + ((size_t)u * 16 + 4 * wv + ff) * 1024 + 16 * L) = h;
   }
-  if (part == 0 && tid < 16) J.xs[(size_t)u * 16 + tid] = ldexpf(1.f, -e);
+  if (part == 0 && tid < 16) J.xs[(size_t)u * 16 + tid] = inf ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
 }
 
 static hipError_t launch_sb_prep_rows(SbBatch &b, hipStream_t s, bool *fits) {

@@ -34,8 +34,9 @@
  * verified by svq_pack; tables that admit no such split are multiplied
  * four activation rows at a time by the m <= 4 kernels instead).  The activations enter the dot products as fp16
  * after a power-of-two scale chosen per 512-slot block of permuted inputs
- * (per row of x): the block's largest magnitude is scaled into [2^14, 2^15),
- * which keeps every bf16 value of magnitude at least 2^-31 times that
+ * (per row of x): the block's largest finite magnitude is scaled into
+ * [2^14, 2^15) (infinities and NaN keep their value, and give the infinite
+ * and NaN outputs that the products and sums have), which keeps every bf16 value of magnitude at least 2^-31 times that
  * largest one exact; smaller values round to fp16 subnormals (an absolute
  * error of at most 2^-39 times the block's largest magnitude).  For m > 16
  * (the dequant GEMM on the matrix cores) a weight enters as RNE_bf16(R*D)

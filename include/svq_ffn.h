@@ -14,8 +14,10 @@
  * power-of-two scale) and activations as fp16 after a power-of-two scale per
  * row (a bf16 value keeps its bits down to 2^-29 of the row's largest finite
  * magnitude; below, the error is at most 2^-38 of it); matrices whose tables
- * admit no exact split run svq.h's bf16 form.  Accumulation is fp32.  Bias,
- * activation, gating, residual and the sum over a token's experts are fp32;
+ * admit no exact split run svq.h's bf16 form.  Accumulation is fp32.  Scales are taken from finite
+ * magnitudes; an infinite activation gives the infinite or NaN output that
+ * the products and sums have (NaN also where its weight rounds to zero in
+ * fp16).  Bias, activation, gating, residual and the sum over a token's experts are fp32;
  * each output is rounded once, to nearest even.  The inner activation of an
  * expert layer (act(gate) * up) enters the down product as fp16 (11
  * significant bits) after a power-of-two scale: for few slots
