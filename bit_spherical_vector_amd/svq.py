@@ -642,6 +642,9 @@ def encode(w, perm, bd: int, codebook, radius, stream=None):
 # it many times: tensors are the caller's and must outlive the object, and
 # objects that share a workspace must be called in one stream's order.  Each
 # call goes to the given stream, or to the one that is current when it is made.
+# A workspace that an object allocates itself follows the streams its calls go
+# to; calls of one object on several streams are the caller's to order, and an
+# object whose calls a graph has captured must outlive that graph's replays.
 # ---------------------------------------------------------------------------
 
 def _dt(t, what: str) -> int:
@@ -705,18 +708,43 @@ class _Call:
 
     def _prepare(self, name: str, args, device, workspace, stream) -> None:
         import torch
+        if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is one of {stream.device}, not of {device}")
         self.name, self.args, self.device = name, tuple(args), device
         self.fn = getattr(LIB, name)
         self.stream = None if stream is None else int(stream.cuda_stream)
         nbytes = ctypes.c_size_t(0)
+        self.home = None  # the stream whose memory an own workspace is
         with torch.cuda.device(device):  # the plan follows the device's compute units
             _check(self.fn(*self.args, None, ctypes.byref(nbytes), None), f"{name} (workspace query)")
-        if workspace is None or workspace.numel() * workspace.element_size() < nbytes.value:
-            workspace = torch.empty(max(nbytes.value, 1), dtype=torch.uint8, device=device)
+            if workspace is None or workspace.numel() * workspace.element_size() < nbytes.value:
+                # from the pool of the stream that uses it: the allocator may
+                # hand out memory whose last user is still queued there, and
+                # takes it back in that stream's order
+                self.home = torch.cuda.current_stream(device) if stream is None else stream
+                with torch.cuda.stream(self.home):
+                    workspace = torch.empty(max(nbytes.value, 1), dtype=torch.uint8, device=device)
+                self.ordered = {int(self.home.cuda_stream)}
         self.workspace = workspace
         self.ws_ptr = workspace.data_ptr()
         self.ws_size = ctypes.c_size_t(workspace.numel() * workspace.element_size())
         self.ws_size_ref = ctypes.byref(self.ws_size)
+
+    def _order(self, stream: int) -> None:
+        """First call on the current stream, not the one that the workspace
+        was allocated on: it waits for what that one had queued (whose memory
+        the workspace may have been), and the memory is not given away before
+        this stream is done with it.  Captured: a capture cannot wait for
+        other streams' work, and its graph replays after it."""
+        import torch
+        with torch.cuda.device(self.device):
+            current = torch.cuda.current_stream(self.device)
+            self.workspace.record_stream(current)
+            if not torch.cuda.is_current_stream_capturing():
+                current.wait_stream(self.home)
+                self.ordered.add(stream)
 
     def __call__(self) -> None:
         # the raw handle of the current stream: torch.cuda.current_stream()
@@ -724,6 +752,8 @@ class _Call:
         # launch costs 4.3 us in all
         index = self.device.index
         stream = self.stream if self.stream is not None else torch._C._cuda_getCurrentRawStream(index)
+        if self.home is not None and stream not in self.ordered:
+            self._order(stream)
         if index == torch.cuda.current_device():
             st = self.fn(*self.args, self.ws_ptr, self.ws_size_ref, stream)
         else:
