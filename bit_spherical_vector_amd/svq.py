@@ -692,14 +692,43 @@ def _choice(name: str, names, what: str) -> int:
 
 
 def _overlaps(a, b) -> bool:
-    """Whether the address ranges of two tensors meet."""
+    """Whether two 2-D operands may share an element.  Rows of one stride in
+    bytes are compared column range by column range (two operands may be
+    columns of one wider buffer); otherwise whole address ranges."""
     def span(t):
-        if t.numel() == 0:
-            return t.data_ptr(), t.data_ptr()
-        last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
-        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
+        (rows, cols), size = t.shape, t.element_size()
+        return t.data_ptr(), rows * cols and (rows - 1) * t.stride(0) * size + cols * size
+    (a0, na), (b0, nb) = span(a), span(b)
+    if not (na and nb and a0 < b0 + nb and b0 < a0 + na):
+        return False
+    wa, wb = a.shape[1] * a.element_size(), b.shape[1] * b.element_size()
+    step = a.stride(0) * a.element_size()
+    if a.shape[0] > 1 and b.shape[0] > 1 and step == b.stride(0) * b.element_size() and max(wa, wb) <= step:
+        at = (b0 - a0) % step  # b's columns in a's rows
+        return at < wa or at + wb > step
+    return True
+
+
+def _same_rows(a, b) -> bool:
+    """Whether two operands of one row count are the same memory, row by row."""
+    return a.data_ptr() == b.data_ptr() and a.dtype == b.dtype and (a.shape[0] == 1 or a.stride(0) == b.stride(0))
+
+
+def _not_over(x, y) -> None:
+    """Refuses an output over the activations, which blocks still read while
+    others write."""
+    if _overlaps(x, y):
+        raise ValueError("y overlaps x")
+
+
+def _residual_arg(residual, y, m: int, n: int, ldy: int, device):
+    """Checks a residual of the output y; returns its row stride and type."""
+    ldr = _matrix_arg(residual, "residual", m, n, device, (torch.bfloat16, torch.float32))
+    if _same_rows(residual, y):
+        return ldy, _dt(residual, "residual")
+    if _overlaps(residual[:, :n], y[:, :n]):
+        raise ValueError("residual overlaps y without being y")
+    return ldr, _dt(residual, "residual")
 
 
 class _Call:
@@ -777,18 +806,14 @@ class EpilogueCall(_Call):
         _matrices_on(dev, (pm,))
         ldx = _matrix_arg(x, "x", m, pm.k, dev, (torch.bfloat16,))
         ldy = _matrix_arg(y, "y", m, pm.n, dev, (torch.bfloat16, torch.float32))
+        _not_over(x[:, :pm.k], y[:, :pm.n])
         ep = Epilogue(act=_choice(act, ACTIVATIONS, "act"))
         if bias is not None:
             _vector_arg(bias, "bias", pm.n, dev)
             ep.bias, ep.bias_dt = bias.data_ptr(), _dt(bias, "bias")
         if residual is not None:
-            ep.ldr = _matrix_arg(residual, "residual", m, pm.n, dev, (torch.bfloat16, torch.float32))
-            ep.residual, ep.residual_dt = residual.data_ptr(), _dt(residual, "residual")
-            same = residual.data_ptr() == y.data_ptr() and residual.dtype == y.dtype and (m == 1 or ep.ldr == ldy)
-            if not same and _overlaps(residual, y):
-                raise ValueError("residual overlaps y without being y")
-            if same:
-                ep.ldr = ldy
+            ep.residual = residual.data_ptr()
+            ep.ldr, ep.residual_dt = _residual_arg(residual, y, m, pm.n, ldy, dev)
         self.keep = (pm, x, y, bias, residual, ep)
         self._prepare("svq_linear_epilogue", (ctypes.byref(pm.handle), x.data_ptr(), m, ldx, ctypes.byref(ep),
                                               y.data_ptr(), ldy, _dt(y, "y")), dev, workspace, stream)
@@ -807,6 +832,7 @@ class GluCall(_Call):
         _matrices_on(dev, (pm_gate, pm_up))
         ldx = _matrix_arg(x, "x", m, pm_gate.k, dev, (torch.bfloat16,))
         ldy = _matrix_arg(y, "y", m, pm_gate.n, dev, (torch.bfloat16, torch.float32))
+        _not_over(x[:, :pm_gate.k], y[:, :pm_gate.n])
         kinds = []
         for b, what in ((bias_gate, "bias_gate"), (bias_up, "bias_up")):
             if b is not None:
@@ -865,18 +891,14 @@ class MoeFfnCall(_Call):
         _matrices_on(dev, gates, ups, downs)
         ldx = _matrix_arg(x, "x", m, k, dev, (torch.bfloat16,))
         ldy = _matrix_arg(y, "y", m, n, dev, (torch.bfloat16, torch.float32))
+        if not (_same_rows(x, y) and k == n):
+            _not_over(x[:, :k], y[:, :n])
         for t, what, dtype in ((expert_ids, "expert_ids", torch.int32), (weights, "weights", torch.float32)):
             if tuple(t.shape) != (m, topk) or not t.is_contiguous() or t.dtype != dtype or t.device != dev:
                 raise ValueError(f"{what} must be a contiguous {dtype} tensor of [m, topk] on {dev}")
         ldr, rdt = 0, SVQ_BF16
         if residual is not None:
-            ldr = _matrix_arg(residual, "residual", m, n, dev, (torch.bfloat16, torch.float32))
-            rdt = _dt(residual, "residual")
-            same = residual.data_ptr() == y.data_ptr() and residual.dtype == y.dtype and (m == 1 or ldr == ldy)
-            if not same and _overlaps(residual, y):
-                raise ValueError("residual overlaps y without being y")
-            if same:
-                ldr = ldy
+            ldr, rdt = _residual_arg(residual, y, m, n, ldy, dev)
         sets = [handle_array(p) for p in (gates, ups, downs)]
         self.keep = (list(gates), list(ups), list(downs), sets, x, expert_ids, weights, y, residual)
         self._prepare("svq_moe_ffn",

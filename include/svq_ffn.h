@@ -60,7 +60,8 @@ typedef struct {
 
 /* svq_linear_epilogue: y = act(x * What^T + bias) + residual for one packed
  * matrix; svq_linear with the epilogue applied to the fp32 sums.
- *   w, x, m, ldx, y, ldy, ydt, workspace, stream: as for svq_linear.
+ *   w, x, m, ldx, y, ldy, ydt, workspace, stream: as for svq_linear; y must
+ *             not overlap x.
  *   ep: host, not NULL (a zeroed struct means no epilogue). */
 svq_status svq_linear_epilogue(const svq_handle *w, const void *x, int64_t m, int64_t ldx,
                                const svq_epilogue *ep, void *y, int64_t ldy, svq_dtype ydt,
@@ -111,7 +112,9 @@ svq_status svq_moe_route(const void *x, int64_t m, int64_t ldx, const void *w, s
  *   residual:       device [m][ldr] of residual_dt, ldr >= down's n, or NULL;
  *                   it may be y itself (ldr == ldy, same type), no other
  *                   overlap with y is allowed.
- *   y:              device [m][ldy] of type ydt, ldy >= down's n.
+ *   y:              device [m][ldy] of type ydt, ldy >= down's n.  It may be x
+ *                   itself (ldx == ldy, bf16, down's n the columns of x), with
+ *                   or without x as the residual; no other overlap with x.
  *   workspace, stream: as for svq_moe_linear.
  * SVQ_ERR_UNSUPPORTED: up to 64 slots, rows too long for a block's LDS (an
  * inner width beyond 36864, or beyond about 20000 with matrices that admit no

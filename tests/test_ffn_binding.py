@@ -1,6 +1,7 @@
 """The binding of the feed-forward calls without a GPU: which stream a
 workspace is allocated on and tied to, with stand-ins for the library's entry
-points and for torch's streams."""
+points and for torch's streams; and the operands that it refuses, each by its
+own message beside a call that passes."""
 import contextlib
 import types
 
@@ -137,3 +138,142 @@ def test_given_workspace(gpu):
         _call(workspace=elsewhere)
     with pytest.raises(ValueError, match="stream is one of"):
         _call(stream=Stream(7, torch.device("cuda", 1)))
+
+
+@pytest.fixture
+def prepared(monkeypatch):
+    """What a call object hands to the library, in place of the call."""
+    seen = []
+    monkeypatch.setattr(svq._Call, "_prepare", lambda self, name, args, *rest: seen.append((name, args)))
+    return seen
+
+
+def z(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+PM, SQUARE = svq.PackedMatrix(None, _handle(96, 520)), svq.PackedMatrix(None, _handle(520, 520))
+WIDE = z(4, 96)
+
+
+@pytest.mark.parametrize("over,message", [
+    ({}, None), (dict(y=z(3, 96, dtype=torch.float32)), None), (dict(bias=z(96)), None), (dict(x=z(3, 600)), None),
+    (dict(residual=z(3, 100)[:, 2:98]), None),
+    (dict(x=z(3, 520, dtype=torch.float32)), "x has the wrong type"), (dict(x=z(3, 512)), "x must be 2-D, 3 rows of 520"),
+    (dict(x=z(520, 3).t()), "x must be 2-D"), (dict(x=z(3 * 520)[:520]), "x must be 2-D"),
+    (dict(y=z(3, 96, dtype=torch.float16)), "y has the wrong type"), (dict(y=z(2, 96)), "y must be 2-D, 3 rows"),
+    (dict(y=z(3, 95)), "y must be 2-D, 3 rows of 96"), (dict(bias=z(95)), "bias must be a contiguous vector of 96"),
+    (dict(bias=z(192)[::2]), "bias must be a contiguous vector"),
+    (dict(bias=z(96, dtype=torch.float64)), "bias must be bf16 or fp32"), (dict(act="swish"), "act must be one of"),
+    (dict(residual=z(3, 90)), "residual must be 2-D"), (dict(residual=z(3, 96, dtype=torch.float64)), "residual has the wrong"),
+    (dict(residual=z(300).unfold(0, 96, 95)[:3]), "rows of residual overlap"),
+    (dict(y=WIDE[:3], residual=WIDE[:3]), None), (dict(y=WIDE[:3], residual=WIDE[1:]), "residual overlaps y"),
+    (dict(y=z(3, 96).cpu(), residual=torch.zeros((3, 96), device="meta")), "residual is on meta"),
+])
+def test_epilogue_operands(prepared, over, message):
+    args = dict(x=z(3, 520), y=z(3, 96))
+    args.update(over)
+    if message is None:
+        svq.EpilogueCall(PM, **args)
+        assert len(prepared) == 1
+        return
+    with pytest.raises(ValueError, match=message):
+        svq.EpilogueCall(PM, **args)
+    assert not prepared
+
+
+@pytest.mark.parametrize("over,message", [
+    ({}, None), (dict(bias_up=z(96, dtype=torch.float32)), None), (dict(up=PM), None),
+    (dict(x=z(3, 519)), "x must be 2-D"), (dict(x=z(4, 520)), "y must be 2-D, 4 rows"),
+    (dict(y=z(3, 96, dtype=torch.int16)), "y has the wrong type"), (dict(bias_gate=z(97)), "bias_gate must be a contiguous"),
+    (dict(bias_gate=z(96), bias_up=z(96, dtype=torch.float32)), "of one type"), (dict(act="silu2"), "act must be one of"),
+])
+def test_glu_operands(prepared, over, message):
+    args = dict(up=PM, x=z(3, 520), y=z(3, 96))
+    args.update(over)
+    if message is None:
+        svq.GluCall(PM, args.pop("up"), **args)
+        assert len(prepared) == 1
+        return
+    with pytest.raises(ValueError, match=message):
+        svq.GluCall(PM, args.pop("up"), **args)
+
+
+@pytest.mark.parametrize("over,message", [
+    ({}, None), (dict(w=z(4, 520, dtype=torch.float32)), None), (dict(select_bias=z(4, dtype=torch.float32)), None),
+    (dict(ids=z(3, 2, dtype=torch.int64)), "ids must be a contiguous torch.int32"),
+    (dict(ids=z(3, 4, dtype=torch.int32)[:, ::2]), "ids must be a contiguous"),
+    (dict(weights=z(3, 2)), "weights must be a contiguous torch.float32"),
+    (dict(weights=z(2, 3, dtype=torch.float32)), "weights must be a contiguous"),
+    (dict(w=z(4, 520, dtype=torch.float16)), "w has the wrong type"), (dict(x=z(3, 512)), "x must be 2-D"),
+    (dict(x=z(2, 520)), "x must be 2-D, 3 rows"), (dict(select_bias=z(4)), "select_bias must be torch.float32"),
+    (dict(select_bias=z(5, dtype=torch.float32)), "select_bias must be a contiguous"), (dict(score="tanh"), "score must be one of"),
+])
+def test_route_operands(prepared, over, message):
+    args = dict(x=z(3, 520), w=z(4, 520), ids=z(3, 2, dtype=torch.int32), weights=z(3, 2, dtype=torch.float32))
+    args.update(over)
+    if message is None:
+        svq.MoeRouteCall(**args)
+        assert len(prepared) == 1
+        return
+    with pytest.raises(ValueError, match=message):
+        svq.MoeRouteCall(**args)
+
+
+@pytest.mark.parametrize("over,message", [
+    ({}, None), (dict(residual=z(3, 520, dtype=torch.float32)), None), (dict(downs=[]), "sequences of one length"),
+    (dict(gates=[], ups=[], downs=[]), "sequences of one length"), (dict(ups=[PM] * 2), "sequences of one length"),
+    (dict(expert_ids=z(2, 2, dtype=torch.int32)), "x must be 2-D, 2 rows"),
+    (dict(expert_ids=z(3, 2, dtype=torch.int64)), "expert_ids must be a contiguous torch.int32"),
+    (dict(weights=z(3, 2, dtype=torch.float64)), "weights must be a contiguous torch.float32"),
+    (dict(weights=z(3, 1, dtype=torch.float32)), "weights must be a contiguous"), (dict(y=z(3, 519)), "y must be 2-D"),
+    (dict(residual=z(3, 519)), "residual must be 2-D"), (dict(act="x"), "act must be one of"),
+])
+def test_expert_layer_operands(prepared, over, message):
+    down = svq.PackedMatrix(None, _handle(520, 96))
+    args = dict(gates=[PM], ups=[PM], downs=[down], x=z(3, 520), expert_ids=z(3, 2, dtype=torch.int32),
+                weights=z(3, 2, dtype=torch.float32), y=z(3, 520))
+    args.update(over)
+    if message is None:
+        svq.MoeFfnCall(**args)
+        assert len(prepared) == 1
+        return
+    with pytest.raises(ValueError, match=message):
+        svq.MoeFfnCall(**args)
+
+
+def test_outputs_over_the_activations(prepared):
+    """An output over x is refused, except an expert layer's that is x itself;
+    columns of one wider buffer do not overlap."""
+    wide = z(4, 1100)
+    x = wide[:3, :520]
+    other = z(3, 520)
+    call = lambda y, **over: svq.EpilogueCall(SQUARE, x, y, **over)
+    call(wide[:3, 520:1040])
+    call(wide[:3, 580:])
+    call(wide[:3, 520:1040], residual=wide[:3, 520:1040])
+    call(other, residual=x)  # the residual may be x
+    call(wide[:3, 520:1040], residual=x)
+    assert len(prepared) == 5
+    for y in (x, wide[1:, :520], wide[:3, 519:1039], wide[1:, 4:524], wide.view(-1)[1000:1000 + 3 * 520].view(3, 520)):
+        with pytest.raises(ValueError, match="y overlaps x"):
+            call(y)
+        with pytest.raises(ValueError, match="y overlaps x"):
+            svq.GluCall(SQUARE, SQUARE, x, y)
+    with pytest.raises(ValueError, match="residual overlaps y"):
+        svq.EpilogueCall(SQUARE, other, wide[:3, 520:1040], residual=wide[:3, 519:1039])
+    ids, wt = z(3, 2, dtype=torch.int32), z(3, 2, dtype=torch.float32)
+    moe = lambda y, **over: svq.MoeFfnCall([SQUARE], [SQUARE], [SQUARE], x, ids, wt, y, **over)
+    before = len(prepared)
+    moe(x)
+    moe(x, residual=x)
+    moe(wide[:3, 520:1040])
+    assert len(prepared) == before + 3
+    for y in (wide[1:, :520], wide[:3, 1:521]):
+        with pytest.raises(ValueError, match="y overlaps x"):
+            moe(y)
+    # one row: the row strides say nothing
+    one = wide[:1, :520]
+    svq.MoeFfnCall([SQUARE], [SQUARE], [SQUARE], one, ids[:1], wt[:1], one)
+    with pytest.raises(ValueError, match="y overlaps x"):
+        svq.EpilogueCall(SQUARE, one, wide[:1, 519:1039])

@@ -1,5 +1,5 @@
 """Uses of the feed-forward calls beside one call on one stream's operands:
-workspaces across streams."""
+workspaces across streams, outputs over or beside their inputs."""
 import pytest
 
 import synth
@@ -81,3 +81,40 @@ def test_captured_on_a_fresh_object(svq):
         (graph.replay if i % 2 else call)()
         torch.cuda.synchronize()
         assert torch.equal(y, want), i
+
+
+@pytest.mark.parametrize("m", [1, 20, 40])
+@pytest.mark.parametrize("split", [True, False])
+def test_expert_layer_over_its_input(svq, m, split):
+    """y is x itself, with and without x as the residual: as into a fresh y,
+    in the per-slot form, the grouped one and the one of separate products."""
+    e, f, k, topk = 4, 72, 136, 2
+    sets = []
+    for s, (n, kk) in enumerate(((f, k), (f, k), (k, f))):
+        mats = [synth.random_matrix(n, kk, 7, seed=(132, s, i)) for i in range(e)]
+        if not split:  # tables that admit no two fp16 halves
+            mats[1].radius, mats[1].codebook = mats[1].radius.copy(), mats[1].codebook.copy()
+            mats[1].radius[0], mats[1].radius[1], mats[1].codebook[0, :] = 0x3C01, 0x7B53, 0x0001
+        sets.append([svq.pack(a) for a in mats])
+    x = to_device_bf16(synth.random_activations(m, k, seed=(132, m)))
+    g = torch.Generator().manual_seed(24)
+    ids = torch.stack([torch.randperm(e, generator=g)[:topk] for _ in range(m)]).to(torch.int32).cuda()
+    wt = torch.rand((m, topk), generator=g).cuda()
+    for res in (False, True):
+        want = svq.moe_ffn(*sets, x, ids, wt, residual=x if res else None)
+        y = x.clone()
+        svq.moe_ffn(*sets, y, ids, wt, residual=y if res else None, out=y)
+        assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("m", [1, 7, 40, 150])
+def test_operands_as_columns_of_one_buffer(svq, m):
+    """x, residual and y side by side in the rows of one buffer."""
+    n, k = 96, 264
+    pm = svq.pack(synth.random_matrix(n, k, 7, seed=(133, n, k)))
+    wide = torch.randn((m, k + 2 * n), generator=torch.Generator().manual_seed(25)).bfloat16().cuda()
+    before = wide.clone()
+    x, r, y = wide[:, n:n + k], wide[:, n + k:], wide[:, :n]
+    want = svq.linear_epilogue(pm, x.contiguous(), residual=r.contiguous(), act="relu")
+    svq.linear_epilogue(pm, x, residual=r, act="relu", out=y)
+    assert torch.equal(y, want) and torch.equal(wide[:, n:], before[:, n:])
