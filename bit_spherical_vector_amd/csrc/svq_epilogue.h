@@ -30,8 +30,7 @@ __device__ __forceinline__ float act_apply(float v, int act) {
   }
 }
 
-// Cheaper forms for values that are rounded to 11 bits or fewer next, or are
-// sums over weights so rounded: the
+// Cheaper forms for values that are rounded to 11 bits or fewer next: the
 // hardware's exp2 and reciprocal (each within about 1 ulp) in place of expf
 // and a division; the argument's rounding adds |v| 2^-24.
 template <int ACT>
@@ -54,6 +53,13 @@ __device__ __forceinline__ float act_fast(float v, int act) {
     case SVQ_ACT_GELU_TANH: return act_fast<SVQ_ACT_GELU_TANH>(v);
     default: return v;
   }
+}
+
+// Beyond 16 rows, where tiles and the join of K ranges finish parts of one
+// output: the cheap forms where it is rounded to bf16, in all of them, and
+// expf and a division for an fp32 output.
+__device__ __forceinline__ float act_out(float v, int act, bool bf) {
+  return bf ? act_fast(v, act) : act_apply(v, act);
 }
 
 __device__ __forceinline__ float load_f(const void *p, size_t i, int f32) {
@@ -80,27 +86,28 @@ struct NoEpi {
 struct Epi {
   static constexpr bool on = true, partial = false, f16 = false;
   EpiArgs a;
+  bool bf = false;  // act_out's
   // output row `row`, column n
   __device__ __forceinline__ float operator()(float v, int row, int n) const {
     if (a.bias) v += load_f(a.bias, n, a.bias_f32);
-    v = act_apply(v, a.act);
+    v = act_out(v, a.act, bf);
     if (a.res) v += load_f(a.res, (size_t)row * a.ldr + n, a.res_f32);
     return v;
   }
   // columns n0 .. n0 + 3 (n0 a multiple of 4; those below nlim) of row `row`
-  __device__ __forceinline__ void store4(void *y, int64_t ldy, bool bf, bool yvec, f4 v, int row, int n0,
+  __device__ __forceinline__ void store4(void *y, int64_t ldy, bool ybf, bool yvec, f4 v, int row, int n0,
                                          int nlim) const {
     const size_t at = (size_t)row * ldy + n0;
     if (n0 + 4 > nlim) {
-      for (int l = 0; n0 + l < nlim; ++l) store_out(y, at + l, (*this)(v[l], row, n0 + l), bf ? 0 : 1);
+      for (int l = 0; n0 + l < nlim; ++l) store_out(y, at + l, (*this)(v[l], row, n0 + l), ybf ? 0 : 1);
       return;
     }
     if (a.bias) v += load_f4(a.bias, n0, a.bias_f32, a.bias_vec != 0);
     if (a.act != SVQ_ACT_NONE)
 #pragma unroll
-      for (int l = 0; l < 4; ++l) v[l] = act_apply(v[l], a.act);
+      for (int l = 0; l < 4; ++l) v[l] = act_out(v[l], a.act, bf);
     if (a.res) v += load_f4(a.res, (size_t)row * a.ldr + n0, a.res_f32, a.res_vec != 0);
-    store_f4(y, at, v, bf, yvec);
+    store_f4(y, at, v, ybf, yvec);
   }
   static __device__ __forceinline__ void store_f4(void *y, size_t at, f4 v, bool bf, bool vec) {
     if (bf) {

@@ -1030,17 +1030,21 @@ hipError_t launch_prefill_batched(PrefillBatch &b, int bm, int blocks, hipStream
 // * otherwise fp32 partial tiles and one reduce launch that sums the K ranges
 //   and applies epilogue or gating.
 
-template <int ACT>
+// act_out of an accumulator block (act is uniform; BF: the output's type, a
+// parameter of the kernels, since both forms in one kernel would double code
+// that is repeated for every accumulator register).
+template <int ACT, bool BF>
 __device__ __forceinline__ void act16(f16x &v) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = act_fast<ACT>(v[e]);
+  for (int e = 0; e < 16; ++e) v[e] = BF ? act_fast<ACT>(v[e]) : act_apply(v[e], ACT);
 }
-__device__ __forceinline__ void act16(f16x &v, int act) {  // act is uniform
+template <bool BF>
+__device__ __forceinline__ void act16(f16x &v, int act) {
   switch (act) {
-    case SVQ_ACT_RELU: act16<SVQ_ACT_RELU>(v); break;
-    case SVQ_ACT_SILU: act16<SVQ_ACT_SILU>(v); break;
-    case SVQ_ACT_GELU: act16<SVQ_ACT_GELU>(v); break;
-    case SVQ_ACT_GELU_TANH: act16<SVQ_ACT_GELU_TANH>(v); break;
+    case SVQ_ACT_RELU: act16<SVQ_ACT_RELU, BF>(v); break;
+    case SVQ_ACT_SILU: act16<SVQ_ACT_SILU, BF>(v); break;
+    case SVQ_ACT_GELU: act16<SVQ_ACT_GELU, BF>(v); break;
+    case SVQ_ACT_GELU_TANH: act16<SVQ_ACT_GELU_TANH, BF>(v); break;
     default: break;
   }
 }
@@ -1111,6 +1115,7 @@ __device__ __forceinline__ void lds_rows(float *s_c, const f16x (&v)[NJ], int la
     for (int e = 0; e < 16; ++e)
       s_c[lds_at((e & 3) + 8 * (e >> 2) + 4 * (lane >> 5), 32 * j + (lane & 31))] = v[j][e];
 }
+template <bool BF>
 __device__ __forceinline__ void out_rows(const DqTile &T, const float *s_c, int row0, int n0, int lane,
                                          const EpiArgs &a) {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // lanes read what other lanes wrote
@@ -1142,7 +1147,7 @@ __device__ __forceinline__ void out_rows(const DqTile &T, const float *s_c, int 
     for (int t = 0; t < 4; ++t) {
       if (a.bias) o[t] += bias;
 #pragma unroll
-      for (int l = 0; l < 4; ++l) o[t][l] = act_fast(o[t][l], a.act);
+      for (int l = 0; l < 4; ++l) o[t][l] = act_out(o[t][l], a.act, BF);
       o[t] += res[t];
     }
 #pragma unroll
@@ -1198,7 +1203,7 @@ struct MixTile {
 
 // act(p + bias) + residual: straight from the accumulators, or (ROWS, see
 // out_rows) through LDS.
-template <bool ROWS>
+template <bool ROWS, bool BF>
 struct LinTile {
   static constexpr bool on = true, partial = false, f16 = true;
   EpiArgs a;
@@ -1219,7 +1224,7 @@ struct LinTile {
           for (int j = 0; j < NJ; ++j) v[j] = scaled16(C[i + h][j], re, xexp);
           lds_rows(s_c + h * 32 * 64, v, lane);
         }
-        out_rows(T, s_c, TM * wm + 32 * i, rt0 * UNIT_ROWS + TN * wn, lane, a);
+        out_rows<BF>(T, s_c, TM * wm + 32 * i, rt0 * UNIT_ROWS + TN * wn, lane, a);
       }
       return;
     }
@@ -1240,7 +1245,7 @@ struct LinTile {
         }
         f16x v = scaled16(C[i][j], re, xexp);
         if (a.bias) v += load_f(a.bias, nc, a.bias_f32);
-        act16(v, a.act);
+        act16<BF>(v, a.act);
         if (a.res) v += res;
         put16(T, v, rr0, n);
       }
@@ -1249,6 +1254,7 @@ struct LinTile {
 };
 
 // act(g + bg) * (u + bu), the other matrix's tile through memory.
+template <bool BF>
 struct GluTile {
   static constexpr bool on = true, partial = false, f16 = true;
   const void *bias_g, *bias_u;
@@ -1304,7 +1310,7 @@ struct GluTile {
         f16x g = scaled16(up ? o : C[i][j], re, xexp_g), u = scaled16(up ? C[i][j] : o, re, xexp_u);
         if (bias_g) g += load_f(bias_g, nc, bias_f32);
         if (bias_u) u += load_f(bias_u, nc, bias_f32);
-        act16(g, act);
+        act16<BF>(g, act);
         put16(T, g * u, rr0, n);
       }
     }
@@ -1473,25 +1479,27 @@ __global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2
   if (!ffn_tile(a, 256, T, jn, tile, part)) return;
   dq_tile_w8<PartTile>(T, smem, PartTile{part, a.part_ld});
 }
-template <bool ROWS>
+template <bool ROWS, bool BF>
 __global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void ffn_linear_kernel(FfnGemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   DqTile T;
   int jn, tile;
   float *part;
   if (!ffn_tile(a, 256, T, jn, tile, part)) return;
-  dq_tile_w8<MixTile<LinTile<ROWS>>>(T, smem, MixTile<LinTile<ROWS>>{{a.epi, a.rs, a.job[0].xexp}, {part, a.part_ld}});
+  using Tile = MixTile<LinTile<ROWS, BF>>;
+  dq_tile_w8<Tile>(T, smem, Tile{{a.epi, a.rs, a.job[0].xexp}, {part, a.part_ld}});
 }
+template <bool BF>
 __global__ __launch_bounds__(W8_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void ffn_glu_kernel(FfnGemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   DqTile T;
   int jn, tile;
   float *part;
   if (!ffn_tile(a, 256, T, jn, tile, part)) return;
-  const GluTile g{a.bias_g, a.epi.bias, a.epi.bias_f32, a.epi.act, a.rs, a.job[0].xexp, a.job[1].xexp, jn != 0,
+  const GluTile<BF> g{a.bias_g, a.epi.bias, a.epi.bias_f32, a.epi.act, a.rs, a.job[0].xexp, a.job[1].xexp, jn != 0,
                   (uint64_t *)a.swap + (size_t)(2 * tile + jn) * (256 * 256 / 2),
                   (const uint64_t *)a.swap + (size_t)(2 * tile + 1 - jn) * (256 * 256 / 2), a.cnt + tile};
-  dq_tile_w8<MixTile<GluTile>>(T, smem, MixTile<GluTile>{g, {part, a.part_ld}});
+  dq_tile_w8<MixTile<GluTile<BF>>>(T, smem, MixTile<GluTile<BF>>{g, {part, a.part_ld}});
 }
 
 // Sum of the K ranges in range order, then epilogue (one matrix) or gating
@@ -1515,7 +1523,7 @@ __global__ __launch_bounds__(256) void ffn_reduce_kernel(FfnGemmArgs a) {
     }
   }
   if (a.jobs == 1) {
-    const Epi epi{a.epi};
+    const Epi epi{a.epi, a.ydt == 0};
     epi.store4(a.y, a.ldy, a.ydt == 0, a.yvec != 0, v[0], row, n, n_all);
     return;
   }
@@ -1524,7 +1532,7 @@ __global__ __launch_bounds__(256) void ffn_reduce_kernel(FfnGemmArgs a) {
     if (n + l >= n_all) break;
     if (a.bias_g) v[0][l] += load_f(a.bias_g, n + l, a.epi.bias_f32);
     if (a.epi.bias) v[1][l] += load_f(a.epi.bias, n + l, a.epi.bias_f32);
-    v[0][l] = act_apply(v[0][l], a.epi.act) * v[1][l];
+    v[0][l] = act_out(v[0][l], a.epi.act, a.ydt == 0) * v[1][l];
   }
   if (n + 4 <= n_all)
     Epi::store_f4(a.y, (size_t)row * a.ldy + n, v[0], a.ydt == 0, a.yvec != 0);
@@ -1550,15 +1558,17 @@ hipError_t launch_ffn_gemm(const FfnGemmArgs &a, bool xvec, hipStream_t s) {
   if (e != hipSuccess) return e;
   const int tail = a.tiles_m * a.tiles_n - a.full;
   const int blocks = (a.full + 7) / 8 * 8 * a.jobs + tail * a.splits * a.jobs;
+  const bool bf = a.ydt == 0;
   if (bm == 64)
     e = ffn_launch(ffn_part64_kernel, blocks, 256, P_SMEM, a, s);
   else if (a.full == 0)
     e = ffn_launch(ffn_part256_kernel, blocks, W8_THREADS, W8_SMEM, a, s);
   else if (a.jobs == 1)
-    e = ffn_launch(a.epi.res && a.epi.res_vec && a.yvec ? ffn_linear_kernel<true> : ffn_linear_kernel<false>, blocks,
-                   W8_THREADS, W8_SMEM, a, s);
+    e = ffn_launch(a.epi.res && a.epi.res_vec && a.yvec ? (bf ? ffn_linear_kernel<true, true> : ffn_linear_kernel<true, false>)
+                                                        : (bf ? ffn_linear_kernel<false, true> : ffn_linear_kernel<false, false>),
+                   blocks, W8_THREADS, W8_SMEM, a, s);
   else
-    e = ffn_launch(ffn_glu_kernel, blocks, W8_THREADS, W8_SMEM, a, s);
+    e = ffn_launch(bf ? ffn_glu_kernel<true> : ffn_glu_kernel<false>, blocks, W8_THREADS, W8_SMEM, a, s);
   if (e != hipSuccess || tail == 0) return e;
   hipLaunchKernelGGL(ffn_reduce_kernel, dim3(tail * (bm / 4)), dim3(256), 0, s, a);
   return hipGetLastError();
