@@ -645,7 +645,9 @@ static hipError_t check_no_static_lds(Kern k) {
 
 template <int M>
 static hipError_t launch_gemv_m(GemvBatch &b, int blocks, size_t smem, hipStream_t s) {
-  if (b.pair) {
+  if constexpr (M == 1) {
+    if (b.pair) return hipErrorInvalidValue;  // a pair's single row has a launch of its own (glu_fused_kernel)
+  } else if (b.pair) {
     static const hipError_t pair_ok = check_no_static_lds(gemv_pair_kernel<M>);
     if (pair_ok != hipSuccess) return pair_ok;
     const hipError_t e = allow_smem(gemv_pair_kernel<M>, GV_HALF + smem);
