@@ -458,7 +458,8 @@ svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_h
   bool split = true;
   for (int c = 0; c < 3 && !few; ++c)
     for (int32_t e = 0; e < num_experts; ++e) split = split && has_split(&sets[c][e]);
-  const bool grouped = split && down->k <= MOE_GROUPED_MAX_INNER;
+  // up to 64 slots the inner width has its documented limit
+  const bool grouped = split && (S > 64 || down->k <= MOE_FEW_MAX_INNER);
   // what is left runs as separate products, which need more slots than the
   // per-slot launch takes
   if (!few && !grouped && S <= 64) return SVQ_ERR_UNSUPPORTED;

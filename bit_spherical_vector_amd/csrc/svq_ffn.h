@@ -107,9 +107,11 @@ bool moe_ffn_few_fits(const svq_handle *gate, const svq_handle *up, const svq_ha
                       int64_t slots);
 // ws null: only *need.
 hipError_t launch_moe_ffn_few(const MoeFfnArgs &f, void *ws, size_t *need, hipStream_t s);
-// The grouped form; every matrix has an exact split and the inner width is at
-// most MOE_GROUPED_MAX_INNER (its rows are staged in LDS as fp32).
-constexpr int MOE_GROUPED_MAX_INNER = 36 * 1024;
+// The grouped form; every matrix has an exact split (its rows are staged in
+// LDS as fp16, one at a time if need be, so any width up to SVQ_MAX_K fits).
+// MOE_FEW_MAX_INNER: the widest inner row that svq_moe_ffn takes for up to 64
+// slots (a documented refusal, which callers may rely on).
+constexpr int MOE_FEW_MAX_INNER = 36 * 1024;
 hipError_t launch_moe_ffn_grouped(const MoeFfnArgs &f, void *ws, size_t *need, hipStream_t s);
 
 // ---- router --------------------------------------------------------------------

@@ -116,9 +116,9 @@ svq_status svq_moe_route(const void *x, int64_t m, int64_t ldx, const void *w, s
  *                   itself (ldx == ldy, bf16, down's n the columns of x), with
  *                   or without x as the residual; no other overlap with x.
  *   workspace, stream: as for svq_moe_linear.
- * SVQ_ERR_UNSUPPORTED: up to 64 slots, rows too long for a block's LDS (an
- * inner width beyond 36864, or beyond about 20000 with matrices that admit no
- * exact split). */
+ * SVQ_ERR_UNSUPPORTED: up to 64 slots, an inner width beyond 36864, or, with
+ * matrices that admit no exact split, rows too long for a block's LDS (an
+ * inner width beyond about 20000). */
 svq_status svq_moe_ffn(const svq_handle *gate, const svq_handle *up, const svq_handle *down,
                        int32_t num_experts, const void *x, int64_t ldx, const int32_t *expert_ids,
                        const float *weights, int64_t m, int32_t topk, svq_act act,
