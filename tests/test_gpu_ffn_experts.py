@@ -66,6 +66,90 @@ def _run(svq, sets, x_bits, ids, wt, **kw):
     return svq.moe_ffn(gp, up, dp, to_device_bf16(x_bits), torch.from_numpy(ids).cuda(), torch.from_numpy(wt).cuda(), **kw)
 
 
+@pytest.mark.parametrize("e,topk,m", [(5, 3, 2731), (6, 1, 8193), (200, 3, 2800), (5, 5, 4100)])
+def test_more_slots_than_a_chunk(svq, e, topk, m):
+    """Chunks of at most 8192 slots of whole tokens (2730 tokens at three slots
+    each, so the first chunk does not fill them), one token in the last one or
+    many; slots without an expert, one expert twice, strided operands and the
+    residual in place, in the last chunk as in the first; ids of more than 128
+    experts (gate and up launched apart)."""
+    f, k, n = 24, 40, 56
+    sets = [experts(svq, e, f, k, 150), experts(svq, e, f, k, 151), experts(svq, e, n, f, 152)]
+    x_bits = synth.random_activations(m, k, seed=(150, e, m))
+    ids, wt = _routing(e, m, topk, [150, e, m])
+    for t in (0, m - 1):
+        ids[t, 0] = -1
+    if topk > 1:
+        ids[m - 1, -1], ids[1, 0], ids[m - 2, 0] = e, ids[1, 1], ids[m - 2, 1]
+    wide = vec(m * (n + 5), torch.bfloat16, 26).view(m, n + 5)
+    before, y = wide.clone(), wide[:, 2:2 + n]
+    r = f64(y)
+    _run(svq, sets, x_bits, ids, wt, residual=y, out=y)
+    ref, bound = layer64([s[0] for s in sets], x_bits, ids, wt, "silu", True)
+    ref = ref + r
+    check(y, ref, bound + U32 * (np.abs(ref) + bound), f"e={e} m={m}")
+    wide[:, 2:2 + n] = before[:, 2:2 + n]
+    assert torch.equal(wide, before)
+
+
+def test_chunks_captured_and_replayed(svq):
+    """A call of two chunks, whose second reuses the first's workspace,
+    replayed on a workspace that holds anything."""
+    e, f, k, m, topk = 4, 24, 40, 4200, 2
+    (_, gp), (_, up), (_, dp) = [experts(svq, e, f, k, 153), experts(svq, e, f, k, 154), experts(svq, e, k, f, 155)]
+    ids, wt = _routing(e, m, topk, [153])
+    x = torch.zeros((m, k), dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros((m, k), dtype=torch.float32, device="cuda")
+    call = svq.MoeFfnCall(gp, up, dp, x, torch.from_numpy(ids).cuda(), torch.from_numpy(wt).cuda(), y)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for i in range(4):
+        xi = to_device_bf16(synth.random_activations(m, k, seed=(153, i)))
+        want = svq.moe_ffn(gp, up, dp, xi, call.keep[5], call.keep[6], out_dtype=torch.float32)
+        x.copy_(xi)
+        y.fill_(float("nan"))
+        call.workspace.fill_((0xFF, 0x5A)[i % 2])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), f"replay {i}"
+
+
+@pytest.mark.parametrize("f,k,m", [(2056, 40, 3), (4616, 24, 1), (1032, 40, 40), (4104, 24, 40), (9224, 16, 33),
+                                   (40, 2056, 40), (40, 4616, 40), (24, 2568, 3)])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_wide_inner_and_outer_widths(svq, f, k, m, act):
+    """Inner widths past the values a thread prefetches in the per-slot form
+    (2048), past what a lane keeps of act(gate) * up (1024) and past the rows
+    that fit in one staging pass (4096) in the grouped one; the same for the
+    rows of x (2048, 4096)."""
+    e, topk = 3, 2
+    sets = [experts(svq, e, f, k, 156), experts(svq, e, f, k, 157), experts(svq, e, 24, f, 158)]
+    x_bits = synth.random_activations(m, k, seed=(156, f, m))
+    ids, wt = _routing(e, m, topk, [156, f])
+    y = _run(svq, sets, x_bits, ids, wt, act=act, out_dtype=torch.float32)
+    ref, bound = layer64([s[0] for s in sets], x_bits, ids, wt, act, m * topk > 64)
+    check(y, ref, bound, f"f={f} k={k} m={m}")
+
+
+@pytest.mark.parametrize("e,m", [(1, 97), (1, 1000), (2, 700)])
+def test_experts_of_many_items(svq, e, m):
+    """More rows an expert than a work item takes (48); all tokens on one
+    expert, or on one of two."""
+    f, k = 136, 264
+    sets = [experts(svq, e, f, k, 159), experts(svq, e, f, k, 160), experts(svq, e, k, f, 161)]
+    x_bits = synth.random_activations(m, k, seed=(159, m))
+    ids = np.full((m, 1), e - 1, dtype=np.int32)
+    wt = np.ones((m, 1), dtype=np.float32)
+    for rows in (m, 65):
+        y = _run(svq, sets, x_bits[:rows], ids[:rows], wt[:rows], out_dtype=torch.float32)
+        ref, bound = layer64([s[0] for s in sets], x_bits[:rows], ids[:rows], wt[:rows], "silu", rows > 64)
+        check(y, ref, bound, f"e={e} m={rows}")
+
+
 def test_inner_width_beyond_the_refused_one(svq):
     """Beyond 64 slots any inner width runs in the documented numerics: inner
     activations and weights in fp16, not through bf16."""
