@@ -1,9 +1,12 @@
 """Uses of the feed-forward calls beside one call on one stream's operands:
-workspaces across streams, outputs over or beside their inputs."""
+workspaces across streams, their exact size, outputs over or beside their
+inputs, offsets past 32 bits."""
+import numpy as np
 import pytest
 
 import synth
 from tests.gpu_common import require_gpu, to_device_bf16, torch
+from tests.test_gpu_ffn import SLOPE, U32, act64, half_step, product
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +121,107 @@ def test_operands_as_columns_of_one_buffer(svq, m):
     want = svq.linear_epilogue(pm, x.contiguous(), residual=r.contiguous(), act="relu")
     svq.linear_epilogue(pm, x, residual=r, act="relu", out=y)
     assert torch.equal(y, want) and torch.equal(wide[:, n:], before[:, n:])
+
+
+def _calls(svq, m):
+    """One call of each kind at m rows, as (make, outputs)."""
+    e, f, k, topk = 4, 72, 1032, 2
+    pg, pu, pd = [svq.pack(synth.random_matrix(n, kk, bd, seed=(134, n, bd))) for n, kk, bd in
+                  ((f, k, 7), (f, k, 8), (k, f, 6))]
+    sets = [[svq.pack(synth.random_matrix(n, kk, 7, seed=(135, s, i))) for i in range(e)]
+            for s, (n, kk) in enumerate(((f, k), (f, k), (k, f)))]
+    x = to_device_bf16(synth.random_activations(m, k, seed=(134, m)))
+    g = torch.Generator().manual_seed(27)
+    w = torch.randn((e, k), generator=g).cuda()
+    ids = torch.stack([torch.randperm(e, generator=g)[:topk] for _ in range(m)]).to(torch.int32).cuda()
+    wt = torch.rand((m, topk), generator=g).cuda()
+    new = lambda n, t=torch.bfloat16: torch.zeros((m, n), dtype=t, device="cuda")
+    h, y, ri, rw, z = new(f), new(f, torch.float32), new(topk, torch.int32), new(topk, torch.float32), new(k)
+    return [(lambda ws: svq.GluCall(pg, pu, x, h, workspace=ws), (h,)),
+            (lambda ws: svq.EpilogueCall(pg, x, y, act="gelu", workspace=ws), (y,)),
+            (lambda ws: svq.MoeRouteCall(x, w, ri, rw, workspace=ws), (ri, rw)),
+            (lambda ws: svq.MoeFfnCall(*sets, x, ids, wt, z, workspace=ws), (z,))]
+
+
+@pytest.mark.parametrize("m", [1, 3, 9, 16, 20, 40, 150, 300, 5000])
+def test_nothing_beyond_the_workspace(svq, m):
+    """A workspace of exactly the queried size inside a larger buffer: what
+    lies around it stays, whatever it held the result is the same, and a byte
+    less is replaced."""
+    for make, outs in _calls(svq, m):
+        call = make(None)
+        call()
+        want, need = [o.clone() for o in outs], call.workspace.numel()
+        buf = torch.empty(need + 8192, dtype=torch.uint8, device="cuda")
+        ws = buf[4096:4096 + need]
+        for fill in (0xFF, 0x00, 0x5A):
+            buf.fill_(fill)
+            for o in outs:
+                o.zero_()
+            call = make(ws)
+            assert call.workspace is ws
+            call()
+            assert all(torch.equal(o, w) for o, w in zip(outs, want)), call.name
+            assert bool((buf[:4096] == fill).all()) and bool((buf[4096 + need:] == fill).all()), call.name
+        assert make(buf[4096:4095 + need]).workspace.numel() >= need
+
+
+def _far_rows(m, n, dtype):
+    """[m, n] of which the last row starts past element 2^31."""
+    ld = -(-2 ** 31 // max(m - 1, 1)) + 24
+    return torch.empty((m - 1) * ld + n, dtype=dtype, device="cuda").as_strided((m, n), (ld, 1))
+
+
+@pytest.mark.parametrize("m", [2, 9, 40, 300])
+def test_row_strides_past_32_bits(svq, m):
+    """x, residual and y whose last rows lie beyond 2^31 elements, and ids
+    that name them."""
+    e, n, k, topk = 3, 40, 72, 2
+    pg, pu = [svq.pack(synth.random_matrix(n, k, bd, seed=(136, n, bd))) for bd in (7, 8)]
+    near = to_device_bf16(synth.random_activations(m, k, seed=(136, m)))
+    x = _far_rows(m, k, torch.bfloat16)
+    x.copy_(near)
+    res = torch.randn((m, k), generator=torch.Generator().manual_seed(28)).bfloat16().cuda()
+    y = _far_rows(m, n, torch.float32)
+    r = _far_rows(m, n, torch.bfloat16)
+    r.copy_(res[:, :n])
+    svq.linear_epilogue(pg, x, residual=r, act="silu", out=y)
+    assert torch.equal(y, svq.linear_epilogue(pg, near, residual=res[:, :n].contiguous(), act="silu", out_dtype=torch.float32))
+    svq.linear_glu(pg, pu, x, out=y)
+    assert torch.equal(y, svq.linear_glu(pg, pu, near, out_dtype=torch.float32))
+    del y, r
+    w = torch.randn((e, k), generator=torch.Generator().manual_seed(29)).cuda()
+    ids, wt = svq.moe_route(x, w, topk)
+    near_ids, near_wt = svq.moe_route(near, w, topk)
+    assert torch.equal(ids, near_ids) and torch.equal(wt, near_wt)
+    sets = [[svq.pack(synth.random_matrix(nn, kk, 7, seed=(137, s, i))) for i in range(e)]
+            for s, (nn, kk) in enumerate(((n, k), (n, k), (k, n)))]
+    want = svq.moe_ffn(*sets, near, ids, wt, residual=res)
+    z, r = _far_rows(m, k, torch.bfloat16), _far_rows(m, k, torch.bfloat16)
+    r.copy_(res)
+    svq.moe_ffn(*sets, x, ids, wt, residual=r, out=z)
+    assert torch.equal(z, want)
+
+
+def test_staged_activations_past_32_bits(svq):
+    """More than 2^31 staged activations, 300 rows over and over: every copy
+    within the bound of tests/test_gpu_ffn.py (the plan, and with it the order
+    of sums, follows the row count)."""
+    m, n, k = (1 << 20) + 3, 24, 2104
+    mats = [synth.random_matrix(n, k, bd, seed=(138, n, bd)) for bd in (7, 8)]
+    pg, pu = [svq.pack(a) for a in mats]
+    bits = synth.random_activations(300, k, seed=(138,))
+    few = to_device_bf16(bits)
+    x = few.repeat(m // 300 + 1, 1)[:m]
+    assert m * k > 2 ** 31
+    (g, gb), (u, ub) = [product(a, bits, True) for a in mats]
+    a = act64(g, "silu")
+    ea = SLOPE * gb + 16 * U32 * np.abs(a)
+    for run, ref, bound in ((lambda: svq.linear_epilogue(pg, x, act="silu"), a, ea),
+                            (lambda: svq.linear_glu(pg, pu, x), a * u,
+                             ea * np.abs(u) + ub * np.abs(a) + ea * ub + U32 * np.abs(a * u))):
+        y = run()
+        ref, tol = [torch.from_numpy(v).cuda() for v in (ref, bound + half_step(y.dtype) * (np.abs(ref) + bound))]
+        whole = m // 300 * 300
+        assert bool(((y[:whole].view(-1, 300, n).double() - ref).abs() <= tol).all())
+        assert bool(((y[whole:].double() - ref[:m - whole]).abs() <= tol[:m - whole]).all())
