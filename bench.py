@@ -48,32 +48,32 @@ COLD_BYTES = 600 << 20  # > 2 x 256 MB MALL
 # sources the traffic is reported as null.
 TRAFFIC = {
     # gemv_fused_kernel (profiles/gemv_fused_kernel_layer4b_m1_counters.md)
-    "layer4b_m1": {"sources": ("svq_kernels.hip", "svq_device.h"),
-                   "kernel_src_sha256": "4a04759af7c578a4",
-                   "fetch_kib": 14658.1, "fetch_factor": 2.0,
+    "layer4b_m1": {"sources": ("svq_kernels.hip", "svq_device.h", "svq_epilogue.h"),
+                   "kernel_src_sha256": "9f8426ebb98039fe",
+                   "fetch_kib": 14670.1, "fetch_factor": 2.0,
                    "write_kib": 60.0, "write_factor": 1.0},
     # sb_gemm_kernel (profiles/sb_gemm_kernel_layer4b_m16_counters.md)
-    "layer4b_m16": {"sources": ("svq_small.hip", "svq_device.h"),
-                    "kernel_src_sha256": "974c4e39f679f926",
-                    "fetch_kib": 17732.6, "fetch_factor": 2.0,
+    "layer4b_m16": {"sources": ("svq_small.hip", "svq_device.h", "svq_epilogue.h"),
+                    "kernel_src_sha256": "113eac6ebfa555e2",
+                    "fetch_kib": 17735.0, "fetch_factor": 2.0,
                     "write_kib": 1604.0, "write_factor": 1.0},
     # prefill_w8_kernel (profiles/prefill_w8_kernel_prefill_m2048_counters.md)
-    "prefill_m2048": {"sources": ("svq_prefill.hip", "svq_device.h"),
-                      "kernel_src_sha256": "4c0343ef209bd03b",
-                      "fetch_kib": 127727.7, "fetch_factor": 2.0,
+    "prefill_m2048": {"sources": ("svq_prefill.hip", "svq_device.h", "svq_epilogue.h"),
+                      "kernel_src_sha256": "9b5795208d5ccdee",
+                      "fetch_kib": 127727.1, "fetch_factor": 2.0,
                       "write_kib": 88064.0, "write_factor": 1.0},
     # moe_sb_kernel, mean over the step's two launches (gate + up batched,
     # down; profiles/moe_sb_kernel_moe128_m512_counters.md)
-    "moe128_m512": {"sources": ("svq_moe.hip", "svq_device.h"),
-                    "kernel_src_sha256": "09001c6073b1e389",
-                    "fetch_kib": 89439.5, "fetch_factor": 2.0,
-                    "write_kib": 16928.9, "write_factor": 1.0},
+    "moe128_m512": {"sources": ("svq_moe.hip", "svq_device.h", "svq_epilogue.h"),
+                    "kernel_src_sha256": "9062d46691cf97af",
+                    "fetch_kib": 89467.2, "fetch_factor": 2.0,
+                    "write_kib": 16942.3, "write_factor": 1.0},
 }
 
 
-def kernel_source_hash(sources=("svq_kernels.hip", "svq_device.h")) -> str:
+def kernel_source_hash(sources=("svq_kernels.hip", "svq_device.h", "svq_epilogue.h")) -> str:
     """sha256 prefix of a kernel's sources (translation unit and the device
-    header it includes)."""
+    headers it includes)."""
     import hashlib
     h = hashlib.sha256()
     for name in sources:

@@ -1018,7 +1018,7 @@ hipError_t launch_prefill_batched(PrefillBatch &b, int bm, int blocks, hipStream
 // activations in fp16 after a power-of-two scale per row (largest finite
 // magnitude into [2^14, 2^15): a bf16 value keeps its 8 bits down to 2^-29 of
 // it).  Same instructions per tile, and the weights' rounding, most of the
-// error of the bf16 form (2^-9 a weight), falls to 2^-12.
+// error of the bf16 form (up to 2^-8 of a weight), falls to 2^-11.
 //
 // One prep launch stages the rows once for both matrices of a pair.  Then:
 // * 256-row tiles, no K split: a product's epilogue applies to the

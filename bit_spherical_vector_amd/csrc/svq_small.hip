@@ -204,8 +204,10 @@ __device__ __forceinline__ void sb_redo(const MatView &w, const uint8_t *xa_all,
 // last of all to arrive finishes the pair.  (The body stands in the
 // kernel itself: behind a function call the job records, indexed at run time,
 // would be copied out of the kernel arguments.)
-// HI: with the weights' high halves only (RNE_fp16, 2^-12 a weight at most:
-// an eighth of a bf16 output's own half step; for calls that round to bf16).
+// HI: with the weights' high halves only (RNE_fp16, 2^-11 of a weight at most,
+// an eighth of a bf16 output's own half step; for calls that round to bf16,
+// whose relative error against 64 bits, 0.0017 in 2-norm for a gated pair of
+// 13 rows of 9728 x 2560, is that of exact weights in fp32 too).
 // Half the table reads, which bound the loop, and half the MFMAs.
 template <bool HI, typename... EA>
 __global__ __launch_bounds__(256) void sb_gemm_kernel(SbBatch b, EA... ea) {

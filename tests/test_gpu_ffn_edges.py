@@ -1,12 +1,12 @@
 """Uses of the feed-forward calls beside one call on one stream's operands:
 workspaces across streams, their exact size, outputs over or beside their
-inputs, offsets past 32 bits."""
+inputs, offsets past 32 bits, functions inside a capture, calls at once."""
 import numpy as np
 import pytest
 
 import synth
 from tests.gpu_common import require_gpu, to_device_bf16, torch
-from tests.test_gpu_ffn import SLOPE, U32, act64, half_step, product
+from tests.test_gpu_ffn import SLOPE, U32, _block, _block_weights, act64, half_step, product
 
 pytestmark = pytest.mark.gpu
 
@@ -225,3 +225,39 @@ def test_staged_activations_past_32_bits(svq):
         whole = m // 300 * 300
         assert bool(((y[:whole].view(-1, 300, n).double() - ref).abs() <= tol).all())
         assert bool(((y[whole:].double() - ref[:m - whole]).abs() <= tol[:m - whole]).all())
+
+
+@pytest.mark.parametrize("m", [1, 12, 48, 300])
+def test_functions_captured(svq, m):
+    """The plain functions inside a capture: outputs and workspaces come from
+    the graph's own memory, one call's workspace perhaps the next one's."""
+    _, _, pms = _block_weights(svq)
+    x = torch.zeros((m, 264), dtype=torch.bfloat16, device="cuda")
+    _block(svq, pms, x, True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = _block(svq, pms, x, True)
+    for i in range(4):
+        xi = to_device_bf16(synth.random_activations(m, 264, seed=(141, i, m)))
+        want = _block(svq, pms, xi, True)
+        x.copy_(xi)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), f"replay {i}"
+
+
+def test_two_calls_at_once(svq):
+    """Calls on two streams, each object with a workspace of its own."""
+    jobs = []
+    for i, m in enumerate((9, 300)):
+        pair, x, y = _pair(svq, m)
+        s = torch.cuda.Stream()
+        jobs.append((svq.GluCall(*pair, x, y, stream=s), y, svq.linear_glu(*pair, x)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for call, y, _ in jobs:
+            call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for _, y, want in jobs)

@@ -57,7 +57,7 @@ def check(y, ref, bound, label):
     bad = odd & ~same
     assert not bad.any(), f"{label}: {int(bad.sum())} of {int(odd.sum())} non-finite outputs at {np.argwhere(bad)[:4].tolist()}: " \
                           f"{got[bad][:4].tolist()} for {ref[bad][:4].tolist()}"
-    ok = np.abs(got - ref)[~odd] <= (bound + half_step(y.dtype) * (np.abs(ref) + bound))[~odd]
+    ok = np.abs(got[~odd] - ref[~odd]) <= bound[~odd] + half_step(y.dtype) * (np.abs(ref[~odd]) + bound[~odd])
     assert ok.all(), f"{label}: {int((~ok).sum())} finite outputs outside tolerance"
 
 
@@ -65,11 +65,13 @@ SIZES = [(40, 72, 1), (40, 4104, 1), (24, 1032, 3), (40, 520, 4), (40, 520, 5), 
          (40, 1032, 66), (40, 264, 129), (280, 264, 300)]
 
 
-@pytest.mark.parametrize("first", range(len(KINDS)))
-@pytest.mark.parametrize("n,k,m", SIZES)
+def cases(sizes):
+    """Every kind in turn where a call has fewer rows than there are kinds."""
+    return [(n, k, m, first) for n, k, m in sizes for first in range(len(KINDS) if m < len(KINDS) else 2)]
+
+
+@pytest.mark.parametrize("n,k,m,first", cases(SIZES))
 def test_epilogue(svq, n, k, m, first):
-    if m >= len(KINDS) and first > 1:
-        pytest.skip("the rows hold every kind")
     mat = synth.random_matrix(n, k, 7, seed=(120, n, k))
     x_bits = rows(m, k, first, (120, k, m))
     pm, x = svq.pack(mat), to_device_bf16(x_bits)
@@ -82,11 +84,8 @@ def test_epilogue(svq, n, k, m, first):
             check(y, a, slope_of(act) * b + 16 * U32 * np.abs(a), f"{act} {out} m={m}")
 
 
-@pytest.mark.parametrize("first", range(len(KINDS)))
-@pytest.mark.parametrize("n,k,m", SIZES + [(24, 16384, 1), (20, 4608, 9)])
+@pytest.mark.parametrize("n,k,m,first", cases(SIZES + [(24, 16384, 1), (20, 4608, 9)]))
 def test_glu(svq, n, k, m, first):
-    if m >= len(KINDS) and first > 1:
-        pytest.skip("the rows hold every kind")
     mats = [synth.random_matrix(n, k, bd, seed=(121, n + bd, k)) for bd in (6, 8)]
     x_bits = rows(m, k, first, (121, k, m))
     pg, pu = [svq.pack(a) for a in mats]
