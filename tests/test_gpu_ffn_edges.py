@@ -1,12 +1,13 @@
 """Uses of the feed-forward calls beside one call on one stream's operands:
 workspaces across streams, their exact size, outputs over or beside their
-inputs, offsets past 32 bits, functions inside a capture, calls at once."""
+inputs, offsets past 32 bits, functions inside a capture, calls at once,
+long rows."""
 import numpy as np
 import pytest
 
 import synth
 from tests.gpu_common import require_gpu, to_device_bf16, torch
-from tests.test_gpu_ffn import SLOPE, U32, _block, _block_weights, act64, half_step, product
+from tests.test_gpu_ffn import SLOPE, U32, _block, _block_weights, act64, check, half_step, no_split, product, product_bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -261,3 +262,42 @@ def test_two_calls_at_once(svq):
             call()
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for _, y, want in jobs)
+
+
+@pytest.mark.parametrize("k,m", [(53248, 1), (65536, 1), (53248, 3), (65536, 4), (65536, 7), (40000, 300)])
+def test_long_rows(svq, k, m):
+    """Rows too long for the forms that stage them whole, through the epilogue
+    and the gated pair, the residual in place."""
+    n = 24
+    mats = [synth.random_matrix(n, k, bd, seed=(142, bd, k)) for bd in (7, 8)]
+    bits = synth.random_activations(m, k, seed=(142, k, m))
+    x, (pg, pu) = to_device_bf16(bits), [svq.pack(a) for a in mats]
+    (g, gb), (u, ub) = [product(a, bits, m > 16) for a in mats]
+    y = torch.randn((m, n), generator=torch.Generator().manual_seed(30)).cuda()
+    r = y.double().cpu().numpy()
+    svq.linear_epilogue(pg, x, act="relu", residual=y, out=y)
+    a = np.maximum(g, 0)
+    check(y, a + r, gb + U32 * (a + np.abs(r)), "epilogue")
+    y = svq.linear_glu(pg, pu, x, act="relu", out_dtype=torch.float32)
+    check(y, a * u, gb * np.abs(u) + ub * a + gb * ub + U32 * np.abs(a * u), "glu")
+
+
+@pytest.mark.parametrize("m", [2, 13, 20, 200, 300])
+@pytest.mark.parametrize("n", [40, 500])
+def test_no_split_in_k_ranges(svq, n, m):
+    """Tables without two fp16 halves and a K of nine units: beyond 16 rows
+    the bf16 form's K ranges, joined by the launch that applies the epilogue."""
+    k = 4608
+    (mat, pm), (mat2, pm2) = no_split(svq, n, k, 11), no_split(svq, n, k, 12)
+    bits = synth.random_activations(m, k, seed=(143, n, m))
+    x = to_device_bf16(bits)
+    (g, gb), (u, ub) = product_bf16(mat, bits, m), product_bf16(mat2, bits, m)
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(31)).cuda()
+    y = torch.randn((m, n + 3), generator=torch.Generator().manual_seed(32)).cuda()[:, 1:1 + n]
+    r, v = y.double().cpu().numpy(), g + bias.double().cpu().numpy()
+    svq.linear_epilogue(pm, x, bias=bias, act="relu", residual=y, out=y)
+    a = np.maximum(v, 0)
+    check(y, a + r, gb + U32 * np.abs(v) + U32 * (a + np.abs(r)), "epilogue")
+    a = np.maximum(g, 0)
+    y = svq.linear_glu(pm, pm2, x, act="relu", out_dtype=torch.float32)
+    check(y, a * u, gb * np.abs(u) + ub * a + gb * ub + U32 * np.abs(a * u), "glu")

@@ -151,3 +151,29 @@ def test_one_infinite_inner_value(svq, m):
     assert (W[:, j] != 0).all()
     want = np.sign(h[j]) * np.sign(W[:, j]) * math.inf
     assert np.array_equal(out_to_f64(y), np.repeat(want[None], m, axis=0))
+
+
+@pytest.mark.parametrize("m", [2, 4, 6, 16, 30, 150, 300])
+def test_other_rows_are_the_same(svq, m):
+    """Rows without an infinity or NaN, bit for bit as beside rows without
+    one, in every call and output type."""
+    n, k, e, f, topk = 72, 1032, 3, 40, 2
+    clean = synth.random_activations(m, k, seed=(125, m))
+    dirty = clean.copy()
+    for i, t in enumerate(range(0, m, 3)):
+        dirty[t, (i * 37) % k] = (INF, NINF, NAN)[i % 3]
+    keep = torch.tensor([t for t in range(m) if t % 3], device="cuda")
+    pg, pu = [svq.pack(synth.random_matrix(n, k, bd, seed=(125, bd))) for bd in (7, 8)]
+    sets = [[svq.pack(synth.random_matrix(a, b, 7, seed=(126, s, i))) for i in range(e)]
+            for s, (a, b) in enumerate(((f, k), (f, k), (k, f)))]
+    g = torch.Generator().manual_seed(33)
+    ids = torch.stack([torch.randperm(e, generator=g)[:topk] for _ in range(m)]).to(torch.int32).cuda()
+    wt = torch.rand((m, topk), generator=g).cuda()
+    router = torch.randn((e, k), generator=g).cuda()
+    for out in (torch.float32, torch.bfloat16):
+        for run in (lambda x: svq.linear_epilogue(pg, x, act="silu", out_dtype=out),
+                    lambda x: svq.linear_glu(pg, pu, x, out_dtype=out),
+                    lambda x: svq.moe_ffn(*sets, x, ids, wt, residual=x, out_dtype=out),
+                    lambda x: svq.moe_route(x, router, topk)[1]):
+            a, b = run(to_device_bf16(clean)), run(to_device_bf16(dirty))
+            assert torch.isfinite(a).all() and torch.equal(a[keep], b[keep])
