@@ -32,6 +32,9 @@ SOURCES = [
     ("csrc/svq_scratch.hip", []),
     ("csrc/svq_ffn.cpp", []),
     ("csrc/svq_ffn.hip", []),
+    ("csrc/svq_attn.cpp", []),
+    ("csrc/svq_attn.hip", []),
+    ("csrc/svq_kv.hip", []),
 ]
 # kept for callers that list the flags of the exact-path kernels
 HIPCC_FLAGS = COMMON_FLAGS + ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]

@@ -38,6 +38,8 @@ EXPORTED = ("svq_pack", "svq_linear", "svq_linear_batched", "svq_linear_noalloc"
             "svq_status_string")
 # the feed-forward calls (include/svq_ffn.h)
 EXPORTED_FFN = ("svq_linear_epilogue", "svq_linear_glu", "svq_moe_route", "svq_moe_ffn")
+# the attention calls (include/svq_attn.h)
+EXPORTED_ATTN = ("svq_attn_prompt", "svq_kv_bytes", "svq_kv_write", "svq_kv_read", "svq_attn_cache")
 ACTIVATIONS = ("none", "relu", "silu", "gelu", "gelu_tanh")  # svq_act by name
 ROUTE_SCORES = ("softmax", "sigmoid")                        # svq_route_score by name
 SVQ_SCRATCH_BYTES = 64 << 20
@@ -78,6 +80,13 @@ class Epilogue(ctypes.Structure):
     _fields_ = [
         ("bias", ctypes.c_void_p), ("bias_dt", ctypes.c_int), ("act", ctypes.c_int),
         ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("residual_dt", ctypes.c_int),
+    ]
+
+
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [
+        ("dev", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("group", ctypes.c_int32),
     ]
 
 
@@ -155,6 +164,18 @@ def _load() -> ctypes.CDLL:
     lib.svq_moe_ffn.restype = en
     lib.svq_moe_ffn.argtypes = [hp, hp, hp, i32, ptr, i64, ptr, ptr, i64, i32, en, ptr, i64, en, ptr, i64, en,
                                 ptr, size_p, ptr]
+    cp, f32 = ctypes.POINTER(KvCacheDesc), ctypes.c_float
+    lib.svq_attn_prompt.restype = en
+    lib.svq_attn_prompt.argtypes = [ptr, i64, ptr, i64, ptr, i64, i32, i32, i32, ptr, ptr, i64, i64, i64, i32, i32, f32,
+                                    ptr, i64, ptr, size_p, ptr]
+    lib.svq_kv_bytes.restype = en
+    lib.svq_kv_bytes.argtypes = [cp, size_p]
+    lib.svq_kv_write.restype = en
+    lib.svq_kv_write.argtypes = [cp, ptr, i64, ptr, i64, i64, ptr, ptr]
+    lib.svq_kv_read.restype = en
+    lib.svq_kv_read.argtypes = [cp, ptr, i64, ptr, i64, ptr, i64, en, ptr]
+    lib.svq_attn_cache.restype = en
+    lib.svq_attn_cache.argtypes = [cp, ptr, i64, i32, ptr, i64, ptr, i64, i32, i64, i32, f32, ptr, i64, ptr, size_p, ptr]
     return lib
 
 
@@ -970,3 +991,222 @@ def moe_ffn(gates: Sequence[PackedMatrix], ups: Sequence[PackedMatrix], downs: S
         MoeFfnCall(gates, ups, downs, x, expert_ids, weights, y, act=act, residual=residual)()
         return y
     return _run_on(stream, x.device, make)
+
+
+# ---------------------------------------------------------------------------
+# The attention calls (include/svq_attn.h), with the same kinds of prepared
+# calls.  Queries, keys, values and outputs are 2-D: a row per token, heads
+# side by side, as the linears write them (q, k and v may be columns of one
+# wider buffer).
+# ---------------------------------------------------------------------------
+
+class KvCache:
+    """A paged cache of keys and values held in 4 bits: ``pages`` pages of
+    ``page_size`` token slots, slot s being place s % page_size of page
+    s // page_size.  ``group`` channels share a scale and a minimum.  ``buf``
+    (uint8, optional) is the memory to use; nothing has to be in it."""
+
+    def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int, group: int = 64, device="cuda",
+                 buf=None):
+        import torch
+        self.desc = KvCacheDesc(dev=None, pages=pages, page_size=page_size, kv_heads=kv_heads, head_dim=head_dim,
+                                group=group)
+        nbytes = ctypes.c_size_t(0)
+        _check(LIB.svq_kv_bytes(ctypes.byref(self.desc), ctypes.byref(nbytes)), "svq_kv_bytes")
+        self.nbytes = nbytes.value
+        if buf is None:
+            buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
+        elif buf.dtype != torch.uint8 or not buf.is_contiguous() or buf.numel() < self.nbytes:
+            raise ValueError(f"buf must be a contiguous uint8 tensor of at least {self.nbytes} bytes")
+        self.buf = buf
+        self.desc.dev = buf.data_ptr()
+
+    @property
+    def slots(self) -> int:
+        return int(self.desc.pages) * int(self.desc.page_size)
+
+    @property
+    def width(self) -> int:
+        """Columns of a row of keys or values."""
+        return int(self.desc.kv_heads) * int(self.desc.head_dim)
+
+
+def _ids_arg(t, what: str, n: int, device) -> None:
+    """Checks a contiguous int32 vector on the operands' device."""
+    import torch
+    _vector_arg(t, what, n, device, torch.int32)
+
+
+class _BareCall(_Call):
+    """A prepared call without a workspace."""
+
+    def _prepare(self, name: str, args, device, stream) -> None:
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is one of {stream.device}, not of {device}")
+        self.name, self.args, self.device = name, tuple(args), device
+        self.fn = getattr(LIB, name)
+        self.stream = None if stream is None else int(stream.cuda_stream)
+
+    def __call__(self) -> None:
+        import torch
+        index = self.device.index
+        stream = self.stream if self.stream is not None else torch._C._cuda_getCurrentRawStream(index)
+        if index == torch.cuda.current_device():
+            st = self.fn(*self.args, stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = self.fn(*self.args, stream)
+        if st != SVQ_OK:
+            _check(st, self.name)
+
+
+class KvWriteCall(_BareCall):
+    """Quantises keys and values (bf16 [tokens, kv_heads * head_dim]) into the
+    cache's slots (int32 [tokens]; negative: the token is skipped)
+    (svq_kv_write)."""
+
+    def __init__(self, cache: KvCache, k, v, slots, stream=None):
+        import torch
+        n, dev = slots.shape[0], cache.buf.device
+        ldk = _matrix_arg(k, "k", n, cache.width, dev, (torch.bfloat16,))
+        ldv = _matrix_arg(v, "v", n, cache.width, dev, (torch.bfloat16,))
+        _ids_arg(slots, "slots", n, dev)
+        self.keep = (cache, k, v, slots)
+        self._prepare("svq_kv_write", (ctypes.byref(cache.desc), k.data_ptr(), ldk, v.data_ptr(), ldv, n,
+                                       slots.data_ptr()), dev, stream)
+
+
+class KvReadCall(_BareCall):
+    """The values that the cache's slots (int32 [tokens]; negative: zeros)
+    stand for, into k and v (bf16 or fp32, of one type) (svq_kv_read)."""
+
+    def __init__(self, cache: KvCache, slots, k, v, stream=None):
+        import torch
+        n, dev = slots.shape[0], cache.buf.device
+        kinds = (torch.bfloat16, torch.float32)
+        ldk = _matrix_arg(k, "k", n, cache.width, dev, kinds)
+        ldv = _matrix_arg(v, "v", n, cache.width, dev, kinds)
+        if k.dtype != v.dtype:
+            raise ValueError("k and v must be of one type")
+        if _overlaps(k[:, :cache.width], v[:, :cache.width]):
+            raise ValueError("k overlaps v")
+        _ids_arg(slots, "slots", n, dev)
+        self.keep = (cache, slots, k, v)
+        self._prepare("svq_kv_read", (ctypes.byref(cache.desc), slots.data_ptr(), n, k.data_ptr(), ldk, v.data_ptr(),
+                                      ldv, _dt(k, "k")), dev, stream)
+
+
+class AttnPromptCall(_Call):
+    """Attention of whole sequences packed one behind another
+    (svq_attn_prompt): sequence i has the rows starts[i] .. starts[i + 1] - 1
+    of q and y and, with starts_k, the rows starts_k[i] .. of k and v.
+
+    q: bf16 [tokens, q_heads * head_dim]; k, v: bf16 [tokens_k, kv_heads *
+    head_dim]; y: bf16, as q; starts, starts_k: int32 [sequences + 1]; scale:
+    1 / sqrt(head_dim) unless given."""
+
+    def __init__(self, q, k, v, y, starts, head_dim: int, starts_k=None, causal: bool = True, window: int = 0,
+                 scale: Optional[float] = None, workspace=None, stream=None):
+        import torch
+        bf, dev = (torch.bfloat16,), q.device
+        for x, what in ((q, "q"), (k, "k"), (v, "v")):
+            if x.dim() != 2 or head_dim < 1 or x.shape[1] < head_dim or x.shape[1] % head_dim:
+                raise ValueError(f"{what} must be 2-D, its rows whole heads of {head_dim} channels")
+        if k.shape[1] != v.shape[1]:
+            raise ValueError("k and v must have one number of heads")
+        (n, cols), (nk, cols_k) = q.shape, k.shape
+        ldq, ldk = _matrix_arg(q, "q", n, cols, dev, bf), _matrix_arg(k, "k", nk, cols_k, dev, bf)
+        ldv, ldy = _matrix_arg(v, "v", nk, cols_k, dev, bf), _matrix_arg(y, "y", n, cols, dev, bf)
+        for x, what in ((q, "q"), (k, "k"), (v, "v")):
+            if _overlaps(x, y[:, :cols]):
+                raise ValueError(f"y overlaps {what}")
+        _ids_arg(starts, "starts", starts.shape[0], dev)
+        if starts_k is not None:
+            _ids_arg(starts_k, "starts_k", starts.shape[0], dev)
+        elif nk != n:
+            raise ValueError("without starts_k there are as many keys as queries")
+        self.keep = (q, k, v, y, starts, starts_k)
+        self._prepare("svq_attn_prompt",
+                      (q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, cols // head_dim, cols_k // head_dim,
+                       head_dim, starts.data_ptr(), None if starts_k is None else starts_k.data_ptr(),
+                       starts.shape[0] - 1, n, nk, int(bool(causal)), window,
+                       head_dim ** -0.5 if scale is None else float(scale), y.data_ptr(), ldy), dev, workspace, stream)
+
+
+class AttnCacheCall(_Call):
+    """Attention of the newest q_len tokens of each sequence over a cache that
+    holds them too (svq_attn_cache).
+
+    q: bf16 [batch * q_len, q_heads * head_dim]; y: bf16, as q; table: int32
+    [batch, pages a sequence], the pages of each sequence in order; lens:
+    int32 [batch], tokens of each sequence, at most max_len (which is all that
+    the table can hold unless given; the launch is planned for it)."""
+
+    def __init__(self, cache: KvCache, q, y, table, lens, q_len: int = 1, max_len: Optional[int] = None,
+                 window: int = 0, scale: Optional[float] = None, workspace=None, stream=None):
+        import torch
+        bf, dev, dim = (torch.bfloat16,), q.device, int(cache.desc.head_dim)
+        if cache.buf.device != dev:
+            raise ValueError(f"the cache is on {cache.buf.device}, not on {dev}")
+        if q.dim() != 2 or q.shape[1] < dim or q.shape[1] % dim:
+            raise ValueError(f"q must be 2-D, its rows whole heads of {dim} channels")
+        batch = lens.shape[0]
+        n, cols = q.shape
+        if n != batch * q_len:
+            raise ValueError("q must have q_len rows for each of lens")
+        ldq, ldy = _matrix_arg(q, "q", n, cols, dev, bf), _matrix_arg(y, "y", n, cols, dev, bf)
+        if _overlaps(q, y[:, :cols]):
+            raise ValueError("y overlaps q")
+        _ids_arg(lens, "lens", batch, dev)
+        ldt = _matrix_arg(table, "table", batch, table.shape[1], dev, (torch.int32,))
+        if max_len is None:
+            max_len = table.shape[1] * int(cache.desc.page_size)
+        if max_len > table.shape[1] * int(cache.desc.page_size):
+            raise ValueError("max_len is more than the table can hold")
+        self.keep = (cache, q, y, table, lens)
+        self._prepare("svq_attn_cache",
+                      (ctypes.byref(cache.desc), q.data_ptr(), ldq, cols // dim, table.data_ptr(), ldt,
+                       lens.data_ptr(), batch, q_len, max_len, window, dim ** -0.5 if scale is None else float(scale),
+                       y.data_ptr(), ldy), dev, workspace, stream)
+
+
+def kv_write(cache: KvCache, k, v, slots, stream=None) -> None:
+    """Quantises tokens into a cache; see :class:`KvWriteCall`."""
+    _run_on(stream, cache.buf.device, lambda: KvWriteCall(cache, k, v, slots)())
+
+
+def kv_read(cache: KvCache, slots, out_dtype=None, stream=None):
+    """(k, v) that a cache holds for slots; see :class:`KvReadCall`."""
+    import torch
+
+    def make():
+        k, v = (torch.empty((slots.shape[0], cache.width), dtype=out_dtype or torch.bfloat16, device=cache.buf.device)
+                for _ in range(2))
+        KvReadCall(cache, slots, k, v)()
+        return k, v
+    return _run_on(stream, cache.buf.device, make)
+
+
+def attn_prompt(q, k, v, starts, head_dim: int, starts_k=None, causal: bool = True, window: int = 0,
+                scale: Optional[float] = None, out=None, stream=None):
+    """Attention of whole sequences; see :class:`AttnPromptCall`.  Without
+    ``out``, rows that no sequence has are zero."""
+    import torch
+
+    def make():
+        y = out if out is not None else torch.zeros((q.shape[0], q.shape[1]), dtype=torch.bfloat16, device=q.device)
+        AttnPromptCall(q, k, v, y, starts, head_dim, starts_k=starts_k, causal=causal, window=window, scale=scale)()
+        return y
+    return _run_on(stream, q.device, make)
+
+
+def attn_cache(cache: KvCache, q, table, lens, q_len: int = 1, max_len: Optional[int] = None, window: int = 0,
+               scale: Optional[float] = None, out=None, stream=None):
+    """Attention of new tokens over a cache; see :class:`AttnCacheCall`."""
+    import torch
+
+    def make():
+        y = out if out is not None else torch.empty((q.shape[0], q.shape[1]), dtype=torch.bfloat16, device=q.device)
+        AttnCacheCall(cache, q, y, table, lens, q_len=q_len, max_len=max_len, window=window, scale=scale)()
+        return y
+    return _run_on(stream, q.device, make)
