@@ -1,70 +1,374 @@
 // Attention over whole prompts (include/svq_attn.h).
+//
+// One pass over the keys with a running maximum and sum.  A block takes BM
+// rows of one key head, row r being query head r % G of the group's G and
+// token r / G of its sequence, so the heads that share keys share their reads
+// and a block's rows span few positions under a causal mask.  A wave owns 32
+// rows and forms everything transposed:
+//
+//   S^T = K Q^T     32 keys x 32 rows (v_mfma_f32_32x32x16_bf16, A = keys)
+//   O^T += V^T P^T  32 channels x 32 rows per step of 16 keys
+//
+// so a lane holds scores of one row only: the maximum, the exponentials and
+// their sum stay in the lane, but for one exchange between the wave's halves,
+// and P^T leaves the scores' registers in the layout that the second product
+// reads, when the keys of a step are taken in the order of those registers
+// (keys 16t + 4h + 0..3 and 16t + 8 + 4h + 0..3 in half h).  V is read
+// transposed out of LDS (ds_read_b64_tr_b16: four keys of one channel a lane).
 #include "svq_attn.h"
 #include "svq_device.h"
+
+#include <type_traits>
 
 namespace svq {
 namespace {
 
-// A wave a (row, query head): 64 keys at a time, one a lane, for the scores
-// and the running maximum and sum; then every lane D/64 channels over them.
+constexpr int KT = 64;  // keys of a tile
+
+typedef __attribute__((address_space(3))) uint8_t lds_t;
+typedef short s4v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s4v lds_s4v;
+typedef __attribute__((address_space(3))) u4 lds_u4;
+
+// 16 bytes a lane from base + off to LDS bytes dst + 16 * lane, waited for by
+// vmcnt.  (The builtin makes every LDS read behind it wait for the copy.)  The
+// wait states stand between the scalar values' writers and their use as M0 and
+// as a base: the compiler does not look into the block.
+__device__ __forceinline__ void copy_to_lds(const uint8_t *base, uint32_t off, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(off), "s"(base) : "memory", "m0");
+}
+
+// Rows of a staged tile are D bf16 values, 16-byte chunk c at place
+// c ^ swizzle(key): 16 consecutive keys' equal chunks (a fragment of K) and
+// four consecutive keys' 64-byte pieces (a transposed fragment of V) fill all
+// 64 banks.
 template <int D>
-__global__ __launch_bounds__(256) void attn_prompt_kernel(AttnPromptArgs a) {
+__device__ __forceinline__ int swizzle(int key) {
+  return D == 64 ? ((key >> 1 & 1) << 2) | (key >> 2 & 3) : ((key & 3) << 2) | (key >> 2 & 3);
+}
+
+// v of the lane's place in the lower half and in the upper half.
+__device__ __forceinline__ float2 both_halves(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const uint32_t lower = r[0], upper = r[1];
+  return make_float2(__builtin_bit_cast(float, lower), __builtin_bit_cast(float, upper));
+}
+__device__ __forceinline__ float max_halves(float v) {
+  const float2 r = both_halves(v);
+  return fmaxf(r.x, r.y);
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  const float2 r = both_halves(v);
+  return r.x + r.y;
+}
+
+__device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
+  return (uint32_t)f32_to_bf16_bits(a) | (uint32_t)f32_to_bf16_bits(b) << 16;
+}
+__device__ __forceinline__ f16x mfma_bf16(const u4 &a, const u4 &b, const f16x &c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
+}
+
+// The sequence and tile of block `u` of the row tiles of all sequences in
+// order; false beyond the last.  Every wave looks for itself, 64 sequences at
+// a time.
+struct TileOf {
+  int q_at, n, k_at, keys, tile;
+};
+__device__ __forceinline__ bool find_tile(const AttnPromptArgs &a, int rows_shift, int G, int u, TileOf &o) {
   const int lane = threadIdx.x & 63;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= a.tokens) return;
-  const int h = blockIdx.y, kvh = h / (a.heads / a.kv_heads);
-  int n = -1, t = 0, k_at = 0, keys = 0;
-  for (int s = 0; s < a.sequences; ++s) {
-    const int b = min(max(a.starts[s], 0), a.tokens), e = min(max(a.starts[s + 1], b), a.tokens);
-    if (row >= b && row < e) {
-      n = e - b;
-      t = row - b;
-      k_at = min(max(a.starts_k[s], 0), a.tokens_k);
-      keys = min(max(a.starts_k[s + 1], k_at), a.tokens_k) - k_at;
-      break;
+  int before = 0;
+  for (int s0 = 0; s0 < a.sequences; s0 += 64) {
+    const int s = s0 + lane;
+    int b = 0, e = 0;
+    if (s < a.sequences) {
+      b = min(max(a.starts[s], 0), a.tokens);
+      e = min(max(a.starts[s + 1], b), a.tokens);
+    }
+    const int tiles = ((e - b) * G + (1 << rows_shift) - 1) >> rows_shift;
+    int sum = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int other = __shfl_up(sum, d);
+      if (lane >= d) sum += other;
+    }
+    const uint64_t past = __ballot(before + sum > u);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      o.q_at = __builtin_amdgcn_readlane(b, at);
+      o.n = __builtin_amdgcn_readlane(e, at) - o.q_at;
+      o.tile = u - before - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(tiles, at));
+      o.k_at = min(max(a.starts_k[s0 + at], 0), a.tokens_k);
+      o.keys = min(max(a.starts_k[s0 + at + 1], o.k_at), a.tokens_k) - o.k_at;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return false;
+}
+
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t x) {
+  const uint32_t lo = x & 0xFFFFu, hi = x & 0xFFFF0000u;
+  return ((lo & 0x7F80u) == 0x7F80u ? 0u : lo) | ((hi & 0x7F800000u) == 0x7F800000u ? 0u : hi);
+}
+
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(AttnPromptArgs a, int tiles) {
+  constexpr int BM = 32 * NW, ROWS_SHIFT = NW == 8 ? 8 : 7;
+  constexpr int ROW = 2 * D, CH = D / 8, SIDE = KT * ROW;  // bytes of a row, its chunks, bytes of a tile
+  constexpr int NB = D / 32, NS = D / 16;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // K, V of two tiles
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, h = lane >> 5;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kvh = blockIdx.x % a.kv_heads, G = a.heads / a.kv_heads;
+  // the last tiles first: under a causal mask they have the most keys
+  TileOf T;
+  if (!find_tile(a, ROWS_SHIFT, G, tiles - 1 - (int)(blockIdx.x / a.kv_heads), T)) return;
+  const int rows = T.n * G, r0 = T.tile * BM;
+
+  // what a row sees: keys [lo, hi)
+  auto hi_of = [&](int r) {
+    const int p = T.keys - T.n + r / G;
+    return a.causal ? min(max(p + 1, 0), T.keys) : T.keys;
+  };
+  auto lo_of = [&](int r) {
+    const int p = T.keys - T.n + r / G;
+    return a.window > 0 ? max(0, p - a.window + 1) : 0;
+  };
+  const int r_end = min(r0 + BM, rows) - 1;
+  const int t0 = lo_of(r0) / KT, t1 = (hi_of(r_end) + KT - 1) / KT;
+  const int wr = r0 + 32 * wv;
+  const bool mine = wr < rows;  // the wave has rows
+  const int w_first = min(wr, rows - 1), w_last = min(wr + 31, rows - 1);
+  const int w_lo0 = lo_of(w_first), w_lo1 = lo_of(w_last), w_hi0 = hi_of(w_first), w_hi1 = hi_of(w_last);
+  const int r = min(wr + col, rows - 1);
+  const int lo = lo_of(r), hi = hi_of(r);
+  const int64_t row_off = (int64_t)(T.q_at + r / G);
+  const int head = kvh * G + r % G;
+
+  u4 qf[NS];
+  {
+    const uint16_t *q = a.q + row_off * a.ldq + head * D + 8 * h;
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      qf[s] = *(const u4 *)(q + 16 * s);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) qf[s][w] ^= flip;
     }
   }
-  if (n < 0) return;
-  const int pos = keys - n + t;
-  const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0, hi = a.causal ? max(0, pos + 1) : keys;
-  const uint16_t *q = a.q + row * a.ldq + h * D;
-  float m = -__builtin_inff(), l = 0.f, acc[D / 64] = {};
-  for (int k0 = lo; k0 < hi; k0 += 64) {
-    const int j = k0 + lane;
-    const bool in = j < hi;
-    const uint16_t *k = a.k + (int64_t)(k_at + (in ? j : lo)) * a.ldk + kvh * D;
-    float s = 0.f;
-    for (int d = 0; d < D; ++d) s += bf16_bits_to_f32(q[d]) * bf16_bits_to_f32(k[d]);
-    s = in ? s * a.scale : -__builtin_inff();
-    float top = s;
-    for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    const float mn = fmaxf(m, top), ref = mn == -__builtin_inff() ? 0.f : mn;
-    const float p = in ? expf(s - ref) : 0.f, alpha = m == -__builtin_inff() ? 0.f : expf(m - ref);
-    float sum = p;
-    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
-    l = l * alpha + sum;
-    m = mn;
-    for (int i = 0; i < D / 64; ++i) acc[i] *= alpha;
-    for (int e = 0; e < 64 && k0 + e < hi; ++e) {
-      const float pe = __shfl(p, e);
-      const uint16_t *v = a.v + (int64_t)(k_at + k0 + e) * a.ldv + kvh * D;
-      for (int i = 0; i < D / 64; ++i) acc[i] += pe * bf16_bits_to_f32(v[lane + 64 * i]);
-    }
+  // exponents are base 2; a scale of zero stays a number that keeps hidden
+  // scores at -infinity
+  const float sc = fmaxf(fabsf(a.scale) * 1.44269504088896f, 1e-38f);
+
+  // staging: pieces of 1 KB (1024 / ROW keys), piece i * NW + wv by wave wv; a
+  // lane's place in a piece is the same for every i (i & 1 with 256 channels
+  // and four waves)
+  const uint8_t *kg = (const uint8_t *)(a.k + (int64_t)T.k_at * a.ldk + kvh * D);
+  const uint8_t *vg = (const uint8_t *)(a.v + (int64_t)T.k_at * a.ldv + kvh * D);
+  constexpr int PER = SIDE / 1024 / NW, KEYS = 1024 / ROW, KINDS = D == 256 && NW == 4 ? 2 : 1;
+  const uint32_t ldk = (uint32_t)a.ldk * 2, ldv = (uint32_t)a.ldv * 2;
+  uint32_t chunk[KINDS];
+#pragma unroll
+  for (int i = 0; i < KINDS; ++i) {
+    const int key = (i * NW + wv) * KEYS + lane / CH;
+    chunk[i] = ((lane % CH) ^ swizzle<D>(key)) * 16;
   }
-  for (int i = 0; i < D / 64; ++i)
-    a.y[row * a.ldy + h * D + lane + 64 * i] = f32_to_bf16_bits(l == 0.f ? 0.f : acc[i] / l);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_t *)smem;
+  auto stage = [&](int t, int buf) {
+    const uint8_t *kt = kg + (int64_t)t * KT * ldk, *vt = vg + (int64_t)t * KT * ldv;
+    const int last = T.keys - 1 - t * KT;  // keys past the last are copies of it
+    const uint32_t dst = lds0 + buf * 2 * SIDE + wv * 1024;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint32_t key = min((i * NW + wv) * KEYS + lane / CH, last);
+      copy_to_lds(kt, key * ldk + chunk[i % KINDS], dst + i * NW * 1024);
+      copy_to_lds(vt, key * ldv + chunk[i % KINDS], dst + i * NW * 1024 + SIDE);
+    }
+  };
+
+  // fragment addresses, a chunk's place an exclusive or: K chunk 2s + h of key
+  // col (32 kb more: 32 rows on); V^T keys 8jj + 4h + r4 (16t more: 16 rows
+  // on), channels 32db + 16g + 4c
+  const uint32_t ka = col * ROW + ((h ^ swizzle<D>(col)) << 4);
+  uint32_t va[2];
+#pragma unroll
+  for (int jj = 0; jj < 2; ++jj) {
+    const int g = lane >> 4 & 1, c = lane & 3, key = 8 * jj + 4 * h + (lane >> 2 & 3);
+    va[jj] = SIDE + key * ROW + (((2 * g + (c >> 1)) ^ swizzle<D>(key)) << 4) + 8 * (c & 1);
+  }
+
+  f16x O[NB];
+#pragma unroll
+  for (int db = 0; db < NB; ++db) O[db] = (f16x){};
+  float m = -__FLT_MAX__, mref = 0.f, l = 0.f;
+  bool dirty = false, far_any = false;
+
+  auto work = [&](uint32_t base, int k0, auto partial) {
+    f16x S[2] = {(f16x){}, (f16x){}};
+    u4 kf[2][2];
+    auto load_k = [&](int s) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) kf[s & 1][kb] = *(const lds_u4 *)(lds_t *)(uintptr_t)(((base + ka) ^ (s << 5)) + kb * 32 * ROW);
+    };
+    load_k(0);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      if (s + 1 < NS) load_k(s + 1);
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) S[kb] = mfma_bf16(kf[s & 1][kb], qf[s], S[kb]);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // DS reads
+      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // MFMA
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (partial) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = k0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3);
+          S[kb][i] = key >= lo && key < hi ? S[kb][i] : -__builtin_inff();
+        }
+    }
+    float top = fmaxf(S[0][0], S[1][0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, fmaxf(S[0][i], S[1][i]));
+    top = max_halves(top);
+    // a new reference only once the maximum has grown by 2^8: weights up to
+    // 256 are as exact as weights up to 1
+    if (__any(top * sc > (m == -__FLT_MAX__ ? -__builtin_inff() : mref + 8.f))) {
+      const float old = mref;
+      const bool first = m == -__FLT_MAX__;
+      m = fmaxf(m, top);
+      mref = m == -__FLT_MAX__ ? 0.f : m * sc;
+      far_any = __any(fabsf(mref) > 16777216.f);
+      const float alpha = first ? 0.f : __builtin_amdgcn_exp2f(old - mref);
+      l *= alpha;
+#pragma unroll
+      for (int db = 0; db < NB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) O[db][i] *= alpha;
+    }
+    u4 pf[4];
+    // A reference beyond 2^24 is rounded by more than one: there the scores'
+    // differences are formed before the scale
+    auto weights = [&](auto far) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          float p[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            p[e] = __builtin_amdgcn_exp2f(far ? (S[kb][i + e] - m) * sc : fmaf(S[kb][i + e], sc, -mref));
+            l += p[e];
+          }
+          pf[2 * kb + (i >> 3)][(i & 7) >> 1] = pk_bf16(p[0], p[1]);
+        }
+    };
+    if (__builtin_expect(far_any, 0)) weights(std::integral_constant<bool, true>());
+    else weights(std::integral_constant<bool, false>());
+    u4 vf[2][NB];
+    auto load_v = [&](int t) {
+#pragma unroll
+      for (int db = 0; db < NB; ++db) {
+        const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(lds_t *)(uintptr_t)(((base + va[0]) ^ (db << 6)) + t * 16 * ROW));
+        const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(lds_t *)(uintptr_t)(((base + va[1]) ^ (db << 6)) + t * 16 * ROW));
+        const u2 xx = __builtin_bit_cast(u2, x), yy = __builtin_bit_cast(u2, y);
+        vf[t & 1][db] = (u4){xx[0], xx[1], yy[0], yy[1]};
+      }
+    };
+    __builtin_amdgcn_sched_barrier(0);
+    load_v(0);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (t + 1 < 4) load_v(t + 1);
+      u4 (&vt)[NB] = vf[t & 1];
+      if constexpr (partial) {
+        // P^T is zero for a hidden key, but zero times infinity is not: the
+        // product takes values that are not finite as zero, and the rows that
+        // do see them get them at the end
+        uint32_t top_mag = 0;
+#pragma unroll
+        for (int db = 0; db < NB; ++db)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) top_mag = pk_max_mag(top_mag, vt[db][w]);
+        if (__builtin_expect(__any((top_mag & 0xFFFF) >= 0x7F80 || top_mag >= 0x7F800000u), 0)) {
+          dirty = true;
+#pragma unroll
+          for (int db = 0; db < NB; ++db)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) vt[db][w] = finite_or_zero(vt[db][w]);
+        }
+      }
+#pragma unroll
+      for (int db = 0; db < NB; ++db) O[db] = mfma_bf16(vt[db], pf[t], O[db]);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * NB, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);
+    }
+  };
+
+  if (t0 < t1) stage(t0, 0);
+  for (int t = t0; t < t1; ++t) {
+    const int buf = (t - t0) & 1;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();  // the tile is there, and nobody reads the other buffer
+    if (t + 1 < t1) stage(t + 1, buf ^ 1);
+    const int k0 = t * KT;
+    if (!mine || k0 >= w_hi1 || k0 + KT <= w_lo0) continue;
+    const uint32_t base = lds0 + buf * 2 * SIDE;
+    if (k0 >= w_lo1 && k0 + KT <= w_hi0) work(base, k0, std::integral_constant<bool, false>());
+    else work(base, k0, std::integral_constant<bool, true>());
+  }
+  if (!mine || wr + col >= rows) return;
+  if (dirty)
+    for (int t = t0; t < t1; ++t) {
+      const int k0 = t * KT;
+      if (k0 >= w_hi1 || k0 + KT <= w_lo0 || (k0 >= w_lo1 && k0 + KT <= w_hi0)) continue;
+      for (int key = max(k0, lo); key < min(k0 + KT, hi); ++key) {
+        const uint16_t *v = (const uint16_t *)(vg + (int64_t)key * ldv) + 4 * h;
+#pragma unroll
+        for (int db = 0; db < NB; ++db)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t x = v[32 * db + 8 * (i >> 2) + (i & 3)];
+            O[db][i] += (x & 0x7F80u) == 0x7F80u ? bf16_bits_to_f32(x) : 0.f;
+          }
+      }
+    }
+  // the lane's half of the row's sum is added to its partner's, which is in
+  // the same state
+  l = sum_halves(l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t *y = a.y + row_off * a.ldy + head * D;
+#pragma unroll
+  for (int db = 0; db < NB; ++db)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *(u2 *)(y + 32 * db + 2 * i + 4 * h) = (u2){pk_bf16(O[db][i] * inv, O[db][i + 1] * inv),
+                                                 pk_bf16(O[db][i + 2] * inv, O[db][i + 3] * inv)};
+}
+
+template <int D, int NW>
+hipError_t launch(const AttnPromptArgs &a, hipStream_t s) {
+  constexpr int BM = 32 * NW;
+  constexpr size_t lds = (size_t)4 * KT * 2 * D;
+  const int64_t tiles = (int64_t)a.tokens * (a.heads / a.kv_heads) / BM + a.sequences;
+  const hipError_t e = allow_smem(attn_prompt_kernel<D, NW>, lds);
+  if (e != hipSuccess) return e;
+  attn_prompt_kernel<D, NW><<<dim3((unsigned)(tiles * a.kv_heads)), 64 * NW, lds, s>>>(a, (int)tiles);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_attn_prompt(const AttnPromptArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.tokens + 3) / 4), a.heads);
   switch (a.dim) {
-    case 64: attn_prompt_kernel<64><<<grid, 256, 0, s>>>(a); break;
-    case 128: attn_prompt_kernel<128><<<grid, 256, 0, s>>>(a); break;
-    default: attn_prompt_kernel<256><<<grid, 256, 0, s>>>(a);
+    case 64: return launch<64, 4>(a, s);
+    case 128: return launch<128, 4>(a, s);
+    default: return launch<256, 4>(a, s);
   }
-  return hipGetLastError();
 }
 
 }  // namespace svq
