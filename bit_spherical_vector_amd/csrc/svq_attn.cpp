@@ -176,7 +176,18 @@ svq_status svq_attn_cache(const svq_kv_cache *cache, const void *q, int64_t ldq,
     return SVQ_ERR_INVALID_ARG;
   if (ldq < cols || ldy < cols || window < 0 || !std::isfinite(scale)) return SVQ_ERR_INVALID_ARG;
   if (!on_16(q, ldq, 2) || !on_16(y, ldy, 2)) return SVQ_ERR_UNSUPPORTED;
-  const size_t need = 256;  // unused
+  const int R = q_heads / a.c.heads * q_len;
+  a.row_tiles = (R + CACHE_ROWS - 1) / CACHE_ROWS;
+  // ranges of keys: enough blocks for three a compute unit, each with two
+  // steps or more
+  const int64_t blocks = batch * a.c.heads * a.row_tiles;
+  if (blocks > (1 << 23)) return SVQ_ERR_UNSUPPORTED;
+  const int64_t keys = window > 0 && window + q_len < max_len ? window + q_len : max_len;
+  const int64_t most = (keys + 2 * CACHE_BLOCK_KEYS - 1) / (2 * CACHE_BLOCK_KEYS);
+  int64_t splits = (3 * compute_units() + blocks - 1) / blocks;
+  a.splits = (int32_t)(splits < most ? splits : most);
+  const size_t part = a.splits > 1 ? align256((size_t)batch * q_heads * q_len * a.splits * a.c.dim * 4) : 0;
+  const size_t need = a.splits > 1 ? part + align256((size_t)batch * q_heads * q_len * a.splits * 8) : 256;
   if (!workspace) {
     *workspace_bytes = need;
     return SVQ_OK;
@@ -196,6 +207,10 @@ svq_status svq_attn_cache(const svq_kv_cache *cache, const void *q, int64_t ldq,
   a.max_len = (int32_t)max_len;
   a.window = window;
   a.scale = scale;
+  if (a.splits > 1) {
+    a.part = (float *)workspace;
+    a.sums = (float *)((uint8_t *)workspace + part);
+  }
   return of(launch_attn_cache(a, (hipStream_t)stream));
 }
 

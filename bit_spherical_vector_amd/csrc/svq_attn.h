@@ -85,7 +85,10 @@ struct AttnCacheArgs {
   const int32_t *table, *lens;
   int32_t batch, q_len, heads, max_len, window;
   float scale;
+  int32_t row_tiles, splits;  // tiles of 16 rows, ranges of keys
+  float *part, *sums;         // splits > 1: [batch][kv head][row][split] numerators [dim] and (reference, sum)
 };
+constexpr int CACHE_ROWS = 16, CACHE_BLOCK_KEYS = 128;  // rows of a tile, keys of a block's step
 hipError_t launch_attn_cache(const AttnCacheArgs &a, hipStream_t s);
 
 }  // namespace svq

@@ -3,6 +3,8 @@
 #include "svq_attn.h"
 #include "svq_device.h"
 
+#include <type_traits>
+
 namespace svq {
 namespace {
 
@@ -161,61 +163,438 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
   for (int i = 0; i < N; ++i) store_out(SIDE ? a.v : a.k, row + (SIDE ? 16 * i + r : r * N + i), x[i], a.f32);
 }
 
-// A wave a (row, query head): 64 keys at a time, one a lane, for the scores
-// and the running maximum and sum; then every lane D/64 channels over them.
-template <int D>
-__global__ __launch_bounds__(256) void attn_cache_kernel(AttnCacheArgs a) {
+// ---- attention over the cache -------------------------------------------
+//
+// A block takes 16 rows (query token t of q_len, query head g of the G that
+// share a key head: row t * G + g) of one sequence and key head, and one of
+// `splits` ranges of its keys; a wave every fourth chunk of 32 keys in it.
+// Codes enter the matrix cores as they are: a nibble left in place by a mask
+// is a subnormal fp16 number, c * 2^-24 or c * 16 * 2^-24, which
+// v_mfma_f32_16x16x32_f16 multiplies exactly.  So, transposed (a lane holds
+// one row, and four keys of each 16):
+//
+//   A_g[key][row] = sum over the group's channels of c * q     (q in fp16
+//        under a power-of-two scale per row, a sixteenth of it where the
+//        nibble stands for 16 c)
+//   score         = sum over groups of s_g A_g + m_g sum q     (fp32)
+//   O_t[channel][row] += sum over keys of c * (p s_g)          (p s_g in units
+//        of 2^(E - 8) as the sum of two fp16 numbers, 22 bits: the minimum's
+//        term below cancels much of this one, and with 11 bits a value near
+//        zero would carry the rounding of its whole range)
+//   M_g[row]          += sum over keys of p m_g                (fp32)
+//
+// and the row is (2^24 O + M) / sum p.  The weight p is exp2(score - ref), ref
+// = m + E - 8: m a running maximum, raised once a score exceeds it by 6, E an
+// exponent that is raised once a p s_g overflows fp16 (it starts so low that
+// the first chunk raises it to the exponent of that chunk's greatest scale or
+// minimum).
+constexpr int CACHE_WAVES = 4, CHUNK = 32, ROWS = 16;
+
+__device__ __forceinline__ float lo_bf16(uint32_t p) { return bf16_bits_to_f32(p & 0xFFFFu); }
+__device__ __forceinline__ float hi_bf16(uint32_t p) { return __builtin_bit_cast(float, p & 0xFFFF0000u); }
+
+// Over the four lanes that hold a row (lane % 16): maximum, sum.
+__device__ __forceinline__ float2 swap32(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const uint32_t x = r[0], y = r[1];
+  return make_float2(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ __forceinline__ float2 swap16(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const uint32_t x = r[0], y = r[1];
+  return make_float2(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ __forceinline__ float row_max(float v) {
+  const float2 a = swap32(v);
+  const float2 b = swap16(fmaxf(a.x, a.y));
+  return fmaxf(b.x, b.y);
+}
+__device__ __forceinline__ float row_sum(float v) {
+  const float2 a = swap32(v);
+  const float2 b = swap16(a.x + a.y);
+  return b.x + b.y;
+}
+
+// What a lane holds of a chunk: the key words, value runs and parameters of
+// two runs of 16 keys.
+template <int D, int G>
+struct Chunk {
+  uint32_t k[2][D / 32], v[2][D / 32];
+  u4 kp[2][G], vp[2][G];
+};
+
+// Four key words' steps of 8 channels as fp16 pairs (see kv_nibble).
+__device__ __forceinline__ u4 nibbles(uint32_t w) {
+  const uint32_t x = w >> 8;
+  return (u4){w & 0x000F000Fu, w & 0x00F000F0u, x & 0x000F000Fu, x & 0x00F000F0u};
+}
+
+__device__ __forceinline__ f4 mfma_f16(const u4 &a, const u4 &b, const f4 &c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t pk_f16(_Float16 a, _Float16 b) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, a) | (uint32_t)__builtin_bit_cast(uint16_t, b) << 16;
+}
+
+template <int D, int GROUP>
+__global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache_kernel(AttnCacheArgs a) {
+  constexpr int G = D / GROUP, NS = D / 32, NT = D / 16, TPG = GROUP / 16, SPG = GROUP / 32;
   const KvView &c = a.c;
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= (int64_t)a.batch * a.q_len) return;
-  const int h = blockIdx.y, kvh = h / (a.heads / c.heads);
-  const int b = (int)(row / a.q_len), t = (int)(row % a.q_len);
-  const int len = min(max(a.lens[b], 0), a.max_len), pos = len - a.q_len + t;
-  const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0, hi = max(0, pos + 1);
-  const uint16_t *q = a.q + row * a.ldq + h * D;
-  float m = -__builtin_inff(), l = 0.f, acc[D / 64] = {};
-  for (int k0 = lo; k0 < hi; k0 += 64) {
-    const int j = k0 + lane;
-    int32_t page = -1;
-    if (j < hi) page = a.table[b * a.ld_table + (j >> c.page_shift)];
-    const bool in = page >= 0 && page < c.pages;
-    const uint8_t *blk = kv_block(c, in ? page : 0, kvh);
-    const int place = in ? j & ((1 << c.page_shift) - 1) : 0;
-    float s = 0.f;
-    if (in)
-      for (int n = 0; n < D / 8; ++n) {
-        const uint32_t w = *(const uint32_t *)(blk + kv_key_word(c, place, (n & 3) * (D / 32) + (n >> 2)));
-        const uint32_t p = *(const uint32_t *)(blk + kv_param(c, 0, place, 8 * n >> c.group_shift));
-        for (int e = 0; e < 8; ++e)
-          s += bf16_bits_to_f32(q[8 * n + e]) * fmaf((float)((w >> 4 * kv_nibble(e)) & 15), bf16_bits_to_f32(p & 0xFFFFu),
-                                                     __builtin_bit_cast(float, p & 0xFFFF0000u));
-      }
-    s = in ? s * a.scale : -__builtin_inff();
-    float top = s;
-    for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    const float mn = fmaxf(m, top), ref = mn == -__builtin_inff() ? 0.f : mn;
-    const float p = in ? expf(s - ref) : 0.f, alpha = m == -__builtin_inff() ? 0.f : expf(m - ref);
-    float sum = p;
-    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
-    l = l * alpha + sum;
-    m = mn;
-    for (int i = 0; i < D / 64; ++i) acc[i] *= alpha;
-    for (int e = 0; e < 64 && k0 + e < hi; ++e) {
-      const float pe = __shfl(p, e);
-      const int pg = __shfl(in ? page : -1, e), pl = (k0 + e) & ((1 << c.page_shift) - 1);
-      if (pg < 0) continue;
-      const uint8_t *vb = kv_block(c, pg, kvh);
-      for (int i = 0; i < D / 64; ++i) {
-        const int d = lane + 64 * i, tile = d >> 4;
-        const uint32_t pr = *(const uint32_t *)(vb + kv_param(c, 1, pl, d >> c.group_shift));
-        const uint32_t code = (vb[kv_value_run(c, pl, d & 15) + (tile >> 1)] >> 4 * (tile & 1)) & 15;
-        acc[i] += pe * fmaf((float)code, bf16_bits_to_f32(pr & 0xFFFFu), __builtin_bit_cast(float, pr & 0xFFFF0000u));
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, h = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int id = blockIdx.x;
+  const int kvh = id % c.heads;
+  id /= c.heads;
+  const int sp = id % a.splits;
+  id /= a.splits;
+  const int rt = id % a.row_tiles, b = id / a.row_tiles;
+  const int shared = a.heads / c.heads, R = shared * a.q_len;
+  const int len = min(max(a.lens[b], 0), a.max_len);
+  const int r = min(rt * ROWS + col, R - 1);
+
+  // what a row sees: keys [lo, hi)
+  auto hi_of = [&](int row) { return max(len - a.q_len + row / shared + 1, 0); };
+  auto lo_of = [&](int row) { return a.window > 0 ? max(0, len - a.q_len + row / shared + 1 - a.window) : 0; };
+  const int r_first = rt * ROWS, r_last = min(rt * ROWS + ROWS, R) - 1;
+  const int lo_min = lo_of(r_first), lo_max = lo_of(r_last), hi_min = hi_of(r_first), hi_max = hi_of(r_last);
+  const int lo = lo_of(r), hi = hi_of(r);
+  const int c_first = lo_min / CHUNK, chunks = max((hi_max + CHUNK - 1) / CHUNK - c_first, 0);
+  const int per = (chunks + a.splits - 1) / a.splits;
+  const int c0 = c_first + min(sp * per, chunks) + wv, c1 = c_first + min(sp * per + per, chunks);
+
+  // queries: step s takes channels 32s + 8h + j, a sixteenth of them where the
+  // nibble pair is 16 times its code (j = 2, 3, 6, 7)
+  const int token = b * a.q_len + r / shared, head = kvh * shared + r % shared;
+  h8 qf[NS];
+  float qsum[G];
+  int qe;
+  {
+    const uint16_t *q = a.q + (int64_t)token * a.ldq + head * D + 8 * h;
+    u4 raw[NS];
+    uint32_t mx = 0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      raw[s] = *(const u4 *)(q + 32 * s);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mx = pk_max_finite(mx, raw[s][w]);
+    }
+    const float top = row_max(fmaxf(lo_bf16(mx), hi_bf16(mx)));
+    qe = top > 0.f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) qsum[g] = 0.f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float x = ldexpf(lo_bf16(raw[s][w]), qe), y = ldexpf(hi_bf16(raw[s][w]), qe);
+        qsum[s / SPG] += x + y;
+        const float f = w & 1 ? 0.0625f : 1.f;
+        qf[s][2 * w] = (_Float16)(x * f);
+        qf[s][2 * w + 1] = (_Float16)(y * f);
       }
     }
+#pragma unroll
+    for (int g = 0; g < G; ++g) qsum[g] = row_sum(qsum[g]) * 0x1p-24f;
   }
-  for (int i = 0; i < D / 64; ++i)
-    a.y[row * a.ldy + h * D + lane + 64 * i] = f32_to_bf16_bits(l == 0.f ? 0.f : acc[i] / l);
+  const float sc = a.scale * 1.44269504088896f;
+  const int se = 24 - qe;
+
+  f4 O[NT];
+  float M[G], l = 0.f, m = -__FLT_MAX__;
+  int E = -80;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) O[t] = (f4){};
+#pragma unroll
+  for (int g = 0; g < G; ++g) M[g] = 0.f;
+
+  // pages of 32 chunks of the wave at a time: lane 2i + j holds that of run j
+  // of chunk i
+  const int32_t *table = a.table + b * a.ld_table;
+  int32_t pages = -1;
+  auto load_pages = [&](int at) {
+    const int ch = at + (lane >> 1) * CACHE_WAVES, key = ch * CHUNK + 16 * (lane & 1);
+    pages = ch < c1 && key < hi_max ? table[key >> c.page_shift] : -1;
+  };
+  const uint32_t k_off = col * (D / 2) + h * (D / 8), v_off = c.off_v + h * (2 * D) + col * (D / 8);
+  const uint32_t kp_off = c.off_kp + h * G * 16, vp_off = c.off_vp + h * G * 16;
+  // the chunk in place i of the 32; bit j of the result: run j's page exists
+  auto load = [&](int ch, int i, Chunk<D, G> &x) {
+    int ok = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int32_t page = __builtin_amdgcn_readlane(pages, 2 * i + j);
+      const bool in = page >= 0 && page < c.pages;
+      ok |= in ? 1 << j : 0;
+      const int place = (ch * CHUNK + 16 * j) & ((1 << c.page_shift) - 1);
+      const uint8_t *blk = kv_block(c, in ? page : 0, kvh);
+      const uint8_t *kb = blk + place * (D / 2), *pb = blk + place * (G * 4);
+#pragma unroll
+      for (int w = 0; w < NS; ++w) {
+        x.k[j][w] = *(const uint32_t *)(kb + k_off + 4 * w);
+        x.v[j][w] = *(const uint32_t *)(kb + v_off + 4 * w);
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        x.kp[j][g] = *(const u4 *)(pb + kp_off + 16 * g);
+        x.vp[j][g] = *(const u4 *)(pb + vp_off + 16 * g);
+      }
+    }
+    return ok;
+  };
+
+  auto work = [&](const Chunk<D, G> &x, int k0, int ok, auto partial) {
+    float t[2][4];
+    bool seen[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      f4 A[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        A[g] = (f4){};
+#pragma unroll
+        for (int s = 0; s < SPG; ++s)
+          A[g] = mfma_f16(nibbles(x.k[j][g * SPG + s]), __builtin_bit_cast(u4, qf[g * SPG + s]), A[g]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float s = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) s = fmaf(lo_bf16(x.kp[j][g][i]), A[g][i], fmaf(hi_bf16(x.kp[j][g][i]), qsum[g], s));
+        t[j][i] = ldexpf(s * sc, se);
+        if constexpr (partial) {
+          const int key = k0 + 16 * j + 4 * h + i;
+          seen[j][i] = key >= lo && key < hi && (ok >> j & 1);
+          t[j][i] = seen[j][i] ? t[j][i] : -__builtin_inff();
+        } else {
+          seen[j][i] = true;
+        }
+      }
+    }
+    auto rescale = [&](float f) {
+      l *= f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) M[g] *= f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) O[n] *= f;
+    };
+    float top = t[0][0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, t[i >> 2][i & 3]);
+    if (__any(top > m + 6.f)) {
+      const float now = fmaxf(m, row_max(top));
+      rescale(__builtin_amdgcn_exp2f(m - now));
+      m = now;
+    }
+    float p[2][4], pm[G];
+    u4 w[G], rest[G];
+    auto weigh = [&]() {
+      const float ref = m + (float)(E - 8);
+#pragma unroll
+      for (int g = 0; g < G; ++g) pm[g] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[j][i] = __builtin_amdgcn_exp2f(t[j][i] - ref);
+      uint32_t most = 0;
+      float far = 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            const uint32_t a0 = x.vp[j][g][i], a1 = x.vp[j][g][i + 1];
+            float w0 = p[j][i] * lo_bf16(a0), w1 = p[j][i + 1] * lo_bf16(a1);
+            float m0 = p[j][i] * hi_bf16(a0), m1 = p[j][i + 1] * hi_bf16(a1);
+            if constexpr (partial) {
+              w0 = seen[j][i] ? w0 : 0.f;
+              w1 = seen[j][i + 1] ? w1 : 0.f;
+              m0 = seen[j][i] ? m0 : 0.f;
+              m1 = seen[j][i + 1] ? m1 : 0.f;
+            }
+            pm[g] += m0 + m1;
+            const _Float16 h0 = (_Float16)w0, h1 = (_Float16)w1;
+            const uint32_t hh = pk_f16(h0, h1);
+            w[g][2 * j + (i >> 1)] = hh;
+            rest[g][2 * j + (i >> 1)] = pk_f16((_Float16)(w0 - (float)h0), (_Float16)(w1 - (float)h1));
+            most = pk_max_mag(most, hh);
+          }
+        far = fmaxf(far, fabsf(pm[g]));
+      }
+      return (most & 0xFFFF) >= 0x7C00 || most >= 0x7C000000u || far > 0x1p100f;
+    };
+    if (__any(weigh())) {
+      // E from the greatest finite scale or minimum that a row sees here
+      float big = 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float v = fmaxf(finite_mag(lo_bf16(x.vp[j][g][i])), finite_mag(hi_bf16(x.vp[j][g][i])));
+            big = fmaxf(big, seen[j][i] ? v : 0.f);
+          }
+      for (int d = 32; d; d >>= 1) big = fmaxf(big, __shfl_xor(big, d));
+      const int now = __builtin_amdgcn_readfirstlane(big > 0.f ? __builtin_amdgcn_frexp_expf(big) : E);
+      if (now > E) {
+        rescale(ldexpf(1.f, E - now));
+        E = now;
+        weigh();
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l += p[i >> 2][i & 3];
+#pragma unroll
+    for (int g = 0; g < G; ++g) M[g] += pm[g];
+    // value runs: dword w of a key holds tiles 8w .. 8w + 7 (at 64 channels
+    // a half dword, two keys a dword)
+#pragma unroll
+    for (int n4 = 0; n4 < NT / 4; ++n4) {
+      u4 v4;  // tiles 4 n4 .. 4 n4 + 3, key pairs of both runs
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (D == 64) {
+            v4[2 * j + e] = x.v[j][e];
+          } else {
+            constexpr int W = D / 128;  // dwords of a key's run
+            const uint32_t x0 = x.v[j][2 * e * W + (n4 >> 1)], x1 = x.v[j][(2 * e + 1) * W + (n4 >> 1)];
+            v4[2 * j + e] = __builtin_amdgcn_perm(x1, x0, n4 & 1 ? 0x07060302u : 0x05040100u);
+          }
+        }
+      const u4 v8 = v4 >> 8;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const u4 f = (n & 2 ? v8 : v4) & (n & 1 ? 0x00F000F0u : 0x000F000Fu);
+        const int g = (4 * n4 + n) / TPG;
+        O[4 * n4 + n] = mfma_f16(f, w[g], O[4 * n4 + n]);
+        O[4 * n4 + n] = mfma_f16(f, rest[g], O[4 * n4 + n]);
+      }
+    }
+  };
+
+  if (c0 < c1) {
+    Chunk<D, G> x, next;
+    load_pages(c0);
+    int ok = load(c0, 0, x);
+    for (int ch = c0, i = 0; ch < c1; ch += CACHE_WAVES) {
+      int ok_next = 0;
+      if (++i == 32) {
+        i = 0;
+        load_pages(ch + CACHE_WAVES);
+      }
+      if (ch + CACHE_WAVES < c1) ok_next = load(ch + CACHE_WAVES, i, next);
+      const int k0 = ch * CHUNK;
+      if (ok == 3 && k0 >= lo_max && k0 + CHUNK <= hi_min) work(x, k0, ok, std::integral_constant<bool, false>());
+      else work(x, k0, ok, std::integral_constant<bool, true>());
+      x = next;
+      ok = ok_next;
+    }
+  }
+
+  // the waves meet in LDS: numerators [wave][row][D], then references and sums
+  extern __shared__ __attribute__((aligned(16))) float s_o[];
+  float *s_ref = s_o + CACHE_WAVES * ROWS * (D + 4), *s_l = s_ref + CACHE_WAVES * ROWS;
+  l = row_sum(l);
+  float *mine = s_o + (wv * ROWS + col) * (D + 4);
+#pragma unroll
+  for (int g = 0; g < G; ++g) M[g] = row_sum(M[g]);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const float f = n & 1 ? 0x1p20f : 0x1p24f;
+    *(f4 *)(mine + 16 * n + 4 * h) = O[n] * f + M[n / TPG];
+  }
+  if (h == 0) {
+    s_ref[wv * ROWS + col] = m + (float)(E - 8);
+    s_l[wv * ROWS + col] = l;
+  }
+  __syncthreads();
+  const int row = tid >> 4, part = tid & 15;  // 16 threads a row, D / 16 channels each
+  if (rt * ROWS + row >= R) return;
+  float ref = -__FLT_MAX__, sum = 0.f, f[CACHE_WAVES];
+#pragma unroll
+  for (int w = 0; w < CACHE_WAVES; ++w)
+    if (s_l[w * ROWS + row] != 0.f) ref = fmaxf(ref, s_ref[w * ROWS + row]);
+#pragma unroll
+  for (int w = 0; w < CACHE_WAVES; ++w) {
+    const float lw = s_l[w * ROWS + row];
+    f[w] = lw != 0.f ? __builtin_amdgcn_exp2f(s_ref[w * ROWS + row] - ref) : 0.f;
+    sum += lw * f[w];
+  }
+  f4 out[D / 64];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    out[i] = (f4){};
+#pragma unroll
+    for (int w = 0; w < CACHE_WAVES; ++w)
+      if (f[w] != 0.f) out[i] += *(const f4 *)(s_o + (w * ROWS + row) * (D + 4) + 64 * i + 4 * part) * f[w];
+  }
+  const int q_row = rt * ROWS + row;
+  if (a.splits == 1) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint16_t *y = a.y + (int64_t)(b * a.q_len + q_row / shared) * a.ldy + (kvh * shared + q_row % shared) * D;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const f4 o = out[i] * inv;
+      *(u2 *)(y + 64 * i + 4 * part) =
+          (u2){(uint32_t)f32_to_bf16_bits(o[0]) | (uint32_t)f32_to_bf16_bits(o[1]) << 16,
+               (uint32_t)f32_to_bf16_bits(o[2]) | (uint32_t)f32_to_bf16_bits(o[3]) << 16};
+    }
+    return;
+  }
+  const int64_t at = (((int64_t)b * c.heads + kvh) * R + q_row) * a.splits + sp;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) *(f4 *)(a.part + at * D + 64 * i + 4 * part) = out[i];
+  if (part == 0) *(float2 *)(a.sums + 2 * at) = make_float2(ref, sum);
+}
+
+// Joins the key ranges of a row: a wave a row, D / 64 channels a lane.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnCacheArgs a) {
+  constexpr int N = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int shared = a.heads / a.c.heads, R = shared * a.q_len;
+  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (at >= (int64_t)a.batch * a.c.heads * R) return;
+  const float2 *sums = (const float2 *)a.sums + at * a.splits;
+  float ref = -__FLT_MAX__;
+  for (int s = lane; s < a.splits; s += 64)
+    if (sums[s].y != 0.f) ref = fmaxf(ref, sums[s].x);
+  for (int d = 32; d; d >>= 1) ref = fmaxf(ref, __shfl_xor(ref, d));
+  float sum = 0.f, o[N] = {};
+  const float *part = a.part + at * a.splits * D + lane * N;
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 x = sums[s];
+    if (x.y == 0.f) continue;
+    const float f = __builtin_amdgcn_exp2f(x.x - ref);
+    sum += x.y * f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] += part[(int64_t)s * D + i] * f;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int q_row = (int)(at % R), kvh = (int)(at / R % a.c.heads);
+  const int64_t b = at / R / a.c.heads;
+  uint16_t *y = a.y + (b * a.q_len + q_row / shared) * a.ldy + (kvh * shared + q_row % shared) * D + lane * N;
+#pragma unroll
+  for (int i = 0; i < N; ++i) y[i] = f32_to_bf16_bits(o[i] * inv);
+}
+
+template <int D, int GROUP>
+hipError_t launch_cache(const AttnCacheArgs &a, hipStream_t s) {
+  constexpr size_t lds = (size_t)CACHE_WAVES * ROWS * (D + 6) * 4;
+  const hipError_t e = allow_smem(attn_cache_kernel<D, GROUP>, lds);
+  if (e != hipSuccess) return e;
+  const int64_t blocks = (int64_t)a.batch * a.row_tiles * a.splits * a.c.heads;
+  attn_cache_kernel<D, GROUP><<<dim3((unsigned)blocks), 64 * CACHE_WAVES, lds, s>>>(a);
+  if (a.splits > 1) {
+    const int64_t rows = (int64_t)a.batch * a.heads * a.q_len;
+    attn_join_kernel<D><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, s>>>(a);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -257,13 +636,18 @@ hipError_t launch_kv_read(const KvReadArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_attn_cache(const AttnCacheArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)a.batch * a.q_len + 3) / 4), a.heads);
+  const int group = 1 << a.c.group_shift;
   switch (a.c.dim) {
-    case 64: attn_cache_kernel<64><<<grid, 256, 0, s>>>(a); break;
-    case 128: attn_cache_kernel<128><<<grid, 256, 0, s>>>(a); break;
-    default: attn_cache_kernel<256><<<grid, 256, 0, s>>>(a);
+    case 64: return group == 32 ? launch_cache<64, 32>(a, s) : launch_cache<64, 64>(a, s);
+    case 128:
+      return group == 32   ? launch_cache<128, 32>(a, s)
+             : group == 64 ? launch_cache<128, 64>(a, s)
+                           : launch_cache<128, 128>(a, s);
+    default:
+      return group == 32   ? launch_cache<256, 32>(a, s)
+             : group == 64 ? launch_cache<256, 64>(a, s)
+                           : launch_cache<256, 128>(a, s);
   }
-  return hipGetLastError();
 }
 
 }  // namespace svq

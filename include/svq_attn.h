@@ -20,7 +20,11 @@
  * Numerics.  Inputs and outputs of the attention calls are bf16.  Scores are
  * products of the bf16 inputs (of the stored values, for the cache) summed in
  * fp32; the softmax's maximum, exponentials and sum are fp32; each output is
- * rounded once, to nearest even.  A query that sees no key gives a row of
+ * rounded once, to nearest even.  Over a prompt a weight (at most 256, the
+ * greatest at least 1/256 of that) meets its value rounded to bf16.  Over the
+ * cache, where codes are multiplied as they are, the product of a weight and a
+ * scale is held in 22 bits, down to 2^-32 of the greatest scale or minimum that
+ * the rows of a launch's tile see.  A query that sees no key gives a row of
  * zeros.  A key that a query does not see has no influence on it, whatever
  * it, its value or its stored scales hold (infinities and NaN included).
  */

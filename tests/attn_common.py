@@ -6,9 +6,12 @@ Tolerances count roundings.  An output is rounded to bf16 once (at most 2^-8
 of it); ``p_step`` is the rounding of a weight before it meets its value, per
 key at most p_step * p_j |v_j|, which sums to p_step * A with A = sum p_j |v_j|;
 fp32 sums of n terms are off by at most n 2^-24 A; a score is off by at most
-(D + 8) 2^-24 scale sum_d |q_d k_d| =: e, which moves p_j and the softmax's sum
-by a factor within 1 +- 2e each, and the exponentials and their sum add a few
-2^-23.
+(D + 8) 2^-24 scale sum_d |q_d k_d| =: e at most.  With scores s_j + d_j, |d_j|
+<= e, a weight exp(s_j + d_j) / sum exp(s_i + d_i) lies between p_j exp(-2e)
+and p_j exp(2e), which moves y by (exp(2e) - 1) A at most: 2e A for a small e,
+where another 2e A is left for the exponentials and their sum (a few 2^-23),
+but not 4e A for a large one (e = 2.8 allows 270 A, queries of 1024 against
+keys near 100).
 """
 import numpy as np
 import torch
@@ -67,14 +70,24 @@ def visible(n, keys, causal=True, window=0):
     return seen
 
 
-def bound(y, amount, err, keys, p_step):
-    return 2.0 ** -8 * y.abs() + (p_step * 1.01 + (keys + 64) * 2.0 ** -24 + 4 * err) * amount + 1e-37
+def bound(y, amount, err, keys, p_step, floor=0.0):
+    return floor + 2.0 ** -8 * y.abs() + (p_step * 1.01 + (keys + 64) * 2.0 ** -24 + 2 * err + torch.expm1(2 * err)) * amount + 1e-37
 
 
-def check(got, want, amount, err, keys, p_step, label=""):
+def cache_floor(v, keys):
+    """How far attention over the cache may be off beside its roundings: a
+    product of a weight and a scale is held as two fp16 numbers in units of
+    2^(E - 8), so it is off by half a subnormal step, 2^-25 units, where 2^E is
+    at most twice the greatest scale or minimum among the tokens seen (at most
+    the greatest |v|): 2^-32 of it a key, times a code of 15 at most, over a sum
+    of weights of at least 1."""
+    return keys * 2.0 ** -28 * v.abs().max().item()
+
+
+def check(got, want, amount, err, keys, p_step, label="", floor=0.0):
     got = got.detach().cpu().double()
     off = (got - want).abs()
-    lim = bound(want, amount, err, keys, p_step)
+    lim = bound(want, amount, err, keys, p_step, floor)
     bad = ~(off <= lim)
     assert not bad.any(), (f"{label}: {int(bad.sum())} of {bad.numel()} outside, first {torch.nonzero(bad)[0].tolist()}: "
                            f"{got[bad][0].item()} for {want[bad][0].item()}, bound {lim[bad][0].item()}")

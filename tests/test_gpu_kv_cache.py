@@ -2,7 +2,7 @@
 bits."""
 import pytest
 
-from tests.attn_common import P_F16, attend, check, stored, visible
+from tests.attn_common import P_F16, attend, cache_floor, check, stored, visible
 from tests.gpu_common import require_gpu, torch
 
 pytestmark = pytest.mark.gpu
@@ -239,8 +239,9 @@ def test_values_of_every_size(dim, group):
         q = _rows(3, heads * dim, 14, q_size)
         for last in (10, 15, 40, 70, n):  # later tokens are larger
             y = svq.attn_cache(cache, q, table, _ints([last]), q_len=3)
-            ref = attend(q, stored(k, group)[:last], stored(v, group)[:last], heads, kv, dim ** -0.5, visible(3, last))
-            check(y, *ref, last, P_F16, f"{last} tokens, queries of {q_size}")
+            values = stored(v, group)[:last]
+            ref = attend(q, stored(k, group)[:last], values, heads, kv, dim ** -0.5, visible(3, last))
+            check(y, *ref, last, P_F16, f"{last} tokens, queries of {q_size}", floor=cache_floor(values, last))
 
 
 @pytest.mark.parametrize("dim,group", FORMS)
