@@ -15,9 +15,9 @@ int compute_units();  // of the current device
 //
 // Both code layouts give a lane of v_mfma_f32_16x16x32_f16 its operand with
 // wide loads and no exchange between lanes:
-//   keys    [slot][word p]: head_dim/8 dwords a slot; word p = h * (D/32) + c
-//           holds channels 32c + 8h .. 32c + 8h + 7, so lane 16h + r reads
-//           slot r's words of all steps c of 32 channels in one piece;
+//   keys    [slot/16][h][slot%16][word c]: word c of D/32 holds channels
+//           32c + 8h .. 32c + 8h + 7, so lane 16h + r reads slot r's words of
+//           all steps c of 32 channels in one piece, and a wave one stretch;
 //   values  [slot/4][r][slot%4]: 16 runs a slot, run r = channels r, 16 + r,
 //           32 + r ... (D/16 of them, D/32 bytes): lane 16h + r reads channel
 //           16t + r of four slots for every 16-channel tile t in one piece,
@@ -38,7 +38,10 @@ struct KvView {
 __host__ __device__ inline int kv_nibble(int j) { return (j >> 1) | ((j & 1) << 2); }
 
 // Bytes of a view's block at which a slot's data lie.
-__host__ __device__ inline int kv_key_word(const KvView &c, int place, int p) { return (place * (c.dim / 8) + p) * 4; }
+// (key word: channels 8n .. 8n + 7)
+__host__ __device__ inline int kv_key_word(const KvView &c, int place, int n) {
+  return (((place >> 4) * 64 + (n & 3) * 16 + (place & 15)) * (c.dim / 32) + (n >> 2)) * 4;
+}
 __host__ __device__ inline int kv_value_run(const KvView &c, int place, int r) {
   return c.off_v + ((place >> 2) * 64 + r * 4 + (place & 3)) * (c.dim / 32);
 }

@@ -104,8 +104,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvWriteArgs a) {
 #pragma unroll
     for (int w = 0; w < (N + 7) / 8; ++w) {
       const int n = N == 4 ? r >> 1 : r * (N / 8) + w;  // channels 8n ..
-      const int p8 = (n & 3) * (D / 32) + (n >> 2);
-      if (N > 4 || !(r & 1)) *(uint32_t *)(blk + kv_key_word(a.c, place, p8)) = word[w];
+      if (N > 4 || !(r & 1)) *(uint32_t *)(blk + kv_key_word(a.c, place, n)) = word[w];
     }
     if (r % lanes == 0) *(uint32_t *)(blk + kv_param(a.c, 0, place, r / lanes)) = p.bits;
   } else {
@@ -150,7 +149,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
     uint32_t code;
     if constexpr (SIDE == 0) {
       const int n = d >> 3;
-      const uint32_t w = *(const uint32_t *)(blk + kv_key_word(a.c, place, (n & 3) * (D / 32) + (n >> 2)));
+      const uint32_t w = *(const uint32_t *)(blk + kv_key_word(a.c, place, n));
       code = (w >> 4 * kv_nibble(d & 7)) & 15;
     } else {
       code = (blk[kv_value_run(a.c, place, r) + (i >> 1)] >> 4 * (i & 1)) & 15;
@@ -188,7 +187,27 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
 // exponent that is raised once a p s_g overflows fp16 (it starts so low that
 // the first chunk raises it to the exponent of that chunk's greatest scale or
 // minimum).
-constexpr int CACHE_WAVES = 4, CHUNK = 32, ROWS = 16;
+constexpr int CACHE_WAVES = 4, CACHE_STAGES = 3, CHUNK = 32, ROWS = 16;
+
+typedef __attribute__((address_space(3))) uint8_t lds_t;
+__device__ __forceinline__ uint32_t lds_u32(uint32_t at) {
+  return *(const __attribute__((address_space(3))) uint32_t *)(lds_t *)(uintptr_t)at;
+}
+__device__ __forceinline__ u4 lds_u128(uint32_t at) {
+  return *(const __attribute__((address_space(3))) u4 *)(lds_t *)(uintptr_t)at;
+}
+// 16 bytes a lane from base + off to LDS bytes dst + 16 * lane, waited for by
+// vmcnt.  (The builtin makes every LDS read behind it wait for the copy.)  The
+// wait states stand between the scalar values' writers and their use as M0 and
+// as a base: the compiler does not look into the block.
+__device__ __forceinline__ void copy_to_lds(const uint8_t *base, uint32_t off, uint32_t dst) {
+  const uint32_t d = __builtin_amdgcn_readfirstlane(dst);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(d), "v"(off), "s"(base) : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
+}
 
 __device__ __forceinline__ float lo_bf16(uint32_t p) { return bf16_bits_to_f32(p & 0xFFFFu); }
 __device__ __forceinline__ float hi_bf16(uint32_t p) { return __builtin_bit_cast(float, p & 0xFFFF0000u); }
@@ -217,14 +236,6 @@ __device__ __forceinline__ float row_sum(float v) {
   return b.x + b.y;
 }
 
-// What a lane holds of a chunk: the key words, value runs and parameters of
-// two runs of 16 keys.
-template <int D, int G>
-struct Chunk {
-  uint32_t k[2][D / 32], v[2][D / 32];
-  u4 kp[2][G], vp[2][G];
-};
-
 // Four key words' steps of 8 channels as fp16 pairs (see kv_nibble).
 __device__ __forceinline__ u4 nibbles(uint32_t w) {
   const uint32_t x = w >> 8;
@@ -239,7 +250,7 @@ __device__ __forceinline__ uint32_t pk_f16(_Float16 a, _Float16 b) {
 }
 
 template <int D, int GROUP>
-__global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache_kernel(AttnCacheArgs a) {
+__global__ __launch_bounds__(64 * CACHE_WAVES, 2) void attn_cache_kernel(AttnCacheArgs a) {
   constexpr int G = D / GROUP, NS = D / 32, NT = D / 16, TPG = GROUP / 16, SPG = GROUP / 32;
   const KvView &c = a.c;
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, h = lane >> 4;
@@ -251,7 +262,7 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache
   id /= a.splits;
   const int rt = id % a.row_tiles, b = id / a.row_tiles;
   const int shared = a.heads / c.heads, R = shared * a.q_len;
-  const int len = min(max(a.lens[b], 0), a.max_len);
+  const int len = __builtin_amdgcn_readfirstlane(min(max(a.lens[b], 0), a.max_len));
   const int r = min(rt * ROWS + col, R - 1);
 
   // what a row sees: keys [lo, hi)
@@ -263,6 +274,7 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache
   const int c_first = lo_min / CHUNK, chunks = max((hi_max + CHUNK - 1) / CHUNK - c_first, 0);
   const int per = (chunks + a.splits - 1) / a.splits;
   const int c0 = c_first + min(sp * per, chunks) + wv, c1 = c_first + min(sp * per + per, chunks);
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 
   // queries: step s takes channels 32s + 8h + j, a sixteenth of them where the
   // nibble pair is 16 times its code (j = 2, 3, 6, 7)
@@ -316,11 +328,16 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache
   auto load_pages = [&](int at) {
     const int ch = at + (lane >> 1) * CACHE_WAVES, key = ch * CHUNK + 16 * (lane & 1);
     pages = ch < c1 && key < hi_max ? table[key >> c.page_shift] : -1;
+    asm volatile("" : "+v"(pages));  // waited for here, not at every use among the copies
   };
-  const uint32_t k_off = col * (D / 2) + h * (D / 8), v_off = c.off_v + h * (2 * D) + col * (D / 8);
-  const uint32_t kp_off = c.off_kp + h * G * 16, vp_off = c.off_vp + h * G * 16;
+  // A wave copies its chunks into its own part of LDS, STAGES of them in
+  // flight: per run of 16 keys the key words, the value runs and the
+  // parameters of both, each one stretch of the page.
+  constexpr int KB = 8 * D, PB = 64 * G, RUN = 2 * KB + 2 * PB;
+  constexpr int COPIES = 2 * (2 * KB / 1024 + (2 * PB + 1023) / 1024);  // copies a chunk
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_t *)smem + wv * CACHE_STAGES * 2 * RUN;
   // the chunk in place i of the 32; bit j of the result: run j's page exists
-  auto load = [&](int ch, int i, Chunk<D, G> &x) {
+  auto load = [&](int ch, int i, int stage) {
     int ok = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -329,40 +346,50 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache
       ok |= in ? 1 << j : 0;
       const int place = (ch * CHUNK + 16 * j) & ((1 << c.page_shift) - 1);
       const uint8_t *blk = kv_block(c, in ? page : 0, kvh);
-      const uint8_t *kb = blk + place * (D / 2), *pb = blk + place * (G * 4);
+      const uint32_t dst = lds0 + (stage * 2 + j) * RUN;
+      const uint8_t *codes = blk + place * (D / 2), *par = blk + c.off_kp + place * (G * 4);
+      if constexpr (D == 64) {
+        copy_to_lds(codes, lane < 32 ? lane * 16 : c.off_v + (lane - 32) * 16, dst);
+      } else {
 #pragma unroll
-      for (int w = 0; w < NS; ++w) {
-        x.k[j][w] = *(const uint32_t *)(kb + k_off + 4 * w);
-        x.v[j][w] = *(const uint32_t *)(kb + v_off + 4 * w);
+        for (int n = 0; n < KB / 1024; ++n) {
+          copy_to_lds(codes + n * 1024, lane * 16, dst + n * 1024);
+          copy_to_lds(codes + c.off_v + n * 1024, lane * 16, dst + KB + n * 1024);
+        }
       }
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        x.kp[j][g] = *(const u4 *)(pb + kp_off + 16 * g);
-        x.vp[j][g] = *(const u4 *)(pb + vp_off + 16 * g);
-      }
+      if (lane < 2 * PB / 16)
+        copy_to_lds(par, lane < PB / 16 ? lane * 16 : c.off_vp - c.off_kp + (lane - PB / 16) * 16, dst + 2 * KB);
     }
     return ok;
   };
 
-  auto work = [&](const Chunk<D, G> &x, int k0, int ok, auto partial) {
+  auto work = [&](uint32_t src, int k0, int ok, auto partial) {
     float t[2][4];
     bool seen[2][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       f4 A[G];
+      uint32_t kw[NS];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) kw[s] = lds_u32(src + j * RUN + lane * (4 * NS) + 4 * s);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         A[g] = (f4){};
 #pragma unroll
         for (int s = 0; s < SPG; ++s)
-          A[g] = mfma_f16(nibbles(x.k[j][g * SPG + s]), __builtin_bit_cast(u4, qf[g * SPG + s]), A[g]);
+          A[g] = mfma_f16(nibbles(kw[g * SPG + s]), __builtin_bit_cast(u4, qf[g * SPG + s]), A[g]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[j][i] = 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const u4 kp = lds_u128(src + j * RUN + 2 * KB + (h * G + g) * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[j][i] = fmaf(lo_bf16(kp[i]), A[g][i], fmaf(hi_bf16(kp[i]), qsum[g], t[j][i]));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float s = 0.f;
-#pragma unroll
-        for (int g = 0; g < G; ++g) s = fmaf(lo_bf16(x.kp[j][g][i]), A[g][i], fmaf(hi_bf16(x.kp[j][g][i]), qsum[g], s));
-        t[j][i] = ldexpf(s * sc, se);
+        t[j][i] = ldexpf(t[j][i] * sc, se);
         if constexpr (partial) {
           const int key = k0 + 16 * j + 4 * h + i;
           seen[j][i] = key >= lo && key < hi && (ok >> j & 1);
@@ -387,12 +414,21 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache
       rescale(__builtin_amdgcn_exp2f(m - now));
       m = now;
     }
+    u4 vp[2][G];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        vp[j][g] = lds_u128(src + j * RUN + 2 * KB + PB + (h * G + g) * 16);
+        if constexpr (partial) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vp[j][g][i] = seen[j][i] ? vp[j][g][i] : 0u;
+        }
+      }
     float p[2][4], pm[G];
     u4 w[G], rest[G];
     auto weigh = [&]() {
       const float ref = m + (float)(E - 8);
-#pragma unroll
-      for (int g = 0; g < G; ++g) pm[g] = 0.f;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -401,20 +437,15 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache
       float far = 0.f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
+        pm[g] = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int i = 0; i < 4; i += 2) {
-            const uint32_t a0 = x.vp[j][g][i], a1 = x.vp[j][g][i + 1];
-            float w0 = p[j][i] * lo_bf16(a0), w1 = p[j][i + 1] * lo_bf16(a1);
-            float m0 = p[j][i] * hi_bf16(a0), m1 = p[j][i + 1] * hi_bf16(a1);
-            if constexpr (partial) {
-              w0 = seen[j][i] ? w0 : 0.f;
-              w1 = seen[j][i + 1] ? w1 : 0.f;
-              m0 = seen[j][i] ? m0 : 0.f;
-              m1 = seen[j][i + 1] ? m1 : 0.f;
-            }
-            pm[g] += m0 + m1;
+            const uint32_t a0 = vp[j][g][i], a1 = vp[j][g][i + 1];
+            const float w0 = p[j][i] * lo_bf16(a0), w1 = p[j][i + 1] * lo_bf16(a1);
+            pm[g] = fmaf(p[j][i], hi_bf16(a0), pm[g]);
+            pm[g] = fmaf(p[j][i + 1], hi_bf16(a1), pm[g]);
             const _Float16 h0 = (_Float16)w0, h1 = (_Float16)w1;
             const uint32_t hh = pk_f16(h0, h1);
             w[g][2 * j + (i >> 1)] = hh;
@@ -433,10 +464,8 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v = fmaxf(finite_mag(lo_bf16(x.vp[j][g][i])), finite_mag(hi_bf16(x.vp[j][g][i])));
-            big = fmaxf(big, seen[j][i] ? v : 0.f);
-          }
+          for (int i = 0; i < 4; ++i)
+            big = fmaxf(big, fmaxf(finite_mag(lo_bf16(vp[j][g][i])), finite_mag(hi_bf16(vp[j][g][i]))));
       for (int d = 32; d; d >>= 1) big = fmaxf(big, __shfl_xor(big, d));
       const int now = __builtin_amdgcn_readfirstlane(big > 0.f ? __builtin_amdgcn_frexp_expf(big) : E);
       if (now > E) {
@@ -449,6 +478,11 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache
     for (int i = 0; i < 8; ++i) l += p[i >> 2][i & 3];
 #pragma unroll
     for (int g = 0; g < G; ++g) M[g] += pm[g];
+    uint32_t vw[2][NS];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) vw[j][s] = lds_u32(src + j * RUN + KB + lane * (4 * NS) + 4 * s);
     // value runs: dword w of a key holds tiles 8w .. 8w + 7 (at 64 channels
     // a half dword, two keys a dword)
 #pragma unroll
@@ -459,10 +493,10 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           if constexpr (D == 64) {
-            v4[2 * j + e] = x.v[j][e];
+            v4[2 * j + e] = vw[j][e];
           } else {
             constexpr int W = D / 128;  // dwords of a key's run
-            const uint32_t x0 = x.v[j][2 * e * W + (n4 >> 1)], x1 = x.v[j][(2 * e + 1) * W + (n4 >> 1)];
+            const uint32_t x0 = vw[j][2 * e * W + (n4 >> 1)], x1 = vw[j][(2 * e + 1) * W + (n4 >> 1)];
             v4[2 * j + e] = __builtin_amdgcn_perm(x1, x0, n4 & 1 ? 0x07060302u : 0x05040100u);
           }
         }
@@ -478,26 +512,35 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache
   };
 
   if (c0 < c1) {
-    Chunk<D, G> x, next;
+    const int count = (c1 - c0 + CACHE_WAVES - 1) / CACHE_WAVES;
     load_pages(c0);
-    int ok = load(c0, 0, x);
-    for (int ch = c0, i = 0; ch < c1; ch += CACHE_WAVES) {
-      int ok_next = 0;
-      if (++i == 32) {
-        i = 0;
-        load_pages(ch + CACHE_WAVES);
+    int oks = 0;  // two bits a stage
+    auto fetch = [&](int n) {
+      if (n % 32 == 0 && n > 0) load_pages(c0 + n * CACHE_WAVES);
+      const int stage = n % CACHE_STAGES;
+      oks = (oks & ~(3 << 2 * stage)) | load(c0 + n * CACHE_WAVES, n % 32, stage) << 2 * stage;
+    };
+    for (int n = 0; n < CACHE_STAGES - 1 && n < count; ++n) fetch(n);
+    for (int n = 0; n < count; ++n) {
+      // the chunk's reads are over before its place is written again
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (n + CACHE_STAGES - 1 < count) {
+        fetch(n + CACHE_STAGES - 1);
+        wait_copies<(CACHE_STAGES - 1) * COPIES>();
+      } else {
+        wait_copies<0>();
       }
-      if (ch + CACHE_WAVES < c1) ok_next = load(ch + CACHE_WAVES, i, next);
-      const int k0 = ch * CHUNK;
-      if (ok == 3 && k0 >= lo_max && k0 + CHUNK <= hi_min) work(x, k0, ok, std::integral_constant<bool, false>());
-      else work(x, k0, ok, std::integral_constant<bool, true>());
-      x = next;
-      ok = ok_next;
+      const int stage = n % CACHE_STAGES, ok = oks >> 2 * stage & 3;
+      const uint32_t src = lds0 + stage * 2 * RUN;
+      const int k0 = (c0 + n * CACHE_WAVES) * CHUNK;
+      if (ok == 3 && k0 >= lo_max && k0 + CHUNK <= hi_min) work(src, k0, ok, std::integral_constant<bool, false>());
+      else work(src, k0, ok, std::integral_constant<bool, true>());
     }
   }
+  __syncthreads();  // the waves' copies share their place with what follows
 
   // the waves meet in LDS: numerators [wave][row][D], then references and sums
-  extern __shared__ __attribute__((aligned(16))) float s_o[];
+  float *s_o = (float *)smem;
   float *s_ref = s_o + CACHE_WAVES * ROWS * (D + 4), *s_l = s_ref + CACHE_WAVES * ROWS;
   l = row_sum(l);
   float *mine = s_o + (wv * ROWS + col) * (D + 4);
@@ -552,47 +595,60 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D == 256 ? 1 : 2) void attn_cache
   if (part == 0) *(float2 *)(a.sums + 2 * at) = make_float2(ref, sum);
 }
 
-// Joins the key ranges of a row: a wave a row, D / 64 channels a lane.
+// Joins the key ranges of a row: a block a row, D / 4 threads a range, four
+// channels a thread.
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnCacheArgs a) {
-  constexpr int N = D / 64;
-  const int lane = threadIdx.x & 63;
+  constexpr int T = D / 4, N = 256 / T;
+  __shared__ f4 s_o[N][T];
+  __shared__ float s_l[N];
+  const int tid = threadIdx.x, lane = tid & 63, part = tid % T, first = tid / T;
   const int shared = a.heads / a.c.heads, R = shared * a.q_len;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (at >= (int64_t)a.batch * a.c.heads * R) return;
+  const int64_t at = blockIdx.x;
   const float2 *sums = (const float2 *)a.sums + at * a.splits;
   float ref = -__FLT_MAX__;
   for (int s = lane; s < a.splits; s += 64)
     if (sums[s].y != 0.f) ref = fmaxf(ref, sums[s].x);
   for (int d = 32; d; d >>= 1) ref = fmaxf(ref, __shfl_xor(ref, d));
-  float sum = 0.f, o[N] = {};
-  const float *part = a.part + at * a.splits * D + lane * N;
-  for (int s = 0; s < a.splits; ++s) {
+  float sum = 0.f;
+  f4 o = {};
+  const f4 *num = (const f4 *)(a.part + at * a.splits * D) + part;
+#pragma unroll 4
+  for (int s = first; s < a.splits; s += N) {
     const float2 x = sums[s];
-    if (x.y == 0.f) continue;
-    const float f = __builtin_amdgcn_exp2f(x.x - ref);
+    const f4 v = num[(int64_t)s * T];
+    const float f = x.y != 0.f ? __builtin_amdgcn_exp2f(x.x - ref) : 0.f;
     sum += x.y * f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] += part[(int64_t)s * D + i] * f;
+    o += v * f;  // a range without keys has left zeros
+  }
+  s_o[first][part] = o;
+  if (part == 0) s_l[first] = sum;
+  __syncthreads();
+  if (tid >= T) return;
+  for (int n = 1; n < N; ++n) {
+    o += s_o[n][part];
+    sum += s_l[n];
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int q_row = (int)(at % R), kvh = (int)(at / R % a.c.heads);
   const int64_t b = at / R / a.c.heads;
-  uint16_t *y = a.y + (b * a.q_len + q_row / shared) * a.ldy + (kvh * shared + q_row % shared) * D + lane * N;
-#pragma unroll
-  for (int i = 0; i < N; ++i) y[i] = f32_to_bf16_bits(o[i] * inv);
+  uint16_t *y = a.y + (b * a.q_len + q_row / shared) * a.ldy + (kvh * shared + q_row % shared) * D + 4 * part;
+  o *= inv;
+  *(u2 *)y = (u2){(uint32_t)f32_to_bf16_bits(o[0]) | (uint32_t)f32_to_bf16_bits(o[1]) << 16,
+                  (uint32_t)f32_to_bf16_bits(o[2]) | (uint32_t)f32_to_bf16_bits(o[3]) << 16};
 }
 
 template <int D, int GROUP>
 hipError_t launch_cache(const AttnCacheArgs &a, hipStream_t s) {
-  constexpr size_t lds = (size_t)CACHE_WAVES * ROWS * (D + 6) * 4;
+  constexpr int G = D / GROUP, copies = CACHE_STAGES * 2 * (16 * D + 128 * G), joined = ROWS * (D + 6) * 4;
+  constexpr size_t lds = (size_t)CACHE_WAVES * (copies > joined ? copies : joined);
   const hipError_t e = allow_smem(attn_cache_kernel<D, GROUP>, lds);
   if (e != hipSuccess) return e;
   const int64_t blocks = (int64_t)a.batch * a.row_tiles * a.splits * a.c.heads;
   attn_cache_kernel<D, GROUP><<<dim3((unsigned)blocks), 64 * CACHE_WAVES, lds, s>>>(a);
   if (a.splits > 1) {
     const int64_t rows = (int64_t)a.batch * a.heads * a.q_len;
-    attn_join_kernel<D><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, s>>>(a);
+    attn_join_kernel<D><<<dim3((unsigned)rows), 256, 0, s>>>(a);
   }
   return hipGetLastError();
 }
