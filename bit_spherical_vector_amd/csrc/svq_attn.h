@@ -88,10 +88,11 @@ struct AttnCacheArgs {
   const int32_t *table, *lens;
   int32_t batch, q_len, heads, max_len, window;
   float scale;
-  int32_t row_tiles, splits;  // tiles of 16 rows, ranges of keys
+  int32_t row_tiles, splits, per;  // tiles of 16 rows; ranges of keys, each of `per` chunks of 32
   float *part, *sums;         // splits > 1: [batch][kv head][row][split] numerators [dim] and (reference, sum)
 };
-constexpr int CACHE_ROWS = 16, CACHE_BLOCK_KEYS = 128;  // rows of a tile, keys of a block's step
+// rows of a tile, keys of a block's step, steps of a block at most
+constexpr int CACHE_ROWS = 16, CACHE_BLOCK_KEYS = 128, CACHE_MAX_STEPS = 16;
 hipError_t launch_attn_cache(const AttnCacheArgs &a, hipStream_t s);
 
 }  // namespace svq

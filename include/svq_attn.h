@@ -53,7 +53,7 @@ extern "C" {
  *             [0, tokens] and [0, tokens_k] (values beyond are taken as the
  *             nearest that is not).  Rows of y before starts[0] and from
  *             starts[sequences] on are left as they were.
- *   tokens, tokens_k: 1 .. 2^24; sequences: 1 .. 65536; scale: finite. */
+ *   tokens, tokens_k: 1 .. 2^24; sequences: 1 .. 65535; scale: finite. */
 svq_status svq_attn_prompt(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                            int32_t q_heads, int32_t kv_heads, int32_t head_dim, const int32_t *starts,
                            const int32_t *starts_k, int64_t sequences, int64_t tokens, int64_t tokens_k,
@@ -113,7 +113,7 @@ svq_status svq_kv_read(const svq_kv_cache *cache, const int32_t *slots, int64_t 
  *             taken as the nearest that is not).
  *   max_len:  1 .. ld_table * page_size, at most 2^30: what the launch is
  *             planned for.
- *   batch:    1 .. 65536; q_len: 1 .. 1024; scale: finite.
+ *   batch:    1 .. 65535; q_len: 1 .. 1024; scale: finite.
  *   y:        device bf16 [batch * q_len][ldy], out; must not overlap q. */
 svq_status svq_attn_cache(const svq_kv_cache *cache, const void *q, int64_t ldq, int32_t q_heads,
                           const int32_t *table, int64_t ld_table, const int32_t *lens, int64_t batch,

@@ -65,7 +65,7 @@ def _cache(ws=None, nbytes=0, desc=None, **over):
     (dict(q_heads=2050, kv_heads=1025, ldq=1 << 20, ldk=1 << 20, ldv=1 << 20, ldy=1 << 20), UNSUPPORTED),
     (dict(q_heads=16448, kv_heads=257, ldq=1 << 22, ldk=1 << 20, ldv=1 << 20, ldy=1 << 22), UNSUPPORTED),
     (dict(tokens=0), BAD), (dict(tokens=(1 << 24) + 1), BAD), (dict(tokens_k=0), BAD),
-    (dict(tokens_k=(1 << 24) + 1), BAD), (dict(sequences=0), BAD), (dict(sequences=65537), BAD),
+    (dict(tokens_k=(1 << 24) + 1), BAD), (dict(sequences=0), BAD), (dict(sequences=65536), BAD),
     (dict(ldq=504), BAD), (dict(ldk=248), BAD), (dict(ldv=248), BAD), (dict(ldy=504), BAD),
     (dict(causal=2), BAD), (dict(causal=0, window=4), BAD), (dict(window=-1), BAD),
     (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD),
@@ -157,8 +157,8 @@ def test_read_types():
 
 @pytest.mark.parametrize("over,status", [
     (dict(cache=None), BAD), (dict(q_heads=0), BAD), (dict(q_heads=3), BAD),
-    (dict(q_heads=130, ldq=130 * 128, ldy=130 * 128), UNSUPPORTED), (dict(batch=0), BAD), (dict(batch=65537), BAD),
-    (dict(q_len=0), BAD), (dict(q_len=1025), BAD), (dict(batch=65536, q_len=1000), BAD), (dict(max_len=0), BAD),
+    (dict(q_heads=130, ldq=130 * 128, ldy=130 * 128), UNSUPPORTED), (dict(batch=0), BAD), (dict(batch=65536), BAD),
+    (dict(q_len=0), BAD), (dict(q_len=1025), BAD), (dict(batch=65535, q_len=1000), BAD), (dict(max_len=0), BAD),
     (dict(max_len=81), BAD), (dict(ld_table=4), BAD), (dict(ld_table=0), BAD),
     (dict(ld_table=1 << 40, max_len=(1 << 30) + 1), BAD), (dict(ldq=504), BAD), (dict(ldy=504), BAD),
     (dict(window=-1), BAD), (dict(scale=float("inf")), BAD), (dict(scale=float("nan")), BAD),
@@ -171,7 +171,7 @@ def test_attention_over_the_cache_refusals(over, status):
 
 
 @pytest.mark.parametrize("shape", [dict(), dict(batch=1, max_len=1, ld_table=1), dict(q_len=7, window=5),
-                                   dict(ld_table=1 << 26, max_len=1 << 30), dict(batch=65536, q_len=256)])
+                                   dict(ld_table=1 << 26, max_len=1 << 30), dict(batch=65535, q_len=256)])
 def test_attention_over_the_cache_workspace(shape):
     st, need = _cache(**shape)
     assert st == svq.SVQ_OK and 0 < need < 1 << 36
