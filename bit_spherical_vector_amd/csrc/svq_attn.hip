@@ -58,13 +58,22 @@ __device__ __forceinline__ float max_halves(float v) {
   const float2 r = both_halves(v);
   return fmaxf(r.x, r.y);
 }
+// The greater value, NaN if one is (one instruction for three; fmaxf takes one
+// more for each value that a matrix product has left).
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float sum_halves(float v) {
   const float2 r = both_halves(v);
   return r.x + r.y;
 }
 
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+typedef float f2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
-  return (uint32_t)f32_to_bf16_bits(a) | (uint32_t)f32_to_bf16_bits(b) << 16;
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, b2));
+}
+// c plus both halves of a.
+__device__ __forceinline__ float add_bf16(uint32_t a, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, a), (b2){(__bf16)1.f, (__bf16)1.f}, c, false);
 }
 __device__ __forceinline__ f16x mfma_bf16(const u4 &a, const u4 &b, const f16x &c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
@@ -205,7 +214,18 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   float m = -__FLT_MAX__, mref = 0.f, l = 0.f;
   bool dirty = false, far_any = false;
 
-  auto work = [&](uint32_t base, int k0, auto partial) {
+  if (t0 < t1) stage(t0, 0);
+#pragma unroll 1
+  for (int t = t0; t < t1; ++t) {
+    const int buf = (t - t0) & 1;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();  // the tile is there, and nobody reads the other buffer
+    if (t + 1 < t1) stage(t + 1, buf ^ 1);
+    const int k0 = t * KT;
+    if (!mine || k0 >= w_hi1 || k0 + KT <= w_lo0) continue;
+    const bool partial = k0 < w_lo1 || k0 + KT > w_hi0;  // some row does not see all of it
+    const uint32_t base = lds0 + buf * 2 * SIDE;
+
     f16x S[2] = {(f16x){}, (f16x){}};
     u4 kf[2][2];
     auto load_k = [&](int s) {
@@ -222,7 +242,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // MFMA
     }
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (partial) {
+    if (partial) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -231,16 +251,15 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
           S[kb][i] = key >= lo && key < hi ? S[kb][i] : -__builtin_inff();
         }
     }
-    float top = fmaxf(S[0][0], S[1][0]);
+    float top = max_nan(S[0][0], S[1][0]);
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, fmaxf(S[0][i], S[1][i]));
-    top = max_halves(top);
+    for (int i = 1; i < 16; ++i) top = max_nan(max_nan(top, S[0][i]), S[1][i]);
     // a new reference only once the maximum has grown by 2^8: weights up to
     // 256 are as exact as weights up to 1
     if (__any(top * sc > (m == -__FLT_MAX__ ? -__builtin_inff() : mref + 8.f))) {
       const float old = mref;
       const bool first = m == -__FLT_MAX__;
-      m = fmaxf(m, top);
+      m = fmaxf(m, max_halves(top));
       mref = m == -__FLT_MAX__ ? 0.f : m * sc;
       far_any = __any(fabsf(mref) > 16777216.f);
       const float alpha = first ? 0.f : __builtin_amdgcn_exp2f(old - mref);
@@ -262,64 +281,61 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             p[e] = __builtin_amdgcn_exp2f(far ? (S[kb][i + e] - m) * sc : fmaf(S[kb][i + e], sc, -mref));
-            l += p[e];
           }
-          pf[2 * kb + (i >> 3)][(i & 7) >> 1] = pk_bf16(p[0], p[1]);
+          const uint32_t pp = pk_bf16(p[0], p[1]);
+          l = add_bf16(pp, l);
+          pf[2 * kb + (i >> 3)][(i & 7) >> 1] = pp;
         }
     };
     if (__builtin_expect(far_any, 0)) weights(std::integral_constant<bool, true>());
     else weights(std::integral_constant<bool, false>());
     u4 vf[2][NB];
-    auto load_v = [&](int t) {
+    auto load_v = [&](int n) {
 #pragma unroll
       for (int db = 0; db < NB; ++db) {
-        const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(lds_t *)(uintptr_t)(((base + va[0]) ^ (db << 6)) + t * 16 * ROW));
-        const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(lds_t *)(uintptr_t)(((base + va[1]) ^ (db << 6)) + t * 16 * ROW));
+        const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(lds_t *)(uintptr_t)(((base + va[0]) ^ (db << 6)) + n * 16 * ROW));
+        const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(lds_t *)(uintptr_t)(((base + va[1]) ^ (db << 6)) + n * 16 * ROW));
         const u2 xx = __builtin_bit_cast(u2, x), yy = __builtin_bit_cast(u2, y);
-        vf[t & 1][db] = (u4){xx[0], xx[1], yy[0], yy[1]};
+        vf[n & 1][db] = (u4){xx[0], xx[1], yy[0], yy[1]};
       }
     };
-    __builtin_amdgcn_sched_barrier(0);
-    load_v(0);
+    // P^T is zero for a hidden key, but zero times infinity is not: where some
+    // row does not see all keys, the product takes values that are not finite
+    // as zero, and the rows that do see them get them at the end
+    bool odd = false;
+    if (partial) {
+      uint32_t mag = 0;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      if (t + 1 < 4) load_v(t + 1);
-      u4 (&vt)[NB] = vf[t & 1];
-      if constexpr (partial) {
-        // P^T is zero for a hidden key, but zero times infinity is not: the
-        // product takes values that are not finite as zero, and the rows that
-        // do see them get them at the end
-        uint32_t top_mag = 0;
+      for (int i = 0; i < SIDE / 1024; ++i) {
+        const u4 x = *(const lds_u4 *)(lds_t *)(uintptr_t)(base + SIDE + i * 1024 + lane * 16);
 #pragma unroll
-        for (int db = 0; db < NB; ++db)
+        for (int w = 0; w < 4; ++w) mag = pk_max_mag(mag, x[w]);
+      }
+      odd = __any((mag & 0xFFFF) >= 0x7F80 || mag >= 0x7F800000u);
+      dirty |= odd;
+    }
+    auto values = [&](auto mend) {
+      load_v(0);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) top_mag = pk_max_mag(top_mag, vt[db][w]);
-        if (__builtin_expect(__any((top_mag & 0xFFFF) >= 0x7F80 || top_mag >= 0x7F800000u), 0)) {
-          dirty = true;
+      for (int n = 0; n < 4; ++n) {
+        if (n + 1 < 4) load_v(n + 1);
 #pragma unroll
-          for (int db = 0; db < NB; ++db)
+        for (int db = 0; db < NB; ++db) {
+          u4 x = vf[n & 1][db];
+          if constexpr (mend) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) vt[db][w] = finite_or_zero(vt[db][w]);
+            for (int w = 0; w < 4; ++w) x[w] = finite_or_zero(x[w]);
+          }
+          O[db] = mfma_bf16(x, pf[n], O[db]);
+        }
+        if constexpr (!mend) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 2 * NB, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);
         }
       }
-#pragma unroll
-      for (int db = 0; db < NB; ++db) O[db] = mfma_bf16(vt[db], pf[t], O[db]);
-      __builtin_amdgcn_sched_group_barrier(0x100, 2 * NB, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);
-    }
-  };
-
-  if (t0 < t1) stage(t0, 0);
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) & 1;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();  // the tile is there, and nobody reads the other buffer
-    if (t + 1 < t1) stage(t + 1, buf ^ 1);
-    const int k0 = t * KT;
-    if (!mine || k0 >= w_hi1 || k0 + KT <= w_lo0) continue;
-    const uint32_t base = lds0 + buf * 2 * SIDE;
-    if (k0 >= w_lo1 && k0 + KT <= w_hi0) work(base, k0, std::integral_constant<bool, false>());
-    else work(base, k0, std::integral_constant<bool, true>());
+    };
+    if (__builtin_expect(odd, 0)) values(std::integral_constant<bool, true>());
+    else values(std::integral_constant<bool, false>());
   }
   if (!mine || wr + col >= rows) return;
   if (dirty)
