@@ -146,11 +146,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     return a.window > 0 ? max(0, p - a.window + 1) : 0;
   };
   const int r_end = min(r0 + BM, rows) - 1;
-  const int t0 = lo_of(r0) / KT, t1 = (hi_of(r_end) + KT - 1) / KT;
+  const int t0 = lo_of(r0) / KT, t1 = (hi_of(r_end) + KT - 1) / KT, b_lo1 = lo_of(r_end), b_hi0 = hi_of(r0);
   const int wr = r0 + 32 * wv;
   const bool mine = wr < rows;  // the wave has rows
   const int w_first = min(wr, rows - 1), w_last = min(wr + 31, rows - 1);
-  const int w_lo0 = lo_of(w_first), w_lo1 = lo_of(w_last), w_hi0 = hi_of(w_first), w_hi1 = hi_of(w_last);
+  const int w_lo1 = lo_of(w_last), w_hi0 = hi_of(w_first);
   const int r = min(wr + col, rows - 1);
   const int lo = lo_of(r), hi = hi_of(r);
   const int64_t row_off = (int64_t)(T.q_at + r / G);
@@ -184,28 +184,28 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     const int key = (i * NW + wv) * KEYS + lane / CH;
     chunk[i] = ((lane % CH) ^ swizzle<D>(key)) * 16;
   }
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_t *)smem;
-  auto stage = [&](int t, int buf) {
-    const uint8_t *kt = kg + (int64_t)t * KT * ldk, *vt = vg + (int64_t)t * KT * ldv;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_t *)smem;  // K of even and odd tiles, V of even and odd tiles
+  auto stage = [&](const uint8_t *from, uint32_t ld, int t, uint32_t dst) {
+    const uint8_t *at = from + (int64_t)t * KT * ld;
     const int last = T.keys - 1 - t * KT;  // keys past the last are copies of it
-    const uint32_t dst = lds0 + buf * 2 * SIDE + wv * 1024;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const uint32_t key = min((i * NW + wv) * KEYS + lane / CH, last);
-      copy_to_lds(kt, key * ldk + chunk[i % KINDS], dst + i * NW * 1024);
-      copy_to_lds(vt, key * ldv + chunk[i % KINDS], dst + i * NW * 1024 + SIDE);
+      copy_to_lds(at, key * ld + chunk[i % KINDS], dst + (i * NW + wv) * 1024);
     }
   };
+  auto stage_k = [&](int t) { stage(kg, ldk, t, lds0 + (t & 1) * SIDE); };
+  auto stage_v = [&](int t) { stage(vg, ldv, t, lds0 + (2 + (t & 1)) * SIDE); };
 
   // fragment addresses, a chunk's place an exclusive or: K chunk 2s + h of key
   // col (32 kb more: 32 rows on); V^T keys 8jj + 4h + r4 (16t more: 16 rows
   // on), channels 32db + 16g + 4c
-  const uint32_t ka = col * ROW + ((h ^ swizzle<D>(col)) << 4);
+  const uint32_t ka = lds0 + col * ROW + ((h ^ swizzle<D>(col)) << 4);
   uint32_t va[2];
 #pragma unroll
   for (int jj = 0; jj < 2; ++jj) {
     const int g = lane >> 4 & 1, c = lane & 3, key = 8 * jj + 4 * h + (lane >> 2 & 3);
-    va[jj] = SIDE + key * ROW + (((2 * g + (c >> 1)) ^ swizzle<D>(key)) << 4) + 8 * (c & 1);
+    va[jj] = lds0 + 2 * SIDE + key * ROW + (((2 * g + (c >> 1)) ^ swizzle<D>(key)) << 4) + 8 * (c & 1);
   }
 
   f16x O[NB];
@@ -214,35 +214,47 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   float m = -__FLT_MAX__, mref = 0.f, l = 0.f;
   bool dirty = false, far_any = false;
 
-  if (t0 < t1) stage(t0, 0);
-#pragma unroll 1
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) & 1;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();  // the tile is there, and nobody reads the other buffer
-    if (t + 1 < t1) stage(t + 1, buf ^ 1);
-    const int k0 = t * KT;
-    if (!mine || k0 >= w_hi1 || k0 + KT <= w_lo0) continue;
-    const bool partial = k0 < w_lo1 || k0 + KT > w_hi0;  // some row does not see all of it
-    const uint32_t base = lds0 + buf * 2 * SIDE;
+  u4 kf[2][2];
+  auto load_k = [&](int t, int s) {
+    const uint32_t at = (ka + (t & 1) * SIDE) ^ (s << 5);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) kf[s & 1][kb] = *(const lds_u4 *)(lds_t *)(uintptr_t)(at + kb * 32 * ROW);
+  };
 
-    f16x S[2] = {(f16x){}, (f16x){}};
-    u4 kf[2][2];
-    auto load_k = [&](int s) {
+  // One tile: S holds its scores and N takes the next tile's.
+  auto step = [&](int t, f16x (&S)[2], f16x (&N)[2]) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();  // V of t and K of t + 1 are there; nobody reads V of t - 1 and K of t
+    if (t + 2 < t1) stage_k(t + 2);
+    if (t + 1 < t1) stage_v(t + 1);
+    const int k0 = t * KT;
+    if (k0 < b_lo1 || k0 + KT > b_hi0) {
+      // Some row of the block does not see all keys.  P^T is zero for a hidden
+      // key, but zero times infinity is not: values that are not finite become
+      // zero here, and the rows that do see them get them at the end.
+      uint32_t mag = 0;
+      const uint32_t at = lds0 + (2 + (t & 1)) * SIDE + lane * 16;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) kf[s & 1][kb] = *(const lds_u4 *)(lds_t *)(uintptr_t)(((base + ka) ^ (s << 5)) + kb * 32 * ROW);
-    };
-    load_k(0);
+      for (int i = 0; i < SIDE / 1024; ++i) {
+        const u4 x = *(const lds_u4 *)(lds_t *)(uintptr_t)(at + i * 1024);
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      if (s + 1 < NS) load_k(s + 1);
+        for (int w = 0; w < 4; ++w) mag = pk_max_mag(mag, x[w]);
+      }
+      if (__builtin_expect(__any((mag & 0xFFFF) >= 0x7F80 || mag >= 0x7F800000u), 0)) {  // the same in every wave
+        dirty = true;
+        __syncthreads();
+        for (int i = wv; i < SIDE / 1024; i += NW) {
+          lds_u4 *x = (lds_u4 *)(lds_t *)(uintptr_t)(at + i * 1024);
+          u4 v = *x;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) S[kb] = mfma_bf16(kf[s & 1][kb], qf[s], S[kb]);
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // DS reads
-      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // MFMA
+          for (int w = 0; w < 4; ++w) v[w] = finite_or_zero(v[w]);
+          *x = v;
+        }
+        __syncthreads();
+      }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    if (partial) {
+    if (!mine) return;
+    if (k0 < w_lo1 || k0 + KT > w_hi0) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -269,79 +281,85 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
 #pragma unroll
         for (int i = 0; i < 16; ++i) O[db][i] *= alpha;
     }
-    u4 pf[4];
-    // A reference beyond 2^24 is rounded by more than one: there the scores'
-    // differences are formed before the scale
-    auto weights = [&](auto far) {
+    float less = mref;
+    if (__builtin_expect(far_any, 0)) {
+      // a reference beyond 2^24 is rounded by more than one: the scores'
+      // differences are formed before the scale
+      less = 0.f;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          float p[2];
+        for (int i = 0; i < 16; ++i) S[kb][i] -= m;
+    }
+    // the weights, between the next tile's score products
+    u4 pf[4];
+    constexpr int EACH = 32 / NS;  // scores a step
+    load_k(t + 1, 0);
+    N[0] = N[1] = (f16x){};
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(far ? (S[kb][i + e] - m) * sc : fmaf(S[kb][i + e], sc, -mref));
-          }
-          const uint32_t pp = pk_bf16(p[0], p[1]);
-          l = add_bf16(pp, l);
-          pf[2 * kb + (i >> 3)][(i & 7) >> 1] = pp;
-        }
-    };
-    if (__builtin_expect(far_any, 0)) weights(std::integral_constant<bool, true>());
-    else weights(std::integral_constant<bool, false>());
+    for (int s = 0; s < NS; ++s) {
+      if (s + 1 < NS) load_k(t + 1, s + 1);
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) N[kb] = mfma_bf16(kf[s & 1][kb], qf[s], N[kb]);
+#pragma unroll
+      for (int e = 0; e < EACH; e += 2) {
+        const int at = EACH * s + e, kb = at >> 4, i = at & 15;
+        const uint32_t p = pk_bf16(__builtin_amdgcn_exp2f(fmaf(S[kb][i], sc, -less)),
+                                   __builtin_amdgcn_exp2f(fmaf(S[kb][i + 1], sc, -less)));
+        l = add_bf16(p, l);
+        pf[at >> 3][(at & 7) >> 1] = p;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
     u4 vf[2][NB];
     auto load_v = [&](int n) {
 #pragma unroll
       for (int db = 0; db < NB; ++db) {
-        const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(lds_t *)(uintptr_t)(((base + va[0]) ^ (db << 6)) + n * 16 * ROW));
-        const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(lds_t *)(uintptr_t)(((base + va[1]) ^ (db << 6)) + n * 16 * ROW));
-        const u2 xx = __builtin_bit_cast(u2, x), yy = __builtin_bit_cast(u2, y);
-        vf[n & 1][db] = (u4){xx[0], xx[1], yy[0], yy[1]};
+        u2 x[2];
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const uint32_t at = ((va[jj] + (t & 1) * SIDE) ^ (db << 6)) + n * 16 * ROW;
+          x[jj] = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(lds_t *)(uintptr_t)at));
+        }
+        vf[n & 1][db] = (u4){x[0][0], x[0][1], x[1][0], x[1][1]};
       }
     };
-    // P^T is zero for a hidden key, but zero times infinity is not: where some
-    // row does not see all keys, the product takes values that are not finite
-    // as zero, and the rows that do see them get them at the end
-    bool odd = false;
-    if (partial) {
-      uint32_t mag = 0;
+    load_v(0);
 #pragma unroll
-      for (int i = 0; i < SIDE / 1024; ++i) {
-        const u4 x = *(const lds_u4 *)(lds_t *)(uintptr_t)(base + SIDE + i * 1024 + lane * 16);
+    for (int n = 0; n < 4; ++n) {
+      if (n + 1 < 4) load_v(n + 1);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) mag = pk_max_mag(mag, x[w]);
-      }
-      odd = __any((mag & 0xFFFF) >= 0x7F80 || mag >= 0x7F800000u);
-      dirty |= odd;
+      for (int db = 0; db < NB; ++db) O[db] = mfma_bf16(vf[n & 1][db], pf[n], O[db]);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * NB, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);
     }
-    auto values = [&](auto mend) {
-      load_v(0);
+  };
+
+  if (t0 < t1) {
+    stage_k(t0);
+    stage_v(t0);
+    if (t0 + 1 < t1) stage_k(t0 + 1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    f16x A[2] = {(f16x){}, (f16x){}}, B[2];
+    load_k(t0, 0);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        if (n + 1 < 4) load_v(n + 1);
+    for (int s = 0; s < NS; ++s) {
+      if (s + 1 < NS) load_k(t0, s + 1);
 #pragma unroll
-        for (int db = 0; db < NB; ++db) {
-          u4 x = vf[n & 1][db];
-          if constexpr (mend) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) x[w] = finite_or_zero(x[w]);
-          }
-          O[db] = mfma_bf16(x, pf[n], O[db]);
-        }
-        if constexpr (!mend) {
-          __builtin_amdgcn_sched_group_barrier(0x100, 2 * NB, 0);
-          __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);
-        }
-      }
-    };
-    if (__builtin_expect(odd, 0)) values(std::integral_constant<bool, true>());
-    else values(std::integral_constant<bool, false>());
+      for (int kb = 0; kb < 2; ++kb) A[kb] = mfma_bf16(kf[s & 1][kb], qf[s], A[kb]);
+    }
+#pragma unroll 1
+    for (int t = t0; t < t1; t += 2) {
+      step(t, A, B);
+      if (t + 1 < t1) step(t + 1, B, A);
+    }
   }
   if (!mine || wr + col >= rows) return;
   if (dirty)
     for (int t = t0; t < t1; ++t) {
       const int k0 = t * KT;
-      if (k0 >= w_hi1 || k0 + KT <= w_lo0 || (k0 >= w_lo1 && k0 + KT <= w_hi0)) continue;
+      if (k0 >= b_lo1 && k0 + KT <= b_hi0) continue;
       for (int key = max(k0, lo); key < min(k0 + KT, hi); ++key) {
         const uint16_t *v = (const uint16_t *)(vg + (int64_t)key * ldv) + 4 * h;
 #pragma unroll
