@@ -291,26 +291,41 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
 #pragma unroll
         for (int i = 0; i < 16; ++i) S[kb][i] -= m;
     }
-    // the weights, between the next tile's score products
+    // The weights, between the next tile's score products: one product, then
+    // the exponentials of EACH scores and the rounding of the EACH before them,
+    // which keeps the vector unit busy for as long as the product runs.
     u4 pf[4];
-    constexpr int EACH = 32 / NS;  // scores a step
-    load_k(t + 1, 0);
-    N[0] = N[1] = (f16x){};
+    constexpr int EACH = NS < 8 ? 4 : 2, EVERY = NS > 8 ? 2 : 1;  // scores; after every product or every second one
+    float x[EACH], y[EACH];
+    auto exps = [&](int n) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      if (s + 1 < NS) load_k(t + 1, s + 1);
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) N[kb] = mfma_bf16(kf[s & 1][kb], qf[s], N[kb]);
+      for (int e = 0; e < EACH; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(S[(EACH * n + e) >> 4][(EACH * n + e) & 15], sc, -less));
+    };
+    auto round = [&](int n) {
 #pragma unroll
       for (int e = 0; e < EACH; e += 2) {
-        const int at = EACH * s + e, kb = at >> 4, i = at & 15;
-        const uint32_t p = pk_bf16(__builtin_amdgcn_exp2f(fmaf(S[kb][i], sc, -less)),
-                                   __builtin_amdgcn_exp2f(fmaf(S[kb][i + 1], sc, -less)));
+        const int at = EACH * n + e;
+        const uint32_t p = pk_bf16(y[e], y[e + 1]);
         l = add_bf16(p, l);
         pf[at >> 3][(at & 7) >> 1] = p;
       }
+    };
+    load_k(t + 1, 0);
+    N[0] = N[1] = (f16x){};
+#pragma unroll
+    for (int n = 0; n < 2 * NS; ++n) {
+      const int s = n >> 1, kb = n & 1;
+      if (kb == 0 && s + 1 < NS) load_k(t + 1, s + 1);
+      N[kb] = mfma_bf16(kf[s & 1][kb], qf[s], N[kb]);
+      if (n % EVERY == 0) {
+        exps(n / EVERY);
+        if (n > 0) round(n / EVERY - 1);
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) y[e] = x[e];
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
+    round(32 / EACH - 1);
     u4 vf[2][NB];
     auto load_v = [&](int n) {
 #pragma unroll
