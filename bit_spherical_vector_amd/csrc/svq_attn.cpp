@@ -11,7 +11,7 @@ using namespace svq;
 
 namespace {
 
-constexpr int64_t MAX_TOKENS = 1 << 24, MAX_SEQUENCES = 65535;
+constexpr int64_t MAX_TOKENS = 1 << 24, MAX_LD = 1 << 24, MAX_SEQUENCES = 65535;
 constexpr int MAX_HEADS = 1024, MAX_Q_HEADS = 16384, MAX_SHARED = 64, MAX_Q_LEN = 1024;
 
 bool bad_workspace(const void *ws) { return ((uintptr_t)ws & 15) != 0; }
@@ -128,6 +128,9 @@ svq_status svq_attn_prompt(const void *q, int64_t ldq, const void *k, int64_t ld
   if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal)) return SVQ_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return SVQ_ERR_INVALID_ARG;
   if (!on_16(q, ldq, 2) || !on_16(k, ldk, 2) || !on_16(v, ldv, 2) || !on_16(y, ldy, 2)) return SVQ_ERR_UNSUPPORTED;
+  if (ldk > MAX_LD || ldv > MAX_LD) return SVQ_ERR_UNSUPPORTED;  // bytes within a tile of 64 keys are 32-bit
+  // a grid of at most 2^23 blocks
+  if (tokens * q_heads > (int64_t)1 << 29 || sequences * kv_heads > 1 << 21) return SVQ_ERR_UNSUPPORTED;
   const size_t need = 256;  // unused
   if (!workspace) {
     *workspace_bytes = need;

@@ -30,12 +30,22 @@ typedef short s4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s4v lds_s4v;
 typedef __attribute__((address_space(3))) u4 lds_u4;
 
-// 16 bytes a lane from base + off to LDS bytes dst + 16 * lane, waited for by
-// vmcnt.  (The builtin makes every LDS read behind it wait for the copy.)  The
-// wait states stand between the scalar values' writers and their use as M0 and
-// as a base: the compiler does not look into the block.
-__device__ __forceinline__ void copy_to_lds(const uint8_t *base, uint32_t off, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(off), "s"(base) : "memory", "m0");
+// A buffer of `bytes` bytes: reads beyond give zeros.  The compiler does not
+// look into the copies below, so the wait states between the vector unit's
+// writes of these scalars and their first use there stand here (and between
+// M0 and its use, there); nothing but scalar instructions touches them after.
+__device__ __forceinline__ u4 buffer_of(const uint8_t *base, uint32_t bytes) {
+  const uint64_t at = (uint64_t)base;
+  u4 b = {(uint32_t)__builtin_amdgcn_readfirstlane((int)at), (uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32) & 0xFFFF),
+          (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+  asm volatile("s_nop 4" : "+s"(b));
+  return b;
+}
+// 16 bytes a lane from byte off + first of the buffer to LDS bytes dst + 16 *
+// lane, waited for by vmcnt.  (The builtin makes every LDS read behind it wait
+// for the copy.)
+__device__ __forceinline__ void copy_to_lds(const u4 &buffer, uint32_t off, uint32_t first, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(dst), "v"(off), "s"(buffer), "s"(first) : "memory", "m0");
 }
 
 // Rows of a staged tile are D bf16 values, 16-byte chunk c at place
@@ -178,24 +188,26 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   const uint8_t *vg = (const uint8_t *)(a.v + (int64_t)T.k_at * a.ldv + kvh * D);
   constexpr int PER = SIDE / 1024 / NW, KEYS = 1024 / ROW, KINDS = D == 256 && NW == 4 ? 2 : 1;
   const uint32_t ldk = (uint32_t)a.ldk * 2, ldv = (uint32_t)a.ldv * 2;
-  uint32_t chunk[KINDS];
+  uint32_t off_k[KINDS], off_v[KINDS];
 #pragma unroll
   for (int i = 0; i < KINDS; ++i) {
-    const int key = (i * NW + wv) * KEYS + lane / CH;
-    chunk[i] = ((lane % CH) ^ swizzle<D>(key)) * 16;
+    const int key = (i * NW + wv) * KEYS + lane / CH, chunk = ((lane % CH) ^ swizzle<D>(key)) * 16;
+    off_k[i] = key * ldk + chunk;
+    off_v[i] = key * ldv + chunk;
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_t *)smem;  // K of even and odd tiles, V of even and odd tiles
-  auto stage = [&](const uint8_t *from, uint32_t ld, int t, uint32_t dst) {
-    const uint8_t *at = from + (int64_t)t * KT * ld;
-    const int last = T.keys - 1 - t * KT;  // keys past the last are copies of it
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const uint32_t key = min((i * NW + wv) * KEYS + lane / CH, last);
-      copy_to_lds(at, key * ld + chunk[i % KINDS], dst + (i * NW + wv) * 1024);
-    }
+  // tile t of the keys (values) as a buffer that ends with the sequence: rows
+  // behind it become zeros, a tile behind it is not read
+  auto tile_of = [&](const uint8_t *from, uint32_t ld, int t) {
+    const int left = min(max(T.keys - t * KT, 0), KT);
+    return buffer_of(from + (int64_t)t * KT * ld, left > 0 ? (left - 1) * ld + ROW : 0);
   };
-  auto stage_k = [&](int t) { stage(kg, ldk, t, lds0 + (t & 1) * SIDE); };
-  auto stage_v = [&](int t) { stage(vg, ldv, t, lds0 + (2 + (t & 1)) * SIDE); };
+  auto copy_k = [&](const u4 &buffer, int t, int i) {
+    copy_to_lds(buffer, off_k[i % KINDS], i / KINDS * KINDS * NW * KEYS * ldk, lds0 + (t & 1) * SIDE + (i * NW + wv) * 1024);
+  };
+  auto copy_v = [&](const u4 &buffer, int t, int i) {
+    copy_to_lds(buffer, off_v[i % KINDS], i / KINDS * KINDS * NW * KEYS * ldv, lds0 + (2 + (t & 1)) * SIDE + (i * NW + wv) * 1024);
+  };
 
   // fragment addresses, a chunk's place an exclusive or: K chunk 2s + h of key
   // col (32 kb more: 32 rows on); V^T keys 8jj + 4h + r4 (16t more: 16 rows
@@ -222,11 +234,16 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   };
 
   // One tile: S holds its scores and N takes the next tile's.
+  float top = 0.f;
+  auto maximum = [&](const f16x (&S)[2]) {
+    top = max_nan(S[0][0], S[1][0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = max_nan(max_nan(top, S[0][i]), S[1][i]);
+  };
   auto step = [&](int t, f16x (&S)[2], f16x (&N)[2]) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();  // V of t and K of t + 1 are there; nobody reads V of t - 1 and K of t
-    if (t + 2 < t1) stage_k(t + 2);
-    if (t + 1 < t1) stage_v(t + 1);
+    const u4 next_k = tile_of(kg, ldk, t + 2), next_v = tile_of(vg, ldv, t + 1);
     const int k0 = t * KT;
     if (k0 < b_lo1 || k0 + KT > b_hi0) {
       // Some row of the block does not see all keys.  P^T is zero for a hidden
@@ -253,7 +270,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
         __syncthreads();
       }
     }
-    if (!mine) return;
+    if (!mine) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        copy_k(next_k, t, i);
+        copy_v(next_v, t + 1, i);
+      }
+      return;
+    }
     if (k0 < w_lo1 || k0 + KT > w_hi0) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -262,10 +286,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
           const int key = k0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3);
           S[kb][i] = key >= lo && key < hi ? S[kb][i] : -__builtin_inff();
         }
+      maximum(S);
     }
-    float top = max_nan(S[0][0], S[1][0]);
-#pragma unroll
-    for (int i = 1; i < 16; ++i) top = max_nan(max_nan(top, S[0][i]), S[1][i]);
     // a new reference only once the maximum has grown by 2^8: weights up to
     // 256 are as exact as weights up to 1
     if (__any(top * sc > (m == -__FLT_MAX__ ? -__builtin_inff() : mref + 8.f))) {
@@ -317,6 +339,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       const int s = n >> 1, kb = n & 1;
       if (kb == 0 && s + 1 < NS) load_k(t + 1, s + 1);
       N[kb] = mfma_bf16(kf[s & 1][kb], qf[s], N[kb]);
+      // copies one by one: all at once they hold the wave until the last is taken
+      if (n % 4 == 0 && n / 4 < PER) copy_k(next_k, t, n / 4);
+      if (n % 4 == 2 && n / 4 < PER) copy_v(next_v, t + 1, n / 4);
       if (n % EVERY == 0) {
         exps(n / EVERY);
         if (n > 0) round(n / EVERY - 1);
@@ -345,15 +370,24 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       if (n + 1 < 4) load_v(n + 1);
 #pragma unroll
       for (int db = 0; db < NB; ++db) O[db] = mfma_bf16(vf[n & 1][db], pf[n], O[db]);
-      __builtin_amdgcn_sched_group_barrier(0x100, 2 * NB, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, NB, 0);
+      // the next tile's maximum, a third at a time
+      if (n == 1) top = max_nan(N[0][0], N[1][0]);
+      if (n > 0) {
+#pragma unroll
+        for (int i = 5 * n - 4; i <= 5 * n; ++i) top = max_nan(max_nan(top, N[0][i]), N[1][i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
   if (t0 < t1) {
-    stage_k(t0);
-    stage_v(t0);
-    if (t0 + 1 < t1) stage_k(t0 + 1);
+    const u4 first_k = tile_of(kg, ldk, t0), first_v = tile_of(vg, ldv, t0), second_k = tile_of(kg, ldk, t0 + 1);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      copy_k(first_k, t0, i);
+      copy_k(second_k, t0 + 1, i);
+      copy_v(first_v, t0, i);
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     f16x A[2] = {(f16x){}, (f16x){}}, B[2];
@@ -364,12 +398,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) A[kb] = mfma_bf16(kf[s & 1][kb], qf[s], A[kb]);
     }
+    maximum(A);
 #pragma unroll 1
     for (int t = t0; t < t1; t += 2) {
       step(t, A, B);
       if (t + 1 < t1) step(t + 1, B, A);
     }
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives the block
   if (!mine || wr + col >= rows) return;
   if (dirty)
     for (int t = t0; t < t1; ++t) {

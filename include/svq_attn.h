@@ -53,7 +53,9 @@ extern "C" {
  *             [0, tokens] and [0, tokens_k] (values beyond are taken as the
  *             nearest that is not).  Rows of y before starts[0] and from
  *             starts[sequences] on are left as they were.
- *   tokens, tokens_k: 1 .. 2^24; sequences: 1 .. 65535; scale: finite. */
+ *   tokens, tokens_k: 1 .. 2^24; sequences: 1 .. 65535; scale: finite.
+ * SVQ_ERR_UNSUPPORTED: ldk or ldv beyond 2^24, tokens * q_heads beyond 2^29,
+ * sequences * kv_heads beyond 2^21. */
 svq_status svq_attn_prompt(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                            int32_t q_heads, int32_t kv_heads, int32_t head_dim, const int32_t *starts,
                            const int32_t *starts_k, int64_t sequences, int64_t tokens, int64_t tokens_k,

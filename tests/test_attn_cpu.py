@@ -67,6 +67,9 @@ def _cache(ws=None, nbytes=0, desc=None, **over):
     (dict(tokens=0), BAD), (dict(tokens=(1 << 24) + 1), BAD), (dict(tokens_k=0), BAD),
     (dict(tokens_k=(1 << 24) + 1), BAD), (dict(sequences=0), BAD), (dict(sequences=65536), BAD),
     (dict(ldq=504), BAD), (dict(ldk=248), BAD), (dict(ldv=248), BAD), (dict(ldy=504), BAD),
+    (dict(ldk=(1 << 24) + 8), UNSUPPORTED), (dict(ldv=(1 << 24) + 8), UNSUPPORTED),
+    (dict(tokens=1 << 24, q_heads=34, ldq=34 * 128, ldy=34 * 128), UNSUPPORTED),
+    (dict(sequences=65535, q_heads=34, kv_heads=34, ldq=34 * 128, ldk=34 * 128, ldv=34 * 128, ldy=34 * 128), UNSUPPORTED),
     (dict(causal=2), BAD), (dict(causal=0, window=4), BAD), (dict(window=-1), BAD),
     (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD),
     (dict(q=FAKE + 2), UNSUPPORTED), (dict(k=FAKE + 8), UNSUPPORTED), (dict(v=FAKE + 4), UNSUPPORTED),
