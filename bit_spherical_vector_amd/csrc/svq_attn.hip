@@ -1,9 +1,9 @@
 // Attention over whole prompts (include/svq_attn.h).
 //
-// One pass over the keys with a running maximum and sum.  A block takes BM
-// rows of one key head, row r being query head r % G of the group's G and
-// token r / G of its sequence, so the heads that share keys share their reads
-// and a block's rows span few positions under a causal mask.  A wave owns 32
+// One pass over the keys with a running maximum and sum.  A block takes a tile
+// of tokens of one key head, row r being query head r % G of the G that share
+// it and token r / G of the tile, so the heads that share keys share their
+// reads and a block's rows span few positions under a causal mask.  A wave owns 32
 // rows and forms everything transposed:
 //
 //   S^T = K Q^T     32 keys x 32 rows (v_mfma_f32_32x32x16_bf16, A = keys)
@@ -24,6 +24,14 @@ namespace svq {
 namespace {
 
 constexpr int KT = 64;  // keys of a tile
+
+// A tile of rows: `tokens` tokens of a sequence, each with the G query heads
+// that share the key head.
+struct PromptPlan {
+  int32_t tiles, half;               // see attn_prompt_kernel
+  int32_t tokens, G;                 // tokens = 32 * waves / G
+  uint32_t tokens_mul, g_mul;        // quotient, quotient16
+};
 
 typedef __attribute__((address_space(3))) uint8_t lds_t;
 typedef short s4v __attribute__((ext_vector_type(4)));
@@ -89,23 +97,33 @@ __device__ __forceinline__ f16x mfma_bf16(const u4 &a, const u4 &b, const f16x &
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
 }
 
-// The sequence and tile of block `u` of the row tiles of all sequences in
-// order; false beyond the last.  Every wave looks for itself, 64 sequences at
-// a time.
+// Divisions by launch constants, exact where n * divisor < 2^32 (2^16).
+__device__ __forceinline__ int quotient(int n, uint32_t mul) { return (int)__umulhi((uint32_t)n, mul); }
+__device__ __forceinline__ int quotient16(int n, uint32_t mul) { return (int)((uint32_t)n * mul >> 16); }
+
+// The sequence and tile of number `u` of the tiles of all sequences in order;
+// false beyond the last.  Every wave looks for itself, 64 sequences at a time,
+// in one trip to memory.
 struct TileOf {
   int q_at, n, k_at, keys, tile;
 };
-__device__ __forceinline__ bool find_tile(const AttnPromptArgs &a, int rows_shift, int G, int u, TileOf &o) {
+__device__ __forceinline__ bool find_tile(const AttnPromptArgs &a, const PromptPlan &plan, int u, TileOf &o) {
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int s0 = 0; s0 < a.sequences; s0 += 64) {
     const int s = s0 + lane;
-    int b = 0, e = 0;
+    int b = 0, e = 0, kb = 0, ke = 0;
     if (s < a.sequences) {
-      b = min(max(a.starts[s], 0), a.tokens);
-      e = min(max(a.starts[s + 1], b), a.tokens);
+      b = a.starts[s];
+      e = a.starts[s + 1];
+      kb = a.starts_k[s];
+      ke = a.starts_k[s + 1];
     }
-    const int tiles = ((e - b) * G + (1 << rows_shift) - 1) >> rows_shift;
+    b = min(max(b, 0), a.tokens);
+    e = min(max(e, b), a.tokens);
+    kb = min(max(kb, 0), a.tokens_k);
+    ke = min(max(ke, kb), a.tokens_k);
+    const int tiles = quotient(e - b + plan.tokens - 1, plan.tokens_mul);
     int sum = tiles;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -118,8 +136,8 @@ __device__ __forceinline__ bool find_tile(const AttnPromptArgs &a, int rows_shif
       o.q_at = __builtin_amdgcn_readlane(b, at);
       o.n = __builtin_amdgcn_readlane(e, at) - o.q_at;
       o.tile = u - before - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(tiles, at));
-      o.k_at = min(max(a.starts_k[s0 + at], 0), a.tokens_k);
-      o.keys = min(max(a.starts_k[s0 + at + 1], o.k_at), a.tokens_k) - o.k_at;
+      o.k_at = __builtin_amdgcn_readlane(kb, at);
+      o.keys = __builtin_amdgcn_readlane(ke, at) - o.k_at;
       return true;
     }
     before += __builtin_amdgcn_readlane(sum, 63);
@@ -133,53 +151,36 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t x) {
 }
 
 template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(AttnPromptArgs a, int tiles) {
-  constexpr int BM = 32 * NW, ROWS_SHIFT = NW == 8 ? 8 : 7;
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(AttnPromptArgs a, PromptPlan plan) {
   constexpr int ROW = 2 * D, CH = D / 8, SIDE = KT * ROW;  // bytes of a row, its chunks, bytes of a tile
   constexpr int NB = D / 32, NS = D / 16;
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // K, V of two tiles
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // K and V of two tiles each, from LDS byte 0 on
+  int(*odd)[NW] = (int(*)[NW])(smem + 4 * SIDE);  // which waves have met values that are not finite
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, h = lane >> 5;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int kvh = blockIdx.x % a.kv_heads, G = a.heads / a.kv_heads;
-  // the last tiles first: under a causal mask they have the most keys
+  const int kvh = blockIdx.x, G = plan.G;
+  // The last tiles first: under a causal mask they have the most keys.  With
+  // `half`, one round of blocks, two a compute unit, covers all: there the
+  // second on each takes the tiles from the front on, which leaves every unit
+  // the same number of keys (2048 tokens 51 -> 47 us).
   TileOf T;
-  if (!find_tile(a, ROWS_SHIFT, G, tiles - 1 - (int)(blockIdx.x / a.kv_heads), T)) return;
-  const int rows = T.n * G, r0 = T.tile * BM;
+  const int turn = blockIdx.y;
+  if (!find_tile(a, plan, turn < plan.half ? plan.tiles - 1 - turn : turn - plan.half, T)) return;
+  const int t_first = T.tile * plan.tokens, rows = min(plan.tokens, T.n - t_first) * G;
+  const int shift = T.keys - T.n + t_first;  // position of the tile's first token
 
-  // what a row sees: keys [lo, hi)
-  auto hi_of = [&](int r) {
-    const int p = T.keys - T.n + r / G;
-    return a.causal ? min(max(p + 1, 0), T.keys) : T.keys;
-  };
-  auto lo_of = [&](int r) {
-    const int p = T.keys - T.n + r / G;
-    return a.window > 0 ? max(0, p - a.window + 1) : 0;
-  };
-  const int r_end = min(r0 + BM, rows) - 1;
-  const int t0 = lo_of(r0) / KT, t1 = (hi_of(r_end) + KT - 1) / KT, b_lo1 = lo_of(r_end), b_hi0 = hi_of(r0);
-  const int wr = r0 + 32 * wv;
-  const bool mine = wr < rows;  // the wave has rows
-  const int w_first = min(wr, rows - 1), w_last = min(wr + 31, rows - 1);
-  const int w_lo1 = lo_of(w_last), w_hi0 = hi_of(w_first);
-  const int r = min(wr + col, rows - 1);
-  const int lo = lo_of(r), hi = hi_of(r);
-  const int64_t row_off = (int64_t)(T.q_at + r / G);
-  const int head = kvh * G + r % G;
-
-  u4 qf[NS];
-  {
-    const uint16_t *q = a.q + row_off * a.ldq + head * D + 8 * h;
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      qf[s] = *(const u4 *)(q + 16 * s);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) qf[s][w] ^= flip;
-    }
-  }
-  // exponents are base 2; a scale of zero stays a number that keeps hidden
-  // scores at -infinity
-  const float sc = fmaxf(fabsf(a.scale) * 1.44269504088896f, 1e-38f);
+  // what a row sees, by its token: keys [lo, hi)
+  auto hi_of = [&](int token) { return a.causal ? min(max(shift + token + 1, 0), T.keys) : T.keys; };
+  auto lo_of = [&](int token) { return a.window > 0 ? max(0, shift + token + 1 - a.window) : 0; };
+  const int last = min(plan.tokens, T.n - t_first) - 1;
+  const int t0 = lo_of(0) / KT, t1 = (hi_of(last) + KT - 1) / KT, b_lo1 = lo_of(last), b_hi0 = hi_of(0);
+  const bool mine = 32 * wv < rows;  // the wave has rows
+  const int w_hi0 = hi_of(quotient16(min(32 * wv, rows - 1), plan.g_mul));
+  const int w_lo1 = lo_of(quotient16(min(32 * wv + 31, rows - 1), plan.g_mul));
+  const int r = min(32 * wv + col, rows - 1), token = quotient16(r, plan.g_mul);
+  const int lo = lo_of(token), hi = hi_of(token);
+  const int64_t row_off = (int64_t)(T.q_at + t_first + token);
+  const int head = kvh * G + r - token * G;
 
   // staging: pieces of 1 KB (1024 / ROW keys), piece i * NW + wv by wave wv; a
   // lane's place in a piece is the same for every i (i & 1 with 256 channels
@@ -220,6 +221,31 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     va[jj] = lds0 + 2 * SIDE + key * ROW + (((2 * g + (c >> 1)) ^ swizzle<D>(key)) << 4) + 8 * (c & 1);
   }
 
+  // the first tiles are on their way before the queries are asked for
+  const u4 first_k = tile_of(kg, ldk, t0), first_v = tile_of(vg, ldv, t0), second_k = tile_of(kg, ldk, t0 + 1);
+  if (t0 < t1) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      copy_k(first_k, t0, i);
+      copy_k(second_k, t0 + 1, i);
+      copy_v(first_v, t0, i);
+    }
+  }
+  u4 qf[NS];
+  {
+    const uint16_t *q = a.q + row_off * a.ldq + head * D + 8 * h;
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) qf[s] = *(const u4 *)(q + 16 * s);
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) qf[s][w] ^= flip;
+  }
+  // exponents are base 2; a scale of zero stays a number that keeps hidden
+  // scores at -infinity
+  const float sc = fmaxf(fabsf(a.scale) * 1.44269504088896f, 1e-38f);
+
   f16x O[NB];
 #pragma unroll
   for (int db = 0; db < NB; ++db) O[db] = (f16x){};
@@ -242,26 +268,33 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   };
   auto step = [&](int t, f16x (&S)[2], f16x (&N)[2]) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();  // V of t and K of t + 1 are there; nobody reads V of t - 1 and K of t
-    const u4 next_k = tile_of(kg, ldk, t + 2), next_v = tile_of(vg, ldv, t + 1);
     const int k0 = t * KT;
-    if (k0 < b_lo1 || k0 + KT > b_hi0) {
-      // Some row of the block does not see all keys.  P^T is zero for a hidden
-      // key, but zero times infinity is not: values that are not finite become
-      // zero here, and the rows that do see them get them at the end.
+    const bool edge = k0 < b_lo1 || k0 + KT > b_hi0;  // some row of the block does not see all keys
+    if (edge) {
+      // P^T is zero for a hidden key, but zero times infinity is not.  A wave
+      // looks at the values that it has copied itself.
       uint32_t mag = 0;
-      const uint32_t at = lds0 + (2 + (t & 1)) * SIDE + lane * 16;
+      const uint32_t at = lds0 + (2 + (t & 1)) * SIDE + wv * 1024 + lane * 16;
 #pragma unroll
-      for (int i = 0; i < SIDE / 1024; ++i) {
-        const u4 x = *(const lds_u4 *)(lds_t *)(uintptr_t)(at + i * 1024);
+      for (int i = 0; i < PER; ++i) {
+        const u4 x = *(const lds_u4 *)(lds_t *)(uintptr_t)(at + i * NW * 1024);
 #pragma unroll
         for (int w = 0; w < 4; ++w) mag = pk_max_mag(mag, x[w]);
       }
-      if (__builtin_expect(__any((mag & 0xFFFF) >= 0x7F80 || mag >= 0x7F800000u), 0)) {  // the same in every wave
+      odd[t & 1][wv] = __any((mag & 0xFFFF) >= 0x7F80 || mag >= 0x7F800000u);
+    }
+    __syncthreads();  // V of t and K of t + 1 are there; nobody reads V of t - 1 and K of t
+    const u4 next_k = tile_of(kg, ldk, t + 2), next_v = tile_of(vg, ldv, t + 1);
+    if (edge) {
+      int any = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) any |= odd[t & 1][w];
+      if (__builtin_expect(__builtin_amdgcn_readfirstlane(any), 0)) {
+        // values that are not finite become zero, and the rows that do see
+        // them get them at the end
         dirty = true;
-        __syncthreads();
         for (int i = wv; i < SIDE / 1024; i += NW) {
-          lds_u4 *x = (lds_u4 *)(lds_t *)(uintptr_t)(at + i * 1024);
+          lds_u4 *x = (lds_u4 *)(lds_t *)(uintptr_t)(lds0 + (2 + (t & 1)) * SIDE + i * 1024 + lane * 16);
           u4 v = *x;
 #pragma unroll
           for (int w = 0; w < 4; ++w) v[w] = finite_or_zero(v[w]);
@@ -279,13 +312,20 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       return;
     }
     if (k0 < w_lo1 || k0 + KT > w_hi0) {
+      // register i of half h is key 32 kb + 8 (i / 4) + 4 h + i % 4 of the tile
+      const int first = lo - k0 - 4 * h, end = hi - k0 - 4 * h;
+      if (k0 + KT > w_hi0) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = k0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3);
-          S[kb][i] = key >= lo && key < hi ? S[kb][i] : -__builtin_inff();
-        }
+          for (int i = 0; i < 16; ++i) S[kb][i] = 32 * kb + 8 * (i >> 2) + (i & 3) < end ? S[kb][i] : -__builtin_inff();
+      }
+      if (k0 < w_lo1) {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) S[kb][i] = 32 * kb + 8 * (i >> 2) + (i & 3) >= first ? S[kb][i] : -__builtin_inff();
+      }
       maximum(S);
     }
     // a new reference only once the maximum has grown by 2^8: weights up to
@@ -348,7 +388,6 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
 #pragma unroll
         for (int e = 0; e < EACH; ++e) y[e] = x[e];
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
     round(32 / EACH - 1);
     u4 vf[2][NB];
@@ -381,13 +420,6 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   };
 
   if (t0 < t1) {
-    const u4 first_k = tile_of(kg, ldk, t0), first_v = tile_of(vg, ldv, t0), second_k = tile_of(kg, ldk, t0 + 1);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      copy_k(first_k, t0, i);
-      copy_k(second_k, t0 + 1, i);
-      copy_v(first_v, t0, i);
-    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     f16x A[2] = {(f16x){}, (f16x){}}, B[2];
@@ -406,7 +438,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives the block
-  if (!mine || wr + col >= rows) return;
+  if (32 * wv + col >= rows) return;
   if (dirty)
     for (int t = t0; t < t1; ++t) {
       const int k0 = t * KT;
@@ -437,12 +469,28 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
 
 template <int D, int NW>
 hipError_t launch(const AttnPromptArgs &a, hipStream_t s) {
-  constexpr int BM = 32 * NW;
-  constexpr size_t lds = (size_t)4 * KT * 2 * D;
-  const int64_t tiles = (int64_t)a.tokens * (a.heads / a.kv_heads) / BM + a.sequences;
+  constexpr size_t lds = (size_t)4 * KT * 2 * D + 2 * NW * sizeof(int);
   const hipError_t e = allow_smem(attn_prompt_kernel<D, NW>, lds);
   if (e != hipSuccess) return e;
-  attn_prompt_kernel<D, NW><<<dim3((unsigned)(tiles * a.kv_heads)), 64 * NW, lds, s>>>(a, (int)tiles);
+  const int G = a.heads / a.kv_heads;
+  PromptPlan plan;
+  plan.G = G;
+  plan.tokens = 32 * NW / G;
+  plan.tokens_mul = (uint32_t)((1ull << 32) / plan.tokens) + 1;
+  plan.g_mul = 65536 / G + 1;
+  // a sequence adds a tile at most to what its tokens fill; most of these are
+  // not there when the tiles are counted into rounds
+  plan.tiles = a.tokens / plan.tokens + a.sequences;
+  const int round = compute_units() / a.kv_heads;
+  plan.half = round > 0 && plan.tiles > round && plan.tiles - a.sequences <= 2 * round ? round : plan.tiles;
+  for (int done = 0; done < plan.tiles;) {
+    const int n = plan.tiles - done < 65535 ? plan.tiles - done : 65535;
+    PromptPlan p = plan;
+    p.tiles -= done;  // the grid's second dimension ends at 65535
+    if (done) p.half = p.tiles;
+    attn_prompt_kernel<D, NW><<<dim3(a.kv_heads, n), 64 * NW, lds, s>>>(a, p);
+    done += n;
+  }
   return hipGetLastError();
 }
 
