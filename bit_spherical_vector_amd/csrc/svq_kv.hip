@@ -388,6 +388,14 @@ __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
   }
 }
 
+// Whether the greater magnitudes of two halves (pk_max_mag) are not finite.
+__device__ __forceinline__ bool not_finite(uint32_t mag) { return (mag & 0xFFFF) >= 0x7F80 || mag >= 0x7F800000u; }
+// v, with no part of what is made of it moved ahead of the branch it stands in.
+__device__ __forceinline__ uint32_t hidden(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 template <int D, int GROUP>
 __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn_cache_kernel(AttnCacheArgs a) {
   constexpr int G = D / GROUP, NS = D / 32, NT = D / 16, TPG = GROUP / 16, SPG = GROUP / 32;
@@ -483,7 +491,14 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
 #pragma unroll
   for (int s = 0; s < NS; ++s)
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mx = pk_max_finite(mx, raw[s][w]);
+    for (int w = 0; w < 4; ++w) mx = pk_max_mag(mx, raw[s][w]);
+  if (__builtin_expect(__any(not_finite(mx)), 0)) {
+    mx = 0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mx = pk_max_finite(mx, raw[s][w]);
+  }
   const float q_top = row_max(fmaxf(lo_bf16(mx), hi_bf16(mx)));
   const int qe = q_top > 0.f ? 15 - __builtin_amdgcn_frexp_expf(q_top) : 0;
 #pragma unroll
@@ -492,13 +507,13 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
   for (int s = 0; s < NS; ++s)
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const float x = ldexpf(lo_bf16(raw[s][w]), qe), y = ldexpf(hi_bf16(raw[s][w]), qe);
-      qsum[s / SPG] += x + y;
-      const float f = w & 1 ? 0.0625f : 1.f;
-      qf[s][w] = __builtin_bit_cast(uint32_t, (h2){(_Float16)(x * f), (_Float16)(y * f)});
+      const float x = lo_bf16(raw[s][w]), y = hi_bf16(raw[s][w]);
+      qsum[s / SPG] += ldexpf(x, -8) + ldexpf(y, -8);  // 256 of the greatest numbers stay a number
+      const int e = w & 1 ? qe - 4 : qe;
+      qf[s][w] = __builtin_bit_cast(uint32_t, (h2){(_Float16)ldexpf(x, e), (_Float16)ldexpf(y, e)});
     }
 #pragma unroll
-  for (int g = 0; g < G; ++g) qsum[g] = row_sum(qsum[g]) * 0x1p-24f;
+  for (int g = 0; g < G; ++g) qsum[g] = ldexpf(row_sum(qsum[g]), qe + 8 - 24);
   const float sc = a.scale * 1.44269504088896f;
   const int se = 24 - qe;
 
@@ -582,17 +597,23 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
     // E to the greatest finite scale or minimum that a row sees here; true if
     // it has risen
     auto raise = [&]() {
-      float big = 0.f;
+      uint32_t most = 0;
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t v = vp[j][g][i];
-            asm volatile("" : "+v"(v));  // stays in this rare branch
-            big = fmaxf(big, fmaxf(finite_mag(lo_bf16(v)), finite_mag(hi_bf16(v))));
-          }
+          for (int i = 0; i < 4; ++i) most = pk_max_mag(most, hidden(vp[j][g][i]));
+      if (__builtin_expect(__any(not_finite(most)), 0)) {
+        most = 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) most = pk_max_finite(most, hidden(vp[j][g][i]));
+      }
+      float big = fmaxf(lo_bf16(most), hi_bf16(most));
       big = row_max(lanes_max(big, 16));
       const int now = __builtin_amdgcn_readfirstlane(big > 0.f ? __builtin_amdgcn_frexp_expf(big) : E);
       if (now <= E) return false;
