@@ -181,20 +181,24 @@ svq_status svq_attn_cache(const svq_kv_cache *cache, const void *q, int64_t ldq,
   if (!on_16(q, ldq, 2) || !on_16(y, ldy, 2)) return SVQ_ERR_UNSUPPORTED;
   const int R = q_heads / a.c.heads * q_len;
   a.row_tiles = (R + CACHE_ROWS - 1) / CACHE_ROWS;
-  // ranges of keys: for one round of blocks, two a compute unit (b1_32768 18.6
-  // us for one, 16.7 for two, 19.6 for three), of 32 steps at most, so that
-  // sequences of different lengths share the units evenly (64 sequences of up to
-  // 8192 tokens: 8 steps 101 us, 16 78, 32 75)
+  // Ranges of keys: for one round of blocks, two a compute unit (one sequence of
+  // 32768 tokens 18.6 us for one, 16.7 for two, 19.6 for three).  Sequences of
+  // different lengths share the units evenly if no block is long: at most
+  // CACHE_MAX_STEPS steps a block (64 sequences of up to 8192 tokens: 101 us for
+  // 8 steps, 77 for 16, 75 for 32), in at most sixteen rounds, which bounds the
+  // workspace (many rows need no ranges).
   const int64_t blocks = batch * a.c.heads * a.row_tiles;
   const int64_t spread = (int64_t)window + q_len + 31;  // a window and the chunk that it starts in
   const int64_t keys = window > 0 && spread < max_len ? spread : max_len;
   const int64_t steps = (keys + CACHE_BLOCK_KEYS - 1) / CACHE_BLOCK_KEYS;
   const int64_t slots = 2 * compute_units();
-  const int64_t ranges = blocks < slots ? slots / blocks : 1;
-  int64_t per = (steps + ranges - 1) / ranges;
-  per = per > CACHE_MAX_STEPS ? CACHE_MAX_STEPS : per;
-  a.per = (int32_t)per * (CACHE_BLOCK_KEYS / 32);
-  a.splits = (int32_t)((steps + per - 1) / per);
+  int64_t splits = blocks < slots ? slots / blocks : 1;
+  if (batch > 1) {
+    const int64_t even = (steps + CACHE_MAX_STEPS - 1) / CACHE_MAX_STEPS, most = 16 * slots / blocks;
+    const int64_t want = even < most ? even : most;
+    splits = want > splits ? want : splits;
+  }
+  a.splits = (int32_t)(splits < steps ? splits : steps);
   const size_t part = a.splits > 1 ? align256((size_t)batch * q_heads * q_len * a.splits * a.c.dim * 4) : 0;
   const size_t need = a.splits > 1 ? part + align256((size_t)batch * q_heads * q_len * a.splits * 8) : 256;
   if (!workspace) {

@@ -80,6 +80,39 @@ struct AttnPromptArgs {
 };
 hipError_t launch_attn_prompt(const AttnPromptArgs &a, hipStream_t s);
 
+// Divisions by launch constants d, with multipliers 2^32 / d + 1 and
+// 2^16 / d + 1: exact where n * d < 2^32 and 2^16.
+__host__ __device__ inline int quotient(int n, uint32_t mul) { return (int)((uint64_t)(uint32_t)n * mul >> 32); }
+__host__ __device__ inline int quotient16(int n, uint32_t mul) { return (int)((uint32_t)n * mul >> 16); }
+
+// A block's tile of rows: `tokens` tokens of a sequence, each with the G query
+// heads that share a key head, in 32 rows a wave.
+struct PromptPlan {
+  int32_t tiles, half;         // see prompt_tile
+  int32_t tokens, G;           // tokens = 32 * waves / G
+  uint32_t tokens_mul, g_mul;  // for quotient, quotient16
+};
+inline PromptPlan prompt_plan(int tokens, int sequences, int heads, int kv_heads, int waves, int units) {
+  PromptPlan p;
+  p.G = heads / kv_heads;
+  p.tokens = 32 * waves / p.G;
+  p.tokens_mul = (uint32_t)((1ull << 32) / (uint32_t)p.tokens) + 1;
+  p.g_mul = 65536u / (uint32_t)p.G + 1;
+  // a sequence adds a tile at most to what its tokens fill; most of these are
+  // not there when the tiles are counted into rounds
+  p.tiles = tokens / p.tokens + sequences;
+  const int round = units / kv_heads;
+  p.half = round > 0 && p.tiles > round && p.tiles - sequences <= 2 * round ? round : p.tiles;
+  return p;
+}
+// The tile that takes its turn.  The last tiles come first: under a causal
+// mask they have the most keys.  Where one round of blocks, two a compute unit,
+// covers all, the second on each unit takes the tiles from the front on, which
+// leaves every unit about as many keys (2048 tokens 51 -> 47 us).
+__host__ __device__ inline int prompt_tile(const PromptPlan &p, int turn) {
+  return turn < p.half ? p.tiles - 1 - turn : turn - p.half;
+}
+
 struct AttnCacheArgs {
   KvView c;
   const uint16_t *q;
@@ -88,7 +121,7 @@ struct AttnCacheArgs {
   const int32_t *table, *lens;
   int32_t batch, q_len, heads, max_len, window;
   float scale;
-  int32_t row_tiles, splits, per;  // tiles of 16 rows; ranges of keys, each of `per` chunks of 32
+  int32_t row_tiles, splits;  // tiles of 16 rows, ranges of keys
   float *part, *sums;         // splits > 1: [batch][kv head][row][split] numerators [dim] and (reference, sum)
 };
 // rows of a tile, keys of a block's step, steps of a block at most

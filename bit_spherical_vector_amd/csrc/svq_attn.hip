@@ -25,14 +25,6 @@ namespace {
 
 constexpr int KT = 64;  // keys of a tile
 
-// A tile of rows: `tokens` tokens of a sequence, each with the G query heads
-// that share the key head.
-struct PromptPlan {
-  int32_t tiles, half;               // see attn_prompt_kernel
-  int32_t tokens, G;                 // tokens = 32 * waves / G
-  uint32_t tokens_mul, g_mul;        // quotient, quotient16
-};
-
 typedef __attribute__((address_space(3))) uint8_t lds_t;
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s4v lds_s4v;
@@ -97,10 +89,6 @@ __device__ __forceinline__ f16x mfma_bf16(const u4 &a, const u4 &b, const f16x &
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
 }
 
-// Divisions by launch constants, exact where n * divisor < 2^32 (2^16).
-__device__ __forceinline__ int quotient(int n, uint32_t mul) { return (int)__umulhi((uint32_t)n, mul); }
-__device__ __forceinline__ int quotient16(int n, uint32_t mul) { return (int)((uint32_t)n * mul >> 16); }
-
 // The sequence and tile of number `u` of the tiles of all sequences in order;
 // false beyond the last.  Every wave looks for itself, 64 sequences at a time,
 // in one trip to memory.
@@ -159,13 +147,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, h = lane >> 5;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kvh = blockIdx.x, G = plan.G;
-  // The last tiles first: under a causal mask they have the most keys.  With
-  // `half`, one round of blocks, two a compute unit, covers all: there the
-  // second on each takes the tiles from the front on, which leaves every unit
-  // the same number of keys (2048 tokens 51 -> 47 us).
   TileOf T;
-  const int turn = blockIdx.y;
-  if (!find_tile(a, plan, turn < plan.half ? plan.tiles - 1 - turn : turn - plan.half, T)) return;
+  if (!find_tile(a, plan, prompt_tile(plan, blockIdx.y), T)) return;
   const int t_first = T.tile * plan.tokens, rows = min(plan.tokens, T.n - t_first) * G;
   const int shift = T.keys - T.n + t_first;  // position of the tile's first token
 
@@ -472,22 +455,12 @@ hipError_t launch(const AttnPromptArgs &a, hipStream_t s) {
   constexpr size_t lds = (size_t)4 * KT * 2 * D + 2 * NW * sizeof(int);
   const hipError_t e = allow_smem(attn_prompt_kernel<D, NW>, lds);
   if (e != hipSuccess) return e;
-  const int G = a.heads / a.kv_heads;
-  PromptPlan plan;
-  plan.G = G;
-  plan.tokens = 32 * NW / G;
-  plan.tokens_mul = (uint32_t)((1ull << 32) / plan.tokens) + 1;
-  plan.g_mul = 65536 / G + 1;
-  // a sequence adds a tile at most to what its tokens fill; most of these are
-  // not there when the tiles are counted into rounds
-  plan.tiles = a.tokens / plan.tokens + a.sequences;
-  const int round = compute_units() / a.kv_heads;
-  plan.half = round > 0 && plan.tiles > round && plan.tiles - a.sequences <= 2 * round ? round : plan.tiles;
+  const PromptPlan plan = prompt_plan(a.tokens, a.sequences, a.heads, a.kv_heads, NW, compute_units());
   for (int done = 0; done < plan.tiles;) {
+    // the grid's second dimension ends at 65535
     const int n = plan.tiles - done < 65535 ? plan.tiles - done : 65535;
     PromptPlan p = plan;
-    p.tiles -= done;  // the grid's second dimension ends at 65535
-    if (done) p.half = p.tiles;
+    p.tiles -= done;
     attn_prompt_kernel<D, NW><<<dim3(a.kv_heads, n), 64 * NW, lds, s>>>(a, p);
     done += n;
   }

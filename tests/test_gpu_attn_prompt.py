@@ -210,3 +210,40 @@ def test_same_bits_every_time_captured_and_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(y, svq.attn_prompt(q, k, v, starts, dim))
         starts.copy_(_starts(lens))
+
+
+def test_rows_past_32_bits():
+    """Sequences whose rows lie beyond 2^32 bytes of their buffers."""
+    svq = require_gpu()
+    heads, kv, dim, lens = 2, 1, 128, [40, 100]
+    total, ld = 140000, 16384
+    wide = torch.zeros((total, ld), dtype=torch.bfloat16, device="cuda")
+    first = total - sum(lens)
+    assert first * ld * 2 > 1 << 32
+    cols = (heads + 2 * kv) * dim
+    wide[first:, 512:512 + cols] = _rows(sum(lens), cols, 23)
+    q = wide[:, 512:512 + heads * dim]
+    k = wide[:, 512 + heads * dim:512 + (heads + kv) * dim]
+    v = wide[:, 512 + (heads + kv) * dim:512 + cols]
+    y = wide[:, 8192:8192 + heads * dim]
+    svq.attn_prompt(q, k, v, _starts(lens, first), dim, out=y)
+    torch.cuda.synchronize()
+    _check(y, q, k, v, lens, lens, heads, kv, dim, True, 0, first=first, first_k=first)
+    assert torch.all(y[:first] == 0)
+
+
+def test_more_tiles_than_one_launch_takes():
+    """64 query heads a key head leave two tokens a tile: 2^17 tokens are more
+    tiles than the grid's second dimension."""
+    svq = require_gpu()
+    heads, kv, dim, n, each = 64, 1, 64, 1 << 17, 61
+    lens = [each] * (n // each) + [n % each]
+    q = _rows(n, heads * dim, 24)
+    k, v = _rows(n, kv * dim, 25), _rows(n, kv * dim, 26)
+    y = svq.attn_prompt(q, k, v, _starts(lens), dim)
+    torch.cuda.synchronize()
+    for s in (0, 1, 1000, len(lens) - 2, len(lens) - 1):
+        at, m = s * each, lens[s]
+        rows = slice(at, at + m)
+        check(y[rows], *attend(q[rows], k[rows], v[rows], heads, kv, dim ** -0.5, visible(m, m)), m, P_BF16, f"sequence {s}")
+    assert torch.isfinite(y.float()).all() and torch.all(y.float().abs().sum(dim=1) > 0)
