@@ -18,8 +18,6 @@
 #include "svq_attn.h"
 #include "svq_device.h"
 
-#include <type_traits>
-
 namespace svq {
 namespace {
 
@@ -89,6 +87,21 @@ __device__ __forceinline__ f16x mfma_bf16(const u4 &a, const u4 &b, const f16x &
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
 }
 
+// The sum of v over the lanes up to the lane's own: within rows of 16 lanes,
+// then the last lane of a row to the next row and of the lower half to the upper.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_dpp(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int sum_below(int v) {
+  v = add_dpp<0x111, 0xF>(v);  // row_shr:1
+  v = add_dpp<0x112, 0xF>(v);
+  v = add_dpp<0x114, 0xF>(v);
+  v = add_dpp<0x118, 0xF>(v);
+  v = add_dpp<0x142, 0xA>(v);  // row_bcast:15
+  return add_dpp<0x143, 0xC>(v);  // row_bcast:31
+}
+
 // The sequence and tile of number `u` of the tiles of all sequences in order;
 // false beyond the last.  Every wave looks for itself, 64 sequences at a time,
 // in one trip to memory.
@@ -112,12 +125,7 @@ __device__ __forceinline__ bool find_tile(const AttnPromptArgs &a, const PromptP
     kb = min(max(kb, 0), a.tokens_k);
     ke = min(max(ke, kb), a.tokens_k);
     const int tiles = quotient(e - b + plan.tokens - 1, plan.tokens_mul);
-    int sum = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int other = __shfl_up(sum, d);
-      if (lane >= d) sum += other;
-    }
+    const int sum = sum_below(tiles);
     const uint64_t past = __ballot(before + sum > u);
     if (past) {
       const int at = __builtin_ctzll(past);
@@ -138,12 +146,20 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t x) {
   return ((lo & 0x7F80u) == 0x7F80u ? 0u : lo) | ((hi & 0x7F800000u) == 0x7F800000u ? 0u : hi);
 }
 
+// LDS bytes of the tiles: K and V of two each, and (64 channels) 4 KB a wave
+// from the last one on.
+template <int D, int NW>
+constexpr int prompt_tiles() {
+  constexpr int SIDE = KT * 2 * D;
+  return 4 * SIDE > 3 * SIDE + NW * 4096 ? 4 * SIDE : 3 * SIDE + NW * 4096;
+}
+
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(AttnPromptArgs a, PromptPlan plan) {
   constexpr int ROW = 2 * D, CH = D / 8, SIDE = KT * ROW;  // bytes of a row, its chunks, bytes of a tile
   constexpr int NB = D / 32, NS = D / 16;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // K and V of two tiles each, from LDS byte 0 on
-  int(*odd)[NW] = (int(*)[NW])(smem + 4 * SIDE);  // which waves have met values that are not finite
+  int(*odd)[NW] = (int(*)[NW])(smem + prompt_tiles<D, NW>());  // which waves have met values that are not finite
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, h = lane >> 5;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kvh = blockIdx.x, G = plan.G;
@@ -179,18 +195,18 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     off_k[i] = key * ldk + chunk;
     off_v[i] = key * ldv + chunk;
   }
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_t *)smem;  // K of even and odd tiles, V of even and odd tiles
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_t *)smem;  // two places of K, two of V, taken in turn from tile t0 on
   // tile t of the keys (values) as a buffer that ends with the sequence: rows
   // behind it become zeros, a tile behind it is not read
   auto tile_of = [&](const uint8_t *from, uint32_t ld, int t) {
     const int left = min(max(T.keys - t * KT, 0), KT);
     return buffer_of(from + (int64_t)t * KT * ld, left > 0 ? (left - 1) * ld + ROW : 0);
   };
-  auto copy_k = [&](const u4 &buffer, int t, int i) {
-    copy_to_lds(buffer, off_k[i % KINDS], i / KINDS * KINDS * NW * KEYS * ldk, lds0 + (t & 1) * SIDE + (i * NW + wv) * 1024);
+  auto copy_k = [&](const u4 &buffer, int place, int i) {
+    copy_to_lds(buffer, off_k[i % KINDS], i / KINDS * KINDS * NW * KEYS * ldk, lds0 + place * SIDE + (i * NW + wv) * 1024);
   };
-  auto copy_v = [&](const u4 &buffer, int t, int i) {
-    copy_to_lds(buffer, off_v[i % KINDS], i / KINDS * KINDS * NW * KEYS * ldv, lds0 + (2 + (t & 1)) * SIDE + (i * NW + wv) * 1024);
+  auto copy_v = [&](const u4 &buffer, int place, int i) {
+    copy_to_lds(buffer, off_v[i % KINDS], i / KINDS * KINDS * NW * KEYS * ldv, lds0 + (2 + place) * SIDE + (i * NW + wv) * 1024);
   };
 
   // fragment addresses, a chunk's place an exclusive or: K chunk 2s + h of key
@@ -209,21 +225,35 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   if (t0 < t1) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      copy_k(first_k, t0, i);
-      copy_k(second_k, t0 + 1, i);
-      copy_v(first_v, t0, i);
+      copy_k(first_k, 0, i);
+      copy_k(second_k, 1, i);
+      copy_v(first_v, 0, i);
     }
   }
+  // Queries come as whole lines, eight lanes 64 channels of a row, and pass
+  // through LDS (the second place of V, 4 KB a wave) to the lanes of their rows.
   u4 qf[NS];
   {
-    const uint16_t *q = a.q + row_off * a.ldq + head * D + 8 * h;
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u, to = lds0 + 3 * SIDE + wv * 4096;
+    u4 raw[D / 64][4];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) qf[s] = *(const u4 *)(q + 16 * s);
+    for (int i = 0; i < 4; ++i) {
+      const int r = min(32 * wv + 8 * i + (lane >> 3), rows - 1), token = quotient16(r, plan.g_mul);
+      const uint16_t *q = a.q + (int64_t)(T.q_at + t_first + token) * a.ldq + (kvh * G + r - token * G) * D + 8 * (lane & 7);
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+      for (int p = 0; p < D / 64; ++p) raw[p][i] = *(const u4 *)(q + 64 * p);
+    }
 #pragma unroll
-      for (int w = 0; w < 4; ++w) qf[s][w] ^= flip;
+    for (int p = 0; p < D / 64; ++p) {
+      // chunk c of row n at place c ^ (n / 2 % 8)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(lds_u4 *)(lds_t *)(uintptr_t)(to + i * 1024 + (lane >> 3) * 128 + (((lane & 7) ^ ((4 * i + (lane >> 4)) & 7)) << 4)) = raw[p][i] ^ flip;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int s = 0; s < 4; ++s) qf[4 * p + s] = *(const lds_u4 *)(lds_t *)(uintptr_t)(to + col * 128 + (((2 * s + h) ^ (col >> 1 & 7)) << 4));
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
   }
   // exponents are base 2; a scale of zero stays a number that keeps hidden
   // scores at -infinity
@@ -236,20 +266,25 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   bool dirty = false, far_any = false;
 
   u4 kf[2][2];
-  auto load_k = [&](int t, int s) {
-    const uint32_t at = (ka + (t & 1) * SIDE) ^ (s << 5);
+  auto load_k = [&](int place, int s) {
+    const uint32_t at = (ka + place * SIDE) ^ (s << 5);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) kf[s & 1][kb] = *(const lds_u4 *)(lds_t *)(uintptr_t)(at + kb * 32 * ROW);
   };
 
-  // One tile: S holds its scores and N takes the next tile's.
+  // Tile t, its V in `place`: S holds its scores and N takes the next tile's.
   float top = 0.f;
   auto maximum = [&](const f16x (&S)[2]) {
     top = max_nan(S[0][0], S[1][0]);
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = max_nan(max_nan(top, S[0][i]), S[1][i]);
   };
-  auto step = [&](int t, f16x (&S)[2], f16x (&N)[2]) {
+  auto step = [&](int t, int turn, f16x (&S)[2], f16x (&N)[2]) {
+    // A constant saves address arithmetic.  At 256 channels, whose registers are
+    // all taken, the second set of addresses would be spilled (8192 tokens, 16
+    // heads: 629 us against 611).
+    int place = turn;
+    if constexpr (D == 256) asm volatile("" : "+s"(place));
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     const int k0 = t * KT;
     const bool edge = k0 < b_lo1 || k0 + KT > b_hi0;  // some row of the block does not see all keys
@@ -257,27 +292,27 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       // P^T is zero for a hidden key, but zero times infinity is not.  A wave
       // looks at the values that it has copied itself.
       uint32_t mag = 0;
-      const uint32_t at = lds0 + (2 + (t & 1)) * SIDE + wv * 1024 + lane * 16;
+      const uint32_t at = lds0 + (2 + place) * SIDE + wv * 1024 + lane * 16;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const u4 x = *(const lds_u4 *)(lds_t *)(uintptr_t)(at + i * NW * 1024);
 #pragma unroll
         for (int w = 0; w < 4; ++w) mag = pk_max_mag(mag, x[w]);
       }
-      odd[t & 1][wv] = __any((mag & 0xFFFF) >= 0x7F80 || mag >= 0x7F800000u);
+      odd[place][wv] = __any((mag & 0xFFFF) >= 0x7F80 || mag >= 0x7F800000u);
     }
     __syncthreads();  // V of t and K of t + 1 are there; nobody reads V of t - 1 and K of t
     const u4 next_k = tile_of(kg, ldk, t + 2), next_v = tile_of(vg, ldv, t + 1);
     if (edge) {
       int any = 0;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) any |= odd[t & 1][w];
+      for (int w = 0; w < NW; ++w) any |= odd[place][w];
       if (__builtin_expect(__builtin_amdgcn_readfirstlane(any), 0)) {
         // values that are not finite become zero, and the rows that do see
         // them get them at the end
         dirty = true;
         for (int i = wv; i < SIDE / 1024; i += NW) {
-          lds_u4 *x = (lds_u4 *)(lds_t *)(uintptr_t)(lds0 + (2 + (t & 1)) * SIDE + i * 1024 + lane * 16);
+          lds_u4 *x = (lds_u4 *)(lds_t *)(uintptr_t)(lds0 + (2 + place) * SIDE + i * 1024 + lane * 16);
           u4 v = *x;
 #pragma unroll
           for (int w = 0; w < 4; ++w) v[w] = finite_or_zero(v[w]);
@@ -289,8 +324,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     if (!mine) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        copy_k(next_k, t, i);
-        copy_v(next_v, t + 1, i);
+        copy_k(next_k, place, i);
+        copy_v(next_v, place ^ 1, i);
       }
       return;
     }
@@ -314,12 +349,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     // a new reference only once the maximum has grown by 2^8: weights up to
     // 256 are as exact as weights up to 1
     if (__any(top * sc > (m == -__FLT_MAX__ ? -__builtin_inff() : mref + 8.f))) {
-      const float old = mref;
+      const float old = mref, old_m = m;
       const bool first = m == -__FLT_MAX__;
       m = fmaxf(m, max_halves(top));
       mref = m == -__FLT_MAX__ ? 0.f : m * sc;
       far_any = __any(fabsf(mref) > 16777216.f);
-      const float alpha = first ? 0.f : __builtin_amdgcn_exp2f(old - mref);
+      const float alpha = first ? 0.f : __builtin_amdgcn_exp2f(far_any ? (old_m - m) * sc : old - mref);
       l *= alpha;
 #pragma unroll
       for (int db = 0; db < NB; ++db)
@@ -355,16 +390,16 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
         pf[at >> 3][(at & 7) >> 1] = p;
       }
     };
-    load_k(t + 1, 0);
+    load_k(place ^ 1, 0);
     N[0] = N[1] = (f16x){};
 #pragma unroll
     for (int n = 0; n < 2 * NS; ++n) {
       const int s = n >> 1, kb = n & 1;
-      if (kb == 0 && s + 1 < NS) load_k(t + 1, s + 1);
+      if (kb == 0 && s + 1 < NS) load_k(place ^ 1, s + 1);
       N[kb] = mfma_bf16(kf[s & 1][kb], qf[s], N[kb]);
       // copies one by one: all at once they hold the wave until the last is taken
-      if (n % 4 == 0 && n / 4 < PER) copy_k(next_k, t, n / 4);
-      if (n % 4 == 2 && n / 4 < PER) copy_v(next_v, t + 1, n / 4);
+      if (n % 4 == 0 && n / 4 < PER) copy_k(next_k, place, n / 4);
+      if (n % 4 == 2 && n / 4 < PER) copy_v(next_v, place ^ 1, n / 4);
       if (n % EVERY == 0) {
         exps(n / EVERY);
         if (n > 0) round(n / EVERY - 1);
@@ -380,7 +415,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
         u2 x[2];
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
-          const uint32_t at = ((va[jj] + (t & 1) * SIDE) ^ (db << 6)) + n * 16 * ROW;
+          const uint32_t at = ((va[jj] + place * SIDE) ^ (db << 6)) + n * 16 * ROW;
           x[jj] = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v *)(lds_t *)(uintptr_t)at));
         }
         vf[n & 1][db] = (u4){x[0][0], x[0][1], x[1][0], x[1][1]};
@@ -406,18 +441,18 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     f16x A[2] = {(f16x){}, (f16x){}}, B[2];
-    load_k(t0, 0);
+    load_k(0, 0);
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      if (s + 1 < NS) load_k(t0, s + 1);
+      if (s + 1 < NS) load_k(0, s + 1);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) A[kb] = mfma_bf16(kf[s & 1][kb], qf[s], A[kb]);
     }
     maximum(A);
 #pragma unroll 1
     for (int t = t0; t < t1; t += 2) {
-      step(t, A, B);
-      if (t + 1 < t1) step(t + 1, B, A);
+      step(t, 0, A, B);
+      if (t + 1 < t1) step(t + 1, 1, B, A);
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives the block
@@ -452,7 +487,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
 
 template <int D, int NW>
 hipError_t launch(const AttnPromptArgs &a, hipStream_t s) {
-  constexpr size_t lds = (size_t)4 * KT * 2 * D + 2 * NW * sizeof(int);
+  constexpr size_t lds = prompt_tiles<D, NW>() + 2 * NW * sizeof(int);
   const hipError_t e = allow_smem(attn_prompt_kernel<D, NW>, lds);
   if (e != hipSuccess) return e;
   const PromptPlan plan = prompt_plan(a.tokens, a.sequences, a.heads, a.kv_heads, NW, compute_units());
