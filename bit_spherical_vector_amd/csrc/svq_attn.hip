@@ -28,17 +28,16 @@ typedef short s4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s4v lds_s4v;
 typedef __attribute__((address_space(3))) u4 lds_u4;
 
-// A buffer of `bytes` bytes: reads beyond give zeros.  The compiler does not
-// look into the copies below, so the wait states between the vector unit's
-// writes of these scalars and their first use there stand here (and between
-// M0 and its use, there); nothing but scalar instructions touches them after.
-__device__ __forceinline__ u4 buffer_of(const uint8_t *base, uint32_t bytes) {
+// A buffer from `base` on: reads beyond its bytes (element 2) give zeros.
+__device__ __forceinline__ u4 buffer_at(const uint8_t *base) {
   const uint64_t at = (uint64_t)base;
-  u4 b = {(uint32_t)__builtin_amdgcn_readfirstlane((int)at), (uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32) & 0xFFFF),
-          (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
-  asm volatile("s_nop 4" : "+s"(b));
-  return b;
+  return (u4){(uint32_t)__builtin_amdgcn_readfirstlane((int)at), (uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32)) & 0xFFFFu, 0u, 0x00020000u};
 }
+// The compiler does not look into the copies below, so the wait states between
+// the vector unit's writes of these scalars and their first use there stand here
+// (and between M0 and its use, there); nothing but scalar instructions touches
+// them after.
+__device__ __forceinline__ void settle(u4 &a, u4 &b) { asm volatile("s_nop 4" : "+s"(a), "+s"(b)); }
 // 16 bytes a lane from byte off + first of the buffer to LDS bytes dst + 16 *
 // lane, waited for by vmcnt.  (The builtin makes every LDS read behind it wait
 // for the copy.)
@@ -198,9 +197,15 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_t *)smem;  // two places of K, two of V, taken in turn from tile t0 on
   // tile t of the keys (values) as a buffer that ends with the sequence: rows
   // behind it become zeros, a tile behind it is not read
-  auto tile_of = [&](const uint8_t *from, uint32_t ld, int t) {
-    const int left = min(max(T.keys - t * KT, 0), KT);
-    return buffer_of(from + (int64_t)t * KT * ld, left > 0 ? (left - 1) * ld + ROW : 0);
+  auto ends = [&](u4 &buffer, uint32_t ld, int t) {
+    const int left = T.keys - t * KT;
+    buffer[2] = left > 0 ? (uint32_t)(min(left, KT) - 1) * ld + ROW : 0u;
+  };
+  auto advance = [&](u4 &buffer, uint32_t ld, int t) {
+    const uint64_t at = ((uint64_t)buffer[1] << 32 | buffer[0]) + (uint64_t)(KT * ld);
+    buffer[0] = (uint32_t)at;
+    buffer[1] = (uint32_t)(at >> 32);
+    ends(buffer, ld, t);
   };
   auto copy_k = [&](const u4 &buffer, int place, int i) {
     copy_to_lds(buffer, off_k[i % KINDS], i / KINDS * KINDS * NW * KEYS * ldk, lds0 + place * SIDE + (i * NW + wv) * 1024);
@@ -221,14 +226,20 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   }
 
   // the first tiles are on their way before the queries are asked for
-  const u4 first_k = tile_of(kg, ldk, t0), first_v = tile_of(vg, ldv, t0), second_k = tile_of(kg, ldk, t0 + 1);
+  u4 buf_k = buffer_at(kg + (int64_t)t0 * KT * ldk), buf_v = buffer_at(vg + (int64_t)t0 * KT * ldv);
+  ends(buf_k, ldk, t0);
+  ends(buf_v, ldv, t0);
+  settle(buf_k, buf_v);
   if (t0 < t1) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      copy_k(first_k, 0, i);
-      copy_k(second_k, 1, i);
-      copy_v(first_v, 0, i);
+      copy_k(buf_k, 0, i);
+      copy_v(buf_v, 0, i);
     }
+    advance(buf_k, ldk, t0 + 1);
+    settle(buf_k, buf_v);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) copy_k(buf_k, 1, i);
   }
   // Queries come as whole lines, eight lanes 64 channels of a row, and pass
   // through LDS (the second place of V, 4 KB a wave) to the lanes of their rows.
@@ -302,7 +313,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       odd[place][wv] = __any((mag & 0xFFFF) >= 0x7F80 || mag >= 0x7F800000u);
     }
     __syncthreads();  // V of t and K of t + 1 are there; nobody reads V of t - 1 and K of t
-    const u4 next_k = tile_of(kg, ldk, t + 2), next_v = tile_of(vg, ldv, t + 1);
+    advance(buf_k, ldk, t + 2);
+    advance(buf_v, ldv, t + 1);
+    settle(buf_k, buf_v);
     if (edge) {
       int any = 0;
 #pragma unroll
@@ -324,8 +337,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     if (!mine) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        copy_k(next_k, place, i);
-        copy_v(next_v, place ^ 1, i);
+        copy_k(buf_k, place, i);
+        copy_v(buf_v, place ^ 1, i);
       }
       return;
     }
@@ -398,8 +411,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       if (kb == 0 && s + 1 < NS) load_k(place ^ 1, s + 1);
       N[kb] = mfma_bf16(kf[s & 1][kb], qf[s], N[kb]);
       // copies one by one: all at once they hold the wave until the last is taken
-      if (n % 4 == 0 && n / 4 < PER) copy_k(next_k, place, n / 4);
-      if (n % 4 == 2 && n / 4 < PER) copy_v(next_v, place ^ 1, n / 4);
+      if (n % 4 == 0 && n / 4 < PER) copy_k(buf_k, place, n / 4);
+      if (n % 4 == 2 && n / 4 < PER) copy_v(buf_v, place ^ 1, n / 4);
       if (n % EVERY == 0) {
         exps(n / EVERY);
         if (n > 0) round(n / EVERY - 1);
