@@ -48,37 +48,46 @@ __device__ __forceinline__ KvScale kv_scale(float hi, float nlo) {
   p.bits = sb | (__builtin_bit_cast(uint32_t, p.m) & 0xFFFF0000u);
   return p;
 }
-// Codes of N values: the nearest whole numbers to (x - m) / s.  The fp32
-// quotient of a plain group is off by less than 4e-6 and less than 15.1, so
-// only values whose quotients come that near to a border ask for 64 bits,
-// where the difference of two bf16 values 2^45 apart and less is exact.
-template <int N>
-__device__ __forceinline__ void kv_codes(const float (&x)[N], const KvScale &p, float (&q)[N]) {
-  constexpr float WHOLE = 12582912.f;  // 1.5 * 2^23: a sum with it is rounded to a whole number
-  float off = 0.f;
+// Codes of N values, the nearest whole numbers to (x - m) / s (of two as near
+// the even one), two to a dword: of x[i] in the lower half, of x[i + N / 2]
+// (STEP 8) or x[i + 1] in the upper one, each plus KV_CODE0.  The fp32 quotient
+// of a plain group is off by less than 4e-6 and less than 15.1; a sum with 192 +
+// 1/2 + 2^-16 has the code in its upper half and, in the lower one, 2^16 times
+// what the quotient is beyond the border below it plus one, rounded.
+constexpr uint32_t KV_CODE0 = 0x43404340u;
+// A value at a border, its lower half 0 or 1, is held against it: x - m is d and
+// a rest, and d less the border (n - 1/2) s an fp32 number, a multiple of d's
+// last place and not greater than d.  (Borders are met often, all numbers being
+// 8-bit ones times powers of two.)  Where d is on the border and has a rest, or
+// the group is not plain, 64 bits decide, in which the difference of two bf16
+// values 2^45 apart and less is exact.
+template <int N, int STEP>
+__device__ __forceinline__ void kv_codes(const float (&x)[N], const KvScale &p, uint32_t (&code)[N / 2]) {
+  uint32_t u[N];
+  bool wide = !p.plain;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float d = x[i] - p.m;
-    q[i] = fmaf(d, p.r, WHOLE) - WHOLE;
-    off = fmaxf(off, fabsf(fmaf(d, p.r, -q[i])));
+    u[i] = __builtin_bit_cast(uint32_t, fmaf(d, p.r, 192.5f + 0x1p-16f));
+    if ((uint16_t)u[i] < 2) {
+      const float off = fmaf(192.5f - floorf(__builtin_bit_cast(float, u[i])), p.s, d), y = d - x[i];
+      wide = wide || (off == 0.f && (x[i] - (d - y)) - (p.m + y) != 0.f);
+      if (off < 0.f || (off == 0.f && (u[i] & 0x10000u))) u[i] -= 0x10000u;  // to the even one
+    }
   }
-  if (!p.plain || !(off < 0.4999f)) {
+  if (__builtin_expect(wide, 0)) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      q[i] = p.s == 0.f ? 0.f : fminf((float)rint(((double)x[i] - (double)p.m) / (double)p.s), 15.f);
+    for (int i = 0; i < N; ++i) {
+      const double q = p.s == 0.f ? 0. : fmin(rint(((double)x[i] - (double)p.m) / (double)p.s), 15.);
+      u[i] = ((uint32_t)q << 16) + (KV_CODE0 & 0xFFFF0000u);
+    }
   }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) code[i] = STEP == 1 ? __builtin_amdgcn_perm(u[2 * i + 1], u[2 * i], 0x07060302u) : __builtin_amdgcn_perm(u[i + N / 2], u[i], 0x07060302u);
 }
-// Eight codes in nibbles: q[A], q[B] ... in the low nibbles of bytes 0 .. 3,
-// the next four in the high ones.
-__device__ __forceinline__ uint32_t kv_word(float a0, float a1, float a2, float a3, float b0, float b1, float b2, float b3) {
-  uint32_t lo = __builtin_amdgcn_cvt_pk_u8_f32(a0, 0, 0), hi = __builtin_amdgcn_cvt_pk_u8_f32(b0, 0, 0);
-  lo = __builtin_amdgcn_cvt_pk_u8_f32(a1, 1, lo);
-  hi = __builtin_amdgcn_cvt_pk_u8_f32(b1, 1, hi);
-  lo = __builtin_amdgcn_cvt_pk_u8_f32(a2, 2, lo);
-  hi = __builtin_amdgcn_cvt_pk_u8_f32(b2, 2, hi);
-  lo = __builtin_amdgcn_cvt_pk_u8_f32(a3, 3, lo);
-  hi = __builtin_amdgcn_cvt_pk_u8_f32(b3, 3, hi);
-  return lo | hi << 4;
+// A key word of eight codes: pair i at nibble i of both halves.
+__device__ __forceinline__ uint32_t kv_word(const uint32_t (&c)[4]) {
+  return (((((c[3] << 4) + c[2]) << 4) + c[1]) << 4) + c[0] - KV_CODE0 * 0x1111u;
 }
 
 __device__ __forceinline__ float lo_bf16(uint32_t p) { return bf16_bits_to_f32(p & 0xFFFFu); }
@@ -109,6 +118,12 @@ __device__ __forceinline__ float row_sum(float v) {
   return b.x + b.y;
 }
 
+// v, with no part of what is made of it moved ahead of the branch it stands in.
+__device__ __forceinline__ uint32_t hidden(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // Lanes of the key side: token lane % 16 of the wave's 16, channels 32c + 8h ..
 // 32c + 8h + 7 of every step c with h = i = lane / 16, so that a lane's codes
 // are one piece of the layout and the wave's 16 tokens one stretch.  Lanes of
@@ -117,11 +132,11 @@ __device__ __forceinline__ float row_sum(float v) {
 // a row run together: 32768 tokens read back in 53 us against 50).
 struct KvPlace {
   int64_t t;     // token
-  int32_t slot;  // -1: none
+  int32_t slot;  // of the cache, or one that is not there
   int i;
 };
 template <int D>
-__device__ __forceinline__ KvPlace kv_place(const KvView &c, const int32_t *slots, int64_t tokens, int side) {
+__device__ __forceinline__ KvPlace kv_place(const int32_t *slots, int64_t tokens, int side) {
   constexpr int T = D / 16;
   const int lane = threadIdx.x & 63;
   const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -129,8 +144,13 @@ __device__ __forceinline__ KvPlace kv_place(const KvView &c, const int32_t *slot
   p.t = side ? wave * (64 / T) + lane / T : wave * 16 + (lane & 15);
   p.i = side ? lane % T : lane >> 4;
   p.slot = p.t < tokens ? slots[p.t] : -1;
-  if (p.slot >= c.pages << c.page_shift) p.slot = -1;
   return p;
+}
+// Whether the token has a place: asked for after the loads that do not need it,
+// which then are on their way with the slot.
+__device__ __forceinline__ bool kv_in(const KvView &c, KvPlace &p) {
+  asm volatile("" : "+v"(p.slot)::"memory");
+  return p.slot >= 0 && p.slot < c.pages << c.page_shift;
 }
 
 // An exchange with the lane whose number differs in its lowest bits: 7 - i, and
@@ -150,30 +170,37 @@ __device__ __forceinline__ void or_half(uint32_t *w, bool upper) {
   }
 }
 
+// One pass: a value is read once and leaves as a nibble.  Bound by instructions
+// (about 20 a value, a third of them extremes, exchanges and the parameters in
+// 64 bits; the registers are held to what lets 8 waves a unit run, 5 at 256
+// channels, where 4 and 6 take 71 and 66 us against 63): 32768 tokens of 8 heads
+// of 128 channels 45 us, 3.8 TB/s read and written, where a copy of as many
+// bytes takes 35.
 template <int D>
-__global__ __launch_bounds__(256) void kv_write_kernel(KvWriteArgs a) {
+__global__ __launch_bounds__(256, D == 256 ? 5 : 8) void kv_write_kernel(KvWriteArgs a) {
   constexpr int NS = D / 32;
   const int head = blockIdx.y, side = blockIdx.z;
-  const KvPlace P = kv_place<D>(a.c, a.slots, a.tokens, side);
-  const bool in = P.slot >= 0;  // of all lanes of a token
-  const int64_t t = in ? P.t : 0;
-  uint8_t *blk = kv_block(a.c, in ? P.slot >> a.c.page_shift : 0, head);
-  const int place = P.slot & ((1 << a.c.page_shift) - 1);
+  KvPlace P = kv_place<D>(a.slots, a.tokens, side);
+  const int64_t t = min(P.t, a.tokens - 1);
   if (side == 0) {
     const uint16_t *src = a.k + t * a.ldk + head * D + 8 * P.i;
-    float x[NS][8], hi[NS], nlo[NS];
+    u4 raw[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) raw[s] = *(const u4 *)(src + 32 * s);
+    const bool in = kv_in(a.c, P);
+    uint8_t *blk = kv_block(a.c, in ? P.slot >> a.c.page_shift : 0, head);
+    const int place = P.slot & ((1 << a.c.page_shift) - 1);
+    float hi[NS], nlo[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      const u4 raw = *(const u4 *)(src + 32 * s);
       uint32_t mag = 0;
       hi[s] = nlo[s] = -__builtin_inff();
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        x[s][2 * w] = lo_bf16(raw[w]);
-        x[s][2 * w + 1] = hi_bf16(raw[w]);
-        mag = pk_max_mag(mag, raw[w]);
-        hi[s] = fmaxf(fmaxf(hi[s], x[s][2 * w]), x[s][2 * w + 1]);
-        nlo[s] = fmaxf(fmaxf(nlo[s], -x[s][2 * w]), -x[s][2 * w + 1]);
+        const float u = lo_bf16(raw[s][w]), v = hi_bf16(raw[s][w]);
+        mag = pk_max_mag(mag, raw[s][w]);
+        hi[s] = fmaxf(fmaxf(hi[s], u), v);
+        nlo[s] = fmaxf(fmaxf(nlo[s], -u), -v);
       }
       if ((mag & 0xFFFF) >= 0x7F80 || mag >= 0x7F800000u) hi[s] = __builtin_inff();  // not finite
     }
@@ -193,10 +220,16 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvWriteArgs a) {
         p = kv_scale(row_max(h), row_max(l));
         if (in && P.i == 0) *(uint32_t *)(blk + kv_param(a.c, 0, place, s / steps)) = p.bits;
       }
-      float q[8];
-      kv_codes(x[s], p, q);
-      // channel j at nibble kv_nibble(j)
-      word[s] = kv_word(q[0], q[4], q[1], q[5], q[2], q[6], q[3], q[7]);
+      float x[8];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t pair = hidden(raw[s][w]);  // taken apart again: all at once they would fill the registers
+        x[2 * w] = lo_bf16(pair);
+        x[2 * w + 1] = hi_bf16(pair);
+      }
+      uint32_t code[4];
+      kv_codes<8, 1>(x, p, code);
+      word[s] = kv_word(code);  // channel j at nibble kv_nibble(j)
     }
     if (in) __builtin_memcpy(__builtin_assume_aligned(blk + kv_key_word(a.c, place, P.i), D == 64 ? 8 : 16), word, sizeof(word));
   } else {
@@ -204,13 +237,16 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvWriteArgs a) {
     const u4 *src = (const u4 *)(a.v + t * a.ldv + head * D + 16 * P.i);
     float x[16], hi = -__builtin_inff(), nlo = hi;
     uint32_t mag = 0;
+    const u4 raw[2] = {src[0], src[1]};
+    const bool in = kv_in(a.c, P);  // of all lanes of a token
+    uint8_t *blk = kv_block(a.c, in ? P.slot >> a.c.page_shift : 0, head);
+    const int place = P.slot & ((1 << a.c.page_shift) - 1);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const u4 raw = src[n];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float u = lo_bf16(raw[w]), v = hi_bf16(raw[w]);
-        mag = pk_max_mag(mag, raw[w]);
+        const float u = lo_bf16(raw[n][w]), v = hi_bf16(raw[n][w]);
+        mag = pk_max_mag(mag, raw[n][w]);
         hi = fmaxf(fmaxf(hi, u), v);
         nlo = fmaxf(fmaxf(nlo, -u), -v);
         x[8 * n + 2 * w] = u;
@@ -221,17 +257,23 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvWriteArgs a) {
     const int tiles = 1 << (a.c.group_shift - 4);  // of a group: 2, 4 or 8
     const KvScale p = kv_scale(lanes_max(hi, tiles), lanes_max(nlo, tiles));
     if (in && P.i % tiles == 0) *(uint32_t *)(blk + kv_param(a.c, 1, place, P.i / tiles)) = p.bits;
-    float q[16];
-    kv_codes(x, p, q);
-    // Lane i has nibble i of every run.  Three exchanges among eight lanes
-    // (two among the four of 64 channels), each halving the runs that a lane
-    // collects, leave whole dwords.
-    uint32_t w[16];
+    uint32_t w[8];  // codes of runs r and r + 8
+    kv_codes<16, 8>(x, p, w);
+    // Lane i has nibble i of every run.  Exchanges among eight lanes (four with
+    // 64 channels) leave whole dwords (half dwords).
     const int n = P.i & 7;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) w[r] = (uint32_t)q[r] << 4 * n;
     if constexpr (D > 64) {
-      or_half<0x141, 16>(w, n & 4);  // lane 7 - n
+      // Lanes n and 7 - n: the lower takes runs 0 .. 7 of both, the upper the
+      // rest, a code in either half of a dword, then each half shifted to its
+      // nibble.
+      const int e = n & 4 ? 7 - n : n;
+      const uint32_t halves = n & 4 ? 0x03020706u : 0x05040100u;
+      const us2_t shift = {(uint16_t)(4 * e), (uint16_t)(12 - 4 * e)};
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const uint32_t mine = w[r] - KV_CODE0;
+        w[r] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(us2_t, __builtin_amdgcn_perm(dpp<0x141>(mine), mine, halves)) << shift);
+      }
       or_half<0x4E, 8>(w, n & 2);    // lane n ^ 2
       or_half<0xB1, 4>(w, n & 1);    // lane n ^ 1
       if (!in) return;
@@ -239,22 +281,30 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvWriteArgs a) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) *(uint32_t *)(blk + kv_value_run(a.c, place, run + e) + 4 * (P.i >> 3)) = w[e];
     } else {
-      or_half<0x4E, 16>(w, n & 2);
-      or_half<0xB1, 8>(w, n & 1);
-      if (!in) return;
-      const int run = (n & 2 ? 8 : 0) + (n & 1 ? 4 : 0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) *(uint16_t *)(blk + kv_value_run(a.c, place, run + e)) = (uint16_t)w[e];
+      for (int r = 0; r < 8; ++r) w[r] = (w[r] - KV_CODE0) << 4 * n;
+      or_half<0x4E, 8>(w, n & 2);
+      or_half<0xB1, 4>(w, n & 1);
+      if (!in) return;
+      const int run = (n & 2 ? 4 : 0) + (n & 1 ? 2 : 0);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        *(uint16_t *)(blk + kv_value_run(a.c, place, run + e)) = (uint16_t)w[e];
+        *(uint16_t *)(blk + kv_value_run(a.c, place, run + e + 8)) = (uint16_t)(w[e] >> 16);
+      }
     }
   }
 }
 
+// The other way, of the same lanes; bound by its writes (32768 tokens of 8 heads
+// of 128 channels to bf16 50 us, 3.4 TB/s) and by latency where tokens are few
+// (777 tokens 4.5 us).
 template <int D>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
   constexpr int NS = D / 32;
   const int head = blockIdx.y, side = blockIdx.z;
-  const KvPlace P = kv_place<D>(a.c, a.slots, a.tokens, side);
-  const bool in = P.slot >= 0;
+  KvPlace P = kv_place<D>(a.slots, a.tokens, side);
+  const bool in = kv_in(a.c, P);
   const uint8_t *blk = kv_block(a.c, in ? P.slot >> a.c.page_shift : 0, head);
   const int place = in ? P.slot & ((1 << a.c.page_shift) - 1) : 0;
   // eight values from element `at` on
@@ -390,11 +440,6 @@ __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
 
 // Whether the greater magnitudes of two halves (pk_max_mag) are not finite.
 __device__ __forceinline__ bool not_finite(uint32_t mag) { return (mag & 0xFFFF) >= 0x7F80 || mag >= 0x7F800000u; }
-// v, with no part of what is made of it moved ahead of the branch it stands in.
-__device__ __forceinline__ uint32_t hidden(uint32_t v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
 
 template <int D, int GROUP>
 __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn_cache_kernel(AttnCacheArgs a) {
