@@ -157,7 +157,7 @@ svq_status svq_attn_prompt(const void *q, int64_t ldq, const void *k, int64_t ld
   a.kv_heads = kv_heads;
   a.dim = head_dim;
   a.causal = causal;
-  a.window = window;
+  a.window = window < tokens_k ? window : 0;  // none hides a key; positions less the window stay 32-bit numbers
   a.scale = scale;
   return of(launch_attn_prompt(a, (hipStream_t)stream));
 }
@@ -179,6 +179,7 @@ svq_status svq_attn_cache(const svq_kv_cache *cache, const void *q, int64_t ldq,
     return SVQ_ERR_INVALID_ARG;
   if (ldq < cols || ldy < cols || window < 0 || !std::isfinite(scale)) return SVQ_ERR_INVALID_ARG;
   if (!on_16(q, ldq, 2) || !on_16(y, ldy, 2)) return SVQ_ERR_UNSUPPORTED;
+  if (window >= max_len) window = 0;  // hides no key; positions less the window stay 32-bit numbers
   const int R = q_heads / a.c.heads * q_len;
   a.row_tiles = (R + CACHE_ROWS - 1) / CACHE_ROWS;
   // Ranges of keys: for one round of blocks, two a compute unit (one sequence of

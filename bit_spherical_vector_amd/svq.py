@@ -1030,6 +1030,17 @@ class KvCache:
         """Columns of a row of keys or values."""
         return int(self.desc.kv_heads) * int(self.desc.head_dim)
 
+    def apart(self, t, what: str) -> None:
+        """Checks that a 2-D operand has no element in the cache's memory."""
+        if _overlaps(t, self.buf.view(-1)[:self.nbytes].view(1, -1)):
+            raise ValueError(f"{what} overlaps the cache")
+
+
+def _window_arg(window: int) -> int:
+    if not 0 <= window < 2 ** 31:
+        raise ValueError("window must be 0 (none) or a number of tokens below 2^31")
+    return int(window)
+
 
 def _ids_arg(t, what: str, n: int, device) -> None:
     """Checks a contiguous int32 vector on the operands' device."""
@@ -1071,6 +1082,8 @@ class KvWriteCall(_BareCall):
         ldk = _matrix_arg(k, "k", n, cache.width, dev, (torch.bfloat16,))
         ldv = _matrix_arg(v, "v", n, cache.width, dev, (torch.bfloat16,))
         _ids_arg(slots, "slots", n, dev)
+        cache.apart(k, "k")
+        cache.apart(v, "v")
         self.keep = (cache, k, v, slots)
         self._prepare("svq_kv_write", (ctypes.byref(cache.desc), k.data_ptr(), ldk, v.data_ptr(), ldv, n,
                                        slots.data_ptr()), dev, stream)
@@ -1091,6 +1104,8 @@ class KvReadCall(_BareCall):
         if _overlaps(k[:, :cache.width], v[:, :cache.width]):
             raise ValueError("k overlaps v")
         _ids_arg(slots, "slots", n, dev)
+        cache.apart(k, "k")
+        cache.apart(v, "v")
         self.keep = (cache, slots, k, v)
         self._prepare("svq_kv_read", (ctypes.byref(cache.desc), slots.data_ptr(), n, k.data_ptr(), ldk, v.data_ptr(),
                                       ldv, _dt(k, "k")), dev, stream)
@@ -1129,7 +1144,7 @@ class AttnPromptCall(_Call):
         self._prepare("svq_attn_prompt",
                       (q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, cols // head_dim, cols_k // head_dim,
                        head_dim, starts.data_ptr(), None if starts_k is None else starts_k.data_ptr(),
-                       starts.shape[0] - 1, n, nk, int(bool(causal)), window,
+                       starts.shape[0] - 1, n, nk, int(bool(causal)), _window_arg(window),
                        head_dim ** -0.5 if scale is None else float(scale), y.data_ptr(), ldy), dev, workspace, stream)
 
 
@@ -1157,7 +1172,10 @@ class AttnCacheCall(_Call):
         ldq, ldy = _matrix_arg(q, "q", n, cols, dev, bf), _matrix_arg(y, "y", n, cols, dev, bf)
         if _overlaps(q, y[:, :cols]):
             raise ValueError("y overlaps q")
+        cache.apart(y, "y")
         _ids_arg(lens, "lens", batch, dev)
+        if table.dim() != 2:
+            raise ValueError("table must be 2-D, a row of pages for each of lens")
         ldt = _matrix_arg(table, "table", batch, table.shape[1], dev, (torch.int32,))
         if max_len is None:
             max_len = table.shape[1] * int(cache.desc.page_size)
@@ -1166,7 +1184,7 @@ class AttnCacheCall(_Call):
         self.keep = (cache, q, y, table, lens)
         self._prepare("svq_attn_cache",
                       (ctypes.byref(cache.desc), q.data_ptr(), ldq, cols // dim, table.data_ptr(), ldt,
-                       lens.data_ptr(), batch, q_len, max_len, window, dim ** -0.5 if scale is None else float(scale),
+                       lens.data_ptr(), batch, q_len, max_len, _window_arg(window), dim ** -0.5 if scale is None else float(scale),
                        y.data_ptr(), ldy), dev, workspace, stream)
 
 

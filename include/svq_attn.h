@@ -98,7 +98,8 @@ svq_status svq_kv_write(const svq_kv_cache *cache, const void *k, int64_t ldk, c
 /* svq_kv_read: the values that the slots stand for, m + c * s in fp32,
  * rounded to bf16 or as they are; a slot outside [0, pages * page_size) gives
  * zeros.
- *   k, v:   device, out, [tokens][ldk], [tokens][ldv] of type dt. */
+ *   k, v:   device, out, [tokens][ldk], [tokens][ldv] of type dt; apart from
+ *           each other and from the cache. */
 svq_status svq_kv_read(const svq_kv_cache *cache, const int32_t *slots, int64_t tokens, void *k, int64_t ldk,
                        void *v, int64_t ldv, svq_dtype dt, void *stream);
 
@@ -116,7 +117,8 @@ svq_status svq_kv_read(const svq_kv_cache *cache, const int32_t *slots, int64_t 
  *   max_len:  1 .. ld_table * page_size, at most 2^30: what the launch is
  *             planned for.
  *   batch:    1 .. 65535; q_len: 1 .. 1024; scale: finite.
- *   y:        device bf16 [batch * q_len][ldy], out; must not overlap q. */
+ *   y:        device bf16 [batch * q_len][ldy], out; must not overlap q or the
+ *             cache. */
 svq_status svq_attn_cache(const svq_kv_cache *cache, const void *q, int64_t ldq, int32_t q_heads,
                           const int32_t *table, int64_t ld_table, const int32_t *lens, int64_t batch,
                           int32_t q_len, int64_t max_len, int32_t window, float scale, void *y, int64_t ldy,

@@ -264,3 +264,27 @@ def test_cache_attention_operands():
     _refused("table must be 2-D", lambda: make(c, q, y, t[:1], _i(2), q_len=2))
     _refused("table has the wrong type", lambda: make(c, q, y, t.long(), _i(2), q_len=2))
     _refused("more than the table", lambda: make(c, q, y, t, _i(2), q_len=2, max_len=49))
+
+
+def test_windows_are_32_bit_numbers():
+    c, t = _cpu_cache(), torch.zeros(2, 3, dtype=torch.int32)
+    for window in (-1, 2 ** 31, 2 ** 32 + 5):
+        _refused("window must be", lambda: svq.AttnPromptCall(_bf(6, 256), _bf(6, 128), _bf(6, 128), _bf(6, 256), _i(2), 64,
+                                                              window=window))
+        _refused("window must be", lambda: svq.AttnCacheCall(c, _bf(4, 256), _bf(4, 256), t, _i(2), q_len=2, window=window))
+    _refused("table must be 2-D", lambda: svq.AttnCacheCall(c, _bf(2, 256), _bf(2, 256), _i(2), _i(2)))
+
+
+def test_operands_apart_from_the_cache():
+    need = _cpu_cache().nbytes
+    memory = torch.zeros(need + 4 * 5 * 256, dtype=torch.uint8)
+    c = _cpu_cache(buf=memory[:need])
+    rows = lambda at: memory[at:at + 5 * 256].view(torch.bfloat16).view(5, 128)
+    inside, last, behind = rows(0), rows(need - 256), rows(need)
+    svq.KvWriteCall(c, behind, _bf(5, 128), _i(5))
+    svq.KvReadCall(c, _i(5), behind, _bf(5, 128))
+    _refused("k overlaps the cache", lambda: svq.KvWriteCall(c, inside, _bf(5, 128), _i(5)))
+    _refused("v overlaps the cache", lambda: svq.KvWriteCall(c, _bf(5, 128), last, _i(5)))
+    _refused("k overlaps the cache", lambda: svq.KvReadCall(c, _i(5), last, _bf(5, 128)))
+    _refused("v overlaps the cache", lambda: svq.KvReadCall(c, _i(5), behind, inside))
+    _refused("y overlaps the cache", lambda: svq.AttnCacheCall(c, _bf(5, 128), last, torch.zeros(5, 3, dtype=torch.int32), _i(5)))

@@ -247,3 +247,16 @@ def test_more_tiles_than_one_launch_takes():
         rows = slice(at, at + m)
         check(y[rows], *attend(q[rows], k[rows], v[rows], heads, kv, dim ** -0.5, visible(m, m)), m, P_BF16, f"sequence {s}")
     assert torch.isfinite(y.float()).all() and torch.all(y.float().abs().sum(dim=1) > 0)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 45, 3, 0])
+def test_windows_wider_than_the_keys(window):
+    """Queries whose positions lie before the first key beside some that see
+    keys, under windows up to the largest number."""
+    svq = require_gpu()
+    lens, lens_k, dim = [45, 2], [3, 40], 64
+    q, k, v = _rows(47, 4 * dim, 1), _rows(43, 2 * dim, 2), _rows(43, 2 * dim, 3)
+    y = svq.attn_prompt(q, k, v, _starts(lens), dim, starts_k=_starts(lens_k), window=window)
+    torch.cuda.synchronize()
+    _check(y, q, k, v, lens, lens_k, 4, 2, dim, True, window)
+    assert torch.all(y[:42] == 0) and torch.all(y[42:].abs().sum(dim=1) > 0)

@@ -352,3 +352,16 @@ def test_same_bits_captured_and_on_another_stream():
         replayed = y.clone()
         write()
         assert torch.equal(replayed, svq.attn_cache(cache, q, table, now))
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 6, 2, 0])
+def test_windows_wider_than_the_sequence(window):
+    """Queries before the first token beside some that see tokens, under
+    windows up to the largest number."""
+    svq = require_gpu()
+    lens, q_len, heads, kv, dim = [2, 70, 0, 1], 5, 4, 2, 64
+    cache, table, ks, vs = _filled(svq, lens, 16, kv, dim, 32)
+    q = _rows(len(lens) * q_len, heads * dim, 11)
+    y = svq.attn_cache(cache, q, table, _ints(lens), q_len=q_len, window=window)
+    torch.cuda.synchronize()
+    _check_cache(y, q, ks, vs, lens, q_len, heads, kv, dim, window)
