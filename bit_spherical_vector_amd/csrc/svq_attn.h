@@ -26,7 +26,7 @@ int compute_units();  // of the current device
 //           once.
 // Nibble order.  Nibbles 2i and 2i+1 of a byte come out of one shift as two
 // fp16 subnormals (c * 2^-24 and c * 16 * 2^-24), in pairs 4 nibbles apart.
-// Key words hold channel j of their eight at nibble KV_NIBBLE(j), so that the
+// Key words hold channel j of their eight at nibble kv_nibble(j), so that the
 // pairs are consecutive channels; value runs hold tile t at nibble t.
 struct KvView {
   uint8_t *base;

@@ -15,6 +15,24 @@
 // reads, when the keys of a step are taken in the order of those registers
 // (keys 16t + 4h + 0..3 and 16t + 8 + 4h + 0..3 in half h).  V is read
 // transposed out of LDS (ds_read_b64_tr_b16: four keys of one channel a lane).
+//
+// Tiles of 64 keys: two of K and two of V in LDS (64 KB at 128 channels, two
+// blocks a compute unit), copied by buffer loads while earlier ones are worked
+// on.  The next tile's score products are issued between this tile's weights,
+// so that the matrix unit runs while the vector unit takes exponentials.  More
+// rows a block (8 waves) halve the copies but leave one block a unit, which
+// waits for itself at every barrier: 2048 tokens 62 us against 51 of the same
+// kernel with 4.  Two teams of 4 waves on the same rows, every second tile
+// each, are no gain either (49 against 47): a tile takes 1800 cycles instead of
+// 2650, but a block's first loads and its end (18000 cycles) no longer overlap
+// another's tiles.
+//
+// What bounds it: over long prompts the matrix unit with the clock that the
+// power allows (65 % of the cycles busy; 16384 tokens, 32 heads of 128 channels,
+// causal: 1950-1970 us, 1.12 PFLOP/s, where a library product of 8192^3 reaches
+// 1.36); at 2048 tokens (44.7 us, 770 TFLOP/s) the block with the most keys,
+// alone on its unit for most of the time at 2650 cycles a tile, 1024 of them the
+// matrix unit's; for short sequences the first loads (5000 to 8000 cycles).
 #include "svq_attn.h"
 #include "svq_device.h"
 

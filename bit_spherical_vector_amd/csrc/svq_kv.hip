@@ -3,7 +3,6 @@
 #include "svq_attn.h"
 #include "svq_device.h"
 
-
 namespace svq {
 namespace {
 
@@ -128,8 +127,9 @@ __device__ __forceinline__ uint32_t hidden(uint32_t v) {
 // 32c + 8h + 7 of every step c with h = i = lane / 16, so that a lane's codes
 // are one piece of the layout and the wave's 16 tokens one stretch.  Lanes of
 // the value side: D / 16 a token, lane i the 16 channels of tile i.  blockIdx.y
-// is the head, blockIdx.z the side (heads and sides first, so that the blocks of
-// a row run together: 32768 tokens read back in 53 us against 50).
+// is the head, blockIdx.z the side; tokens come first (heads first, so that the
+// blocks of a row run together: 32768 tokens written in 70 us against 68, read
+// in 53 against 50).
 struct KvPlace {
   int64_t t;     // token
   int32_t slot;  // of the cache, or one that is not there
@@ -172,7 +172,7 @@ __device__ __forceinline__ void or_half(uint32_t *w, bool upper) {
 
 // One pass: a value is read once and leaves as a nibble.  Bound by instructions
 // (about 20 a value, a third of them extremes, exchanges and the parameters in
-// 64 bits; the registers are held to what lets 8 waves a unit run, 5 at 256
+// 64 bits; the registers are held to what lets 8 waves a SIMD run, 5 at 256
 // channels, where 4 and 6 take 71 and 66 us against 63): 32768 tokens of 8 heads
 // of 128 channels 45 us, 3.8 TB/s read and written, where a copy of as many
 // bytes takes 35.
@@ -381,6 +381,17 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
 // = m + E - 8: m a running maximum, raised once a score exceeds it by 6, E the
 // exponent of the greatest scale or minimum of a wave's first chunk, raised
 // once a p s_g overflows fp16.
+//
+// What bounds it: vector instructions, which take 89 % of the cycles at 64
+// sequences of up to 8192 tokens (75 us, 4.1 TB/s of the cache, 64 us at the
+// rate of a copy): 16 rows are what one product takes, so the codes of a key are
+// unpacked once for up to 16 query heads, and the weights (12 instructions a
+// pair and group) cost more than the codes.  A wave's chunks reach LDS by
+// copies one chunk ahead (into registers instead: 110 us); three stages gain
+// nothing.  Short contexts are latency: one sequence of 777 tokens 8.2 us, of
+// it 5.4 this launch (the length, the page, the first chunk, code that is not
+// in the instruction cache yet) and 2.4 the join.  More waves a block (8) or
+// more and shorter ranges cost what they gain.
 constexpr int CACHE_WAVES = 4, CACHE_STAGES = 2, CHUNK = 32, ROWS = 16;
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
@@ -777,8 +788,10 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
   if (part == 0) *(float2 *)(a.sums + 2 * at) = make_float2(ref, sum);
 }
 
-// Joins the key ranges of a row: a block a row, D / 4 threads a range, four
-// channels a thread.
+// Joins the key ranges of a row, numerators and sums brought to the greatest
+// reference and added in a fixed order: a block a row, D / 4 threads a range,
+// four channels a thread.  Latency (2.4 to 5 us); the reads are what the ranges
+// have just written.
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnCacheArgs a) {
   constexpr int T = D / 4, N = 256 / T;
