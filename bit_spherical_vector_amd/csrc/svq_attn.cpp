@@ -131,7 +131,12 @@ svq_status svq_attn_prompt(const void *q, int64_t ldq, const void *k, int64_t ld
   if (ldk > MAX_LD || ldv > MAX_LD) return SVQ_ERR_UNSUPPORTED;  // bytes within a tile of 64 keys are 32-bit
   // a grid of at most 2^23 blocks
   if (tokens * q_heads > (int64_t)1 << 29 || sequences * kv_heads > 1 << 21) return SVQ_ERR_UNSUPPORTED;
-  const size_t need = 256;  // unused
+  window = window < tokens_k ? window : 0;  // none hides a key; positions less the window stay 32-bit numbers
+  const PromptPlan plan = prompt_plan((int)tokens, (int)sequences, q_heads, kv_heads, PROMPT_WAVES, compute_units());
+  const int splits = prompt_splits(plan, tokens * q_heads, (int)sequences, (int)tokens_k, kv_heads, head_dim, window, compute_units());
+  const size_t rows = (size_t)tokens * q_heads * splits;  // of partial sums
+  const size_t part = splits > 1 ? align256(rows * head_dim * 4) : 0;
+  const size_t need = splits > 1 ? part + align256(rows * 16) : 256;
   if (!workspace) {
     *workspace_bytes = need;
     return SVQ_OK;
@@ -157,8 +162,13 @@ svq_status svq_attn_prompt(const void *q, int64_t ldq, const void *k, int64_t ld
   a.kv_heads = kv_heads;
   a.dim = head_dim;
   a.causal = causal;
-  a.window = window < tokens_k ? window : 0;  // none hides a key; positions less the window stay 32-bit numbers
+  a.window = window;
   a.scale = scale;
+  a.splits = splits;
+  if (splits > 1) {
+    a.part = (float *)workspace;
+    a.sums = (float *)((uint8_t *)workspace + part);
+  }
   return of(launch_attn_prompt(a, (hipStream_t)stream));
 }
 

@@ -77,7 +77,11 @@ struct AttnPromptArgs {
   int32_t heads, kv_heads, dim;
   int32_t causal, window;
   float scale;
+  int32_t splits;      // ranges of keys
+  float *part, *sums;  // splits > 1, [token][head][split] numerators [dim] and (maximum, reference, sum, far: 1, no keys: -1)
 };
+
+constexpr int PROMPT_WAVES = 4;  // of a block
 hipError_t launch_attn_prompt(const AttnPromptArgs &a, hipStream_t s);
 
 // Divisions by launch constants d, with multipliers 2^32 / d + 1 and
@@ -111,6 +115,26 @@ inline PromptPlan prompt_plan(int tokens, int sequences, int heads, int kv_heads
 // leaves every unit about as many keys (2048 tokens 51 -> 47 us).
 __host__ __device__ inline int prompt_tile(const PromptPlan &p, int turn) {
   return turn < p.half ? p.tiles - 1 - turn : turn - p.half;
+}
+
+// Ranges of keys a tile.  Few tiles (one key head of a long prompt, say) leave
+// units idle while each goes through all its keys.  A range more takes time off
+// the longest tile's `keys` / 64 steps (~1.3 us each at 128 channels) and adds
+// the writing and reading of every row's sums (~0.35 ns a row): the least is
+// near n = sqrt(keys / 64 * 4000 / rows).  No ranges under 1024 keys, where the
+// second launch takes what they give (512 keys, 4 heads: 13.8 us in two ranges,
+// 13.0 without).
+inline int prompt_splits(const PromptPlan &p, int64_t rows, int sequences, int tokens_k, int kv_heads, int dim, int window, int units) {
+  const int64_t blocks = (int64_t)p.tiles * kv_heads, round = dim == 256 ? units : 2 * units;
+  int64_t keys = tokens_k / sequences;
+  if (window > 0 && (int64_t)window + p.tokens < keys) keys = (int64_t)window + p.tokens;
+  if (keys < 1024) return 1;
+  int64_t most = 2 * round / blocks;  // no more than two rounds of blocks
+  if (most > 16) most = 16;
+  if (most > keys / 256) most = keys / 256;
+  int n = 1;
+  while (n < most && (n + 1) * (n + 1) * rows <= keys / 64 * 4000) ++n;
+  return n;
 }
 
 struct AttnCacheArgs {

@@ -84,6 +84,26 @@ hipError_t launch_attn_prompt(const AttnPromptArgs &a, hipStream_t) {
   }
   EXPECT(tiles <= p.tiles, "%ld tiles of %d", (long)tiles, p.tiles);
   EXPECT((int64_t)p.tiles * a.kv_heads <= 1 << 24, "%d tiles of %d heads", p.tiles, a.kv_heads);
+  EXPECT(a.splits >= 1 && a.splits <= 16, "%d ranges", a.splits);
+  if (a.splits > 1) {
+    EXPECT((int64_t)p.tiles * a.kv_heads * a.splits <= 1024, "%d ranges of %d tiles", a.splits, p.tiles);
+    const size_t rows = (size_t)a.tokens * a.heads * a.splits;
+    const uint8_t *part = (const uint8_t *)a.part, *sums = (const uint8_t *)a.sums;
+    EXPECT(part >= ws_base && part + rows * a.dim * 4 <= sums, "numerators");
+    EXPECT(sums + rows * 16 <= ws_base + ws_bytes, "sums");
+    // the ranges of a tile's keys, as the kernel derives them
+    for (int i = 0; i < 16; ++i) {
+      const int t0 = (int)pick(0, 40), t1 = t0 + (int)pick(-3, 300), n = std::max(t1 - t0, 0), per = (n + a.splits - 1) / a.splits;
+      int at = t0;
+      for (int sp = 0; sp < a.splits; ++sp) {
+        const int from = t0 + sp * per, to = std::min(t1, from + per);
+        if (from >= to) continue;
+        EXPECT(from == at, "range %d from %d after %d", sp, from, at);
+        at = to;
+      }
+      EXPECT(at == std::max(t0, t1), "ranges end at %d of %d", at, t1);
+    }
+  }
   if (p.tiles < 20000) {
     // every tile has its turn, over all launches of 65535 turns
     std::vector<int> seen(p.tiles, 0);
@@ -191,9 +211,10 @@ int main() {
         const int64_t ld = (int64_t)heads * dim, ldk = (int64_t)kv * dim;
         const int64_t most = std::min<int64_t>((1 << 29) / heads, 1 << 24);
         const int64_t tokens = pick(1, i < 6 ? std::min<int64_t>(5000, most) : most), seqs = pick(1, i % 2 ? 300 : 3);
+        const int span = i % 3 ? 0 : (int)pick(1, 3000);
         run("prompt", [&](void *ws, size_t *n) {
           return svq_attn_prompt(P, ld, P, ldk, P, ldk, heads, kv, dim, (const int32_t *)P, nullptr, seqs, tokens, tokens, 1,
-                                 0, 0.1f, P, ld, ws, n, nullptr);
+                                 span, 0.1f, P, ld, ws, n, nullptr);
         });
         const int ps = pages[rng() % 5], group = std::min(groups[rng() % 3], dim);
         svq_kv_cache c{P, 1000, ps, kv, dim, group};
