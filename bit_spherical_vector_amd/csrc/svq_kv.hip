@@ -89,6 +89,11 @@ __device__ __forceinline__ uint32_t kv_word(const uint32_t (&c)[4]) {
   return (((((c[3] << 4) + c[2]) << 4) + c[1]) << 4) + c[0] - KV_CODE0 * 0x1111u;
 }
 
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, b2));
+}
 __device__ __forceinline__ float lo_bf16(uint32_t p) { return bf16_bits_to_f32(p & 0xFFFFu); }
 __device__ __forceinline__ float hi_bf16(uint32_t p) { return __builtin_bit_cast(float, p & 0xFFFF0000u); }
 
@@ -297,8 +302,9 @@ __global__ __launch_bounds__(256, D == 256 ? 5 : 8) void kv_write_kernel(KvWrite
 }
 
 // The other way, of the same lanes; bound by its writes (32768 tokens of 8 heads
-// of 128 channels to bf16 50 us, 3.4 TB/s) and by latency where tokens are few
-// (777 tokens 4.5 us).
+// of 128 channels to bf16 48.7 us, 2.8 TB/s written, where a large copy writes
+// 2.4; past the caches, as streams, 2048 tokens take 18 us instead of 14) and by
+// latency where tokens are few (777 tokens 4.4 us).
 template <int D>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
   constexpr int NS = D / 32;
@@ -316,21 +322,25 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
     } else {
       u4 y;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) y[w] = (uint32_t)f32_to_bf16_bits(x[2 * w]) | (uint32_t)f32_to_bf16_bits(x[2 * w + 1]) << 16;
+      for (int w = 0; w < 4; ++w) y[w] = pk_bf16(x[2 * w], x[2 * w + 1]);
       *(u4 *)((uint16_t *)out + at) = y;
     }
   };
-  auto value = [&](uint32_t p, uint32_t code) { return in ? fmaf((float)code, lo_bf16(p), hi_bf16(p)) : 0.f; };
+  // the parameters of a slot that is not there are zeros, and so its values
+  auto param = [&](int s, int g) { return in ? *(const uint32_t *)(blk + kv_param(a.c, s, place, g)) : 0u; };
+  auto value = [&](uint32_t p, uint32_t code) { return fmaf((float)code, lo_bf16(p), hi_bf16(p)); };
   if (side == 0) {
     if (P.t >= a.tokens) return;
     uint32_t word[NS];
     __builtin_memcpy(word, __builtin_assume_aligned(blk + kv_key_word(a.c, place, P.i), D == 64 ? 8 : 16), sizeof(word));
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      const uint32_t p = *(const uint32_t *)(blk + kv_param(a.c, 0, place, s >> (a.c.group_shift - 5)));
+      const uint32_t p = param(0, s >> (a.c.group_shift - 5));
+      // nibble n in byte n / 2 of one of two words: a conversion each
+      const uint32_t nibbles[2] = {word[s] & 0x0F0F0F0Fu, word[s] >> 4 & 0x0F0F0F0Fu};
       float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = value(p, word[s] >> 4 * kv_nibble(j) & 15);
+      for (int j = 0; j < 8; ++j) x[j] = value(p, nibbles[kv_nibble(j) & 1] >> 8 * (kv_nibble(j) >> 1) & 255);
       store(a.k, P.t * a.ldk + head * D + 32 * s + 8 * P.i, x);
     }
   } else {
@@ -344,7 +354,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
       const uint8_t *run = blk + kv_value_run(a.c, place, n * PER + e);
       own[e] = D == 64 ? *(const uint16_t *)run : *(const uint32_t *)(run + 4 * (P.i >> 3));
     }
-    const uint32_t p = *(const uint32_t *)(blk + kv_param(a.c, 1, place, P.i >> (a.c.group_shift - 4)));
+    const uint32_t p = param(1, P.i >> (a.c.group_shift - 4));
     float x[2][8];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
