@@ -93,6 +93,7 @@ __host__ __device__ inline int quotient16(int n, uint32_t mul) { return (int)((u
 // heads that share a key head, in 32 rows a wave.
 struct PromptPlan {
   int32_t tiles, half;         // see prompt_tile
+  int32_t first;               // turn of a launch's first block
   int32_t tokens, G;           // tokens = 32 * waves / G
   uint32_t tokens_mul, g_mul;  // for quotient, quotient16
 };
@@ -107,14 +108,26 @@ inline PromptPlan prompt_plan(int tokens, int sequences, int heads, int kv_heads
   p.tiles = tokens / p.tokens + sequences;
   const int round = units / kv_heads;
   p.half = round > 0 && p.tiles > round && p.tiles - sequences <= 2 * round ? round : p.tiles;
+  p.first = 0;
   return p;
 }
-// The tile that takes its turn.  The last tiles come first: under a causal
+// The tile of a launch's block, by its turn.  The last tiles come first: under a causal
 // mask they have the most keys.  Where one round of blocks, two a compute unit,
 // covers all, the second on each unit takes the tiles from the front on, which
 // leaves every unit about as many keys (2048 tokens 51 -> 47 us).
-__host__ __device__ inline int prompt_tile(const PromptPlan &p, int turn) {
+__host__ __device__ inline int prompt_tile(const PromptPlan &p, int block) {
+  const int turn = p.first + block;
   return turn < p.half ? p.tiles - 1 - turn : turn - p.half;
+}
+// Calls launch(plan, blocks) for all turns, at most 65535 at a time (the end of
+// the grid's second dimension).
+template <typename F>
+inline void prompt_launches(PromptPlan p, F launch) {
+  while (p.first < p.tiles) {
+    const int n = p.tiles - p.first < 65535 ? p.tiles - p.first : 65535;
+    launch(p, n);
+    p.first += n;
+  }
 }
 
 // Ranges of keys a tile.  Few tiles (one key head of a long prompt, say) leave

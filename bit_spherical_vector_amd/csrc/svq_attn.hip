@@ -581,14 +581,9 @@ hipError_t launch(const AttnPromptArgs &a, hipStream_t s) {
   const hipError_t e = allow_smem(attn_prompt_kernel<D, NW>, lds);
   if (e != hipSuccess) return e;
   const PromptPlan plan = prompt_plan(a.tokens, a.sequences, a.heads, a.kv_heads, NW, compute_units());
-  for (int done = 0; done < plan.tiles;) {
-    // the grid's second dimension ends at 65535
-    const int n = plan.tiles - done < 65535 ? plan.tiles - done : 65535;
-    PromptPlan p = plan;
-    p.tiles -= done;
+  prompt_launches(plan, [&](const PromptPlan &p, int n) {
     attn_prompt_kernel<D, NW><<<dim3(a.kv_heads, n, a.splits), 64 * NW, lds, s>>>(a, p);
-    done += n;
-  }
+  });
   if (a.splits > 1) {
     const int64_t rows = (int64_t)a.tokens * a.heads, per = 256 / (D / 4);
     prompt_join_kernel<D><<<dim3((unsigned)((rows + per - 1) / per)), 256, 0, s>>>(a);

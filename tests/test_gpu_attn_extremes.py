@@ -1,0 +1,92 @@
+"""The attention calls at the ends of their range: scores far from zero,
+scales of every size, values and queries of very different sizes, more tiles
+than a launch takes, and rows beside others that see more."""
+import pytest
+
+from tests.attn_common import P_BF16, P_F16, attend, cache_floor, check, stored, visible
+from tests.gpu_common import require_gpu, torch
+
+pytestmark = pytest.mark.gpu
+
+FORMS = [(d, g) for d in (64, 128, 256) for g in (32, 64, 128) if g <= d]
+
+
+def _ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def _rows(n, cols, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (scale * torch.randn(n, cols, generator=g)).to(torch.bfloat16).cuda()
+
+
+def _one_sequence(svq, k, v, kv, dim, group, page=16):
+    """A cache that holds one sequence on pages in falling order."""
+    n = k.shape[0]
+    need = -(-n // page)
+    cache = svq.KvCache(need + 1, page, kv, dim, group=group)
+    cache.buf.fill_(255)
+    pages = list(range(need, 0, -1))
+    _write(svq, cache, k, v, pages, 0)
+    return cache, pages, _ints([pages])
+
+
+def _write(svq, cache, k, v, pages, first):
+    page = int(cache.desc.page_size)
+    slots = [pages[j // page] * page + j % page for j in range(first, first + k.shape[0])]
+    svq.kv_write(cache, k.contiguous(), v.contiguous(), _ints(slots))
+
+
+# ---- turns of tiles ---------------------------------------------------------
+
+def test_more_sequences_than_a_launch_takes():
+    """65535 sequences of one token are as many tiles beside 511 that are not
+    there, in two launches; a token that sees itself alone gets its value."""
+    svq = require_gpu()
+    n, dim = 65535, 64
+    q, k, v = _rows(n, dim, 1), _rows(n, dim, 2), _rows(n, dim, 3)
+    starts = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    y = svq.attn_prompt(q, k, v, starts, dim)
+    torch.cuda.synchronize()
+    gone = torch.nonzero((y != v).any(dim=1))[:, 0].tolist()
+    assert not gone, f"{len(gone)} rows from {gone[0]} on"
+
+
+# ---- scores far from zero ---------------------------------------------------
+#
+# Keys whose scores are fp32 numbers: channel 0 brings 255 * 2^26 (q 255 * 2^13,
+# k 2^13), another channel j * 1024, the fp32 step there.  So the products and
+# their sums are exact, and a score's error is that of its difference to the
+# greatest one times the scale: relative 2^-22 for the product and the rounded
+# scale, of at most 64 where it matters (weights below e^-64 do not): 2^-16.
+FAR_ERR = 2.0 ** -16
+FAR_SCALES = [2.0 ** -14, 2.0 ** -10, 2.0 ** -6, 0.125, 8.0]
+
+
+def _far(n, dim, step, base=True):
+    """q row and keys [n, dim]; key j's score is base + step[j] * 1024.  Every
+    group of 32 channels is held exactly in 4 bits: a constant one, or whole
+    numbers from 0 to 15."""
+    q, k = torch.zeros(1, dim), torch.zeros(n, dim)
+    if base:
+        q[0, 0], k[:, :32] = 255 * 2.0 ** 13, 2.0 ** 13
+    q[0, 32] = 1024.0
+    k[:, 32], k[:, 33] = step, 15.0
+    return q.to(torch.bfloat16).cuda(), k.to(torch.bfloat16).cuda()
+
+
+def _far_reference(step, v, scale):
+    p = torch.softmax(torch.as_tensor(step).double() * 1024 * scale, dim=0)
+    v = v.detach().cpu().double()
+    return (p @ v)[None], (p @ v.abs())[None], torch.full((1, v.shape[1]), FAR_ERR, dtype=torch.float64)
+
+
+def _steps(n, kind):
+    j = torch.arange(n)
+    if kind == "late":      # the greatest by one step, in a late tile
+        return (j == n - 3).float()
+    if kind == "rising":
+        return (j * 16 // n).float()
+    if kind == "falling":
+        return 15.0 - (j * 16 // n).float()
+    return (j * 7 % 16).float()
