@@ -386,8 +386,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       maximum(S);
     }
     // a new reference only once the maximum has grown by 2^8: weights up to
-    // 256 are as exact as weights up to 1
-    if (__any(top * sc > (m == -__FLT_MAX__ ? -__builtin_inff() : mref + 8.f))) {
+    // 256 are as exact as weights up to 1 (the growth formed before the scale:
+    // beyond 2^27 a scaled maximum and the reference are 16 and more apart)
+    if (__any(m == -__FLT_MAX__ ? top > m : (top - m) * sc > 8.f)) {
       const float old = mref, old_m = m;
       const bool first = m == -__FLT_MAX__;
       m = fmaxf(m, max_halves(top));

@@ -90,3 +90,16 @@ def _steps(n, kind):
     if kind == "falling":
         return 15.0 - (j * 16 // n).float()
     return (j * 7 % 16).float()
+
+
+@pytest.mark.parametrize("kind", ["late", "rising", "falling", "mixed"])
+@pytest.mark.parametrize("scale", FAR_SCALES)
+@pytest.mark.parametrize("n", [200, 1300])
+def test_prompt_scores_one_step_apart(n, scale, kind):
+    svq = require_gpu()
+    step = _steps(n, kind)
+    for dim in (64, 128, 256):
+        q, k = _far(n, dim, step)
+        v = _rows(n, dim, 4)
+        y = svq.attn_prompt(q, k, v, _ints([0, 1]), dim, starts_k=_ints([0, n]), scale=scale)
+        check(y, *_far_reference(step, v, scale), n, P_BF16, f"{dim} channels")
