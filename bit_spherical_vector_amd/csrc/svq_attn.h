@@ -78,7 +78,7 @@ struct AttnPromptArgs {
   int32_t causal, window;
   float scale;
   int32_t splits;      // ranges of keys
-  float *part, *sums;  // splits > 1, [token][head][split] numerators [dim] and (maximum, reference, sum, far: 1, no keys: -1)
+  float *part, *sums;  // splits > 1, [token][head][split] numerators [dim] and (maximum, how far it lies above the reference, sum, no keys: -1)
 };
 
 constexpr int PROMPT_WAVES = 4;  // of a block

@@ -309,6 +309,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     for (int kb = 0; kb < 2; ++kb) kf[s & 1][kb] = *(const lds_u4 *)(lds_t *)(uintptr_t)(at + kb * 32 * ROW);
   };
 
+  // How far the scaled maximum lies above the rounded reference that the weights
+  // are taken from (up to a half near 2^24; a far one's are taken from the maximum).
+  auto above = [&]() { return far_any || m == -__FLT_MAX__ ? 0.f : fmaf(m, sc, -mref); };
+
   // Tile t, its V in `place`: S holds its scores and N takes the next tile's.
   float top = 0.f;
   auto maximum = [&](const f16x (&S)[2]) {
@@ -389,12 +393,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     // 256 are as exact as weights up to 1 (the growth formed before the scale:
     // beyond 2^27 a scaled maximum and the reference are 16 and more apart)
     if (__any(m == -__FLT_MAX__ ? top > m : (top - m) * sc > 8.f)) {
-      const float old = mref, old_m = m;
+      const float old_m = m, old_above = above();
       const bool first = m == -__FLT_MAX__;
       m = fmaxf(m, max_halves(top));
       mref = m == -__FLT_MAX__ ? 0.f : m * sc;
       far_any = __any(fabsf(mref) > 16777216.f);
-      const float alpha = first ? 0.f : __builtin_amdgcn_exp2f(far_any ? (old_m - m) * sc : old - mref);
+      const float alpha = first ? 0.f : __builtin_amdgcn_exp2f((old_m - m) * sc + (above() - old_above));
       l *= alpha;
 #pragma unroll
       for (int db = 0; db < NB; ++db)
@@ -517,7 +521,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   l = sum_halves(l);
   if (a.splits > 1) {
     const int64_t at = (row_off * a.heads + head) * a.splits + blockIdx.z;
-    if (h == 0) *(f4 *)(a.sums + 4 * at) = (f4){m, mref, l, t0 >= t1 ? -1.f : far_any ? 1.f : 0.f};
+    if (h == 0) *(f4 *)(a.sums + 4 * at) = (f4){m, above(), l, t0 >= t1 ? -1.f : 0.f};
     if (t0 >= t1) return;  // no keys: its numerators are not read
     float *part = a.part + at * D + 4 * h;
 #pragma unroll
@@ -549,15 +553,9 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(AttnPromptArgs a) {
   if (token < max(a.starts[0], 0) || token >= min(a.starts[a.sequences], a.tokens)) return;
   const f4 *sums = (const f4 *)a.sums + row * a.splits;
   const float sc = exponent_scale(a.scale);
-  float m = -__FLT_MAX__, ref = 0.f;
-  bool far = false;
+  float m = -__FLT_MAX__;
 #pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
-    const f4 x = sums[s];
-    ref = x[0] > m ? x[1] : ref;
-    m = fmaxf(m, x[0]);
-    far = far || x[3] > 0.f;
-  }
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, sums[s][0]);
   f4 o = {};
   float sum = 0.f;
   const f4 *num = (const f4 *)(a.part + row * a.splits * D) + part;
@@ -566,7 +564,7 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(AttnPromptArgs a) {
     const f4 x = sums[s], v = num[(int64_t)s * T];
     // a range in which the row sees nothing has zeros, one without keys has
     // left what was there
-    const float f = x[0] == -__FLT_MAX__ && x[2] == 0.f ? 0.f : __builtin_amdgcn_exp2f(far ? (x[0] - m) * sc : x[1] - ref);
+    const float f = x[0] == -__FLT_MAX__ && x[2] == 0.f ? 0.f : __builtin_amdgcn_exp2f((x[0] - m) * sc - x[1]);
     sum += x[2] * f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] += x[3] < 0.f ? 0.f : fabsf(v[e]) < __builtin_inff() ? v[e] * f : v[e];

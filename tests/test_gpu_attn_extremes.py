@@ -63,13 +63,12 @@ FAR_ERR = 2.0 ** -16
 FAR_SCALES = [2.0 ** -14, 2.0 ** -10, 2.0 ** -6, 0.125, 8.0]
 
 
-def _far(n, dim, step, base=True):
-    """q row and keys [n, dim]; key j's score is base + step[j] * 1024.  Every
+def _far(n, dim, step, base=255):
+    """q row and keys [n, dim]; key j's score is base * 2^26 + step[j] * 1024.  Every
     group of 32 channels is held exactly in 4 bits: a constant one, or whole
     numbers from 0 to 15."""
     q, k = torch.zeros(1, dim), torch.zeros(n, dim)
-    if base:
-        q[0, 0], k[:, :32] = 255 * 2.0 ** 13, 2.0 ** 13
+    q[0, 0], k[:, :32] = base * 2.0 ** 13, 2.0 ** 13
     q[0, 32] = 1024.0
     k[:, 32], k[:, 33] = step, 15.0
     return q.to(torch.bfloat16).cuda(), k.to(torch.bfloat16).cuda()
@@ -100,6 +99,23 @@ def test_prompt_scores_one_step_apart(n, scale, kind):
     step = _steps(n, kind)
     for dim in (64, 128, 256):
         q, k = _far(n, dim, step)
+        v = _rows(n, dim, 4)
+        y = svq.attn_prompt(q, k, v, _ints([0, 1]), dim, starts_k=_ints([0, n]), scale=scale)
+        check(y, *_far_reference(step, v, scale), n, P_BF16, f"{dim} channels")
+
+
+@pytest.mark.parametrize("n", [1000, 1600])  # without and with ranges of keys
+@pytest.mark.parametrize("base,below", [(241, 0.1), (248, 1.1), (250, 0.2), (255, 7.4)])
+def test_prompt_scores_that_pass_two_to_the_24th(base, below, n):
+    """Most keys' scores lie a little below 2^24 (base 2), one ten beyond it;
+    how both are formed changes there."""
+    svq = require_gpu()
+    scale = (2.0 ** 24 - below) / (base * 2.0 ** 26 * 1.4426950408889634)
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    for dim in (64, 128, 256):
+        step = torch.zeros(n)
+        step[600] = 10
+        q, k = _far(n, dim, step, base)
         v = _rows(n, dim, 4)
         y = svq.attn_prompt(q, k, v, _ints([0, 1]), dim, starts_k=_ints([0, n]), scale=scale)
         check(y, *_far_reference(step, v, scale), n, P_BF16, f"{dim} channels")
