@@ -159,7 +159,7 @@ struct AttnCacheArgs {
   int32_t batch, q_len, heads, max_len, window;
   float scale;
   int32_t row_tiles, splits;  // tiles of 16 rows, ranges of keys
-  float *part, *sums;         // splits > 1: [batch][kv head][row][split] numerators [dim] and (reference, sum)
+  float *part, *sums;         // splits > 1: [batch][kv head][row][split] results [dim] and (maximum, sum of weights)
 };
 // rows of a tile, keys of a block's step, steps of a block at most
 constexpr int CACHE_ROWS = 16, CACHE_BLOCK_KEYS = 128, CACHE_MAX_STEPS = 16;

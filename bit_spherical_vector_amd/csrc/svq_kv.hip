@@ -91,6 +91,7 @@ __device__ __forceinline__ uint32_t kv_word(const uint32_t (&c)[4]) {
 
 typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 typedef float f2 __attribute__((ext_vector_type(2)));
+typedef double d4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, b2));
 }
@@ -385,12 +386,13 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
 //        of 2^(E - 8) as the sum of two fp16 numbers, 22 bits: the minimum's
 //        term below cancels much of this one, and with 11 bits a value near
 //        zero would carry the rounding of its whole range)
-//   M_g[row]          += sum over keys of p m_g                (fp32)
+//   M_g[row]          += sum over keys of p m_g                (fp32, in the same units)
 //
-// and the row is (2^24 O + M) / sum p.  The weight p is exp2(score - ref), ref
-// = m + E - 8: m a running maximum, raised once a score exceeds it by 6, E the
-// exponent of the greatest scale or minimum of a wave's first chunk, raised
-// once a p s_g overflows fp16.
+// and the row is 2^(E - 8) (2^24 O + M) / sum p.  The weight p is exp2 of (score
+// - m) times the scale: m a running maximum, raised once a weight exceeds 2^6, E
+// the exponent of the greatest scale or minimum of a wave's first chunk, raised
+// once a p s_g overflows fp16.  The two are kept apart: in one fp32 number a
+// maximum from 2^24 on would round E away.
 //
 // What bounds it: vector instructions, which take 89 % of the cycles at 64
 // sequences of up to 8192 tokens (75 us, 4.1 TB/s of the cache, 64 us at the
@@ -431,17 +433,10 @@ __device__ __forceinline__ u4 nibbles(uint32_t w) {
 __device__ __forceinline__ f4 mfma_f16(const u4 &a, const u4 &b, const f4 &c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
 }
-// Channels 64 i + 4 part .. of a row: numerators over their sum, rounded once.
-template <int D>
-__device__ __forceinline__ void store_row(uint16_t *y, int part, const f4 (&o)[D / 64], float sum) {
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const f4 v = o[i] * inv;
-    *(u2 *)(y + 64 * i + 4 * part) = (u2){(uint32_t)f32_to_bf16_bits(v[0]) | (uint32_t)f32_to_bf16_bits(v[1]) << 16,
-                                          (uint32_t)f32_to_bf16_bits(v[2]) | (uint32_t)f32_to_bf16_bits(v[3]) << 16};
-  }
-}
+__device__ __forceinline__ u2 row_bf16(const f4 &v) { return (u2){pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])}; }
+// Exponents are base 2; a scale of zero stays a number that keeps hidden scores
+// at -infinity.
+__device__ __forceinline__ float exponent_scale(float scale) { return fmaxf(fabsf(scale) * 1.44269504088896f, 0x1p-149f); }
 // The dwords of lane-consecutive pieces of N dwords.
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
@@ -565,6 +560,7 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
 #pragma unroll
       for (int w = 0; w < 4; ++w) mx = pk_max_finite(mx, raw[s][w]);
   }
+  const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
   const float q_top = row_max(fmaxf(lo_bf16(mx), hi_bf16(mx)));
   const int qe = q_top > 0.f ? 15 - __builtin_amdgcn_frexp_expf(q_top) : 0;
 #pragma unroll
@@ -573,14 +569,14 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
   for (int s = 0; s < NS; ++s)
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const float x = lo_bf16(raw[s][w]), y = hi_bf16(raw[s][w]);
+      const float x = lo_bf16(raw[s][w] ^ flip), y = hi_bf16(raw[s][w] ^ flip);
       qsum[s / SPG] += ldexpf(x, -8) + ldexpf(y, -8);  // 256 of the greatest numbers stay a number
       const int e = w & 1 ? qe - 4 : qe;
       qf[s][w] = __builtin_bit_cast(uint32_t, (h2){(_Float16)ldexpf(x, e), (_Float16)ldexpf(y, e)});
     }
 #pragma unroll
   for (int g = 0; g < G; ++g) qsum[g] = ldexpf(row_sum(qsum[g]), qe + 8 - 24);
-  const float sc = a.scale * 1.44269504088896f;
+  const float sc = exponent_scale(a.scale);
   const int se = 24 - qe;
 
   f4 O[NT];
@@ -591,7 +587,6 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
 #pragma unroll
   for (int g = 0; g < G; ++g) M[g] = 0.f;
   auto rescale = [&](float f) {
-    l *= f;
 #pragma unroll
     for (int g = 0; g < G; ++g) M[g] *= f;
 #pragma unroll
@@ -629,7 +624,7 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
         for (int i = 0; i < 4; ++i) t[j][i] = fmaf(lo_bf16(kp[i]), A[i], fmaf(hi_bf16(kp[i]), qsum[g], t[j][i]));
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t[j][i] = ldexpf(t[j][i] * sc, se);
+      for (int i = 0; i < 4; ++i) t[j][i] = ldexpf(t[j][i], se);
     }
     u4 vp[2][G];
 #pragma unroll
@@ -653,14 +648,15 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
     float top = t[0][0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = fmaxf(top, t[i >> 2][i & 3]);
-    if (__any(top > m + 6.f)) {
-      const float now = fmaxf(m, row_max(top));
-      rescale(__builtin_amdgcn_exp2f(m - now));
+    if (__any(m == -__FLT_MAX__ ? top > m : (top - m) * sc > 6.f)) {
+      const float now = fmaxf(m, row_max(top)), f = __builtin_amdgcn_exp2f((m - now) * sc);
+      l *= f;
+      rescale(f);
       m = now;
     }
     float p[2][4], pm[G];
     u4 w[G], rest[G];
-    // E to the greatest finite scale or minimum that a row sees here; true if
+    // E to the greatest finite scale or minimum that a row sees here; by how much
     // it has risen
     auto raise = [&]() {
       uint32_t most = 0;
@@ -682,19 +678,21 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
       float big = fmaxf(lo_bf16(most), hi_bf16(most));
       big = row_max(lanes_max(big, 16));
       const int now = __builtin_amdgcn_readfirstlane(big > 0.f ? __builtin_amdgcn_frexp_expf(big) : E);
-      if (now <= E) return false;
-      rescale(ldexpf(1.f, E - now));
-      E = now;
-      return true;
+      const int by = max(now - E, 0);
+      if (by > 0) rescale(ldexpf(1.f, -by));
+      E += by;
+      return by;
     };
     if (n == 0) raise();
+    const float unit = ldexpf(1.f, 8 - E);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = __builtin_amdgcn_exp2f((t[i >> 2][i & 3] - m) * sc);
+      l += x;
+      p[i >> 2][i & 3] = x * unit;
+    }
 #pragma unroll 1
     for (;;) {
-      const float ref = m + (float)(E - 8);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[j][i] = __builtin_amdgcn_exp2f(t[j][i] - ref);
       us2_t most = {0, 0};
       float far = 0.f;
 #pragma unroll
@@ -716,10 +714,11 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
         far = fmaxf(far, fabsf(pm[g]));
       }
       if (__builtin_expect(!__any(most[0] >= 0x7C00 || most[1] >= 0x7C00 || far > 0x1p100f), 1)) break;
-      if (!raise()) break;  // what does not fit then is not finite
-    }
+      const int by = raise();
+      if (by == 0) break;  // what does not fit then is not finite
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l += p[i >> 2][i & 3];
+      for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = ldexpf(p[i >> 2][i & 3], -by);
+    }
 #pragma unroll
     for (int g = 0; g < G; ++g) M[g] += pm[g];
     // value runs: dword w of a key holds tiles 8w .. 8w + 7 (at 64 channels
@@ -754,10 +753,11 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
   }
   __syncthreads();  // the waves' copies share their place with what follows
 
-  // the waves meet in LDS: numerators [wave][row][D], then references and sums
-  // (a wave without keys brings zeros under the least reference)
+  // the waves meet in LDS: numerators [wave][row][D], then maxima, exponents and
+  // sums (a wave without keys brings zeros under the least maximum)
   float *s_o = (float *)smem;
-  float *s_ref = s_o + CACHE_WAVES * ROWS * (D + 4), *s_l = s_ref + CACHE_WAVES * ROWS;
+  float *s_m = s_o + CACHE_WAVES * ROWS * (D + 4), *s_l = s_m + CACHE_WAVES * ROWS;
+  int *s_e = (int *)(s_l + CACHE_WAVES * ROWS);
   l = row_sum(l);
   float *mine = s_o + (wv * ROWS + col) * (D + 4);
 #pragma unroll
@@ -765,66 +765,79 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
 #pragma unroll
   for (int n = 0; n < NT; ++n) *(f4 *)(mine + 16 * n + 4 * h) = O[n] * (n & 1 ? 0x1p20f : 0x1p24f) + M[n / TPG];
   if (h == 0) {
-    s_ref[wv * ROWS + col] = m + (float)(E - 8);
+    s_m[wv * ROWS + col] = m;
     s_l[wv * ROWS + col] = l;
+    s_e[wv * ROWS + col] = E - 8;
   }
   __syncthreads();
   const int row = tid >> 4, part = tid & 15;  // 16 threads a row, D / 16 channels each
   const int q_row = rt * ROWS + row;
   if (q_row >= R) return;
-  float ref = -__FLT_MAX__, sum = 0.f, f[CACHE_WAVES];
+  float most = -__FLT_MAX__, sum = 0.f, f[CACHE_WAVES];
 #pragma unroll
-  for (int w = 0; w < CACHE_WAVES; ++w) ref = fmaxf(ref, s_ref[w * ROWS + row]);
+  for (int w = 0; w < CACHE_WAVES; ++w) most = fmaxf(most, s_m[w * ROWS + row]);
+  int unit = -1024;  // the greatest exponent of those whose weights count
 #pragma unroll
   for (int w = 0; w < CACHE_WAVES; ++w) {
-    f[w] = __builtin_amdgcn_exp2f(s_ref[w * ROWS + row] - ref);
+    f[w] = __builtin_amdgcn_exp2f((s_m[w * ROWS + row] - most) * sc);
     sum += s_l[w * ROWS + row] * f[w];
+    unit = f[w] > 0.f ? max(unit, s_e[w * ROWS + row]) : unit;
   }
+#pragma unroll
+  for (int w = 0; w < CACHE_WAVES; ++w) f[w] = ldexpf(f[w], s_e[w * ROWS + row] - unit);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   f4 out[D / 64];
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) {
     out[i] = (f4){};
 #pragma unroll
     for (int w = 0; w < CACHE_WAVES; ++w) out[i] += *(const f4 *)(s_o + (w * ROWS + row) * (D + 4) + 64 * i + 4 * part) * f[w];
+    out[i] *= inv;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[i][e] = ldexpf(out[i][e], unit);
   }
   if (a.splits == 1) {
     const int token = a.q_len > 1 ? q_row / shared : 0;
-    store_row<D>(a.y + (int64_t)(b * a.q_len + token) * a.ldy + (kvh * shared + q_row - token * shared) * D, part, out, sum);
+    uint16_t *y = a.y + (int64_t)(b * a.q_len + token) * a.ldy + (kvh * shared + q_row - token * shared) * D + 4 * part;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) *(u2 *)(y + 64 * i) = row_bf16(out[i]);
     return;
   }
   const int64_t at = (((int64_t)b * c.heads + kvh) * R + q_row) * a.splits + sp;
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) *(f4 *)(a.part + at * D + 64 * i + 4 * part) = out[i];
-  if (part == 0) *(float2 *)(a.sums + 2 * at) = make_float2(ref, sum);
+  if (part == 0) *(float2 *)(a.sums + 2 * at) = make_float2(most, sum);
 }
 
-// Joins the key ranges of a row, numerators and sums brought to the greatest
-// reference and added in a fixed order: a block a row, D / 4 threads a range,
-// four channels a thread.  Latency (2.4 to 5 us); the reads are what the ranges
-// have just written.
+// Joins the key ranges of a row, each range's own result under its sum of
+// weights, added in a fixed order: a block a row, D / 4 threads a range, four
+// channels a thread.  (Sums in 64 bits: the weights' sums reach 2^36 where the
+// results may be any fp32 number.)  Latency (2.4 to 5 us); the reads are what the
+// ranges have just written.
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnCacheArgs a) {
   constexpr int T = D / 4, N = 256 / T;
-  __shared__ f4 s_o[N][T];
+  __shared__ d4 s_o[N][T];
   __shared__ float s_l[N];
   const int tid = threadIdx.x, lane = tid & 63, part = tid % T, first = tid / T;
   const int shared = a.heads / a.c.heads, R = shared * a.q_len;
   const int64_t at = blockIdx.x;
+  const float sc = exponent_scale(a.scale);
   const float2 *sums = (const float2 *)a.sums + at * a.splits;
-  float ref = -__FLT_MAX__;
-  for (int s = lane; s < a.splits; s += 64)
-    ref = fmaxf(ref, sums[s].x);
-  for (int d = 32; d; d >>= 1) ref = fmaxf(ref, __shfl_xor(ref, d));
+  float m = -__FLT_MAX__;
+  for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, sums[s].x);
+  m = row_max(lanes_max(m, 16));
   float sum = 0.f;
-  f4 o = {};
-  const f4 *num = (const f4 *)(a.part + at * a.splits * D) + part;
+  d4 o = {};
+  const f4 *value = (const f4 *)(a.part + at * a.splits * D) + part;
 #pragma unroll 4
   for (int s = first; s < a.splits; s += N) {
     const float2 x = sums[s];
-    const f4 v = num[(int64_t)s * T];
-    const float f = __builtin_amdgcn_exp2f(x.x - ref);  // a range without keys has left zeros
-    sum += x.y * f;
-    o += v * f;
+    const f4 v = value[(int64_t)s * T];
+    const float w = x.y * __builtin_amdgcn_exp2f((x.x - m) * sc);  // 0 of a range without keys
+    sum += w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += (double)v[e] * w;
   }
   s_o[first][part] = o;
   if (part == 0) s_l[first] = sum;
@@ -834,18 +847,18 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnCacheArgs a) {
     o += s_o[n][part];
     sum += s_l[n];
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const double inv = sum == 0.f ? 0. : (double)(1.f / sum);
   const int q_row = (int)(at % R), kvh = (int)(at / R % a.c.heads);
   const int64_t b = at / R / a.c.heads;
-  uint16_t *y = a.y + (b * a.q_len + q_row / shared) * a.ldy + (kvh * shared + q_row % shared) * D + 4 * part;
-  o *= inv;
-  *(u2 *)y = (u2){(uint32_t)f32_to_bf16_bits(o[0]) | (uint32_t)f32_to_bf16_bits(o[1]) << 16,
-                  (uint32_t)f32_to_bf16_bits(o[2]) | (uint32_t)f32_to_bf16_bits(o[3]) << 16};
+  f4 y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = (float)(o[e] * inv);
+  *(u2 *)(a.y + (b * a.q_len + q_row / shared) * a.ldy + (kvh * shared + q_row % shared) * D + 4 * part) = row_bf16(y);
 }
 
 template <int D, int GROUP>
 hipError_t launch_cache(const AttnCacheArgs &a, hipStream_t s) {
-  constexpr int G = D / GROUP, copies = CACHE_STAGES * 2 * (16 * D + 128 * G), joined = ROWS * (D + 6) * 4;
+  constexpr int G = D / GROUP, copies = CACHE_STAGES * 2 * (16 * D + 128 * G), joined = ROWS * (D + 7) * 4;
   constexpr size_t lds = (size_t)CACHE_WAVES * (copies > joined ? copies : joined);
   const hipError_t e = allow_smem(attn_cache_kernel<D, GROUP>, lds);
   if (e != hipSuccess) return e;

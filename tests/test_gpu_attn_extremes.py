@@ -119,3 +119,76 @@ def test_prompt_scores_that_pass_two_to_the_24th(base, below, n):
         v = _rows(n, dim, 4)
         y = svq.attn_prompt(q, k, v, _ints([0, 1]), dim, starts_k=_ints([0, n]), scale=scale)
         check(y, *_far_reference(step, v, scale), n, P_BF16, f"{dim} channels")
+
+
+@pytest.mark.parametrize("kind", ["late", "rising", "falling", "mixed"])
+@pytest.mark.parametrize("scale", FAR_SCALES)
+@pytest.mark.parametrize("size", [2.0 ** -20, 1.0, 2.0 ** 20])
+def test_cache_scores_one_step_apart(size, scale, kind):
+    svq = require_gpu()
+    n = 700
+    step = _steps(n, kind)
+    for dim, group in ((64, 32), (128, 32), (256, 32)):
+        q, k = _far(n, dim, step)
+        v = _rows(n, dim, 5, size)
+        cache, _, table = _one_sequence(svq, k, v, 1, dim, group)
+        values = stored(v, group)
+        for plan in (None, 64 * n):
+            if plan:  # many ranges
+                table = torch.cat([table, torch.full((1, 64 * n // 16 + 1), -1, dtype=torch.int32, device="cuda")], dim=1)
+            y = svq.attn_cache(cache, q, table, _ints([n]), max_len=plan, scale=scale)
+            check(y, *_far_reference(step, values, scale), n, P_F16, f"{dim} channels", floor=cache_floor(values, n))
+
+
+@pytest.mark.parametrize("size", [2.0 ** -14, 2.0 ** -20, 1.0, 1e6, 2.0 ** 20])
+@pytest.mark.parametrize("dim,group", FORMS)
+def test_cache_of_one_token_with_a_far_score(dim, group, size):
+    """A token that is seen alone gives its value, whatever its score."""
+    svq = require_gpu()
+    for q0, k0 in ((1e5, 3e4), (-1e5, 3e4), (3e10, 3e10), (1e3, 1e3)):
+        q, k, v = torch.zeros(1, dim).bfloat16().cuda(), torch.zeros(1, dim).bfloat16().cuda(), _rows(1, dim, 6, size)
+        q[0, 0], k[0, 0] = q0, k0
+        cache, _, table = _one_sequence(svq, k, v, 1, dim, group)
+        values = stored(v, group)
+        y = svq.attn_cache(cache, q, table, _ints([1])).double().cpu()
+        lim = cache_floor(values, 1) + 2.0 ** -8 * 1.01 * values.abs() + 64 * 2.0 ** -24 * values.abs()
+        assert bool(((y - values).abs() <= lim).all()), (q0, k0)
+
+
+@pytest.mark.parametrize("offset", [-3e37, -1e4, 1e4, 3e37])
+def test_cache_scores_far_from_zero(offset):
+    """A group of channels shifts every score by about the same amount."""
+    svq = require_gpu()
+    heads, kv, dim, group, n = 4, 2, 128, 32, 300
+    q, k, v = _rows(2, heads * dim, 7), _rows(n, kv * dim, 8), _rows(n, kv * dim, 9)
+    q.view(2, heads, dim)[:, :, :32] = 0
+    q.view(2, heads, dim)[:, :, 0] = 1.0
+    k.view(n, kv, dim)[:, :, :32] = offset
+    if abs(offset) > 1e30:
+        q.view(2, heads, dim)[:, :, 1:] = 0  # in fp32 the shift swallows the rest
+    cache, _, table = _one_sequence(svq, k, v, kv, dim, group)
+    y = svq.attn_cache(cache, q, table, _ints([n]), q_len=2)
+    ks, vs = stored(k, group), stored(v, group)
+    check(y, *attend(q, ks, vs, heads, kv, dim ** -0.5, visible(2, n)), n, P_F16, floor=cache_floor(vs, n))
+
+
+# ---- values and queries of different sizes ----------------------------------
+
+@pytest.mark.parametrize("dim,group", FORMS)
+@pytest.mark.parametrize("size", [2.0 ** 40, 2.0 ** 60, 2.0 ** 100])
+@pytest.mark.parametrize("small", [0.0, 2.0 ** -100, 1.0])
+def test_cache_values_of_different_sizes_side_by_side(small, size, dim, group):
+    """32 tokens of large values among as small ones: which tokens' sums a wave
+    holds does not change their weights."""
+    svq = require_gpu()
+    for n, planned in ((128, None), (600, 20000)):
+        q, k, v = _rows(1, dim, 15), _rows(n, dim, 16), _rows(n, dim, 17).float() * small
+        v[32:64] = _rows(32, dim, 18).float() * size
+        v = v.to(torch.bfloat16)
+        cache, _, table = _one_sequence(svq, k, v, 1, dim, group)
+        if planned:
+            table = torch.cat([table, torch.full((1, planned // 16 + 1), -1, dtype=torch.int32, device="cuda")], dim=1)
+        values = stored(v, group)
+        y = svq.attn_cache(cache, q, table, _ints([n]), max_len=planned)
+        check(y, *attend(q, stored(k, group), values, 1, 1, dim ** -0.5, visible(1, n)), n, P_F16,
+              floor=cache_floor(values, n))
