@@ -581,7 +581,7 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
 
   f4 O[NT];
   float M[G], l = 0.f, m = -__FLT_MAX__;
-  int E = -80;
+  int E = -110;  // 2^(8 - E) times a weight of 2^6 is a number, and the least value far above 2^(E - 32)
 #pragma unroll
   for (int t = 0; t < NT; ++t) O[t] = (f4){};
 #pragma unroll

@@ -175,6 +175,22 @@ def test_cache_scores_far_from_zero(offset):
 # ---- values and queries of different sizes ----------------------------------
 
 @pytest.mark.parametrize("dim,group", FORMS)
+@pytest.mark.parametrize("size", [2.0 ** -112, 2.0 ** -105, 2.0 ** -88, 2.0 ** 90, 2.0 ** 110, 2.0 ** 122])
+def test_cache_values_of_one_size(size, dim, group):
+    """The smallest and the largest values, under weights from 1 to 2^-20."""
+    svq = require_gpu()
+    n = 300
+    q, k = torch.zeros(1, dim), torch.zeros(n, dim)
+    q[0, 0] = 1.0
+    k[:, 0], k[:, 1] = (torch.arange(n) * 5 % 16).float(), 15.0
+    q, k, v = q.to(torch.bfloat16).cuda(), k.to(torch.bfloat16).cuda(), _rows(n, dim, 14, size)
+    cache, _, table = _one_sequence(svq, k, v, 1, dim, group)
+    values = stored(v, group)
+    y = svq.attn_cache(cache, q, table, _ints([n]), scale=1.0)
+    check(y, *attend(q, stored(k, group), values, 1, 1, 1.0, visible(1, n)), n, P_F16, floor=cache_floor(values, n))
+
+
+@pytest.mark.parametrize("dim,group", FORMS)
 @pytest.mark.parametrize("size", [2.0 ** 40, 2.0 ** 60, 2.0 ** 100])
 @pytest.mark.parametrize("small", [0.0, 2.0 ** -100, 1.0])
 def test_cache_values_of_different_sizes_side_by_side(small, size, dim, group):
@@ -192,3 +208,28 @@ def test_cache_values_of_different_sizes_side_by_side(small, size, dim, group):
         y = svq.attn_cache(cache, q, table, _ints([n]), max_len=planned)
         check(y, *attend(q, stored(k, group), values, 1, 1, dim ** -0.5, visible(1, n)), n, P_F16,
               floor=cache_floor(values, n))
+
+
+@pytest.mark.parametrize("dim,group", FORMS)
+@pytest.mark.parametrize("size", [1.0, 20.0, 2.0 ** 40, 2.0 ** 120])
+def test_cache_constant_values_of_both_signs_behind_zeros(size, dim, group):
+    """Groups that are their minimum alone, of another size than a wave has met
+    before.  512 sequences (on the same pages) are blocks enough for one range,
+    three chunks a wave."""
+    svq = require_gpu()
+    n, batch = 300, 512
+    q, k = _rows(1, dim, 37), _rows(n, dim, 38)
+    v = torch.zeros(n, dim)
+    v[150:] = (torch.arange(n - 150) % 2 * 2.0 - 1.0)[:, None] * size
+    v[160:163] *= 0.5
+    v = v.to(torch.bfloat16).cuda()
+    cache, _, table = _one_sequence(svq, k, v, 1, dim, group)
+    values = stored(v, group)
+    assert torch.equal(values, v.cpu().double())
+    call = svq.AttnCacheCall(cache, q.repeat(batch, 1), torch.empty_like(q).repeat(batch, 1), table.repeat(batch, 1),
+                             _ints([n] * batch))
+    assert call.ws_size.value <= 256
+    call()
+    y = call.keep[2]
+    assert torch.equal(y[:1].expand(batch, dim), y)
+    check(y[:1], *attend(q, stored(k, group), values, 1, 1, dim ** -0.5, visible(1, n)), n, P_F16, floor=cache_floor(values, n))
