@@ -68,6 +68,13 @@ struct KvReadArgs {
 hipError_t launch_kv_write(const KvWriteArgs &a, hipStream_t s);
 hipError_t launch_kv_read(const KvReadArgs &a, hipStream_t s);
 
+// Exponents are base 2.  A scale of zero stays a number that keeps hidden scores
+// at -infinity and takes any score to nothing, the largest one that keeps equal
+// scores equal.
+__host__ __device__ inline float exponent_scale(float scale) {
+  return fminf(fmaxf(fabsf(scale) * 1.44269504088896f, 0x1p-149f), 3.40282347e38f);
+}
+
 struct AttnPromptArgs {
   const uint16_t *q, *k, *v;
   uint16_t *y;

@@ -171,10 +171,6 @@ constexpr int prompt_tiles() {
   return 4 * SIDE > 3 * SIDE + NW * 4096 ? 4 * SIDE : 3 * SIDE + NW * 4096;
 }
 
-// Exponents are base 2; a scale of zero stays a number that keeps hidden scores
-// at -infinity.
-__device__ __forceinline__ float exponent_scale(float scale) { return fmaxf(fabsf(scale) * 1.44269504088896f, 1e-38f); }
-
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(AttnPromptArgs a, PromptPlan plan) {
   constexpr int ROW = 2 * D, CH = D / 8, SIDE = KT * ROW;  // bytes of a row, its chunks, bytes of a tile

@@ -434,9 +434,6 @@ __device__ __forceinline__ f4 mfma_f16(const u4 &a, const u4 &b, const f4 &c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
 }
 __device__ __forceinline__ u2 row_bf16(const f4 &v) { return (u2){pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])}; }
-// Exponents are base 2; a scale of zero stays a number that keeps hidden scores
-// at -infinity.
-__device__ __forceinline__ float exponent_scale(float scale) { return fmaxf(fabsf(scale) * 1.44269504088896f, 0x1p-149f); }
 // The dwords of lane-consecutive pieces of N dwords.
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {

@@ -172,6 +172,61 @@ def test_cache_scores_far_from_zero(offset):
     check(y, *attend(q, ks, vs, heads, kv, dim ** -0.5, visible(2, n)), n, P_F16, floor=cache_floor(vs, n))
 
 
+# ---- scales -----------------------------------------------------------------
+
+@pytest.mark.parametrize("over_cache", [False, True])
+@pytest.mark.parametrize("scale", [3.4e38, -3.4e38, 2.5e38])
+def test_largest_scales(scale, over_cache):
+    """One key takes all, where the greatest score is further from the second
+    than fp32 sums are off: (d + 8) 2^-24 of the sum of magnitudes each."""
+    svq = require_gpu()
+    dim, n = 128, 150
+    q, k, v = _rows(n, dim, 10), _rows(n, dim, 11), _rows(n, dim, 12)
+    if over_cache:
+        cache, _, table = _one_sequence(svq, k, v, 1, dim, 32)
+        k, v = stored(k, 32), stored(v, 32)
+        y = svq.attn_cache(cache, q, table, _ints([n]), q_len=n, scale=scale)
+    else:
+        y = svq.attn_prompt(q, k, v, _ints([0, n]), dim, scale=scale)
+    q, k, v, y = (t.cpu().double() for t in (q, k, v, y))
+    s = q @ k.T * (1 if scale > 0 else -1)
+    s = s.masked_fill(~visible(n, n), -float("inf"))
+    mag = (q.abs() @ k.abs().T).max(dim=1).values
+    top = torch.topk(s, 2, dim=1)
+    clear = top.values[:, 0] - top.values[:, 1] > 2 * (dim + 8) * 2.0 ** -24 * mag
+    assert int(clear.sum()) > n - 10
+    want = v[top.indices[:, 0]]
+    lim = 2.0 ** -8 * 1.01 * want.abs() + (cache_floor(v, n) if over_cache else 0) + 64 * 2.0 ** -24 * want.abs()
+    assert bool(((y - want).abs() <= lim)[clear].all())
+
+
+@pytest.mark.parametrize("over_cache", [False, True])
+@pytest.mark.parametrize("scale", [0.0, 1e-39, -1e-39, 2e-38])
+def test_smallest_scales_of_great_scores(scale, over_cache):
+    """Scores from 0 to 2^126 under scales that are subnormal or zero.  The
+    scale is an fp32 number of 2^-149 at least, so its product with log2 e is
+    off by 2^-150, relative 2^-20 at 1e-39: less than the (d + 8) 2^-24 of a
+    score."""
+    svq = require_gpu()
+    dim, n = 64, 160
+    q, k, v = torch.zeros(1, dim), torch.zeros(n, dim), _rows(n, dim, 13)
+    q[0, 0] = 2.0 ** 63
+    k[:, 0] = (torch.arange(n) % 16) * 2.0 ** 59
+    k[:, 1] = 15 * 2.0 ** 59
+    q, k = q.to(torch.bfloat16).cuda(), k.to(torch.bfloat16).cuda()
+    exact = float(torch.tensor(scale, dtype=torch.float32))
+    if over_cache:
+        cache, _, table = _one_sequence(svq, k, v, 1, dim, 32)
+        assert torch.equal(stored(k, 32), k.double().cpu())
+        values = stored(v, 32)
+        y = svq.attn_cache(cache, q, table, _ints([n]), scale=scale)
+    else:
+        values = v
+        y = svq.attn_prompt(q, k, v, _ints([0, 1]), dim, starts_k=_ints([0, n]), scale=scale)
+    check(y, *attend(q, k, values, 1, 1, exact, visible(1, n)), n, P_F16 if over_cache else P_BF16,
+          floor=cache_floor(values, n) if over_cache else 0.0)
+
+
 # ---- values and queries of different sizes ----------------------------------
 
 @pytest.mark.parametrize("dim,group", FORMS)
