@@ -305,9 +305,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     for (int kb = 0; kb < 2; ++kb) kf[s & 1][kb] = *(const lds_u4 *)(lds_t *)(uintptr_t)(at + kb * 32 * ROW);
   };
 
-  // How far the scaled maximum lies above the rounded reference that the weights
-  // are taken from (up to a half near 2^24; a far one's are taken from the maximum).
-  auto above = [&]() { return far_any || m == -__FLT_MAX__ ? 0.f : fmaf(m, sc, -mref); };
+  // A row's reference beyond 2^24 is rounded by more than one: its weights are
+  // taken from the maximum, the scores' differences formed before the scale.
+  auto far = [&]() { return fabsf(mref) > 16777216.f; };
+  // How far the scaled maximum lies above the reference that weights are taken
+  // from (up to a half near 2^24).
+  auto above = [&]() { return far() || m == -__FLT_MAX__ ? 0.f : fmaf(m, sc, -mref); };
 
   // Tile t, its V in `place`: S holds its scores and N takes the next tile's.
   float top = 0.f;
@@ -391,9 +394,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     if (__any(m == -__FLT_MAX__ ? top > m : (top - m) * sc > 8.f)) {
       const float old_m = m, old_above = above();
       const bool first = m == -__FLT_MAX__;
-      m = fmaxf(m, max_halves(top));
+      // of the rows that need one: the others keep theirs, and with it every bit
+      // of their weights, whatever the wave's other rows see
+      const float row = max_halves(top);
+      if (first ? row > m : (row - m) * sc > 8.f) m = row;
       mref = m == -__FLT_MAX__ ? 0.f : m * sc;
-      far_any = __any(fabsf(mref) > 16777216.f);
+      far_any = __any(far());
       const float alpha = first ? 0.f : __builtin_amdgcn_exp2f((old_m - m) * sc + (above() - old_above));
       l *= alpha;
 #pragma unroll
@@ -403,13 +409,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     }
     float less = mref;
     if (__builtin_expect(far_any, 0)) {
-      // a reference beyond 2^24 is rounded by more than one: the scores'
-      // differences are formed before the scale
-      less = 0.f;
+      less = far() ? 0.f : mref;
+      const float before = far() ? m : 0.f;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[kb][i] -= m;
+        for (int i = 0; i < 16; ++i) S[kb][i] -= before;
     }
     // The weights, between the next tile's score products: one product, then
     // the exponentials of EACH scores and the rounding of the EACH before them,

@@ -288,3 +288,24 @@ def test_cache_constant_values_of_both_signs_behind_zeros(size, dim, group):
     y = call.keep[2]
     assert torch.equal(y[:1].expand(batch, dim), y)
     check(y[:1], *attend(q, stored(k, group), values, 1, 1, dim ** -0.5, visible(1, n)), n, P_F16, floor=cache_floor(values, n))
+
+
+# ---- rows beside others -----------------------------------------------------
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("n", [150, 1300])
+def test_prompt_rows_keep_their_bits_beside_hidden_keys(n, window, dim):
+    """Keys and values that a row does not see change no bit of it."""
+    svq = require_gpu()
+    heads, kv = 2, 1
+    q, k, v = _rows(n, heads * dim, 22), _rows(n, kv * dim, 23), _rows(n, kv * dim, 24)
+    before = svq.attn_prompt(q, k, v, _ints([0, n]), dim, window=window)
+    for at in (0, 20, 77, n - 3):
+        for factor in (8.0, -2.0 ** 30, float("nan")):
+            k2, v2 = k.clone(), v.clone()
+            k2[at] *= factor
+            v2[at] *= factor
+            after = svq.attn_prompt(q, k2, v2, _ints([0, n]), dim, window=window)
+            hidden = ~visible(n, n, True, window)[:, at].cuda()
+            assert torch.equal(before[hidden], after[hidden]), f"key {at} times {factor}"
