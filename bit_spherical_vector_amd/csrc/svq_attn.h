@@ -75,6 +75,14 @@ __host__ __device__ inline float exponent_scale(float scale) {
   return fminf(fmaxf(fabsf(scale) * 1.44269504088896f, 0x1p-149f), 3.40282347e38f);
 }
 
+// The score that lies `by` exponents (less a quarter, for the roundings) above a
+// maximum m, or m itself where fp32 has none so near; a row without a maximum
+// takes any score.
+__host__ __device__ inline float raised_by(float m, float by, float sc) {
+  const float to = m + (by - 0.25f) / sc;
+  return m > -3.40282347e38f && (to - m) * sc <= by ? to : m;
+}
+
 struct AttnPromptArgs {
   const uint16_t *q, *k, *v;
   uint16_t *y;

@@ -295,7 +295,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   f16x O[NB];
 #pragma unroll
   for (int db = 0; db < NB; ++db) O[db] = (f16x){};
-  float m = -__FLT_MAX__, mref = 0.f, l = 0.f;
+  float m = -__FLT_MAX__, mref = 0.f, most = m, l = 0.f;  // most: the greatest score without a new reference
   bool dirty = false, far_any = false;
 
   u4 kf[2][2];
@@ -391,13 +391,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     // a new reference only once the maximum has grown by 2^8: weights up to
     // 256 are as exact as weights up to 1 (the growth formed before the scale:
     // beyond 2^27 a scaled maximum and the reference are 16 and more apart)
-    if (__any(m == -__FLT_MAX__ ? top > m : (top - m) * sc > 8.f)) {
+    if (__any(top > most)) {
       const float old_m = m, old_above = above();
       const bool first = m == -__FLT_MAX__;
       // of the rows that need one: the others keep theirs, and with it every bit
       // of their weights, whatever the wave's other rows see
       const float row = max_halves(top);
-      if (first ? row > m : (row - m) * sc > 8.f) m = row;
+      if (row > most) m = row;
+      most = raised_by(m, 8.f, sc);
       mref = m == -__FLT_MAX__ ? 0.f : m * sc;
       far_any = __any(far());
       const float alpha = first ? 0.f : __builtin_amdgcn_exp2f((old_m - m) * sc + (above() - old_above));
