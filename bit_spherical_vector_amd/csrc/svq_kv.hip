@@ -390,9 +390,9 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
 //
 // and the row is 2^(E - 8) (2^24 O + M) / sum p.  The weight p is exp2 of (score
 // - m) times the scale: m a running maximum, raised once a weight exceeds 2^6, E
-// the exponent of the greatest scale or minimum of a wave's first chunk, raised
-// once a p s_g overflows fp16.  The two are kept apart: in one fp32 number a
-// maximum from 2^24 on would round E away.
+// the exponent of the greatest scale or minimum that the row sees in a wave's
+// first chunk, raised once a p s_g overflows fp16.  The two are kept apart: in
+// one fp32 number a maximum from 2^24 on would round E away.
 //
 // What bounds it: vector instructions, which take 89 % of the cycles at 64
 // sequences of up to 8192 tokens (75 us, 4.1 TB/s of the cache, 64 us at the
@@ -577,7 +577,7 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
   const int se = 24 - qe;
 
   f4 O[NT];
-  float M[G], l = 0.f, m = -__FLT_MAX__;
+  float M[G], l = 0.f, m = -__FLT_MAX__, above = m;  // above: the greatest score without a new maximum
   int E = -110;  // 2^(8 - E) times a weight of 2^6 is a number, and the least value far above 2^(E - 32)
 #pragma unroll
   for (int t = 0; t < NT; ++t) O[t] = (f4){};
@@ -645,17 +645,20 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
     float top = t[0][0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = fmaxf(top, t[i >> 2][i & 3]);
-    if (__any(m == -__FLT_MAX__ ? top > m : (top - m) * sc > 6.f)) {
-      const float now = fmaxf(m, row_max(top)), f = __builtin_amdgcn_exp2f((m - now) * sc);
+    if (__any(top > above)) {
+      // of the rows that need one (the others keep every bit, whatever the
+      // tile's other rows see)
+      const float high = row_max(top), now = high > above ? high : m, f = __builtin_amdgcn_exp2f((m - now) * sc);
       l *= f;
       rescale(f);
       m = now;
+      above = raised_by(m, 6.f, sc);
     }
     float p[2][4], pm[G];
     u4 w[G], rest[G];
-    // E to the greatest finite scale or minimum that a row sees here; by how much
-    // it has risen
-    auto raise = [&]() {
+    // E to the greatest finite scale or minimum that the row sees here, where it
+    // needs it; by how much it has risen
+    auto raise = [&](bool need) {
       uint32_t most = 0;
 #pragma unroll
       for (int g = 0; g < G; ++g)
@@ -672,15 +675,13 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
 #pragma unroll
             for (int i = 0; i < 4; ++i) most = pk_max_finite(most, hidden(vp[j][g][i]));
       }
-      float big = fmaxf(lo_bf16(most), hi_bf16(most));
-      big = row_max(lanes_max(big, 16));
-      const int now = __builtin_amdgcn_readfirstlane(big > 0.f ? __builtin_amdgcn_frexp_expf(big) : E);
-      const int by = max(now - E, 0);
-      if (by > 0) rescale(ldexpf(1.f, -by));
+      const float big = row_max(fmaxf(lo_bf16(most), hi_bf16(most)));
+      const int by = need && big > 0.f ? max(__builtin_amdgcn_frexp_expf(big) - E, 0) : 0;
+      rescale(ldexpf(1.f, -by));
       E += by;
       return by;
     };
-    if (n == 0) raise();
+    if (n == 0) raise(true);
     const float unit = ldexpf(1.f, 8 - E);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -710,9 +711,10 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
           }
         far = fmaxf(far, fabsf(pm[g]));
       }
-      if (__builtin_expect(!__any(most[0] >= 0x7C00 || most[1] >= 0x7C00 || far > 0x1p100f), 1)) break;
-      const int by = raise();
-      if (by == 0) break;  // what does not fit then is not finite
+      const bool over = most[0] >= 0x7C00 || most[1] >= 0x7C00 || far > 0x1p100f;
+      if (__builtin_expect(!__any(over), 1)) break;
+      const int by = raise(row_max(over ? 1.f : 0.f) > 0.f);
+      if (!__any(by > 0)) break;  // what does not fit then is not finite
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = ldexpf(p[i >> 2][i & 3], -by);
     }

@@ -309,3 +309,37 @@ def test_prompt_rows_keep_their_bits_beside_hidden_keys(n, window, dim):
             after = svq.attn_prompt(q, k2, v2, _ints([0, n]), dim, window=window)
             hidden = ~visible(n, n, True, window)[:, at].cuda()
             assert torch.equal(before[hidden], after[hidden]), f"key {at} times {factor}"
+
+
+@pytest.mark.parametrize("dim,group", FORMS)
+@pytest.mark.parametrize("window", [0, 40])
+def test_cache_rows_keep_their_bits_beside_hidden_keys(window, dim, group):
+    """Later tokens of a call, and those before a window, change no bit of the
+    rows that do not see them."""
+    svq = require_gpu()
+    heads, kv, n, q_len = 2, 1, 90, 7
+    q, k, v = _rows(q_len, heads * dim, 25), _rows(n, kv * dim, 26), _rows(n, kv * dim, 27)
+    cache, pages, table = _one_sequence(svq, k, v, kv, dim, group)
+    before = svq.attn_cache(cache, q, table, _ints([n]), q_len=q_len, window=window)
+    for at in (n - 1, n - 3, n - q_len - 39, n - q_len - 36):
+        for factor in (8.0, 2.0 ** 20, -2.0 ** 34, float("nan")):
+            _write(svq, cache, k[at:at + 1] * factor, v[at:at + 1] * factor, pages, at)
+            after = svq.attn_cache(cache, q, table, _ints([n]), q_len=q_len, window=window)
+            _write(svq, cache, k[at:at + 1], v[at:at + 1], pages, at)
+            hidden = ~visible(q_len, n, True, window)[:, at].cuda()
+            assert torch.equal(before[hidden], after[hidden]), f"token {at} times {factor}"
+
+
+def test_cache_rows_of_tokens_that_later_ones_dwarf():
+    """Later tokens of a call whose values are 2^34 times greater: the rows
+    before keep the precision of what they see."""
+    svq = require_gpu()
+    heads, kv, dim, group, n, q_len = 4, 1, 128, 64, 70, 4
+    q, k, v = _rows(q_len, heads * dim, 28), _rows(n, kv * dim, 29), _rows(n, kv * dim, 30)
+    v[n - 2:] = (v[n - 2:].float() * 2.0 ** 34).to(torch.bfloat16)
+    cache, _, table = _one_sequence(svq, k, v, kv, dim, group)
+    y = svq.attn_cache(cache, q, table, _ints([n]), q_len=q_len)
+    ks, vs = stored(k, group), stored(v, group)
+    ref = attend(q, ks, vs, heads, kv, dim ** -0.5, visible(q_len, n))
+    check(y[:2], *(r[:2] for r in ref), n, P_F16, floor=cache_floor(vs[:n - 2], n))
+    check(y[2:], *(r[2:] for r in ref), n, P_F16, floor=cache_floor(vs, n))
