@@ -682,15 +682,11 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
       return by;
     };
     if (n == 0) raise(true);
-    const float unit = ldexpf(1.f, 8 - E);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = __builtin_amdgcn_exp2f((t[i >> 2][i & 3] - m) * sc);
-      l += x;
-      p[i >> 2][i & 3] = x * unit;
-    }
 #pragma unroll 1
     for (;;) {
+      const float unit = ldexpf(1.f, 8 - E);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = __builtin_amdgcn_exp2f((t[i >> 2][i & 3] - m) * sc) * unit;
       us2_t most = {0, 0};
       float far = 0.f;
 #pragma unroll
@@ -715,9 +711,11 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
       if (__builtin_expect(!__any(over), 1)) break;
       const int by = raise(row_max(over ? 1.f : 0.f) > 0.f);
       if (!__any(by > 0)) break;  // what does not fit then is not finite
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = ldexpf(p[i >> 2][i & 3], -by);
     }
+    float weights = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) weights += p[i >> 2][i & 3];
+    l += ldexpf(weights, E - 8);
 #pragma unroll
     for (int g = 0; g < G; ++g) M[g] += pm[g];
     // value runs: dword w of a key holds tiles 8w .. 8w + 7 (at 64 channels
@@ -842,6 +840,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnCacheArgs a) {
   if (part == 0) s_l[first] = sum;
   __syncthreads();
   if (tid >= T) return;
+#pragma unroll 4
   for (int n = 1; n < N; ++n) {
     o += s_o[n][part];
     sum += s_l[n];
