@@ -1,5 +1,7 @@
 // The 4-bit cache of keys and values (include/svq_attn.h): quantising tokens
 // into it, reading them back, attention over it.
+#include <type_traits>
+
 #include "svq_attn.h"
 #include "svq_device.h"
 
@@ -379,8 +381,8 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
 // one row, and four keys of each 16):
 //
 //   A_g[key][row] = sum over the group's channels of c * q     (q in fp16
-//        under a power-of-two scale per row, a sixteenth of it where the
-//        nibble stands for 16 c)
+//        under a power-of-two scale per row, per group where a row's channels
+//        need it, a sixteenth of it where the nibble stands for 16 c)
 //   score         = sum over groups of s_g A_g + m_g sum q     (fp32)
 //   O_t[channel][row] += sum over keys of c * (p s_g)          (p s_g in units
 //        of 2^(E - 8) as the sum of two fp16 numbers, 22 bits: the minimum's
@@ -408,6 +410,15 @@ constexpr int CACHE_WAVES = 4, CACHE_STAGES = 2, CHUNK = 32, ROWS = 16;
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) uint8_t lds_t;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
+// LDS bytes of a block: the waves' stages of chunks, whose place what they bring
+// together takes after the last, and 8 bytes a wave and row for the powers of
+// two of its query's groups.
+template <int D, int G>
+constexpr uint32_t cache_lds() {
+  constexpr int copies = CACHE_STAGES * 2 * (16 * D + 128 * G), joined = ROWS * (D + 7) * 4;
+  return CACHE_WAVES * ((copies > joined ? copies : joined) + ROWS * 8);
+}
 __device__ __forceinline__ u4 lds_u128(uint32_t at) {
   return *(const __attribute__((address_space(3))) u4 *)(lds_t *)(uintptr_t)at;
 }
@@ -483,7 +494,6 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
   auto hi_of = [&](int token) { return max(first + token, 0); };
   auto lo_of = [&](int token) { return a.window > 0 ? max(0, first + token - a.window) : 0; };
   const int lo_min = lo_of(t_first), lo_max = lo_of(t_last), hi_min = hi_of(t_first), hi_max = hi_of(t_last);
-  const int lo = lo_of(r_token), hi = hi_of(r_token);
   const int c_first = lo_min / CHUNK, chunks = max((hi_max + CHUNK - 1) / CHUNK - c_first, 0);
   const int per = a.splits > 1 ? (chunks + a.splits - 1) / a.splits : chunks;
   const int c0 = c_first + min(sp * per, chunks) + wv, c1 = c_first + min(sp * per + per, chunks);
@@ -541,10 +551,16 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
   for (int n = 0; n < CACHE_STAGES - 1; ++n)
     if (n < count) fetch(n);
 
-  // queries: step s takes channels 32s + 8h + j, a sixteenth of them where the
-  // nibble pair is 16 times its code (j = 2, 3, 6, 7)
+  // Queries: step s takes channels 32s + 8h + j, a sixteenth of them where the
+  // nibble pair is 16 times its code (j = 2, 3, 6, 7), so all bits of a channel
+  // down to 2^-28 of the row's greatest.  A row with a smaller one takes a
+  // further power of two for each group from its own greatest; the group's
+  // products are divided by it again, from LDS, for want of registers.
   u4 qf[NS];
   float qsum[G];
+  const uint32_t drops = (uint32_t)(uintptr_t)(lds_t *)smem + cache_lds<D, G>() - CACHE_WAVES * ROWS * 8 + (wv * ROWS + col) * 8;
+  uint32_t drop[(G + 3) / 4];
+  bool any_drop = false;
   uint32_t mx = 0;
 #pragma unroll
   for (int s = 0; s < NS; ++s)
@@ -561,6 +577,36 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
   const float q_top = row_max(fmaxf(lo_bf16(mx), hi_bf16(mx)));
   const int qe = q_top > 0.f ? 15 - __builtin_amdgcn_frexp_expf(q_top) : 0;
 #pragma unroll
+  for (int g = 0; g < (G + 3) / 4; ++g) drop[g] = 0;
+  if constexpr (G > 1) {
+    us2_t least = {0xFFFF, 0xFFFF};  // a magnitude's bits less one, zeros on top
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        least = __builtin_elementwise_min(least, __builtin_bit_cast(us2_t, raw[s][w] & 0x7FFF7FFFu) - (us2_t){1, 1});
+    // below 2^(-13 - qe)
+    const int bound = max(-13 - qe + 127, 1) << 7;
+    const bool small = min(least[0], least[1]) < bound - 1;
+    if (__builtin_expect(__any(small), 0)) {
+      const bool row_small = row_max(small ? 1.f : 0.f) > 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int s = g * SPG; s < (g + 1) * SPG; ++s)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) top = pk_max_finite(top, hidden(raw[s][w]));
+        const float most = row_max(fmaxf(lo_bf16(top), hi_bf16(top)));
+        const int more = row_small && most > 0.f ? min(15 - __builtin_amdgcn_frexp_expf(most) - qe, 255) : 0;
+        drop[g / 4] |= (uint32_t)more << 8 * (g % 4);
+      }
+      any_drop = __any(drop[0] != 0 || drop[(G - 1) / 4] != 0);
+#pragma unroll
+      for (int g = 0; g < (G + 3) / 4; ++g) *(lds_u32 *)(lds_t *)(uintptr_t)(drops + 4 * g) = drop[g];
+    }
+  }
+#pragma unroll
   for (int g = 0; g < G; ++g) qsum[g] = 0.f;
 #pragma unroll
   for (int s = 0; s < NS; ++s)
@@ -568,7 +614,7 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
     for (int w = 0; w < 4; ++w) {
       const float x = lo_bf16(raw[s][w] ^ flip), y = hi_bf16(raw[s][w] ^ flip);
       qsum[s / SPG] += ldexpf(x, -8) + ldexpf(y, -8);  // 256 of the greatest numbers stay a number
-      const int e = w & 1 ? qe - 4 : qe;
+      const int e = qe + (int)(drop[s / SPG / 4] >> 8 * (s / SPG % 4) & 255) - (w & 1 ? 4 : 0);
       qf[s][w] = __builtin_bit_cast(uint32_t, (h2){(_Float16)ldexpf(x, e), (_Float16)ldexpf(y, e)});
     }
 #pragma unroll
@@ -605,24 +651,35 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
     const int k0 = (c0 + n * CACHE_WAVES) * CHUNK;
 
     float t[2][4];
+    auto scores = [&](auto divided) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint32_t kw[NS];
-      lds_words<NS>(src + j * RUN + lane * (4 * NS), kw);
+      for (int j = 0; j < 2; ++j) {
+        uint32_t kw[NS];
+        lds_words<NS>(src + j * RUN + lane * (4 * NS), kw);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t[j][i] = 0.f;
+        for (int i = 0; i < 4; ++i) t[j][i] = 0.f;
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        f4 A = {};
+        for (int g = 0; g < G; ++g) {
+          f4 A = {};
 #pragma unroll
-        for (int s = 0; s < SPG; ++s) A = mfma_f16(nibbles(kw[g * SPG + s]), qf[g * SPG + s], A);
-        const u4 kp = lds_u128(src + j * RUN + 2 * KB + (h * G + g) * 16);
+          for (int s = 0; s < SPG; ++s) A = mfma_f16(nibbles(kw[g * SPG + s]), qf[g * SPG + s], A);
+          if constexpr (divided) {
+            const int by = *(lds_u32 *)(lds_t *)(uintptr_t)(drops + 4 * (g / 4)) >> 8 * (g % 4) & 255;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t[j][i] = fmaf(lo_bf16(kp[i]), A[i], fmaf(hi_bf16(kp[i]), qsum[g], t[j][i]));
+            for (int i = 0; i < 4; ++i) A[i] = ldexpf(A[i], -by);
+          }
+          const u4 kp = lds_u128(src + j * RUN + 2 * KB + (h * G + g) * 16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[j][i] = fmaf(lo_bf16(kp[i]), A[i], fmaf(hi_bf16(kp[i]), qsum[g], t[j][i]));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[j][i] = ldexpf(t[j][i], se);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) t[j][i] = ldexpf(t[j][i], se);
-    }
+    };
+    if (__builtin_expect(any_drop, 0))
+      scores(std::true_type());
+    else
+      scores(std::false_type());
     u4 vp[2][G];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -631,6 +688,7 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
     if (!(ok == 3 && k0 >= lo_max && k0 + CHUNK <= hi_min)) {
       // some row does not see all of it: hidden keys have the weight zero and
       // zeros for parameters, whatever lies there
+      const int of_row = (int)hidden(r_token), lo = lo_of(of_row), hi = hi_of(of_row);  // (formed here: two registers less)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -856,8 +914,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnCacheArgs a) {
 
 template <int D, int GROUP>
 hipError_t launch_cache(const AttnCacheArgs &a, hipStream_t s) {
-  constexpr int G = D / GROUP, copies = CACHE_STAGES * 2 * (16 * D + 128 * G), joined = ROWS * (D + 7) * 4;
-  constexpr size_t lds = (size_t)CACHE_WAVES * (copies > joined ? copies : joined);
+  constexpr size_t lds = cache_lds<D, D / GROUP>();
   const hipError_t e = allow_smem(attn_cache_kernel<D, GROUP>, lds);
   if (e != hipSuccess) return e;
   attn_cache_kernel<D, GROUP><<<dim3(a.c.heads, a.row_tiles * a.splits, a.batch), 64 * CACHE_WAVES, lds, s>>>(a);

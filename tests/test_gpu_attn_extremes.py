@@ -290,6 +290,25 @@ def test_cache_constant_values_of_both_signs_behind_zeros(size, dim, group):
     check(y[:1], *attend(q, stored(k, group), values, 1, 1, dim ** -0.5, visible(1, n)), n, P_F16, floor=cache_floor(values, n))
 
 
+@pytest.mark.parametrize("dim,group", [f for f in FORMS if f[0] > f[1]])
+@pytest.mark.parametrize("apart", [2.0 ** 12, 2.0 ** 24, 2.0 ** 32, 2.0 ** 45])
+@pytest.mark.parametrize("keys", ["none", "opposite"])
+def test_cache_queries_of_different_sizes(keys, apart, dim, group):
+    """Queries whose first group of channels is far greater than the others,
+    over keys that are zero there, or as much smaller."""
+    svq = require_gpu()
+    heads, n = 4, 200
+    q, k, v = _rows(1, heads * dim, 19), _rows(n, dim, 20), _rows(n, dim, 21)
+    q, k = q.float(), k.float()
+    q.view(heads, dim)[:, :group] *= apart
+    k[:, :group] *= 0.0 if keys == "none" else 1.0 / apart
+    q, k = q.to(torch.bfloat16), k.to(torch.bfloat16)
+    cache, _, table = _one_sequence(svq, k, v, 1, dim, group)
+    ks, vs = stored(k, group), stored(v, group)
+    y = svq.attn_cache(cache, q, table, _ints([n]), scale=0.25)
+    check(y, *attend(q, ks, vs, heads, 1, 0.25, visible(1, n)), n, P_F16, floor=cache_floor(vs, n))
+
+
 # ---- rows beside others -----------------------------------------------------
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
