@@ -27,9 +27,10 @@
  * of channels, and within 2^-35 of that magnitude below; the product of a weight
  * and a scale is held in 22 bits, down to 2^-32 of the greatest scale or minimum
  * that the row sees.  Weights below 2^-126 of a row's greatest are zero.  A
- * query that sees no key gives a row of zeros.  A key that a query does not see
- * has no influence on it, whatever it, its value or its stored scales hold
- * (infinities and NaN included): not a bit of its row changes.
+ * query that sees no key, or only keys whose scores are minus infinity, gives a
+ * row of zeros.  A key that a query does not see has no influence on it, whatever
+ * it, its value or its stored scales hold (infinities and NaN included): not a
+ * bit of its row changes.
  */
 #ifndef SVQ_ATTN_H
 #define SVQ_ATTN_H

@@ -362,3 +362,37 @@ def test_cache_rows_of_tokens_that_later_ones_dwarf():
     ref = attend(q, ks, vs, heads, kv, dim ** -0.5, visible(q_len, n))
     check(y[:2], *(r[:2] for r in ref), n, P_F16, floor=cache_floor(vs[:n - 2], n))
     check(y[2:], *(r[2:] for r in ref), n, P_F16, floor=cache_floor(vs, n))
+
+
+# ---- long ranges, scores of minus infinity ----------------------------------
+
+def test_cache_ranges_of_more_chunks_than_lanes_hold_pages():
+    """1024 queries of 8 heads are as many blocks as run at once, so one range
+    has all 5000 tokens, 40 chunks a wave."""
+    svq = require_gpu()
+    heads, kv, dim, group, n, q_len = 8, 8, 64, 32, 5000, 1024
+    q, k, v = _rows(q_len, heads * dim, 31), _rows(n, kv * dim, 32), _rows(n, kv * dim, 33)
+    cache, _, table = _one_sequence(svq, k, v, kv, dim, group)
+    call = svq.AttnCacheCall(cache, q, torch.empty_like(q), table, _ints([n]), q_len=q_len)
+    assert call.ws_size.value <= 256
+    y = svq.attn_cache(cache, q, table, _ints([n]), q_len=q_len)
+    rows = [0, 1, 2, 15, 16, 500, 905, 1022, 1023]
+    ks, vs = stored(k, group), stored(v, group)
+    check(y[rows], *attend(q[rows], ks, vs, heads, kv, dim ** -0.5, visible(q_len, n)[rows]), n, P_F16)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n,first", [(40, 1), (40, 7), (1300, 1), (1300, 900)])
+def test_prompt_rows_that_see_scores_of_minus_infinity(n, first, dim):
+    """The first keys' scores are minus infinity for every query: rows that see
+    no others are zeros, as if they saw nothing, and later ones do not feel them."""
+    svq = require_gpu()
+    q, k, v = _rows(n, dim, 34), _rows(n, dim, 35), _rows(n, dim, 36)
+    q[:, 5] = 1.0
+    k2 = k.clone()
+    k2[:first, 5] = -float("inf")
+    y = svq.attn_prompt(q, k2, v, _ints([0, n]), dim)
+    assert torch.all(y[:first] == 0)
+    seen = visible(n, n)
+    seen[:, :first] = False
+    check(y[first:], *(r[first:] for r in attend(q, k, v, 1, 1, dim ** -0.5, seen)), n, P_BF16)
