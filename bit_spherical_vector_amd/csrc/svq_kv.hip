@@ -178,12 +178,16 @@ __device__ __forceinline__ void or_half(uint32_t *w, bool upper) {
   }
 }
 
-// One pass: a value is read once and leaves as a nibble.  Bound by instructions
-// (about 20 a value, a third of them extremes, exchanges and the parameters in
-// 64 bits; the registers are held to what lets 8 waves a SIMD run, 5 at 256
-// channels, where 4 and 6 take 71 and 66 us against 63): 32768 tokens of 8 heads
-// of 128 channels 45 us, 3.8 TB/s read and written, where a copy of as many
-// bytes takes 35.
+// One pass: a value is read once and leaves as a nibble.  Bound by instructions,
+// about 20 a value, a third of them extremes, exchanges and the parameters in 64
+// bits, and by those of waves without a token: a block takes 64 tokens of the key
+// side but 4096 / D of the value side, whose number the grid has for both, so at
+// 128 channels every second block of the key side, at 256 three of four, do all
+// of it for the last token and store nothing (a third and three fifths of the
+// instructions).  The registers are held to what lets 8 waves a SIMD run, 5 at 256
+// channels, where 4 and 6 take 71 and 66 us against 63 (chosen with those waves).
+// 32768 tokens of 8 heads of 128 channels 45 us, 3.8 TB/s read and written, where
+// a copy of as many bytes takes 35.
 template <int D>
 __global__ __launch_bounds__(256, D == 256 ? 5 : 8) void kv_write_kernel(KvWriteArgs a) {
   constexpr int NS = D / 32;
@@ -396,15 +400,15 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
 // first chunk, raised once a p s_g overflows fp16.  The two are kept apart: in
 // one fp32 number a maximum from 2^24 on would round E away.
 //
-// What bounds it: vector instructions, which take 89 % of the cycles at 64
-// sequences of up to 8192 tokens (75 us, 4.1 TB/s of the cache, 64 us at the
+// What bounds it: vector instructions, which take 90 % of the cycles at 64
+// sequences of up to 8192 tokens (77 us, 4.0 TB/s of the cache, 64 us at the
 // rate of a copy): 16 rows are what one product takes, so the codes of a key are
 // unpacked once for up to 16 query heads, and the weights (12 instructions a
 // pair and group) cost more than the codes.  A wave's chunks reach LDS by
 // copies one chunk ahead (into registers instead: 110 us); three stages gain
-// nothing.  Short contexts are latency: one sequence of 777 tokens 8.2 us, of
-// it 5.4 this launch (the length, the page, the first chunk, code that is not
-// in the instruction cache yet) and 2.4 the join.  More waves a block (8) or
+// nothing.  Short contexts are latency: one sequence of 777 tokens 8.5 us, of
+// it 6 this launch (the length, the page, the first chunk, code that is not
+// in the instruction cache yet) and 2.3 the join.  More waves a block (8) or
 // more and shorter ranges cost what they gain.
 constexpr int CACHE_WAVES = 4, CACHE_STAGES = 2, CHUNK = 32, ROWS = 16;
 
@@ -927,8 +931,9 @@ hipError_t launch_cache(const AttnCacheArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Blocks of 4 waves: 64 tokens of the key side, 4096 / dim of the value side
-// (the side with more tokens a block ends early).
+// Blocks of 4 waves: 64 tokens of the key side, 4096 / dim of the value side.
+// Where the value side has more blocks, those of the key side past the last token
+// return at once when reading, and store nothing when writing.
 static dim3 kv_grid(const KvView &c, int64_t tokens) {
   const int per = 4096 / c.dim < 64 ? 4096 / c.dim : 64;
   return dim3((unsigned)((tokens + per - 1) / per), c.heads, 2);
