@@ -413,6 +413,11 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
 constexpr int CACHE_WAVES = 4, CACHE_STAGES = 2, CHUNK = 32, ROWS = 16;
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+// v as one value to all that use it.
+__device__ __forceinline__ h2 once(h2 v) {
+  asm("" : "+v"(v));
+  return v;
+}
 typedef __attribute__((address_space(3))) uint8_t lds_t;
 typedef __attribute__((address_space(3))) uint32_t lds_u32;
 // LDS bytes of a block: the waves' stages of chunks, whose place what they bring
@@ -761,7 +766,10 @@ __global__ __launch_bounds__(64 * CACHE_WAVES, D / GROUP == 8 ? 1 : 2) void attn
             const float s0 = lo_bf16(vp[j][g][i]), s1 = lo_bf16(vp[j][g][i + 1]);
             pm[g] = fmaf(p[j][i], hi_bf16(vp[j][g][i]), pm[g]);
             pm[g] = fmaf(p[j][i + 1], hi_bf16(vp[j][g][i + 1]), pm[g]);
-            const h2 x = {(_Float16)(p[j][i] * s0), (_Float16)(p[j][i + 1] * s1)};
+            // (the compiler would round it twice, from fp32 for the product and at
+            // once for the rest, and one weight in 8000 would get a rest that is
+            // not its own)
+            const h2 x = once((h2){(_Float16)(p[j][i] * s0), (_Float16)(p[j][i + 1] * s1)});
             const h2 y = {(_Float16)fmaf(p[j][i], s0, -(float)x[0]), (_Float16)fmaf(p[j][i + 1], s1, -(float)x[1])};
             w[g][2 * j + (i >> 1)] = __builtin_bit_cast(uint32_t, x);
             rest[g][2 * j + (i >> 1)] = __builtin_bit_cast(uint32_t, y);

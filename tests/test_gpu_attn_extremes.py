@@ -290,6 +290,29 @@ def test_cache_constant_values_of_both_signs_behind_zeros(size, dim, group):
     check(y[:1], *attend(q, stored(k, group), values, 1, 1, dim ** -0.5, visible(1, n)), n, P_F16, floor=cache_floor(values, n))
 
 
+@pytest.mark.parametrize("dim,group", FORMS)
+def test_cache_values_that_cancel(dim, group):
+    """Values that are zero as -7 s + 7 s, s 19/16 (so that a weight times s is no
+    fp32 number): what is left of them is the rounding of the weights.  Two fp16
+    numbers hold a weight within 2^-23 of it, formed from an fp32 product; the sums
+    of the minima take at most 12 roundings of 2^-24 (8 terms a lane, 4 lanes, a
+    step), those of the codes 8 (two products of 16 keys, the join).  Weights lie
+    within a factor of 2 of each other, so no product is cut beside another."""
+    svq = require_gpu()
+    heads, n, q_len = 64, 16, 16
+    for seed in range(3):
+        q, k = _rows(q_len, heads * dim, 100 + seed, 0.02), _rows(n, dim, 200 + seed)
+        v = torch.zeros(n, dim)
+        v.view(n, -1, group)[:, :, 0], v.view(n, -1, group)[:, :, 1] = -7 * 1.1875, 8 * 1.1875
+        v = v.to(torch.bfloat16).cuda()
+        assert torch.equal(stored(v, group), v.double().cpu())
+        cache, _, table = _one_sequence(svq, k, v, 1, dim, group)
+        y = svq.attn_cache(cache, q, table, _ints([n]), q_len=q_len).float().view(q_len, heads, -1, group)[:, :, :, 2:]
+        off = y.abs().amax(dim=(2, 3))
+        lim = 7 * 1.1875 * (2.0 ** -23 + 21 * 2.0 ** -24)
+        assert bool((off <= lim).all()), f"{int((off > lim).sum())} rows, {off.max().item()} over {lim}"
+
+
 @pytest.mark.parametrize("dim,group", [f for f in FORMS if f[0] > f[1]])
 @pytest.mark.parametrize("apart", [2.0 ** 12, 2.0 ** 24, 2.0 ** 32, 2.0 ** 45])
 @pytest.mark.parametrize("keys", ["none", "opposite"])
