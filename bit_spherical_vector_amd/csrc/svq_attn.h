@@ -24,10 +24,10 @@ int compute_units();  // of the current device
 //           and a token's bytes are its own;
 //   parameters [slot/4][group][slot%4]: a lane reads four slots of a group at
 //           once.
-// Nibble order.  Nibbles 2i and 2i+1 of a byte come out of one shift as two
-// fp16 subnormals (c * 2^-24 and c * 16 * 2^-24), in pairs 4 nibbles apart.
-// Key words hold channel j of their eight at nibble kv_nibble(j), so that the
-// pairs are consecutive channels; value runs hold tile t at nibble t.
+// Nibble order.  Nibbles come out as fp16 subnormals in pairs 4 nibbles apart,
+// each pair by a mask and (but for nibbles 1 and 5) a shift.  Key words hold
+// channel j of their eight at nibble kv_nibble(j), so that the pairs are
+// consecutive channels; value runs hold tile t at nibble t.
 struct KvView {
   uint8_t *base;
   int64_t pages;

@@ -26,7 +26,11 @@
  * codes with all its bits down to 2^-28 of the greatest magnitude in its group
  * of channels, and within 2^-35 of that magnitude below; the product of a weight
  * and a scale is held in 22 bits, down to 2^-32 of the greatest scale or minimum
- * that the row sees.  Weights below 2^-126 of a row's greatest are zero.  A
+ * that the row sees; and of 32 products of codes that are added at once each is
+ * kept within 2^-22 of the greatest that any code (15) would give.  Weights below
+ * 2^-126 of a row's greatest are zero.  Over a prompt a row's numerators are sums
+ * of such weights times values in fp32: from about 2^119 over the number of keys
+ * on, finite values may give infinities.  A
  * query that sees no key, or only keys whose scores are minus infinity, gives a
  * row of zeros.  A key that a query does not see has no influence on it, whatever
  * it, its value or its stored scales hold (infinities and NaN included): not a

@@ -313,6 +313,26 @@ def test_cache_values_that_cancel(dim, group):
         assert bool((off <= lim).all()), f"{int((off > lim).sum())} rows, {off.max().item()} over {lim}"
 
 
+@pytest.mark.parametrize("dim,group", FORMS)
+def test_cache_values_that_cancel_under_different_weights(dim, group):
+    """As above with weights from 1 to nearly nothing.  Beside the roundings above,
+    each of the n products of a code and a weight may be off by 2^-22 of the
+    greatest code, 15, times s and the greatest weight, which is at most the sum
+    of the weights."""
+    svq = require_gpu()
+    heads, n, q_len = 64, 16, 16
+    for seed in range(3):
+        q, k = _rows(q_len, heads * dim, 300 + seed, 4.0), _rows(n, dim, 400 + seed)
+        v = torch.zeros(n, dim)
+        v.view(n, -1, group)[:, :, 0], v.view(n, -1, group)[:, :, 1] = -7 * 1.1875, 8 * 1.1875
+        v = v.to(torch.bfloat16).cuda()
+        cache, _, table = _one_sequence(svq, k, v, 1, dim, group)
+        y = svq.attn_cache(cache, q, table, _ints([n]), q_len=q_len).float().view(q_len, heads, -1, group)[:, :, :, 2:]
+        off = y.abs().amax(dim=(2, 3))
+        lim = 7 * 1.1875 * (2.0 ** -23 + 21 * 2.0 ** -24) + n * 15 * 1.1875 * 2.0 ** -22
+        assert bool((off <= lim).all()), f"{int((off > lim).sum())} rows, {off.max().item()} over {lim}"
+
+
 @pytest.mark.parametrize("dim,group", [f for f in FORMS if f[0] > f[1]])
 @pytest.mark.parametrize("apart", [2.0 ** 12, 2.0 ** 24, 2.0 ** 32, 2.0 ** 45])
 @pytest.mark.parametrize("keys", ["none", "opposite"])
