@@ -39,7 +39,8 @@
 namespace svq {
 namespace {
 
-constexpr int KT = 64;  // keys of a tile
+constexpr int KT = 64;       // keys of a tile
+constexpr float GROW = 8.f;  // by how much (base 2) a row's maximum grows before its reference follows
 
 typedef __attribute__((address_space(3))) uint8_t lds_t;
 typedef short s4v __attribute__((ext_vector_type(4)));
@@ -305,12 +306,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     for (int kb = 0; kb < 2; ++kb) kf[s & 1][kb] = *(const lds_u4 *)(lds_t *)(uintptr_t)(at + kb * 32 * ROW);
   };
 
-  // A row's reference beyond 2^24 is rounded by more than one: its weights are
-  // taken from the maximum, the scores' differences formed before the scale.
+  // The reference lies GROW above the maximum, so that weights are at most 1
+  // until the next one.  One beyond 2^24 is rounded by more than one: such a row's
+  // weights are taken from the maximum, the scores' differences formed before the
+  // scale.
   auto far = [&]() { return fabsf(mref) > 16777216.f; };
   // How far the scaled maximum lies above the reference that weights are taken
-  // from (up to a half near 2^24).
-  auto above = [&]() { return far() || m == -__FLT_MAX__ ? 0.f : fmaf(m, sc, -mref); };
+  // from (-GROW, and up to a half off it near 2^24).
+  auto above = [&]() { return far() || m == -__FLT_MAX__ ? -GROW : fmaf(m, sc, -mref); };
 
   // Tile t, its V in `place`: S holds its scores and N takes the next tile's.
   float top = 0.f;
@@ -388,9 +391,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       }
       maximum(S);
     }
-    // a new reference only once the maximum has grown by 2^8: weights up to
-    // 256 are as exact as weights up to 1 (the growth formed before the scale:
-    // beyond 2^27 a scaled maximum and the reference are 16 and more apart)
+    // a new reference only once the maximum has grown by 2^GROW: weights down
+    // from 2^-GROW are as exact as weights from 1 (the growth formed before the
+    // scale: beyond 2^27 a scaled maximum and the reference are 16 and more apart)
     if (__any(top > most)) {
       const float old_m = m, old_above = above();
       const bool first = m == -__FLT_MAX__;
@@ -398,8 +401,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       // of their weights, whatever the wave's other rows see
       const float row = max_halves(top);
       if (row > most) m = row;
-      most = raised_by(m, 8.f, sc);
-      mref = m == -__FLT_MAX__ ? 0.f : m * sc;
+      most = raised_by(m, GROW, sc);
+      mref = m == -__FLT_MAX__ ? 0.f : fmaf(m, sc, GROW);
       far_any = __any(far());
       const float alpha = first ? 0.f : __builtin_amdgcn_exp2f((old_m - m) * sc + (above() - old_above));
       l *= alpha;
@@ -410,7 +413,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     }
     float less = mref;
     if (__builtin_expect(far_any, 0)) {
-      less = far() ? 0.f : mref;
+      less = far() ? GROW : mref;
       const float before = far() ? m : 0.f;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -566,7 +569,7 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(AttnPromptArgs a) {
     const f4 x = sums[s], v = num[(int64_t)s * T];
     // a range in which the row sees nothing has zeros, one without keys has
     // left what was there
-    const float f = x[0] == -__FLT_MAX__ && x[2] == 0.f ? 0.f : __builtin_amdgcn_exp2f((x[0] - m) * sc - x[1]);
+    const float f = x[0] == -__FLT_MAX__ && x[2] == 0.f ? 0.f : __builtin_amdgcn_exp2f((x[0] - m) * sc - (x[1] + GROW));
     sum += x[2] * f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] += x[3] < 0.f ? 0.f : fabsf(v[e]) < __builtin_inff() ? v[e] * f : v[e];

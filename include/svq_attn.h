@@ -20,21 +20,20 @@
  * Numerics.  Inputs and outputs of the attention calls are bf16.  Scores are
  * products of the bf16 inputs (of the stored values, for the cache) summed in
  * fp32; the softmax's maximum, exponentials and sum are fp32; each output is
- * rounded once, to nearest even.  Over a prompt a weight (at most 2^9, the
- * greatest at least 2^-9 of that) meets its value rounded to bf16.  Over the
- * cache, where codes are multiplied as they are, a query's channel meets the
- * codes with all its bits down to 2^-28 of the greatest magnitude in its group
- * of channels, and within 2^-35 of that magnitude below; the product of a weight
- * and a scale is held in 22 bits, down to 2^-32 of the greatest scale or minimum
- * that the row sees; and of 32 products of codes that are added at once each is
- * kept within 2^-22 of the greatest that any code (15) would give.  Weights below
- * 2^-126 of a row's greatest are zero.  Over a prompt a row's numerators are sums
- * of such weights times values in fp32: from about 2^119 over the number of keys
- * on, finite values may give infinities.  A
- * query that sees no key, or only keys whose scores are minus infinity, gives a
- * row of zeros.  A key that a query does not see has no influence on it, whatever
- * it, its value or its stored scales hold (infinities and NaN included): not a
- * bit of its row changes.
+ * rounded once, to nearest even.
+ *   Over a prompt a weight (at most 2^0.5, a row's greatest at least 2^-9) meets
+ * its value rounded to bf16, and the products' sums are fp32: values from 2^127
+ * over the number of keys on may give infinities, results below 2^-126 are zero.
+ *   Over the cache, where codes are multiplied as they are, a query's channel
+ * meets the codes with all its bits down to 2^-28 of the greatest magnitude in
+ * its group of channels, and within 2^-35 of that magnitude below; the product of
+ * a weight and a scale is held in 22 bits, down to 2^-32 of the greatest scale or
+ * minimum that the row sees; and of 32 products of codes that are added at once
+ * each is kept within 2^-22 of the greatest that any code (15) would give.
+ *   Weights below 2^-117 of a row's greatest are zero.  A query that sees no key,
+ * or only keys whose scores are minus infinity, gives a row of zeros.  A key that
+ * a query does not see has no influence on it, whatever it, its value or its
+ * stored scales hold (infinities and NaN included): not a bit of its row changes.
  */
 #ifndef SVQ_ATTN_H
 #define SVQ_ATTN_H

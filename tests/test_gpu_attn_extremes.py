@@ -229,6 +229,24 @@ def test_smallest_scales_of_great_scores(scale, over_cache):
 
 # ---- values and queries of different sizes ----------------------------------
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n", [100, 1100])  # without and with ranges of keys
+def test_prompt_values_near_the_largest(n, dim):
+    """Later keys whose weights are 2^7 times the first ones', which is no reason
+    for a new reference; values of 2^121, so that 30 of them are a number."""
+    svq = require_gpu()
+    q, k = torch.zeros(1, dim), torch.zeros(n, dim)
+    q[0, 0] = 1.0
+    k[70:100, 0] = 4.875
+    v = torch.sign(_rows(n, dim, 39).float()) * 2.0 ** 121
+    v[:70] = 2.0 ** 100
+    v[100:] = 2.0 ** 90
+    v[70:100, ::2] = 2.0 ** 121
+    q, k, v = q.to(torch.bfloat16).cuda(), k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16)
+    y = svq.attn_prompt(q, k, v, _ints([0, 1]), dim, starts_k=_ints([0, n]), scale=1.0)
+    check(y, *attend(q, k, v, 1, 1, 1.0, visible(1, n, False)), n, P_BF16)
+
+
 @pytest.mark.parametrize("dim,group", FORMS)
 @pytest.mark.parametrize("size", [2.0 ** -112, 2.0 ** -105, 2.0 ** -88, 2.0 ** 90, 2.0 ** 110, 2.0 ** 122])
 def test_cache_values_of_one_size(size, dim, group):
