@@ -29,7 +29,7 @@
 //
 // What bounds it: over long prompts the matrix unit with the clock that the
 // power allows (65 % of the cycles busy; 16384 tokens, 32 heads of 128 channels,
-// causal: 1950-2040 us from box to box, 1.08-1.13 PFLOP/s, where a library product
+// causal: 1920-2040 us from box to box, 1.08-1.14 PFLOP/s, where a library product
 // of 8192^3 reaches 1.36); at 2048 tokens (44.8 us, 770 TFLOP/s) the block with the most keys,
 // alone on its unit for most of the time at 2650 cycles a tile, 1024 of them the
 // matrix unit's; for short sequences the first loads (5000 to 8000 cycles).

@@ -23,7 +23,7 @@
  * rounded once, to nearest even.
  *   Over a prompt a weight (at most 2^0.5, a row's greatest at least 2^-9) meets
  * its value rounded to bf16, and the products' sums are fp32: values from 2^127
- * over the number of keys on may give infinities, results below 2^-126 are zero.
+ * over the number of keys on may give infinities, results below 2^-122 lose bits.
  *   Over the cache, where codes are multiplied as they are, a query's channel
  * meets the codes with all its bits down to 2^-28 of the greatest magnitude in
  * its group of channels, and within 2^-35 of that magnitude below; the product of
