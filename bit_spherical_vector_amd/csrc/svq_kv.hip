@@ -398,7 +398,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
 //        zero would carry the rounding of its whole range)
 //   M_g[row]          += sum over keys of p m_g                (fp32, in the same units)
 //
-// and the row is 2^(E - 8) (2^24 O + M) / sum p.  The weight p is exp2 of (score
+// and the row is 2^(E - 8) (2^20 O + M) / sum p.  The weight p is exp2 of (score
 // - m) times the scale: m a running maximum, raised once a weight exceeds 2^6, E
 // the exponent of the greatest scale or minimum that the row sees in a wave's
 // first chunk, raised once a p s_g overflows fp16.  The two are kept apart: in

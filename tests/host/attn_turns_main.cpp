@@ -1,7 +1,10 @@
 // The turns of a prompt's tiles over all launches of a call, on the CPU: every
-// tile has one, in whatever number of launches.  Built with AddressSanitizer and
+// tile has one, in whatever number of launches; and the scores up to which a row
+// keeps its maximum, for scales and maxima of every size.  Built with AddressSanitizer and
 // UndefinedBehaviorSanitizer by tests/test_attn_turns_host.py.
+#include <cmath>
 #include <cstdio>
+#include <cstring>
 #include <random>
 #include <vector>
 
@@ -60,6 +63,21 @@ int main() {
           const int tokens = i < 4 ? pick(1, 70000) : pick(1, 1 << 20);
           check(tokens, sequences, kv * sh, kv, u);
         }
+  // raised_by: not below the maximum, not more than asked for above it, and not
+  // the maximum itself where fp32 has scores between
+  for (int i = 0; i < 200000; ++i) {
+    auto any = [&](int lo, int hi) { return std::ldexp(1.f + (float)(rng() & 0x7FFFFF) * 0x1p-23f, pick(lo, hi)); };
+    const float scale = i % 97 == 0 ? 0.f : any(-149, 127), sc = exponent_scale(i % 2 ? scale : -scale);
+    if (!(sc > 0.f) || !std::isfinite(sc)) ++fails;
+    const float m = i % 11 == 0 ? 0.f : (i % 2 ? 1.f : -1.f) * any(-149, 126), by = i % 3 ? 8.f : 6.f;
+    const float to = raised_by(m, by, sc);
+    const float room = (std::nextafterf(m, INFINITY) - m) * sc;
+    if (!(to >= m) || !((to - m) * sc <= by) || (room < 0.25f && std::isfinite(m + by / sc) && !((to - m) * sc > by - 0.75f) && sc > 1e-37f && sc < 1e37f)) {
+      std::fprintf(stderr, "raised_by(%g, %g, %g) = %g\n", m, by, sc, to);
+      ++fails;
+    }
+  }
+  if (raised_by(-3.40282347e38f, 8.f, 0.1f) != -3.40282347e38f) ++fails;  // no maximum yet
   std::printf("%ld plans, %ld of several launches, %ld of them in two directions, %d failures\n", plans, several, both_ways, fails);
   return fails != 0 || several == 0 || both_ways == 0;
 }
